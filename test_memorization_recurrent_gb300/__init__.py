@@ -2,7 +2,8 @@
 
 The binding only marshals arguments: it turns torch tensors into device
 pointers, fills the ``atlas_mem_cfg`` struct and calls the C entry points of
-``include/atlas_mem.h`` with the same names.  Every step of the update runs
+``include/atlas_mem.h`` with the same names (``ops`` does so for the layer operators
+of ``include/atlas_ops.h``).  Every step of the update runs
 in the library's CUDA kernels; if the library is missing or cannot be loaded,
 importing a function here raises -- there is no CPU fallback.
 """
@@ -12,6 +13,14 @@ import ctypes
 import os
 import threading
 
+from . import ops as _ops
+from .ops import (ACT_NONE, ACT_SILU, BF16, CONV_MAX_W, E4M3, F16, F32, NORM_MAX_D, OPS_EXPORTS,
+                  SCAN_MAX_N, AtlasConvCfg, AtlasNormCfg, AtlasScanCfg, atlas_conv_backward,
+                  atlas_conv_backward_workspace_bytes, atlas_conv_forward, atlas_norm_backward,
+                  atlas_norm_backward_workspace_bytes, atlas_norm_forward, atlas_scan_backward,
+                  atlas_scan_backward_workspace_bytes, atlas_scan_forward,
+                  atlas_scan_workspace_bytes, make_conv_cfg, make_norm_cfg, make_scan_cfg)
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libatlasmem.so")
 
@@ -20,7 +29,6 @@ PHI_IDENTITY, PHI_POLY2, PHI_POLY = 0, 1, 2
 PHI_MAX_DEGREE = 4
 LOSS_L2, LOSS_DOT, LOSS_LP, LOSS_HUBER, LOSS_ROBUST = 0, 1, 2, 3, 4
 RET_L2, RET_ELASTIC, RET_BREGMAN, RET_KL, RET_LQ = 0, 1, 2, 3, 4
-F32, BF16 = 0, 1
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 
@@ -84,6 +92,7 @@ def open_library(path: str):
     lib.atlas_mem_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.atlas_mem_backward.argtypes = [vp] * 7 + [cp] + [vp] * 10
     lib.atlas_mem_backward.restype = ctypes.c_int
+    _ops.declare(lib)
     return lib
 
 

@@ -28,7 +28,7 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        [os.path.join(ROOT, "include", "atlas_mem.h")]
+        glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -1,0 +1,191 @@
+// ops_common.cuh -- helpers of the layer operators (norm, conv, scan): elements of
+// a type known at run or compile time, the tiling of (packed) sequences, and
+// reductions over groups of lanes.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "atlas_ops.h"
+#include "common.cuh"
+#include "ops.h"
+
+namespace atlas {
+
+// ------------------------------------------------------------------ elements
+
+__device__ __forceinline__ float to_f(float v) { return v; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// V consecutive elements as one aligned block of registers.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T e[V];
+  __device__ __forceinline__ float get(int i) const { return to_f(e[i]); }
+  __device__ __forceinline__ void set(int i, float v) { e[i] = from_f<T>(v); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < V; ++i) e[i] = from_f<T>(0.f);
+  }
+};
+
+// V elements from p; aligned to V elements when V > 1.  Inputs that are read once go
+// past L1.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> ld_pack(const T* p) {
+  return *reinterpret_cast<const Pack<T, V>*>(p);
+}
+template <typename T, int V>
+__device__ __forceinline__ void st_pack(T* p, const Pack<T, V>& v) {
+  *reinterpret_cast<Pack<T, V>*>(p) = v;
+}
+
+// Element of a type known at run time (parameters, read once per block).
+__device__ __forceinline__ float ld_any(const void* p, long i, int dtype) {
+  if (dtype == ATLAS_BF16) return to_f(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
+  if (dtype == ATLAS_F16) return to_f(reinterpret_cast<const __half*>(p)[i]);
+  return reinterpret_cast<const float*>(p)[i];
+}
+
+// ------------------------------------------------------------------ functions
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+#define ATLAS_LOG2E 1.4426950408889634f
+// 1 / (1 + exp(-x)); for x < -88 the exponential is infinite and the result 0.
+__device__ __forceinline__ float sigmoidf(float x) { return rcp(1.f + ex2(-ATLAS_LOG2E * x)); }
+// x sigmoid(x), 0 at -infinity.
+__device__ __forceinline__ float siluf(float x) {
+  const float s = sigmoidf(x);
+  return s == 0.f ? 0.f : x * s;
+}
+// d/dx (x sigmoid(x)) given s = sigmoid(x).
+__device__ __forceinline__ float silu_slope(float x, float s) {
+  return s == 0.f ? 0.f : s * (1.f + x * (1.f - s));
+}
+// log(1 + exp(x)); above 20 it is x to 32-bit precision.
+__device__ __forceinline__ float softplusf(float x) { return x > 20.f ? x : log1pf(__expf(x)); }
+
+// ------------------------------------------------------------------ sequences
+
+// Tiles of TT tokens.  With seq_start, tile numbers are handed out so that a tile
+// belongs to one sequence without a prefix sum over lengths: sequence b has the numbers
+// start[b] / TT + b .. start[b + 1] / TT + b, at least as many as its ceil(len / TT)
+// tiles and at least one; L / TT + B numbers in all.
+struct SeqTile {
+  int b;      // sequence
+  int t0;     // the tile's first token in the sequence
+  int len;    // the sequence's tokens
+  int first;  // row of the sequence's first token (packed), 0 otherwise
+  int slot;   // its state
+  bool carry; // whether it starts from its state
+};
+
+inline __host__ __device__ int seq_tiles_of(int L, int TT) { return L > TT ? (L + TT - 1) / TT : 1; }
+
+// Number of tile numbers for a description.
+inline __host__ __device__ long seq_tiles(const SeqArgs& a, int TT) {
+  if (a.B == 0) return 0;
+  return a.start ? (long)a.L / TT + a.B : (long)a.B * seq_tiles_of(a.L, TT);
+}
+
+// Which tile number `i` is; false when it is none (or its sequence is left out).  Called
+// by whole warps with the same i.
+__device__ __forceinline__ bool seq_tile(const SeqArgs& a, long i, int TT, SeqTile& t) {
+  if (a.start) {
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      const int s = min(max(a.start[mid], 0), a.L);
+      if ((long)s / TT + mid <= i) lo = mid; else hi = mid - 1;
+    }
+    const int s = a.start[lo], e = a.start[lo + 1];
+    if (s < 0 || e < s || e > a.L) return false;  // reported by seq_check
+    t.b = lo;
+    t.first = s;
+    t.len = e - s;
+    const long k = i - ((long)s / TT + lo);
+    if (k < 0 || (k > 0 && k * TT >= t.len)) return false;
+    t.t0 = (int)k * TT;
+  } else {
+    const int n = seq_tiles_of(a.L, TT);
+    t.b = (int)(i / n);
+    t.t0 = (int)(i % n) * TT;
+    t.first = 0;
+    t.len = a.L;
+  }
+  t.slot = t.b;
+  if (a.slot) {
+    t.slot = a.slot[t.b];
+    const int lane = threadIdx.x & 31;
+    bool bad = t.slot < 0 || t.slot >= a.n_slots;
+    for (int j = lane; j < t.b; j += 32) bad |= a.slot[j] == t.slot;
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+      if (a.status && t.slot >= 0 && t.t0 == 0 && lane == 0) *a.status = ATLAS_ERR_INVALID;
+      return false;
+    }
+  }
+  t.carry = a.carry ? a.carry[t.b] != 0 : true;
+  return true;
+}
+
+// Report a bad seq_start: called by the threads of one block of the grid.
+__device__ __forceinline__ void seq_check(const SeqArgs& a, int tid, int nthr) {
+  if (!a.start || !a.status) return;
+  for (int b = tid; b < a.B; b += nthr) {
+    const int s = a.start[b], e = a.start[b + 1];
+    if (s < 0 || e < s || e > a.L) *a.status = ATLAS_ERR_INVALID;
+  }
+}
+
+// Offset of token t of the tile's sequence.
+__device__ __forceinline__ long seq_at(const SeqArgs& a, const SeqTile& t, int tok, long sb, long st) {
+  return a.start ? (long)(t.first + tok) * st : (long)t.b * sb + (long)tok * st;
+}
+
+// ------------------------------------------------------------------ reductions
+
+// Sums NV values over LANES lanes (lane bits STRIDE .. STRIDE * LANES / 2) by halving: each
+// step sends half of the values and keeps the sums of the other half.  With NV >= LANES
+// the lane numbered j among the LANES is left with v[0 .. NV / LANES) = the sums of values
+// j * NV / LANES ..; with NV < LANES, value j * NV / LANES is left in LANES / NV lanes.
+template <int NV, int LANES, int STRIDE>
+__device__ __forceinline__ void lane_sums(float* v, int lane) {
+  if constexpr (LANES > 1) {
+    constexpr int M = LANES / 2 * STRIDE;
+    if constexpr (NV > 1) {
+      constexpr int H = NV / 2;
+      const bool up = lane & M;
+#pragma unroll
+      for (int i = 0; i < H; ++i) {
+        const float send = up ? v[i] : v[i + H];
+        const float keep = up ? v[i + H] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, M);
+      }
+      lane_sums<H, LANES / 2, STRIDE>(v, lane);
+    } else {
+      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], M);
+      lane_sums<1, LANES / 2, STRIDE>(v, lane);
+    }
+  }
+}
+
+}  // namespace atlas

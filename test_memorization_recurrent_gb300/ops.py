@@ -1,0 +1,342 @@
+"""Python binding of include/atlas_ops.h: norm, short convolution and selective scan.
+
+Like the binding of the memory update it only marshals: ``make_*_cfg`` fills a C
+description, the calls turn torch tensors into device pointers, enqueue on a stream and
+raise ``AtlasError`` on a non-zero status.  Tensor arguments are checked before the call:
+an element type other than the description's, a tensor that is not on the current CUDA
+device, or one that ends before the elements the description names raises
+``AtlasError(ERR_INVALID)``.  Raw device pointers (ints) are passed on as they are.
+"""
+from __future__ import annotations
+
+import ctypes
+
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
+ACT_NONE, ACT_SILU = 0, 1
+NORM_MAX_D, CONV_MAX_W, SCAN_MAX_N = 32768, 8, 128
+
+OPS_EXPORTS = ("atlas_norm_forward", "atlas_norm_backward", "atlas_norm_backward_workspace_bytes",
+               "atlas_conv_forward", "atlas_conv_backward", "atlas_conv_backward_workspace_bytes",
+               "atlas_scan_forward", "atlas_scan_workspace_bytes", "atlas_scan_backward",
+               "atlas_scan_backward_workspace_bytes")
+
+_int, _long, _vp, _size = ctypes.c_int, ctypes.c_long, ctypes.c_void_p, ctypes.c_size_t
+
+
+class AtlasNormCfg(ctypes.Structure):
+    """Mirror of ``atlas_norm_cfg`` in include/atlas_ops.h."""
+    _fields_ = [("rows", _long), ("d", _int), ("dtype", _int), ("r_dtype", _int),
+                ("w_dtype", _int), ("out_dtype", _int), ("group", _int), ("eps", ctypes.c_float),
+                ("x_stride", _long), ("r_stride", _long), ("y_stride", _long),
+                ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class AtlasConvCfg(ctypes.Structure):
+    """Mirror of ``atlas_conv_cfg`` in include/atlas_ops.h."""
+    _fields_ = [("B", _int), ("L", _int), ("C", _int), ("W", _int), ("act", _int), ("dtype", _int),
+                ("w_dtype", _int), ("head_dim", _int), ("x_batch_stride", _long),
+                ("x_token_stride", _long), ("y_batch_stride", _long), ("y_token_stride", _long),
+                ("y_head_stride", _long), ("seq_start", _vp), ("slot", _vp), ("n_slots", _int),
+                ("carry", _vp), ("status_dev", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+class AtlasScanCfg(ctypes.Structure):
+    """Mirror of ``atlas_scan_cfg`` in include/atlas_ops.h."""
+    _fields_ = [("B", _int), ("L", _int), ("D", _int), ("N", _int), ("G", _int), ("dtype", _int),
+                ("softplus", _int), ("x_batch_stride", _long), ("x_token_stride", _long),
+                ("dt_batch_stride", _long), ("dt_token_stride", _long), ("z_batch_stride", _long),
+                ("z_token_stride", _long), ("y_batch_stride", _long), ("y_token_stride", _long),
+                ("b_batch_stride", _long), ("b_token_stride", _long), ("c_batch_stride", _long),
+                ("c_token_stride", _long), ("seq_start", _vp), ("slot", _vp), ("n_slots", _int),
+                ("carry", _vp), ("status_dev", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
+def declare(lib) -> None:
+    """Argument types of the operators' entry points in an opened library."""
+    norm, conv, scan = (ctypes.POINTER(c) for c in (AtlasNormCfg, AtlasConvCfg, AtlasScanCfg))
+    lib.atlas_norm_forward.argtypes = [_vp] * 3 + [norm] + [_vp] * 4
+    lib.atlas_norm_backward.argtypes = [_vp] * 4 + [norm] + [_vp] * 3
+    lib.atlas_conv_forward.argtypes = [_vp] * 3 + [conv] + [_vp] * 4
+    lib.atlas_conv_backward.argtypes = [_vp] * 3 + [conv] + [_vp] * 7
+    lib.atlas_scan_forward.argtypes = [_vp] * 8 + [scan] + [_vp] * 4
+    lib.atlas_scan_backward.argtypes = [_vp] * 8 + [scan] + [_vp] * 12
+    for name in OPS_EXPORTS:
+        getattr(lib, name).restype = _size if name.endswith("_bytes") else _int
+    lib.atlas_norm_backward_workspace_bytes.argtypes = [norm]
+    lib.atlas_conv_backward_workspace_bytes.argtypes = [conv]
+    lib.atlas_scan_workspace_bytes.argtypes = [scan]
+    lib.atlas_scan_backward_workspace_bytes.argtypes = [scan]
+
+
+# ------------------------------------------------------------------ descriptions
+
+def make_norm_cfg(rows, d, dtype=BF16, r_dtype=None, w_dtype=None, out_dtype=None, group=0,
+                  eps=1e-6, x_stride=0, r_stride=0, y_stride=0, workspace=None,
+                  workspace_bytes=0) -> AtlasNormCfg:
+    """rows x d norm; r_dtype, w_dtype and out_dtype default to dtype.  group: channels per
+    scale of an E4M3 output (0: one scale a row).  Strides in elements, 0 = d."""
+    def or_dtype(t):
+        return int(dtype if t is None else t)
+    cfg = AtlasNormCfg(int(rows), int(d), int(dtype), or_dtype(r_dtype), or_dtype(w_dtype),
+                       or_dtype(out_dtype), int(group), float(eps), int(x_stride), int(r_stride),
+                       int(y_stride), _addr(workspace), int(workspace_bytes))
+    cfg.held = workspace
+    return cfg
+
+
+def make_conv_cfg(B, L, C, W, act=ACT_SILU, dtype=BF16, w_dtype=None, head_dim=0,
+                  x_strides=(0, 0), y_strides=(0, 0, 0), seq_start=None, slot=None, n_slots=0,
+                  carry=None, status_dev=None, workspace=None, workspace_bytes=0) -> AtlasConvCfg:
+    """x_strides: (batch, token), y_strides: (batch, token, head) in elements, all 0 =
+    contiguous.  seq_start, slot, carry, status_dev: device tensors (int32 [B + 1],
+    int32 [B], uint8 [B], int32 [1]), which the description holds on to."""
+    xb, xt = x_strides
+    yb, yt, yh = tuple(y_strides) + (0,) * (3 - len(y_strides))
+    cfg = AtlasConvCfg(int(B), int(L), int(C), int(W), int(act), int(dtype),
+                       int(dtype if w_dtype is None else w_dtype), int(head_dim), int(xb), int(xt),
+                       int(yb), int(yt), int(yh), *_sequences(B, seq_start, slot, n_slots, carry),
+                       _checked(status_dev, "int32", 1, "status_dev"), _addr(workspace),
+                       int(workspace_bytes))
+    cfg.held = (seq_start, slot, carry, status_dev, workspace)  # as long as the description
+    return cfg
+
+
+def make_scan_cfg(B, L, D, N, G=1, dtype=BF16, softplus=True, x_strides=(0, 0),
+                  dt_strides=(0, 0), z_strides=(0, 0), y_strides=(0, 0), B_strides=(0, 0),
+                  C_strides=(0, 0), seq_start=None, slot=None, n_slots=0, carry=None,
+                  status_dev=None, workspace=None, workspace_bytes=0) -> AtlasScanCfg:
+    """Strides: (batch, token) in elements, (0, 0) = contiguous.  Device tensors as for
+    ``make_conv_cfg``."""
+    s = [int(v) for p in (x_strides, dt_strides, z_strides, y_strides, B_strides, C_strides)
+         for v in p]
+    cfg = AtlasScanCfg(int(B), int(L), int(D), int(N), int(G), int(dtype), int(bool(softplus)),
+                       *s, *_sequences(B, seq_start, slot, n_slots, carry),
+                       _checked(status_dev, "int32", 1, "status_dev"), _addr(workspace),
+                       int(workspace_bytes))
+    cfg.held = (seq_start, slot, carry, status_dev, workspace)
+    return cfg
+
+
+# ------------------------------------------------------------------ arguments
+
+def _error(msg):
+    from . import ERR_INVALID, AtlasError
+    return AtlasError(ERR_INVALID, msg)
+
+
+def _addr(t):
+    return None if t is None else t if isinstance(t, int) else t.data_ptr()
+
+
+def _checked(t, dtype, n, name):
+    """Address of a contiguous device tensor of at least n elements of a named type."""
+    if t is None or isinstance(t, int):
+        return t
+    import torch
+    if t.dtype != getattr(torch, dtype) or not t.is_cuda or t.numel() < n or not t.is_contiguous():
+        raise _error(f"{name} must be a contiguous {dtype} CUDA tensor of at least {n} elements")
+    return t.data_ptr()
+
+
+def _sequences(B, seq_start, slot, n_slots, carry):
+    return (_checked(seq_start, "int32", int(B) + 1, "seq_start"),
+            _checked(slot, "int32", int(B), "slot"), int(n_slots),
+            _checked(carry, "uint8", int(B), "carry"))
+
+
+_torch = None
+_types = None
+
+
+def _setup():
+    global _torch, _types
+    import torch
+    _types = (torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn)
+    _torch = torch
+
+
+class _Args:
+    """Checks one call's tensors against what its description says and turns them into
+    addresses."""
+    __slots__ = ("device",)
+
+    def __init__(self):
+        if _torch is None:
+            _setup()
+        self.device = _torch.cuda.current_device()
+
+    def __call__(self, t, code, extent, name):
+        """t: tensor, address or None; extent: elements from its first to its last one."""
+        if t is None or isinstance(t, int):
+            return t
+        if t.dtype is not _types[code]:
+            raise _error(f"{name} is {t.dtype}, the description says {_types[code]}")
+        if t.get_device() != self.device:
+            raise _error(f"{name} is not on the current device (cuda:{self.device})")
+        if t.numel() < extent:  # a strided view ends further on than its elements count
+            if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent:
+                raise _error(f"{name} ends before the {extent} elements the description names")
+        return t.data_ptr()
+
+
+def _stream(stream):
+    if stream is None:
+        return _torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _raise(rc):
+    if rc != 0:
+        from . import AtlasError, atlas_mem_strerror
+        raise AtlasError(rc, atlas_mem_strerror(rc))
+
+
+def _lib():
+    from . import load_library
+    return load_library()
+
+
+def _bytes(fn, cfg):
+    n = int(getattr(_lib(), fn)(ctypes.byref(cfg)))
+    if n == 2 ** 64 - 1:
+        raise _error("invalid or uncovered description")
+    return n
+
+
+def _tokens(cfg, sb, st, width):
+    """Elements from the first to the last one of a [B, L, width] tensor (packed: [L, width])."""
+    if cfg.L < 1 or cfg.B < 1:
+        return 0
+    if not sb and not st:
+        return (1 if cfg.seq_start else cfg.B) * cfg.L * width
+    return (0 if cfg.seq_start else (cfg.B - 1) * sb) + (cfg.L - 1) * st + width
+
+
+def _rows(cfg, stride):
+    return (cfg.rows - 1) * (stride or cfg.d) + cfg.d if cfg.rows > 0 else 0
+
+
+# ------------------------------------------------------------------ norm
+
+def atlas_norm_forward(x, residual, weight, cfg: AtlasNormCfg, y, residual_out=None, scale=None,
+                       stream=None) -> None:
+    """y = norm(x + residual) * weight; residual_out receives x + residual, scale the scales
+    of an E4M3 output.  residual, weight and residual_out may be None."""
+    p = _Args()
+    d, rows, r = cfg.d, cfg.rows, _rows(cfg, cfg.r_stride)
+    groups = 1 if cfg.group <= 0 or cfg.group >= d else -(-d // cfg.group)
+    _raise(_lib().atlas_norm_forward(
+        p(x, cfg.dtype, _rows(cfg, cfg.x_stride), "x"), p(residual, cfg.r_dtype, r, "residual"),
+        p(weight, cfg.w_dtype, d, "weight"), cfg, p(y, cfg.out_dtype, _rows(cfg, cfg.y_stride), "y"),
+        p(residual_out, cfg.r_dtype, r, "residual_out"), p(scale, F32, rows * groups, "scale"),
+        _stream(stream)))
+
+
+def atlas_norm_backward_workspace_bytes(cfg: AtlasNormCfg) -> int:
+    return _bytes("atlas_norm_backward_workspace_bytes", cfg)
+
+
+def atlas_norm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, stream=None) -> None:
+    """dx = dL/dh and dw = dL/d weight from dy = dL/dy and (or None) dh, the gradient that
+    reaches the residual stream from later layers."""
+    p = _Args()
+    r = _rows(cfg, cfg.r_stride)
+    _raise(_lib().atlas_norm_backward(
+        p(h, cfg.r_dtype, r, "h"), p(weight, cfg.w_dtype, cfg.d, "weight"),
+        p(dy, cfg.dtype, _rows(cfg, cfg.y_stride), "dy"), p(dh, cfg.r_dtype, r, "dh"), cfg,
+        p(dx, cfg.r_dtype, r, "dx"), p(dw, F32, cfg.d, "dw"), _stream(stream)))
+
+
+# ------------------------------------------------------------------ conv
+
+def _conv_y(cfg):
+    hd = cfg.head_dim
+    if not hd:
+        return _tokens(cfg, cfg.y_batch_stride, cfg.y_token_stride, cfg.C)
+    if cfg.L < 1 or cfg.B < 1:
+        return 0
+    if not (cfg.y_batch_stride or cfg.y_token_stride or cfg.y_head_stride):
+        return (1 if cfg.seq_start else cfg.B) * cfg.L * cfg.C
+    return ((0 if cfg.seq_start else (cfg.B - 1) * cfg.y_batch_stride)
+            + (cfg.C // hd - 1) * cfg.y_head_stride + (cfg.L - 1) * cfg.y_token_stride + hd)
+
+
+def atlas_conv_forward(x, weight, bias, cfg: AtlasConvCfg, y, state_in=None, state_out=None,
+                       stream=None) -> None:
+    """Short causal convolution of every channel; L = 1 is the single-token form.  state_in
+    and state_out ([B or n_slots, W - 1, C]) may be None or the same tensor."""
+    p = _Args()
+    C, W, t = cfg.C, cfg.W, cfg.dtype
+    n = (cfg.n_slots if cfg.slot else cfg.B) * (W - 1) * C
+    _raise(_lib().atlas_conv_forward(
+        p(x, t, _tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, C), "x"),
+        p(weight, cfg.w_dtype, C * W, "weight"), p(bias, cfg.w_dtype, C, "bias"), cfg,
+        p(y, t, _conv_y(cfg), "y"), p(state_in, t, n, "state_in"), p(state_out, t, n, "state_out"),
+        _stream(stream)))
+
+
+def atlas_conv_backward_workspace_bytes(cfg: AtlasConvCfg) -> int:
+    return _bytes("atlas_conv_backward_workspace_bytes", cfg)
+
+
+def atlas_conv_backward(x, weight, bias, cfg: AtlasConvCfg, state_in, dy, dstate, dx, dw, dbias,
+                        stream=None) -> None:
+    """Gradients of the convolution (see include/atlas_ops.h); dstate is dL/d state_out on
+    entry and dL/d state_in on return."""
+    p = _Args()
+    C, W, t = cfg.C, cfg.W, cfg.dtype
+    n, nx = cfg.B * (W - 1) * C, _tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, C)
+    _raise(_lib().atlas_conv_backward(
+        p(x, t, nx, "x"), p(weight, cfg.w_dtype, C * W, "weight"), p(bias, cfg.w_dtype, C, "bias"),
+        cfg, p(state_in, t, n, "state_in"), p(dy, t, _conv_y(cfg), "dy"),
+        p(dstate, F32, n, "dstate"), p(dx, t, nx, "dx"), p(dw, F32, C * W, "dw"),
+        p(dbias, F32, C, "dbias"), _stream(stream)))
+
+
+# ------------------------------------------------------------------ scan
+
+def atlas_scan_workspace_bytes(cfg: AtlasScanCfg) -> int:
+    return _bytes("atlas_scan_workspace_bytes", cfg)
+
+
+def atlas_scan_backward_workspace_bytes(cfg: AtlasScanCfg) -> int:
+    return _bytes("atlas_scan_backward_workspace_bytes", cfg)
+
+
+def _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg):
+    t, D, gn = cfg.dtype, cfg.D, cfg.G * cfg.N
+    n = (_tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, D),
+         _tokens(cfg, cfg.dt_batch_stride, cfg.dt_token_stride, D),
+         _tokens(cfg, cfg.b_batch_stride, cfg.b_token_stride, gn),
+         _tokens(cfg, cfg.c_batch_stride, cfg.c_token_stride, gn),
+         _tokens(cfg, cfg.z_batch_stride, cfg.z_token_stride, D),
+         _tokens(cfg, cfg.y_batch_stride, cfg.y_token_stride, D))
+    return n, (p(x, t, n[0], "x"), p(dt, t, n[1], "dt"), p(A, F32, D * cfg.N, "A"),
+               p(Bm, t, n[2], "B"), p(Cm, t, n[3], "C"), p(Dskip, F32, D, "Dskip"),
+               p(z, t, n[4], "z"), p(dt_bias, F32, D, "dt_bias"))
+
+
+def atlas_scan_forward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, y, h_in=None,
+                       h_out=None, stream=None) -> None:
+    """Selective scan; L = 1 is the single-token form.  Dskip, z, dt_bias, h_in and h_out
+    may be None; h_in and h_out ([B or n_slots, D, N]) may be the same tensor."""
+    p = _Args()
+    n, inputs = _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg)
+    s = (cfg.n_slots if cfg.slot else cfg.B) * cfg.D * cfg.N
+    _raise(_lib().atlas_scan_forward(*inputs, cfg, p(y, cfg.dtype, n[5], "y"),
+                                     p(h_in, F32, s, "h_in"), p(h_out, F32, s, "h_out"),
+                                     _stream(stream)))
+
+
+def atlas_scan_backward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, h_in, dy, dh, dx,
+                        ddt, dA, dB, dC, dD, dz, ddt_bias, stream=None) -> None:
+    """Gradients of the scan (see include/atlas_ops.h); dh is dL/d h_out on entry and
+    dL/d h_in on return."""
+    p = _Args()
+    n, inputs = _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg)
+    t, D, s = cfg.dtype, cfg.D, cfg.B * cfg.D * cfg.N
+    _raise(_lib().atlas_scan_backward(
+        *inputs, cfg, p(h_in, F32, s, "h_in"), p(dy, t, n[5], "dy"), p(dh, F32, s, "dh"),
+        p(dx, t, n[0], "dx"), p(ddt, t, n[1], "ddt"), p(dA, F32, D * cfg.N, "dA"),
+        p(dB, t, n[2], "dB"), p(dC, t, n[3], "dC"), p(dD, F32, D, "dD"), p(dz, t, n[4], "dz"),
+        p(ddt_bias, F32, D, "ddt_bias"), _stream(stream)))
