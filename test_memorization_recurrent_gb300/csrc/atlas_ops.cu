@@ -186,6 +186,12 @@ bool scan_wide(const ScanArgs& a) {
   return true;
 }
 
+bool scan_wide_n(const ScanArgs& a) {
+  const int v = 16 / size_of(a.type);
+  return a.N % v == 0 && a.bb % v == 0 && a.bt % v == 0 && a.cb % v == 0 && a.ct % v == 0 &&
+         aligned(a.Bm, 16) && aligned(a.Cm, 16);
+}
+
 }  // namespace
 
 extern "C" {
@@ -339,6 +345,7 @@ int atlas_scan_forward(const void* x, const void* dt, const float* A, const void
   a.h_out = h_out;
   a.ws = cfg->workspace;
   a.wide = scan_wide(a);
+  a.wide_n = scan_wide_n(a);
   return scan_forward_launch(a, stream_of(stream));
 }
 
@@ -398,6 +405,7 @@ int atlas_scan_backward(const void* x, const void* dt, const float* A, const voi
   a.dbias = ddt_bias;
   a.ws = cfg->workspace;
   a.wide = scan_wide(a);
+  a.wide_n = scan_wide_n(a);
   return scan_backward_launch(a, stream_of(stream));
 }
 

@@ -73,7 +73,8 @@ struct ScanArgs {
   void* ws;
   int D, N, G, type, softplus;
   long xb, xt, tb, tt, zb, zt, yb, yt, bb, bt, cb, ct;
-  int wide;  // x, dt, z, y allow 16-byte accesses
+  int wide;    // x, dt, z, y allow 16-byte accesses
+  int wide_n;  // and so do B and C
   // backward
   const void* dy;
   float* dh;

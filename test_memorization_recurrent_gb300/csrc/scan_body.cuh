@@ -3,194 +3,419 @@
 //
 //   h_t = exp(dt_t A) h_{t-1} + dt_t x_t B_t,   y_t = (C_t h_t + D x_t) SiLU(z_t)
 //
-// A channel's N states are split over LN lanes with four states a lane, the channel's y is
-// their sum: batches of four tokens are added by halving (three shuffles for four tokens).
-// x, dt, B, C of a tile of tokens lie in shared memory, where softplus has been taken once
-// per token and channel.
+// A lane holds two channels x four states; the N states of a channel are split over LN lanes,
+// whose sums over states are added by halving, four tokens at a time.  A block is two warps.
+// The second takes softplus of a tile's dt, once per token and channel, and writes dt, dt x,
+// B and C to shared memory while the first walks the tile before, and gates and stores the
+// tile before that: one warp alone leaves most issue slots empty.  What bounds the loop is what it reads there (four states'
+// B and C and two channels' steps for eight states' updates, 1.04 cycles of an SM for 32
+// updates against 1 for their exponentials) and instruction issue, so neighbouring lanes
+// share B and C: a load whose lanes agree in pairs takes half the time of one whose
+// addresses repeat every four lanes (2.2 against 4.0 cycles for 16 bytes a lane).
 //
 // When sequences times channels do not fill the machine, the tokens are split into
 // segments: a first pass finds each segment's end state from a zero start (with the sum of
 // its dt: the decay over a segment is exp(A sum dt)), a second one joins them into start
 // states, the third computes the outputs.
 #pragma once
+#include <type_traits>
+
 #include "ops_common.cuh"
 
 namespace atlas {
 namespace scan {
 
-constexpr int kThreads = 128;
-constexpr int kTile = 32;  // tokens in shared memory
+constexpr int kThreads = 32;  // of each of a block's two warps
+constexpr int kTile = 16;     // tokens in shared memory
+constexpr int kRing = 5;      // tiles as they lie in memory: one to finish, one with the other
+                              // warp, one to prepare, two under way
 
 template <int LN>
 struct Shape {
-  static constexpr int kNP = 4 * LN;               // padded states
-  static constexpr int kCW = 32 / LN;              // channels of a warp
-  static constexpr int kCB = kCW * kThreads / 32;  // channels of a block
+  static constexpr int kNP = 4 * LN;       // padded states
+  static constexpr int kPairs = 32 / LN;   // pairs of channels of a block
+  static constexpr int kCB = 2 * kPairs;   // its channels
 };
 
 // The block's channels: blocks do not cross groups.
 struct Channels {
   int c0, n, g;  // first, count, group
 };
-template <int LN>
-__device__ __forceinline__ Channels channels_of(const ScanArgs& a, int by) {
-  const int per = a.D / a.G, bpg = (per + Shape<LN>::kCB - 1) / Shape<LN>::kCB;
+template <int CB>
+__device__ __forceinline__ Channels channels_at(const ScanArgs& a, int by) {
+  const int per = a.D / a.G, bpg = (per + CB - 1) / CB;
   Channels k;
   k.g = by / bpg;
-  const int at = (by % bpg) * Shape<LN>::kCB;
+  const int at = (by % bpg) * CB;
   k.c0 = k.g * per + at;
-  k.n = min(Shape<LN>::kCB, per - at);
+  k.n = min(CB, per - at);
   return k;
 }
-template <int LN>
-inline int channel_blocks(const ScanArgs& a) {
+template <int CB>
+inline int blocks_over(const ScanArgs& a) {
   const int per = a.D / a.G;
-  return a.G * ((per + Shape<LN>::kCB - 1) / Shape<LN>::kCB);
+  return a.G * ((per + CB - 1) / CB);
 }
 
-// dt of a token and channel from its raw value.
-__device__ __forceinline__ float step_of(const ScanArgs& a, float raw, int c) {
-  const float r = a.bias ? raw + a.bias[c] : raw;
-  return a.softplus ? softplusf(r) : r;
+// Rows of one tensor from a tile's sequence: row tok at p + tok * st.
+template <typename T>
+__device__ __forceinline__ const T* rows_of(const void* p, const ScanArgs& a, const SeqTile& t, long sb,
+                                            long st, int c) {
+  return reinterpret_cast<const T*>(p) + seq_at(a.s, t, 0, sb, st) + c;
 }
 
-// Tokens t0 .. t0 + TT of dt (through softplus) and x into sd, those past `end` as zeros.
-template <typename T, int V, int LN, int TT>
-__device__ __forceinline__ void load_dx(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                        int t0, int end, float2 (*sd)[Shape<LN>::kCB]) {
-  constexpr int CV = Shape<LN>::kCB / V;
-  for (int i = threadIdx.x; i < TT * CV; i += kThreads) {
-    const int u = i / CV, cl = (i % CV) * V;
-    if (t0 + u < end && cl < k.n) {
-      const auto x = ld_pack<T, V>(reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, t0 + u, a.xb, a.xt) + k.c0 + cl);
-      const auto d = ld_pack<T, V>(reinterpret_cast<const T*>(a.dt) + seq_at(a.s, t, t0 + u, a.tb, a.tt) + k.c0 + cl);
-#pragma unroll
-      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(step_of(a, d.get(j), k.c0 + cl + j), x.get(j));
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(0.f, 0.f);
-    }
+// A tile of kTile tokens x W elements of a warp: vector i * kThreads + lane, the elements of
+// a token innermost.  The object walks a tensor's rows from tile to tile.
+template <typename T, int V, int W>
+struct Tile {
+  static constexpr int kN = (kTile * W / V + kThreads - 1) / kThreads;
+  static __device__ __forceinline__ int lane() { return threadIdx.x & 31; }
+  static __device__ __forceinline__ int token(int i) { return (i * kThreads + lane()) / (W / V); }
+  static __device__ __forceinline__ int channel(int i) { return (i * kThreads + lane()) % (W / V) * V; }
+  static __device__ __forceinline__ bool inside(int i) {
+    return kTile * W / V % kThreads == 0 || i * kThreads + lane() < kTile * W / V;
   }
-}
+  T* p;      // this lane's first vector of the tile
+  long row;  // elements between tokens
+  // rows from token t0 on at q
+  __device__ __forceinline__ Tile(const T* q, long st, int t0) : row(st) {
+    p = const_cast<T*>(q) + (long)(t0 + token(0)) * st + channel(0);
+  }
+  __device__ __forceinline__ T* at(int i) const {
+    if (i == 0) return p;
+    return p + (token(i) - token(0)) * row + (channel(i) - channel(0));
+  }
+  __device__ __forceinline__ void next() { p += kTile * row; }
+  // the next tile into s; zeros from token `left` on and past element n
+  __device__ __forceinline__ void copy(T (*s)[W], int left, int n) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (!inside(i)) continue;
+      const int u = token(i), c = channel(i);
+      const bool some = u < left && c < n;
+      if constexpr (V * sizeof(T) >= 4) {
+        cp_async<V * sizeof(T)>(&s[u][c], some ? at(i) : p, some);
+      } else {
+        s[u][c] = some ? *at(i) : from_f<T>(0.f);
+      }
+    }
+    next();
+  }
+};
 
-template <typename T, int LN, int TT>
-__device__ __forceinline__ void load_states(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                            int t0, int end, const void* p, long sb, long st,
-                                            float (*s)[Shape<LN>::kNP]) {
-  constexpr int NP = Shape<LN>::kNP;
-  for (int i = threadIdx.x; i < TT * NP; i += kThreads) {
-    const int u = i / NP, n = i % NP;
-    s[u][n] = t0 + u < end && n < a.N
-                  ? to_f(reinterpret_cast<const T*>(p)[seq_at(a.s, t, t0 + u, sb, st) + (long)k.g * a.N + n])
-                  : 0.f;
+// V raw steps of channels c .. c + V to dt.
+template <typename T, int V>
+__device__ __forceinline__ void steps_of(const ScanArgs& a, const Pack<T, V>& raw, const float* bias, float* d) {
+  raw.unpack(d);
+#pragma unroll
+  for (int j = 0; j < V; ++j) d[j] += bias[j];
+  if (a.softplus) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[j] = softplusf(d[j]);
   }
 }
 
 // This lane's four states at p (one channel's N states), 0 past N.
 __device__ __forceinline__ void ld_states4(const float* p, int n0, int N, float* h) {
+  if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if (n0 < N) {
+      const float4 v = *reinterpret_cast<const float4*>(p + n0);
+      h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
+    } else {
+      h[0] = h[1] = h[2] = h[3] = 0.f;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = n0 + i < N ? p[n0 + i] : 0.f;
 }
 __device__ __forceinline__ void st_states4(float* p, int n0, int N, const float* h) {
+  if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+    if (n0 < N) *reinterpret_cast<float4*>(p + n0) = make_float4(h[0], h[1], h[2], h[3]);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (n0 + i < N) p[n0 + i] = h[i];
 }
 
+// Which of a token's pairs of channels lies at place p of its row: a thread stores V
+// neighbouring channels, so the places are turned by the token and the threads of a store
+// fall on different banks, as the pairs of a load do.
+template <int V>
+__device__ __forceinline__ int turned(int u, int p) {
+  return V > 2 ? p ^ (u & (V / 2 - 1)) : p;
+}
+
+// Shared memory of segment_kernel.
+template <typename T, int LN, bool ENDS>
+struct SegmentShared {
+  using P = Shape<LN>;
+  static constexpr int kOther = ENDS ? 1 : kTile;  // what the outputs alone need
+  struct Raw {
+    alignas(16) T x[kTile][P::kCB];
+    alignas(16) T dt[kTile][P::kCB];
+    alignas(16) T z[kOther][P::kCB];
+    alignas(16) T B[kTile][P::kNP];
+    alignas(16) T C[kOther][P::kNP];
+  };
+  alignas(16) float2 d[2][kTile][P::kCB];  // dt, dt x
+  alignas(16) float B[2][kTile][P::kNP];
+  alignas(16) float C[2][kOther][P::kNP];
+  alignas(16) float y[2][kOther][P::kCB + 8];
+  Raw raw[kRing];
+  int swap;
+};
+
 // ENDS: only the end state of each segment but a sequence's last, from a zero start, into
 // seg_h, and the sum of dt into seg_dt.  Otherwise the outputs, from seg_h (or, with one
-// segment a sequence, from the sequence's state) on.
-template <typename T, int V, int LN, bool ENDS>
-__global__ void __launch_bounds__(kThreads)
+// segment a sequence, from the sequence's state) on.  NV: B and C are copied in vectors too.
+template <typename T, int V, int LN, bool ENDS, bool NV>
+__global__ void __launch_bounds__(2 * kThreads)
     segment_kernel(ScanArgs a, int S, float* seg_h, float* seg_dt) {
   using P = Shape<LN>;
-  __shared__ float2 sd[kTile][P::kCB];
-  __shared__ __align__(16) float sB[kTile][P::kNP];
-  __shared__ __align__(16) float sC[ENDS ? 1 : kTile][P::kNP];
-  __shared__ float sy[ENDS ? 1 : kTile][P::kCB];
-  if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, kThreads);
+  using X = Tile<T, V, P::kCB>;
+  constexpr int VN = !NV ? 1 : 16 / sizeof(T) < P::kNP ? 16 / sizeof(T) : P::kNP;
+  using R = Tile<T, VN, P::kNP>;
+  using Shared = SegmentShared<T, LN, ENDS>;
+  using Raw = typename Shared::Raw;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, 2 * kThreads);
   const long seg = blockIdx.x;
   SeqTile t;
   if (!seq_tile(a.s, seg, S, t)) return;
   const int end = min(t.t0 + S, t.len);
   if (ENDS && end == t.len) return;
-  const Channels k = channels_of<LN>(a, blockIdx.y);
-  const int lane = threadIdx.x & 31, nl = lane % LN, n0 = nl * 4;
-  const int cl = (threadIdx.x >> 5) * P::kCW + lane / LN, c = k.c0 + cl;
-  const bool live = cl < k.n;
-  float A2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  if (live) {
-    ld_states4(a.A + (long)c * a.N, n0, a.N, A2);
-    if (!ENDS) {
-      if (seg_h)
-        ld_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h);
-      else if (a.h_in && t.carry)
-        ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h);
-    }
+  const Channels k = channels_at<P::kCB>(a, blockIdx.y);
+  const int tiles = (end - t.t0 + kTile - 1) / kTile;
+  const int lane = threadIdx.x & 31;
+  // A warp stays on one of the four schedulers, by its number modulo 4; the two kinds of warps take
+  // turns, so that each scheduler gets the exponentials of some blocks (without: 1.3 times the time).
+  if (threadIdx.x == 0) {
+    unsigned w;
+    asm volatile("mov.u32 %0, %%warpid;" : "=r"(w));
+    s.swap = (w >> 2) & 1;
   }
+  __syncthreads();
+
+  if ((threadIdx.x >= kThreads) != (s.swap != 0)) {  // the warp that prepares and finishes tiles
+    X px(rows_of<T>(a.x, a, t, a.xb, a.xt, k.c0), a.xt, t.t0);
+    X pd(rows_of<T>(a.dt, a, t, a.tb, a.tt, k.c0), a.tt, t.t0);
+    X pz(rows_of<T>(a.z ? a.z : a.x, a, t, a.zb, a.zt, k.c0), a.zt, t.t0);
+    X py(rows_of<T>(ENDS ? a.x : a.y, a, t, a.yb, a.yt, k.c0), a.yt, t.t0);
+    R pB(rows_of<T>(a.Bm, a, t, a.bb, a.bt, k.g * a.N), a.bt, t.t0);
+    R pC(rows_of<T>(ENDS ? a.Bm : a.Cm, a, t, a.cb, a.ct, k.g * a.N), a.ct, t.t0);
+    // a thread's vectors keep their channels from tile to tile
+    static_assert(kThreads % (P::kCB / V) == 0, "a thread's vectors share their channels");
+    float bias[V], skip[V];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= ATLAS_LOG2E;
-  for (int t0 = t.t0; t0 < end; t0 += kTile) {
+    for (int j = 0; j < V; ++j) {
+      const int ch = X::channel(0) + j;
+      bias[j] = a.bias && ch < k.n ? a.bias[k.c0 + ch] : 0.f;
+      skip[j] = !ENDS && a.Dk && ch < k.n ? a.Dk[k.c0 + ch] : 0.f;
+    }
+    int rf = 0, rp = 0, rn = 0;  // places in the ring to fetch, prepare and finish next
+    const auto step = [](int& r) { r = r + 1 == kRing ? 0 : r + 1; };
+    int left_f = end - t.t0, left_p = left_f, left_n = left_f;  // tokens from there on
+    auto fetch = [&]() {
+      if (left_f > 0) {
+        Raw& r = s.raw[rf];
+        px.copy(r.x, left_f, k.n);
+        pd.copy(r.dt, left_f, k.n);
+        pB.copy(r.B, left_f, a.N);
+        if (!ENDS) {
+          if (a.z) pz.copy(r.z, left_f, k.n);
+          pC.copy(r.C, left_f, a.N);
+        }
+      }
+      cp_commit();
+      left_f -= kTile;
+      step(rf);
+    };
+    auto prepare = [&](int p) {
+      const int left = left_p;
+      if (left <= 0) return;
+      const Raw& r = s.raw[rp];
+      left_p -= kTile;
+      step(rp);
+#pragma unroll
+      for (int i = 0; i < X::kN; ++i)
+        if (X::inside(i)) {
+          const int u = X::token(i), q = X::channel(i);
+          float d[V], g[V];
+          ld_pack<T, V>(&r.x[u][q]).unpack(g);
+          steps_of<T, V>(a, ld_pack<T, V>(&r.dt[u][q]), bias, d);
+          if (left < kTile) {  // past the end the state stays
+#pragma unroll
+            for (int j = 0; j < V; ++j) d[j] = u < left ? d[j] : 0.f;
+          }
+#pragma unroll
+          for (int j = 0; j < V; ++j) g[j] *= d[j];
+          if (V == 1) {
+            s.d[p][u][q] = make_float2(d[0], g[0]);
+          } else {
+#pragma unroll
+            for (int j = 0; j + 1 < V; j += 2)
+              *reinterpret_cast<float4*>(&s.d[p][u][2 * turned<V>(u, (q + j) / 2)]) =
+                  make_float4(d[j], g[j], d[j + 1], g[j + 1]);
+          }
+        }
+#pragma unroll
+      for (int i = lane; i < kTile * P::kNP / 4; i += kThreads) {
+        const int u = i / (P::kNP / 4), n = i % (P::kNP / 4) * 4;
+        float b[4];
+        ld_pack<T, 4>(&r.B[u][n]).unpack(b);
+        *reinterpret_cast<float4*>(&s.B[p][u][n]) = make_float4(b[0], b[1], b[2], b[3]);
+        if (!ENDS) {
+          ld_pack<T, 4>(&r.C[u][n]).unpack(b);
+          *reinterpret_cast<float4*>(&s.C[p][u][n]) = make_float4(b[0], b[1], b[2], b[3]);
+        }
+      }
+    };
+    auto finish = [&](int p) {
+      if (ENDS) return;
+      const Raw& r = s.raw[rn];
+#pragma unroll
+      for (int i = 0; i < X::kN; ++i) {
+        const int u = X::token(i), q = X::channel(i);
+        if (!X::inside(i) || u >= left_n || q >= k.n) continue;
+        float y[V], z[V];
+        ld_pack<T, V>(&r.x[u][q]).unpack(y);
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = fmaf(skip[j], y[j], s.y[p][u][q + j]);
+        if (a.z) {
+          ld_pack<T, V>(&r.z[u][q]).unpack(z);
+#pragma unroll
+          for (int j = 0; j < V; ++j) y[j] *= siluf(z[j]);
+        }
+        Pack<T, V> o;
+        o.pack(y);
+        st_pack<T, V>(py.at(i), o);
+      }
+      py.next();
+      left_n -= kTile;
+      step(rn);
+    };
+    fetch();
+    fetch();
+    fetch();
+    cp_wait<2>();
+    __syncwarp();
+    prepare(0);
     __syncthreads();
-    load_dx<T, V, LN, kTile>(a, t, k, t0, end, sd);
-    load_states<T, LN, kTile>(a, t, k, t0, end, a.Bm, a.bb, a.bt, sB);
-    if (!ENDS) load_states<T, LN, kTile>(a, t, k, t0, end, a.Cm, a.cb, a.ct, sC);
-    __syncthreads();
-    const int nt = min(kTile, end - t0);
-    for (int u0 = 0; u0 < nt; u0 += 4) {
-      float yp[4];
+    for (int m = 0; m < tiles; ++m) {
+      fetch();
+      if (m > 0) finish((m - 1) & 1);
+      cp_wait<2>();
+      __syncwarp();
+      prepare((m + 1) & 1);
+      __syncthreads();
+    }
+    cp_wait<0>();
+    if (tiles > 0) finish((tiles - 1) & 1);
+    return;
+  }
+
+  const int nl = lane / P::kPairs, n0 = nl * 4, cp = lane % P::kPairs;
+  pair32 A01[2], A23[2], h01[2], h23[2];
+  float h4[4], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = k.c0 + 2 * cp + i;
+    float A4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) h4[j] = 0.f;
+    if (2 * cp + i < k.n) {
+      ld_states4(a.A + (long)c * a.N, n0, a.N, A4);
+      if (!ENDS) {
+        if (seg_h)
+          ld_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h4);
+        else if (a.h_in && t.carry)
+          ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
+      }
+    }
+    A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
+    A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
+    h01[i] = pair(h4[0], h4[1]);
+    h23[i] = pair(h4[2], h4[3]);
+  }
+  // four tokens' operands; those of the next four are loaded before the current ones are used,
+  // and the sums over states of the last four taken among the products of the current ones
+  struct Four {
+    float4 d[4];
+    ulonglong2 b[4], q[4];
+  };
+  __syncthreads();
+  for (int m = 0; m < tiles; ++m) {
+    const int p = m & 1;
+    auto load = [&](int u0) {
+      Four f;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float2 d = sd[u0 + u][cl];
-        const float4 b = *reinterpret_cast<const float4*>(&sB[u0 + u][n0]);
-        const float g = d.x * d.y;
-        h[0] = ex2(d.x * A2[0]) * h[0] + g * b.x;
-        h[1] = ex2(d.x * A2[1]) * h[1] + g * b.y;
-        h[2] = ex2(d.x * A2[2]) * h[2] + g * b.z;
-        h[3] = ex2(d.x * A2[3]) * h[3] + g * b.w;
-        if (ENDS) {
-          sum += d.x;
-        } else {
-          const float4 q = *reinterpret_cast<const float4*>(&sC[u0 + u][n0]);
-          yp[u] = h[0] * q.x + h[1] * q.y + h[2] * q.z + h[3] * q.w;
+        f.d[u] = *reinterpret_cast<const float4*>(&s.d[p][u0 + u][2 * turned<V>(u0 + u, cp)]);
+        f.b[u] = *reinterpret_cast<const ulonglong2*>(&s.B[p][u0 + u][n0]);
+        if (!ENDS) f.q[u] = *reinterpret_cast<const ulonglong2*>(&s.C[p][u0 + u][n0]);
+      }
+      return f;
+    };
+    auto reduce = [&](int u0, float* yp) {
+      lane_sums<8, LN, P::kPairs>(yp, lane);
+      constexpr int M = LN <= 4 ? 8 / LN : LN == 8 ? 1 : 0;  // values left, in (token, channel) order
+      if (M >= 2) {
+#pragma unroll
+        for (int i = 0; i < M; i += 2)
+          *reinterpret_cast<float2*>(&s.y[p][u0 + (nl * M + i) / 2][2 * cp]) = make_float2(yp[i], yp[i + 1]);
+      } else if (M == 1) {
+        s.y[p][u0 + nl / 2][2 * cp + nl % 2] = yp[0];
+      } else if (nl % (LN > 8 ? LN / 8 : 1) == 0) {
+        const int v = nl / (LN > 8 ? LN / 8 : 1);
+        s.y[p][u0 + v / 2][2 * cp + v % 2] = yp[0];
+      }
+    };
+    Four f = load(0);
+    float last[8];
+#pragma unroll
+    for (int u0 = 0; u0 < kTile; u0 += 4) {
+      Four next;
+      if (u0 + 4 < kTile) next = load(u0 + 4);
+      float yp[8];  // four tokens x two channels
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float dt = i ? f.d[u].z : f.d[u].x, g = i ? f.d[u].w : f.d[u].y;
+          const pair32 dd = pair(dt, dt), gg = pair(g, g);
+          h01[i] = pair_fma(pair_ex2(pair_mul(dd, A01[i])), h01[i], pair_mul(gg, f.b[u].x));
+          h23[i] = pair_fma(pair_ex2(pair_mul(dd, A23[i])), h23[i], pair_mul(gg, f.b[u].y));
+          if (ENDS)
+            sum[i] += dt;
+          else
+            yp[2 * u + i] = pair_sum(pair_fma(h23[i], f.q[u].y, pair_mul(h01[i], f.q[u].x)));
         }
       }
       if (!ENDS) {
-        lane_sums<4, LN, 1>(yp, lane);
-        if (LN <= 4) {
-          constexpr int NV = LN <= 4 ? 4 / LN : 1;
+        if (u0 > 0) reduce(u0 - 4, last);
 #pragma unroll
-          for (int i = 0; i < NV; ++i) sy[u0 + nl * NV + i][cl] = yp[i];
-        } else if (nl % (LN > 4 ? LN / 4 : 1) == 0) {
-          sy[u0 + nl / (LN > 4 ? LN / 4 : 1)][cl] = yp[0];
-        }
+        for (int i = 0; i < 8; ++i) last[i] = yp[i];
       }
+      if (u0 + 4 < kTile) f = next;
     }
-    if (!ENDS) {
-      __syncthreads();
-      constexpr int CV = P::kCB / V;
-      for (int i = threadIdx.x; i < nt * CV; i += kThreads) {
-        const int u = i / CV, q = (i % CV) * V;
-        if (q >= k.n) continue;
-        Pack<T, V> z, o;
-        if (a.z) z = ld_pack<T, V>(reinterpret_cast<const T*>(a.z) + seq_at(a.s, t, t0 + u, a.zb, a.zt) + k.c0 + q);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          float y = sy[u][q + j];
-          if (a.Dk) y += a.Dk[k.c0 + q + j] * sd[u][q + j].y;
-          if (a.z) y *= siluf(z.get(j));
-          o.set(j, y);
-        }
-        st_pack<T, V>(reinterpret_cast<T*>(a.y) + seq_at(a.s, t, t0 + u, a.yb, a.yt) + k.c0 + q, o);
-      }
-    }
+    if (!ENDS) reduce(kTile - 4, last);
+    __syncthreads();
   }
-  if (!live) return;
-  if (ENDS) {
-    st_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h);
-    if (nl == 0) seg_dt[seg * a.D + c] = sum;
-  } else if (a.h_out && end == t.len) {
-    st_states4(a.h_out + ((long)t.slot * a.D + c) * a.N, n0, a.N, h);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = k.c0 + 2 * cp + i;
+    if (2 * cp + i >= k.n) continue;
+    unpair(h01[i], h4[0], h4[1]);
+    unpair(h23[i], h4[2], h4[3]);
+    if (ENDS) {
+      st_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h4);
+      if (nl == 0) seg_dt[seg * a.D + c] = sum[i];
+    } else if (a.h_out && end == t.len) {
+      st_states4(a.h_out + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
+    }
   }
 }
 
@@ -225,14 +450,14 @@ static __global__ void __launch_bounds__(256)
 
 // One token a sequence: every lane takes four states of a channel, loads and stores them
 // once.  Bound by the state's traffic.
+constexpr int kTokenThreads = 128;
 template <typename T, int LN>
-__global__ void __launch_bounds__(kThreads) token_kernel(ScanArgs a) {
-  using P = Shape<LN>;
+__global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
   SeqTile t;
   const int b = blockIdx.x;
   if (!seq_tile(a.s, b, 1, t)) return;
   const int lane = threadIdx.x & 31, nl = lane % LN, n0 = nl * 4;
-  const int c = blockIdx.y * P::kCB + (threadIdx.x >> 5) * P::kCW + lane / LN;
+  const int c = (blockIdx.y * kTokenThreads + (int)threadIdx.x) / LN;
   const bool live = c < a.D;
   float y = 0.f, x = 0.f;
   if (live) {
@@ -240,7 +465,8 @@ __global__ void __launch_bounds__(kThreads) token_kernel(ScanArgs a) {
     ld_states4(a.A + (long)c * a.N, n0, a.N, A);
     if (a.h_in && t.carry) ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h);
     x = to_f(reinterpret_cast<const T*>(a.x)[b * a.xb + c]);
-    const float d = step_of(a, to_f(reinterpret_cast<const T*>(a.dt)[b * a.tb + c]), c);
+    float d = to_f(reinterpret_cast<const T*>(a.dt)[b * a.tb + c]) + (a.bias ? a.bias[c] : 0.f);
+    if (a.softplus) d = softplusf(d);
     const long g = (long)(c / (a.D / a.G)) * a.N;
     const T* B = reinterpret_cast<const T*>(a.Bm) + b * a.bb + g;
     const T* C = reinterpret_cast<const T*>(a.Cm) + b * a.cb + g;
@@ -260,50 +486,65 @@ __global__ void __launch_bounds__(kThreads) token_kernel(ScanArgs a) {
   }
 }
 
-// Segment length: one segment a sequence when the sequences alone give four blocks an SM;
-// otherwise segments for that many, but not below 128 tokens, where the second pass over
-// them costs more than it brings.  0: no segments.
+// Segment length, 0 for one segment a sequence.  One segment when the sequences alone give
+// six blocks an SM; otherwise segments for that many, but none below 256 tokens.
 inline int segment_tokens(const ScanArgs& a, long blocks_per_seq) {
-  const long want = 152 * 4;
+  const long want = 152 * 6;
   const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
   if (!a.s.start && a.s.B * blocks_per_seq >= want) return 0;
-  if ((a.s.start ? a.s.L : a.s.L) <= 256) return 0;
+  if (a.s.L <= 256) return 0;
   long S = rows * blocks_per_seq / want / kTile * kTile;
-  if (S < 128) S = 128;
+  if (S < 256) S = 256;
   if (S >= a.s.L) return 0;
   return (int)S;
 }
 
 template <int LN>
 size_t workspace(const ScanArgs& a) {
-  const int S = segment_tokens(a, channel_blocks<LN>(a));
+  const int S = segment_tokens(a, blocks_over<Shape<LN>::kCB>(a));
   return S ? (size_t)seq_tiles(a.s, S) * a.D * (a.N + 1) * 4 : 0;
+}
+
+template <typename T, int V, int LN, bool ENDS, bool NV>
+bool segment_pass(const ScanArgs& a, int S, float* seg_h, float* seg_dt, cudaStream_t st) {
+  const dim3 grid((unsigned)seq_tiles(a.s, S), blocks_over<Shape<LN>::kCB>(a));
+  constexpr size_t smem = sizeof(SegmentShared<T, LN, ENDS>);
+  auto* f = segment_kernel<T, V, LN, ENDS, NV>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  f<<<grid, 2 * kThreads, smem, st>>>(a, S, seg_h, seg_dt);
+  return true;
 }
 
 template <typename T, int V, int LN>
 int forward(const ScanArgs& a, cudaStream_t st) {
   constexpr int VV = V < Shape<LN>::kCB ? V : Shape<LN>::kCB;
-  const int by = channel_blocks<LN>(a);
-  if (by > 65535 || a.s.B > 65535) return ATLAS_ERR_UNSUPPORTED;
+  const int by = blocks_over<Shape<LN>::kCB>(a);
+  if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
   if (!a.s.start && a.s.L == 1) {
-    const dim3 grid(a.s.B, (a.D + Shape<LN>::kCB - 1) / Shape<LN>::kCB);
-    token_kernel<T, LN><<<grid, kThreads, 0, st>>>(a);
+    const long rows = ((long)a.D * LN + kTokenThreads - 1) / kTokenThreads;
+    if (rows > 65535) return ATLAS_ERR_UNSUPPORTED;
+    token_kernel<T, LN><<<dim3(a.s.B, (unsigned)rows), kTokenThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
   }
   int S = segment_tokens(a, by);
   float *seg_h = nullptr, *seg_dt = nullptr;
+  auto pass = [&](auto ends) {
+    constexpr bool E = decltype(ends)::value;
+    return VV > 1 && a.wide_n ? segment_pass<T, VV, LN, E, (VV > 1)>(a, S, seg_h, seg_dt, st)
+                              : segment_pass<T, VV, LN, E, false>(a, S, seg_h, seg_dt, st);
+  };
   if (S) {
-    const long segs = seq_tiles(a.s, S);
     seg_h = reinterpret_cast<float*>(a.ws);
-    seg_dt = seg_h + (size_t)segs * a.D * a.N;
-    segment_kernel<T, VV, LN, true><<<dim3((unsigned)segs, by), kThreads, 0, st>>>(a, S, seg_h, seg_dt);
+    seg_dt = seg_h + (size_t)seq_tiles(a.s, S) * a.D * a.N;
+    if (!pass(std::true_type())) return ATLAS_ERR_CUDA;
     const long dn = (long)a.D * a.N;
     join_kernel<<<dim3((unsigned)((dn + 255) / 256), a.s.B), 256, 0, st>>>(a, S, seg_h, seg_dt);
   } else {
     S = a.s.L > 0 ? a.s.L : 1;
   }
-  const long segs = seq_tiles(a.s, S);
-  segment_kernel<T, VV, LN, false><<<dim3((unsigned)segs, by), kThreads, 0, st>>>(a, S, seg_h, seg_dt);
+  if (!pass(std::false_type())) return ATLAS_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 

@@ -22,6 +22,14 @@ namespace atlas {
 namespace scan {
 
 constexpr int kSub = 8;
+constexpr int kBackThreads = 128;
+
+template <int LN>
+struct BackShape {
+  static constexpr int kNP = 4 * LN;                   // padded states
+  static constexpr int kCW = 32 / LN;                  // channels of a warp
+  static constexpr int kCB = kCW * kBackThreads / 32;  // channels of a block
+};
 
 // Sizes and workspace of a backward call.
 template <int LN>
@@ -35,7 +43,7 @@ struct Back {
   float* pbc;               // [cb][rows][2][NP]
   size_t bytes;
   Back(const ScanArgs& a, void* ws) {
-    cb = channel_blocks<LN>(a);
+    cb = blocks_over<BackShape<LN>::kCB>(a);
     S = segment_tokens(a, cb);
     split = S != 0;
     if (!S) S = a.s.L > 0 ? a.s.L : 1;
@@ -57,23 +65,54 @@ struct Back {
     take(pA, segs * DN);
     take(pD, segs * D);
     take(pb, segs * D);
-    take(pbc, (size_t)cb * rows * 2 * Shape<LN>::kNP);
+    take(pbc, (size_t)cb * rows * 2 * BackShape<LN>::kNP);
     bytes *= 4;
   }
 };
 
-// What the main pass needs of dy, z and softplus, per token and channel.
-struct Up {
-  float dyg;    // dy SiLU(z)
-  float slope;  // softplus' slope at the raw dt (1 without softplus)
-  float dyz;    // dy SiLU'(z)
-};
+// Tokens t0 .. t0 + TT of dt (through softplus) and x into sd, those past `end` as zeros.
+template <typename T, int V, int LN, int TT>
+__device__ __forceinline__ void load_dx(const ScanArgs& a, const SeqTile& t, const Channels& k,
+                                        int t0, int end, float2 (*sd)[BackShape<LN>::kCB]) {
+  constexpr int CV = BackShape<LN>::kCB / V;
+  for (int i = threadIdx.x; i < TT * CV; i += kBackThreads) {
+    const int u = i / CV, cl = (i % CV) * V;
+    if (t0 + u < end && cl < k.n) {
+      const auto x = ld_pack<T, V>(reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, t0 + u, a.xb, a.xt) + k.c0 + cl);
+      const auto d = ld_pack<T, V>(reinterpret_cast<const T*>(a.dt) + seq_at(a.s, t, t0 + u, a.tb, a.tt) + k.c0 + cl);
+      float bias[V], step[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) bias[j] = a.bias ? a.bias[k.c0 + cl + j] : 0.f;
+      steps_of<T, V>(a, d, bias, step);
+#pragma unroll
+      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(step[j], x.get(j));
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(0.f, 0.f);
+    }
+  }
+}
+
+template <typename T, int LN, int TT>
+__device__ __forceinline__ void load_states(const ScanArgs& a, const SeqTile& t, const Channels& k,
+                                            int t0, int end, const void* p, long sb, long st,
+                                            float (*s)[BackShape<LN>::kNP]) {
+  constexpr int NP = 4 * LN;
+  const T* q = rows_of<T>(p, a, t, sb, st, k.g * a.N);
+  for (int i = threadIdx.x; i < TT * NP; i += kBackThreads) {
+    const int u = t0 + i / NP, n = i % NP;
+    s[i / NP][n] = u < end && n < a.N ? to_f(q[(long)u * st + n]) : 0.f;
+  }
+}
+
+// What the main pass needs of dy, z and softplus: dy SiLU(z), softplus' slope at the raw
+// step (1 without softplus) and dy SiLU'(z).
 template <typename T, int V, int LN>
 __device__ __forceinline__ void load_up(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                        int t0, int end, float (*dyg)[Shape<LN>::kCB],
-                                        float (*slope)[Shape<LN>::kCB], float (*dyz)[Shape<LN>::kCB]) {
-  constexpr int CV = Shape<LN>::kCB / V;
-  for (int i = threadIdx.x; i < kSub * CV; i += kThreads) {
+                                        int t0, int end, float (*dyg)[BackShape<LN>::kCB],
+                                        float (*slope)[BackShape<LN>::kCB], float (*dyz)[BackShape<LN>::kCB]) {
+  constexpr int CV = BackShape<LN>::kCB / V;
+  for (int i = threadIdx.x; i < kSub * CV; i += kBackThreads) {
     const int u = i / CV, cl = (i % CV) * V;
     if (t0 + u < end && cl < k.n) {
       const auto dy = ld_pack<T, V>(reinterpret_cast<const T*>(a.dy) + seq_at(a.s, t, t0 + u, a.yb, a.yt) + k.c0 + cl);
@@ -85,7 +124,7 @@ __device__ __forceinline__ void load_up(const ScanArgs& a, const SeqTile& t, con
         const float g = dy.get(j);
         if (a.z) {
           const float zv = z.get(j), s = sigmoidf(zv);
-          dyg[u][cl + j] = s == 0.f ? 0.f : g * zv * s;
+          dyg[u][cl + j] = g * zv * s;
           if (dyz) dyz[u][cl + j] = g * silu_slope(zv, s);
         } else {
           dyg[u][cl + j] = g;
@@ -107,18 +146,18 @@ __device__ __forceinline__ void load_up(const ScanArgs& a, const SeqTile& t, con
 }
 
 template <typename T, int V, int LN>
-__global__ void __launch_bounds__(kThreads) keep_kernel(ScanArgs a, Back<LN> w) {
-  using P = Shape<LN>;
+__global__ void __launch_bounds__(kBackThreads) keep_kernel(ScanArgs a, Back<LN> w) {
+  using P = BackShape<LN>;
   __shared__ float2 sd[kSub][P::kCB];
   __shared__ float sg[kSub][P::kCB];
   __shared__ __align__(16) float sB[kSub][P::kNP];
   __shared__ __align__(16) float sC[kSub][P::kNP];
-  if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, kThreads);
+  if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, kBackThreads);
   const long seg = blockIdx.x;
   SeqTile t;
   if (!seq_tile(a.s, seg, w.S, t)) return;
   const int end = min(t.t0 + w.S, t.len);
-  const Channels k = channels_of<LN>(a, blockIdx.y);
+  const Channels k = channels_at<BackShape<LN>::kCB>(a, blockIdx.y);
   const int lane = threadIdx.x & 31, nl = lane % LN, n0 = nl * 4;
   const int cl = (threadIdx.x >> 5) * P::kCW + lane / LN, c = k.c0 + cl;
   const bool live = cl < k.n;
@@ -205,16 +244,16 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
 }
 
 template <typename T, int V, int LN>
-__global__ void __launch_bounds__(kThreads) back_kernel(ScanArgs a, Back<LN> w) {
-  using P = Shape<LN>;
+__global__ void __launch_bounds__(kBackThreads) back_kernel(ScanArgs a, Back<LN> w) {
+  using P = BackShape<LN>;
   __shared__ float2 sd[kSub][P::kCB];
   __shared__ float sg[kSub][P::kCB], ss[kSub][P::kCB], sz[kSub][P::kCB];
   __shared__ __align__(16) float sB[kSub][P::kNP];
   __shared__ __align__(16) float sC[kSub][P::kNP];
-  __shared__ float sp[kThreads / 32][kSub][2 * P::kNP];
+  __shared__ float sp[kBackThreads / 32][kSub][2 * P::kNP];
   __shared__ float so[3][kSub][P::kCB];
   const long seg = blockIdx.x;
-  const Channels k = channels_of<LN>(a, blockIdx.y);
+  const Channels k = channels_at<BackShape<LN>::kCB>(a, blockIdx.y);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nl = lane % LN, n0 = nl * 4;
   const int chl = lane / LN, cl = warp * P::kCW + chl, c = k.c0 + cl;
   const bool live = cl < k.n;
@@ -330,7 +369,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(ScanArgs a, Back<LN> w) 
       }
       __syncthreads();
       constexpr int CV = P::kCB / V;
-      for (int i = threadIdx.x; i < kSub * CV; i += kThreads) {
+      for (int i = threadIdx.x; i < kSub * CV; i += kBackThreads) {
         const int u = i / CV, q = (i % CV) * V;
         if (t0 + u >= end || q >= k.n) continue;
         Pack<T, V> o;
@@ -346,12 +385,12 @@ __global__ void __launch_bounds__(kThreads) back_kernel(ScanArgs a, Back<LN> w) 
           st_pack<T, V>(reinterpret_cast<T*>(a.dz) + seq_at(a.s, t, t0 + u, a.zb, a.zt) + k.c0 + q, o);
         }
       }
-      for (int i = threadIdx.x; i < kSub * 2 * P::kNP; i += kThreads) {
+      for (int i = threadIdx.x; i < kSub * 2 * P::kNP; i += kBackThreads) {
         const int u = i / (2 * P::kNP), q = i % (2 * P::kNP);
         if (t0 + u >= end) continue;
         float s = sp[0][u][q];
 #pragma unroll
-        for (int r = 1; r < kThreads / 32; ++r) s += sp[r][u][q];
+        for (int r = 1; r < kBackThreads / 32; ++r) s += sp[r][u][q];
         w.pbc[((long)blockIdx.y * w.rows + row0 + t0 + u) * 2 * P::kNP + q] = s;
       }
     }
@@ -379,7 +418,7 @@ __global__ void __launch_bounds__(kThreads) back_kernel(ScanArgs a, Back<LN> w) 
 // Adds the partial sums: the first `nbc` blocks dB and dC, the others dA, dD and ddt_bias.
 template <typename T, int LN>
 __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int nbc) {
-  constexpr int NP = Shape<LN>::kNP;
+  constexpr int NP = BackShape<LN>::kNP;
   if ((int)blockIdx.x < nbc) {
     const int bpg = w.cb / a.G;
     long lo = 0, hi = w.rows;
@@ -422,15 +461,15 @@ __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int
 
 template <typename T, int V, int LN>
 int backward(const ScanArgs& a, cudaStream_t st) {
-  constexpr int VV = V < Shape<LN>::kCB ? V : Shape<LN>::kCB;
+  constexpr int VV = V < BackShape<LN>::kCB ? V : BackShape<LN>::kCB;
   const Back<LN> w(a, a.ws);
   if (w.cb > 65535 || a.s.B > 65535 || w.segs > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   const dim3 grid((unsigned)w.segs, w.cb);
-  if (w.segs > 0) keep_kernel<T, VV, LN><<<grid, kThreads, 0, st>>>(a, w);
+  if (w.segs > 0) keep_kernel<T, VV, LN><<<grid, kBackThreads, 0, st>>>(a, w);
   if (w.segs > 0 && w.split)
     join_back_kernel<LN><<<dim3((unsigned)(((long)a.D * a.N + 255) / 256), a.s.B), 256, 0, st>>>(a, w);
-  if (w.segs > 0) back_kernel<T, VV, LN><<<grid, kThreads, 0, st>>>(a, w);
-  const long nb = (w.rows * a.G * 2 * Shape<LN>::kNP + 255) / 256;
+  if (w.segs > 0) back_kernel<T, VV, LN><<<grid, kBackThreads, 0, st>>>(a, w);
+  const long nb = (w.rows * a.G * 2 * BackShape<LN>::kNP + 255) / 256;
   const int nbc = (int)(nb < 152 * 16 ? nb : 152 * 16);
   const long na = ((long)a.D * (a.N + 2) + 255) / 256;
   finish_kernel<T, LN><<<nbc + (int)(na < 4096 ? na : 4096), 256, 0, st>>>(a, w, nbc);
