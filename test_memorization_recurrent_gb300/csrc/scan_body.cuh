@@ -18,8 +18,6 @@
 // its dt: the decay over a segment is exp(A sum dt)), a second one joins them into start
 // states, the third computes the outputs.
 #pragma once
-#include <type_traits>
-
 #include "ops_common.cuh"
 
 namespace atlas {
@@ -64,16 +62,16 @@ __device__ __forceinline__ const T* rows_of(const void* p, const ScanArgs& a, co
   return reinterpret_cast<const T*>(p) + seq_at(a.s, t, 0, sb, st) + c;
 }
 
-// A tile of kTile tokens x W elements of a warp: vector i * kThreads + lane, the elements of
-// a token innermost.  The object walks a tensor's rows from tile to tile.
-template <typename T, int V, int W>
+// A tile of TT tokens x W elements of a warp: vector i * kThreads + lane, the elements of a
+// token innermost.  The object walks a tensor's rows from tile to tile.
+template <typename T, int V, int W, int TT = kTile>
 struct Tile {
-  static constexpr int kN = (kTile * W / V + kThreads - 1) / kThreads;
+  static constexpr int kN = (TT * W / V + kThreads - 1) / kThreads;
   static __device__ __forceinline__ int lane() { return threadIdx.x & 31; }
   static __device__ __forceinline__ int token(int i) { return (i * kThreads + lane()) / (W / V); }
   static __device__ __forceinline__ int channel(int i) { return (i * kThreads + lane()) % (W / V) * V; }
   static __device__ __forceinline__ bool inside(int i) {
-    return kTile * W / V % kThreads == 0 || i * kThreads + lane() < kTile * W / V;
+    return TT * W / V % kThreads == 0 || i * kThreads + lane() < TT * W / V;
   }
   T* p;      // this lane's first vector of the tile
   long row;  // elements between tokens
@@ -85,8 +83,9 @@ struct Tile {
     if (i == 0) return p;
     return p + (token(i) - token(0)) * row + (channel(i) - channel(0));
   }
-  __device__ __forceinline__ void next() { p += kTile * row; }
-  // the next tile into s; zeros from token `left` on and past element n
+  __device__ __forceinline__ void next() { p += TT * row; }
+  __device__ __forceinline__ void back() { p -= TT * row; }
+  // this tile into s; zeros from token `left` on and past element n
   __device__ __forceinline__ void copy(T (*s)[W], int left, int n) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -99,7 +98,6 @@ struct Tile {
         s[u][c] = some ? *at(i) : from_f<T>(0.f);
       }
     }
-    next();
   }
 };
 
@@ -147,9 +145,16 @@ __device__ __forceinline__ int turned(int u, int p) {
   return V > 2 ? p ^ (u & (V / 2 - 1)) : p;
 }
 
+// What a walk over a segment is for: kOut, its outputs; kEnds, its end state from a zero
+// start; kKeep, for the backward pass: the state in front of every kSub tokens too, and what
+// the segment's own tokens add to the adjoint in front of it.
+enum Mode { kOut, kEnds, kKeep };
+constexpr int kSub = 8;
+
 // Shared memory of segment_kernel.
-template <typename T, int LN, bool ENDS>
+template <typename T, int LN, Mode MODE>
 struct SegmentShared {
+  static constexpr bool ENDS = MODE == kEnds;
   using P = Shape<LN>;
   static constexpr int kOther = ENDS ? 1 : kTile;  // what the outputs alone need
   struct Raw {
@@ -158,34 +163,44 @@ struct SegmentShared {
     alignas(16) T z[kOther][P::kCB];
     alignas(16) T B[kTile][P::kNP];
     alignas(16) T C[kOther][P::kNP];
+    alignas(16) T dy[MODE == kKeep ? 1 : 0][kTile][P::kCB];
   };
   alignas(16) float2 d[2][kTile][P::kCB];  // dt, dt x
   alignas(16) float B[2][kTile][P::kNP];
   alignas(16) float C[2][kOther][P::kNP];
-  alignas(16) float y[2][kOther][P::kCB + 8];
+  alignas(16) float y[2][kOther][P::kCB + 8];  // the sums over states; kKeep: dy SiLU(z)
   Raw raw[kRing];
   int swap;
 };
 
-// ENDS: only the end state of each segment but a sequence's last, from a zero start, into
-// seg_h, and the sum of dt into seg_dt.  Otherwise the outputs, from seg_h (or, with one
-// segment a sequence, from the sequence's state) on.  NV: B and C are copied in vectors too.
-template <typename T, int V, int LN, bool ENDS, bool NV>
-__global__ void __launch_bounds__(2 * kThreads)
-    segment_kernel(ScanArgs a, int S, float* seg_h, float* seg_dt) {
+// Where the segments' states go: seg_h and seg_dt of kEnds and kKeep (kOut reads seg_h), the
+// rest of kKeep.
+struct Segments {
+  int S;                          // tokens of a segment
+  float *h, *dt;                  // [segments][D][N], [segments][D]
+  float *g, *keep_h, *keep_dt;    // [segments][D][N], [segments][nsub][D][N], [segments][nsub][D]
+  int nsub;
+};
+
+// kOut starts from seg.h (or, with one segment a sequence, from the sequence's state).  kEnds
+// leaves a sequence's last segment out.  kKeep with seg.h starts from zeros, else from the
+// sequence's state, and then leaves the adjoint out.  NV: B and C are copied in vectors too.
+template <typename T, int V, int LN, Mode MODE, bool NV>
+__global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Segments sg) {
+  constexpr bool ENDS = MODE == kEnds, KEEP = MODE == kKeep, OUT = MODE == kOut;
   using P = Shape<LN>;
   using X = Tile<T, V, P::kCB>;
   constexpr int VN = !NV ? 1 : 16 / sizeof(T) < P::kNP ? 16 / sizeof(T) : P::kNP;
   using R = Tile<T, VN, P::kNP>;
-  using Shared = SegmentShared<T, LN, ENDS>;
+  using Shared = SegmentShared<T, LN, MODE>;
   using Raw = typename Shared::Raw;
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, 2 * kThreads);
   const long seg = blockIdx.x;
   SeqTile t;
-  if (!seq_tile(a.s, seg, S, t)) return;
-  const int end = min(t.t0 + S, t.len);
+  if (!seq_tile(a.s, seg, sg.S, t)) return;
+  const int end = min(t.t0 + sg.S, t.len);
   if (ENDS && end == t.len) return;
   const Channels k = channels_at<P::kCB>(a, blockIdx.y);
   const int tiles = (end - t.t0 + kTile - 1) / kTile;
@@ -203,7 +218,8 @@ __global__ void __launch_bounds__(2 * kThreads)
     X px(rows_of<T>(a.x, a, t, a.xb, a.xt, k.c0), a.xt, t.t0);
     X pd(rows_of<T>(a.dt, a, t, a.tb, a.tt, k.c0), a.tt, t.t0);
     X pz(rows_of<T>(a.z ? a.z : a.x, a, t, a.zb, a.zt, k.c0), a.zt, t.t0);
-    X py(rows_of<T>(ENDS ? a.x : a.y, a, t, a.yb, a.yt, k.c0), a.yt, t.t0);
+    X py(rows_of<T>(OUT ? a.y : a.x, a, t, a.yb, a.yt, k.c0), a.yt, t.t0);
+    X pg(rows_of<T>(KEEP ? a.dy : a.x, a, t, a.yb, a.yt, k.c0), a.yt, t.t0);
     R pB(rows_of<T>(a.Bm, a, t, a.bb, a.bt, k.g * a.N), a.bt, t.t0);
     R pC(rows_of<T>(ENDS ? a.Bm : a.Cm, a, t, a.cb, a.ct, k.g * a.N), a.ct, t.t0);
     // a thread's vectors keep their channels from tile to tile
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(2 * kThreads)
     for (int j = 0; j < V; ++j) {
       const int ch = X::channel(0) + j;
       bias[j] = a.bias && ch < k.n ? a.bias[k.c0 + ch] : 0.f;
-      skip[j] = !ENDS && a.Dk && ch < k.n ? a.Dk[k.c0 + ch] : 0.f;
+      skip[j] = OUT && a.Dk && ch < k.n ? a.Dk[k.c0 + ch] : 0.f;
     }
     int rf = 0, rp = 0, rn = 0;  // places in the ring to fetch, prepare and finish next
     const auto step = [](int& r) { r = r + 1 == kRing ? 0 : r + 1; };
@@ -224,9 +240,15 @@ __global__ void __launch_bounds__(2 * kThreads)
         px.copy(r.x, left_f, k.n);
         pd.copy(r.dt, left_f, k.n);
         pB.copy(r.B, left_f, a.N);
+        px.next(), pd.next(), pB.next();
         if (!ENDS) {
           if (a.z) pz.copy(r.z, left_f, k.n);
           pC.copy(r.C, left_f, a.N);
+          pz.next(), pC.next();
+        }
+        if (KEEP) {
+          pg.copy(r.dy[0], left_f, k.n);
+          pg.next();
         }
       }
       cp_commit();
@@ -261,6 +283,22 @@ __global__ void __launch_bounds__(2 * kThreads)
                   make_float4(d[j], g[j], d[j + 1], g[j + 1]);
           }
         }
+      if (KEEP) {
+#pragma unroll
+        for (int i = 0; i < X::kN; ++i)
+          if (X::inside(i)) {
+            const int u = X::token(i), q = X::channel(i);
+            float y[V], z[V];
+            ld_pack<T, V>(&r.dy[0][u][q]).unpack(y);
+            if (a.z) {
+              ld_pack<T, V>(&r.z[u][q]).unpack(z);
+#pragma unroll
+              for (int j = 0; j < V; ++j) y[j] *= siluf(z[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) s.y[p][u][q + j] = u < left ? y[j] : 0.f;
+          }
+      }
 #pragma unroll
       for (int i = lane; i < kTile * P::kNP / 4; i += kThreads) {
         const int u = i / (P::kNP / 4), n = i % (P::kNP / 4) * 4;
@@ -274,7 +312,7 @@ __global__ void __launch_bounds__(2 * kThreads)
       }
     };
     auto finish = [&](int p) {
-      if (ENDS) return;
+      if (!OUT) return;
       const Raw& r = s.raw[rn];
 #pragma unroll
       for (int i = 0; i < X::kN; ++i) {
@@ -319,43 +357,60 @@ __global__ void __launch_bounds__(2 * kThreads)
 
   const int nl = lane / P::kPairs, n0 = nl * 4, cp = lane % P::kPairs;
   pair32 A01[2], A23[2], h01[2], h23[2];
+  pair32 p01[2], p23[2], g01[2], g23[2];  // kKeep: the decay so far, the adjoint
   float h4[4], sum[2] = {0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
+    p01[i] = p23[i] = pair(1.f, 1.f);
+    g01[i] = g23[i] = pair(0.f, 0.f);
     const int c = k.c0 + 2 * cp + i;
     float A4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 4; ++j) h4[j] = 0.f;
     if (2 * cp + i < k.n) {
       ld_states4(a.A + (long)c * a.N, n0, a.N, A4);
-      if (!ENDS) {
-        if (seg_h)
-          ld_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h4);
-        else if (a.h_in && t.carry)
-          ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
-      }
+      if (OUT && sg.h)
+        ld_states4(sg.h + (seg * a.D + c) * a.N, n0, a.N, h4);
+      else if (!ENDS && !sg.h && a.h_in && t.carry)
+        ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
     }
     A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
     A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
     h01[i] = pair(h4[0], h4[1]);
     h23[i] = pair(h4[2], h4[3]);
   }
-  // four tokens' operands; those of the next four are loaded before the current ones are used,
-  // and the sums over states of the last four taken among the products of the current ones
-  struct Four {
-    float4 d[4];
-    ulonglong2 b[4], q[4];
+  // the operands of G tokens; those of the next G are loaded before the current ones are used,
+  // and the sums over states of the last G taken among the products of the current ones
+  constexpr int G = OUT ? 4 : 2;
+  struct Few {
+    float4 d[G];
+    ulonglong2 b[G], q[G];
+    float2 y[G];
+  };
+  // kKeep: the states in front of the next token, and the sum of dt so far
+  long kept = KEEP ? (seg * sg.nsub) * a.D + k.c0 + 2 * cp : 0;
+  auto keep = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (2 * cp + i >= k.n) continue;
+      unpair(h01[i], h4[0], h4[1]);
+      unpair(h23[i], h4[2], h4[3]);
+      st_states4(sg.keep_h + (kept + i) * a.N, n0, a.N, h4);
+      if (nl == 0) sg.keep_dt[kept + i] = sum[i];
+    }
+    kept += a.D;
   };
   __syncthreads();
   for (int m = 0; m < tiles; ++m) {
     const int p = m & 1;
     auto load = [&](int u0) {
-      Four f;
+      Few f;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < G; ++u) {
         f.d[u] = *reinterpret_cast<const float4*>(&s.d[p][u0 + u][2 * turned<V>(u0 + u, cp)]);
         f.b[u] = *reinterpret_cast<const ulonglong2*>(&s.B[p][u0 + u][n0]);
         if (!ENDS) f.q[u] = *reinterpret_cast<const ulonglong2*>(&s.C[p][u0 + u][n0]);
+        if (KEEP) f.y[u] = *reinterpret_cast<const float2*>(&s.y[p][u0 + u][2 * cp]);
       }
       return f;
     };
@@ -373,35 +428,43 @@ __global__ void __launch_bounds__(2 * kThreads)
         s.y[p][u0 + v / 2][2 * cp + v % 2] = yp[0];
       }
     };
-    Four f = load(0);
+    Few f = load(0);
     float last[8];
 #pragma unroll
-    for (int u0 = 0; u0 < kTile; u0 += 4) {
-      Four next;
-      if (u0 + 4 < kTile) next = load(u0 + 4);
+    for (int u0 = 0; u0 < kTile; u0 += G) {
+      Few next;
+      if (u0 + G < kTile) next = load(u0 + G);
+      if (KEEP && u0 % kSub == 0 && m * kTile + u0 < end - t.t0) keep();
       float yp[8];  // four tokens x two channels
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < G; ++u) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float dt = i ? f.d[u].z : f.d[u].x, g = i ? f.d[u].w : f.d[u].y;
           const pair32 dd = pair(dt, dt), gg = pair(g, g);
-          h01[i] = pair_fma(pair_ex2(pair_mul(dd, A01[i])), h01[i], pair_mul(gg, f.b[u].x));
-          h23[i] = pair_fma(pair_ex2(pair_mul(dd, A23[i])), h23[i], pair_mul(gg, f.b[u].y));
-          if (ENDS)
-            sum[i] += dt;
-          else
-            yp[2 * u + i] = pair_sum(pair_fma(h23[i], f.q[u].y, pair_mul(h01[i], f.q[u].x)));
+          const pair32 e01 = pair_ex2(pair_mul(dd, A01[i])), e23 = pair_ex2(pair_mul(dd, A23[i]));
+          h01[i] = pair_fma(e01, h01[i], pair_mul(gg, f.b[u].x));
+          h23[i] = pair_fma(e23, h23[i], pair_mul(gg, f.b[u].y));
+          if (!OUT) sum[i] += dt;
+          if (KEEP) {
+            const float y = i ? f.y[u].y : f.y[u].x;
+            const pair32 yy = pair(y, y);
+            p01[i] = pair_mul(p01[i], e01);
+            p23[i] = pair_mul(p23[i], e23);
+            g01[i] = pair_fma(p01[i], pair_mul(yy, f.q[u].x), g01[i]);
+            g23[i] = pair_fma(p23[i], pair_mul(yy, f.q[u].y), g23[i]);
+          }
+          if (OUT) yp[2 * u + i] = pair_sum(pair_fma(h23[i], f.q[u].y, pair_mul(h01[i], f.q[u].x)));
         }
       }
-      if (!ENDS) {
-        if (u0 > 0) reduce(u0 - 4, last);
+      if (OUT) {
+        if (u0 > 0) reduce(u0 - G, last);
 #pragma unroll
         for (int i = 0; i < 8; ++i) last[i] = yp[i];
       }
-      if (u0 + 4 < kTile) f = next;
+      if (u0 + G < kTile) f = next;
     }
-    if (!ENDS) reduce(kTile - 4, last);
+    if (OUT) reduce(kTile - G, last);
     __syncthreads();
   }
 #pragma unroll
@@ -410,9 +473,15 @@ __global__ void __launch_bounds__(2 * kThreads)
     if (2 * cp + i >= k.n) continue;
     unpair(h01[i], h4[0], h4[1]);
     unpair(h23[i], h4[2], h4[3]);
-    if (ENDS) {
-      st_states4(seg_h + (seg * a.D + c) * a.N, n0, a.N, h4);
-      if (nl == 0) seg_dt[seg * a.D + c] = sum[i];
+    if (!OUT) {
+      if (!sg.h) continue;
+      st_states4(sg.h + (seg * a.D + c) * a.N, n0, a.N, h4);
+      if (nl == 0) sg.dt[seg * a.D + c] = sum[i];
+      if (KEEP) {
+        unpair(g01[i], h4[0], h4[1]);
+        unpair(g23[i], h4[2], h4[3]);
+        st_states4(sg.g + (seg * a.D + c) * a.N, n0, a.N, h4);
+      }
     } else if (a.h_out && end == t.len) {
       st_states4(a.h_out + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
     }
@@ -440,11 +509,19 @@ static __global__ void __launch_bounds__(256)
   const float A2 = a.A[i] * ATLAS_LOG2E;
   float h = a.h_in && t.carry ? a.h_in[(long)t.slot * dn + i] : 0.f;
   const int n = seq_tiles_of(t.len, S);
-  for (int k = 0; k < n; ++k, ++seg) {
-    const float own = k + 1 < n ? seg_h[seg * dn + i] : 0.f;
-    const float d = k + 1 < n ? seg_dt[seg * a.D + c] : 0.f;
-    seg_h[seg * dn + i] = h;
-    h = ex2(A2 * d) * h + own;
+  constexpr int U = 8;  // segments whose values are under way at a time
+  for (int k0 = 0; k0 < n; k0 += U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      own[j] = k0 + j + 1 < n ? seg_h[(seg + k0 + j) * dn + i] : 0.f;
+      d[j] = k0 + j + 1 < n ? seg_dt[(seg + k0 + j) * a.D + c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (k0 + j < n) seg_h[(seg + k0 + j) * dn + i] = h;
+      h = ex2(A2 * d[j]) * h + own[j];
+    }
   }
 }
 
@@ -505,21 +582,26 @@ size_t workspace(const ScanArgs& a) {
   return S ? (size_t)seq_tiles(a.s, S) * a.D * (a.N + 1) * 4 : 0;
 }
 
-template <typename T, int V, int LN, bool ENDS, bool NV>
-bool segment_pass(const ScanArgs& a, int S, float* seg_h, float* seg_dt, cudaStream_t st) {
-  const dim3 grid((unsigned)seq_tiles(a.s, S), blocks_over<Shape<LN>::kCB>(a));
-  constexpr size_t smem = sizeof(SegmentShared<T, LN, ENDS>);
-  auto* f = segment_kernel<T, V, LN, ENDS, NV>;
+template <typename T, int V, int LN, Mode MODE, bool NV>
+bool segment_pass(const ScanArgs& a, const Segments& sg, cudaStream_t st) {
+  const dim3 grid((unsigned)seq_tiles(a.s, sg.S), blocks_over<Shape<LN>::kCB>(a));
+  constexpr size_t smem = sizeof(SegmentShared<T, LN, MODE>);
+  auto* f = segment_kernel<T, V, LN, MODE, NV>;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return false;
-  f<<<grid, 2 * kThreads, smem, st>>>(a, S, seg_h, seg_dt);
+  f<<<grid, 2 * kThreads, smem, st>>>(a, sg);
   return true;
+}
+template <typename T, int V, int LN, Mode MODE>
+bool segment_pass(const ScanArgs& a, const Segments& sg, cudaStream_t st) {
+  constexpr int VV = V < Shape<LN>::kCB ? V : Shape<LN>::kCB;
+  return VV > 1 && a.wide_n ? segment_pass<T, VV, LN, MODE, (VV > 1)>(a, sg, st)
+                            : segment_pass<T, VV, LN, MODE, false>(a, sg, st);
 }
 
 template <typename T, int V, int LN>
 int forward(const ScanArgs& a, cudaStream_t st) {
-  constexpr int VV = V < Shape<LN>::kCB ? V : Shape<LN>::kCB;
   const int by = blocks_over<Shape<LN>::kCB>(a);
   if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
   if (!a.s.start && a.s.L == 1) {
@@ -528,23 +610,18 @@ int forward(const ScanArgs& a, cudaStream_t st) {
     token_kernel<T, LN><<<dim3(a.s.B, (unsigned)rows), kTokenThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
   }
-  int S = segment_tokens(a, by);
-  float *seg_h = nullptr, *seg_dt = nullptr;
-  auto pass = [&](auto ends) {
-    constexpr bool E = decltype(ends)::value;
-    return VV > 1 && a.wide_n ? segment_pass<T, VV, LN, E, (VV > 1)>(a, S, seg_h, seg_dt, st)
-                              : segment_pass<T, VV, LN, E, false>(a, S, seg_h, seg_dt, st);
-  };
-  if (S) {
-    seg_h = reinterpret_cast<float*>(a.ws);
-    seg_dt = seg_h + (size_t)seq_tiles(a.s, S) * a.D * a.N;
-    if (!pass(std::true_type())) return ATLAS_ERR_CUDA;
+  Segments sg = {};
+  sg.S = segment_tokens(a, by);
+  if (sg.S) {
+    sg.h = reinterpret_cast<float*>(a.ws);
+    sg.dt = sg.h + (size_t)seq_tiles(a.s, sg.S) * a.D * a.N;
+    if (!segment_pass<T, V, LN, kEnds>(a, sg, st)) return ATLAS_ERR_CUDA;
     const long dn = (long)a.D * a.N;
-    join_kernel<<<dim3((unsigned)((dn + 255) / 256), a.s.B), 256, 0, st>>>(a, S, seg_h, seg_dt);
+    join_kernel<<<dim3((unsigned)((dn + 255) / 256), a.s.B), 256, 0, st>>>(a, sg.S, sg.h, sg.dt);
   } else {
-    S = a.s.L > 0 ? a.s.L : 1;
+    sg.S = a.s.L > 0 ? a.s.L : 1;
   }
-  if (!pass(std::false_type())) return ATLAS_ERR_CUDA;
+  if (!segment_pass<T, V, LN, kOut>(a, sg, st)) return ATLAS_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 

@@ -21,15 +21,26 @@
 namespace atlas {
 namespace scan {
 
-constexpr int kSub = 8;
-constexpr int kBackThreads = 128;
+constexpr int kWalkers = 4;                        // warps that walk; as many prepare and finish
+constexpr int kBackThreads = 2 * kWalkers * kThreads;
+constexpr int kBackRing = 4;  // tiles as they lie in memory: finished, walked, prepared, under way
 
 template <int LN>
-struct BackShape {
-  static constexpr int kNP = 4 * LN;                   // padded states
-  static constexpr int kCW = 32 / LN;                  // channels of a warp
-  static constexpr int kCB = kCW * kBackThreads / 32;  // channels of a block
-};
+constexpr int kBackCB = kWalkers * Shape<LN>::kCB;  // channels of a block
+
+// Segment length, 0 for one segment a sequence.  Every pass but the join costs the same for
+// short segments; two blocks an SM, and some more so that the last ones do not stand alone.
+inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
+  const long want = 152 * 2 * 6;
+  const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
+  long S = rows * blocks_per_seq / want / kTile * kTile;
+#ifdef BS
+  S = BS;
+#endif
+  if (S < 128) S = 128;
+  if (S >= a.s.L) return 0;
+  return (int)S;
+}
 
 // Sizes and workspace of a backward call.
 template <int LN>
@@ -43,8 +54,8 @@ struct Back {
   float* pbc;               // [cb][rows][2][NP]
   size_t bytes;
   Back(const ScanArgs& a, void* ws) {
-    cb = blocks_over<BackShape<LN>::kCB>(a);
-    S = segment_tokens(a, cb);
+    cb = blocks_over<kBackCB<LN>>(a);
+    S = back_segment_tokens(a, cb);
     split = S != 0;
     if (!S) S = a.s.L > 0 ? a.s.L : 1;
     nsub = (S + kSub - 1) / kSub;
@@ -65,148 +76,13 @@ struct Back {
     take(pA, segs * DN);
     take(pD, segs * D);
     take(pb, segs * D);
-    take(pbc, (size_t)cb * rows * 2 * BackShape<LN>::kNP);
+    take(pbc, (size_t)cb * rows * 2 * Shape<LN>::kNP);
     bytes *= 4;
   }
+  Segments segments() const {
+    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub};
+  }
 };
-
-// Tokens t0 .. t0 + TT of dt (through softplus) and x into sd, those past `end` as zeros.
-template <typename T, int V, int LN, int TT>
-__device__ __forceinline__ void load_dx(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                        int t0, int end, float2 (*sd)[BackShape<LN>::kCB]) {
-  constexpr int CV = BackShape<LN>::kCB / V;
-  for (int i = threadIdx.x; i < TT * CV; i += kBackThreads) {
-    const int u = i / CV, cl = (i % CV) * V;
-    if (t0 + u < end && cl < k.n) {
-      const auto x = ld_pack<T, V>(reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, t0 + u, a.xb, a.xt) + k.c0 + cl);
-      const auto d = ld_pack<T, V>(reinterpret_cast<const T*>(a.dt) + seq_at(a.s, t, t0 + u, a.tb, a.tt) + k.c0 + cl);
-      float bias[V], step[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) bias[j] = a.bias ? a.bias[k.c0 + cl + j] : 0.f;
-      steps_of<T, V>(a, d, bias, step);
-#pragma unroll
-      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(step[j], x.get(j));
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) sd[u][cl + j] = make_float2(0.f, 0.f);
-    }
-  }
-}
-
-template <typename T, int LN, int TT>
-__device__ __forceinline__ void load_states(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                            int t0, int end, const void* p, long sb, long st,
-                                            float (*s)[BackShape<LN>::kNP]) {
-  constexpr int NP = 4 * LN;
-  const T* q = rows_of<T>(p, a, t, sb, st, k.g * a.N);
-  for (int i = threadIdx.x; i < TT * NP; i += kBackThreads) {
-    const int u = t0 + i / NP, n = i % NP;
-    s[i / NP][n] = u < end && n < a.N ? to_f(q[(long)u * st + n]) : 0.f;
-  }
-}
-
-// What the main pass needs of dy, z and softplus: dy SiLU(z), softplus' slope at the raw
-// step (1 without softplus) and dy SiLU'(z).
-template <typename T, int V, int LN>
-__device__ __forceinline__ void load_up(const ScanArgs& a, const SeqTile& t, const Channels& k,
-                                        int t0, int end, float (*dyg)[BackShape<LN>::kCB],
-                                        float (*slope)[BackShape<LN>::kCB], float (*dyz)[BackShape<LN>::kCB]) {
-  constexpr int CV = BackShape<LN>::kCB / V;
-  for (int i = threadIdx.x; i < kSub * CV; i += kBackThreads) {
-    const int u = i / CV, cl = (i % CV) * V;
-    if (t0 + u < end && cl < k.n) {
-      const auto dy = ld_pack<T, V>(reinterpret_cast<const T*>(a.dy) + seq_at(a.s, t, t0 + u, a.yb, a.yt) + k.c0 + cl);
-      Pack<T, V> z, d;
-      if (a.z) z = ld_pack<T, V>(reinterpret_cast<const T*>(a.z) + seq_at(a.s, t, t0 + u, a.zb, a.zt) + k.c0 + cl);
-      if (slope) d = ld_pack<T, V>(reinterpret_cast<const T*>(a.dt) + seq_at(a.s, t, t0 + u, a.tb, a.tt) + k.c0 + cl);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float g = dy.get(j);
-        if (a.z) {
-          const float zv = z.get(j), s = sigmoidf(zv);
-          dyg[u][cl + j] = g * zv * s;
-          if (dyz) dyz[u][cl + j] = g * silu_slope(zv, s);
-        } else {
-          dyg[u][cl + j] = g;
-        }
-        if (slope) {
-          const int c = k.c0 + cl + j;
-          slope[u][cl + j] = a.softplus ? sigmoidf(d.get(j) + (a.bias ? a.bias[c] : 0.f)) : 1.f;
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        dyg[u][cl + j] = 0.f;
-        if (slope) slope[u][cl + j] = 0.f;
-        if (dyz) dyz[u][cl + j] = 0.f;
-      }
-    }
-  }
-}
-
-template <typename T, int V, int LN>
-__global__ void __launch_bounds__(kBackThreads) keep_kernel(ScanArgs a, Back<LN> w) {
-  using P = BackShape<LN>;
-  __shared__ float2 sd[kSub][P::kCB];
-  __shared__ float sg[kSub][P::kCB];
-  __shared__ __align__(16) float sB[kSub][P::kNP];
-  __shared__ __align__(16) float sC[kSub][P::kNP];
-  if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, kBackThreads);
-  const long seg = blockIdx.x;
-  SeqTile t;
-  if (!seq_tile(a.s, seg, w.S, t)) return;
-  const int end = min(t.t0 + w.S, t.len);
-  const Channels k = channels_at<BackShape<LN>::kCB>(a, blockIdx.y);
-  const int lane = threadIdx.x & 31, nl = lane % LN, n0 = nl * 4;
-  const int cl = (threadIdx.x >> 5) * P::kCW + lane / LN, c = k.c0 + cl;
-  const bool live = cl < k.n;
-  float A2[4] = {0.f, 0.f, 0.f, 0.f}, h[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-  float p[4] = {1.f, 1.f, 1.f, 1.f}, g[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live) {
-    ld_states4(a.A + (long)c * a.N, n0, a.N, A2);
-    if (!w.split && a.h_in && t.carry)
-      ld_states4(a.h_in + ((long)t.b * a.D + c) * a.N, n0, a.N, h);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] *= ATLAS_LOG2E;
-  for (int t0 = t.t0; t0 < end; t0 += kSub) {
-    __syncthreads();
-    load_dx<T, V, LN, kSub>(a, t, k, t0, end, sd);
-    load_states<T, LN, kSub>(a, t, k, t0, end, a.Bm, a.bb, a.bt, sB);
-    if (w.split) {
-      load_states<T, LN, kSub>(a, t, k, t0, end, a.Cm, a.cb, a.ct, sC);
-      load_up<T, V, LN>(a, t, k, t0, end, sg, nullptr, nullptr);
-    }
-    __syncthreads();
-    if (live) {
-      const long at = (seg * w.nsub + (t0 - t.t0) / kSub) * a.D + c;
-      st_states4(w.keep_h + at * a.N, n0, a.N, h);
-      if (nl == 0) w.keep_dt[at] = sum;
-    }
-#pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      const float2 d = sd[u][cl];
-      const float gx = d.x * d.y;
-      sum += d.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = ex2(d.x * A2[i]);
-        h[i] = e * h[i] + gx * sB[u][n0 + i];
-        if (w.split) {
-          p[i] *= e;
-          g[i] += p[i] * (sC[u][n0 + i] * sg[u][cl]);
-        }
-      }
-    }
-  }
-  if (live && w.split) {
-    const long at = seg * a.D + c;
-    st_states4(w.seg_h + at * a.N, n0, a.N, h);
-    st_states4(w.seg_g + at * a.N, n0, a.N, g);
-    if (nl == 0) w.seg_dt[at] = sum;
-  }
-}
 
 // seg_h becomes the state each segment starts from, seg_g the adjoint behind its last token;
 // dh becomes dL/d h_in.
@@ -228,197 +104,429 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
   const int c = (int)(i / a.N);
   const float A2 = a.A[i] * ATLAS_LOG2E;
   const int n = seq_tiles_of(t.len, w.S);
+  // eight segments' values are under way at a time
+  constexpr int U = 8;
   float h = a.h_in && t.carry ? a.h_in[(long)b * dn + i] : 0.f;
-  for (int k = 0; k < n; ++k) {
-    const float own = w.seg_h[(seg + k) * dn + i];
-    w.seg_h[(seg + k) * dn + i] = h;
-    h = ex2(A2 * w.seg_dt[(seg + k) * a.D + c]) * h + own;
+  for (int k0 = 0; k0 < n; k0 += U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      own[j] = k0 + j < n ? w.seg_h[(seg + k0 + j) * dn + i] : 0.f;
+      d[j] = k0 + j < n ? w.seg_dt[(seg + k0 + j) * a.D + c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (k0 + j < n) w.seg_h[(seg + k0 + j) * dn + i] = h;
+      h = ex2(A2 * d[j]) * h + own[j];
+    }
   }
   float g = a.dh ? a.dh[(long)b * dn + i] : 0.f;
-  for (int k = n - 1; k >= 0; --k) {
-    const float own = w.seg_g[(seg + k) * dn + i];
-    w.seg_g[(seg + k) * dn + i] = g;
-    g = ex2(A2 * w.seg_dt[(seg + k) * a.D + c]) * g + own;
+  for (int k0 = n - 1; k0 >= 0; k0 -= U) {
+    float own[U], d[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      own[j] = k0 - j >= 0 ? w.seg_g[(seg + k0 - j) * dn + i] : 0.f;
+      d[j] = k0 - j >= 0 ? w.seg_dt[(seg + k0 - j) * a.D + c] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (k0 - j >= 0) w.seg_g[(seg + k0 - j) * dn + i] = g;
+      g = ex2(A2 * d[j]) * g + own[j];
+    }
   }
   if (a.dh) a.dh[(long)b * dn + i] = t.carry ? g : 0.f;
 }
 
-template <typename T, int V, int LN>
-__global__ void __launch_bounds__(kBackThreads) back_kernel(ScanArgs a, Back<LN> w) {
-  using P = BackShape<LN>;
-  __shared__ float2 sd[kSub][P::kCB];
-  __shared__ float sg[kSub][P::kCB], ss[kSub][P::kCB], sz[kSub][P::kCB];
-  __shared__ __align__(16) float sB[kSub][P::kNP];
-  __shared__ __align__(16) float sC[kSub][P::kNP];
-  __shared__ float sp[kBackThreads / 32][kSub][2 * P::kNP];
-  __shared__ float so[3][kSub][P::kCB];
+// Shared memory of back_kernel.
+template <typename T, int LN>
+struct BackShared {
+  using P = Shape<LN>;
+  struct Raw {  // tiles as they lie in memory, each preparing warp's channels apart
+    alignas(16) T x[kWalkers][kSub][P::kCB];
+    alignas(16) T dt[kWalkers][kSub][P::kCB];
+    alignas(16) T z[kWalkers][kSub][P::kCB];
+    alignas(16) T dy[kWalkers][kSub][P::kCB];
+    alignas(16) T B[kSub][P::kNP];
+    alignas(16) T C[kSub][P::kNP];
+    alignas(16) float h[kWalkers][P::kCB][P::kNP];  // the kept state, and the sum of dt there
+    alignas(16) float cum[kWalkers][P::kCB];
+  };
+  alignas(16) float hs[kWalkers][P::kCB][P::kNP];  // the state the segment starts from
+  alignas(16) float2 d[2][kWalkers][kSub][P::kCB];     // dt, dt x
+  alignas(16) float g[2][kWalkers][kSub][P::kCB];      // dy SiLU(z)
+  alignas(16) float slope[2][kWalkers][kSub][P::kCB];  // of softplus
+  alignas(16) float dz[2][kWalkers][kSub][P::kCB];     // dy SiLU'(z)
+  alignas(16) float B[2][kSub][P::kNP];
+  alignas(16) float C[2][kSub][P::kNP];
+  alignas(16) float sums[2][3][kWalkers][kSub][P::kCB + 8];  // over states: C h, g B, q A
+  alignas(16) float bc[2][kWalkers][kSub][2 * P::kNP];       // over a walker's channels: dB, dC
+  Raw raw[kBackRing];
+};
+
+// ex2 that is not merged with an earlier one of the same argument: the decays of a whole tile
+// would not fit the registers.
+__device__ __forceinline__ pair32 pair_ex2_again(pair32 a) {
+  float x, y;
+  unpair(a, x, y);
+  asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(y));
+  return pair(x, y);
+}
+
+// The main pass.  A walker has two channels x four states a lane, as in the forward pass; it
+// goes through kSub tokens forwards from the kept state, holding the states in registers, and
+// then backwards.  Its partner prepares the tile before, and writes out the tile behind.
+template <typename T, int V, int LN, bool NV>
+__global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<LN> w) {
+  using P = Shape<LN>;
+  using X = Tile<T, V, P::kCB, kSub>;
+  constexpr int VN = !NV ? 1 : 16 / sizeof(T) < P::kNP ? 16 / sizeof(T) : P::kNP;
+  using R = Tile<T, VN, P::kNP, kSub>;
+  using Shared = BackShared<T, LN>;
+  using Raw = typename Shared::Raw;
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared& s = *reinterpret_cast<Shared*>(smem);
   const long seg = blockIdx.x;
-  const Channels k = channels_at<BackShape<LN>::kCB>(a, blockIdx.y);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nl = lane % LN, n0 = nl * 4;
-  const int chl = lane / LN, cl = warp * P::kCW + chl, c = k.c0 + cl;
-  const bool live = cl < k.n;
-  float A2[4] = {0.f, 0.f, 0.f, 0.f}, hs[4] = {0.f, 0.f, 0.f, 0.f}, gp[4] = {0.f, 0.f, 0.f, 0.f};
-  float dA[4] = {0.f, 0.f, 0.f, 0.f}, dD = 0.f, db = 0.f;
+  const Channels kb = channels_at<kBackCB<LN>>(a, blockIdx.y);
+  const int lane = threadIdx.x & 31, wi = (threadIdx.x >> 5) % kWalkers;
+  const bool walks = threadIdx.x < kWalkers * kThreads;
+  Channels k = kb;  // this warp's
+  k.c0 += wi * P::kCB;
+  k.n = max(0, min(P::kCB, kb.n - wi * P::kCB));
   SeqTile t;
   const bool some = seq_tile(a.s, seg, w.S, t);
-  if (some) {
-    const int end = min(t.t0 + w.S, t.len);
-    if (live) {
-      ld_states4(a.A + (long)c * a.N, n0, a.N, A2);
-      if (w.split) {
-        ld_states4(w.seg_h + (seg * a.D + c) * a.N, n0, a.N, hs);
-        ld_states4(w.seg_g + (seg * a.D + c) * a.N, n0, a.N, gp);
-      } else if (a.dh) {
-        ld_states4(a.dh + ((long)t.b * a.D + c) * a.N, n0, a.N, gp);
-      }
+  const int end = some ? min(t.t0 + w.S, t.len) : 0;
+  const int tiles = some ? (end - t.t0 + kSub - 1) / kSub : 0;
+  const int first = tiles > 0 ? t.t0 + (tiles - 1) * kSub : 0;  // the last tile comes first
+
+  if (!walks) {
+    float dD[V], db[V], bias[V], skip[V];
+    static_assert(kThreads % (P::kCB / V) == 0, "a thread's vectors share their channels");
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int ch = X::channel(0) + j;
+      bias[j] = a.bias && ch < k.n ? a.bias[k.c0 + ch] : 0.f;
+      skip[j] = a.Dk && ch < k.n ? a.Dk[k.c0 + ch] : 0.f;
+      dD[j] = db[j] = 0.f;
     }
+    if (tiles > 0) {
+      X px(rows_of<T>(a.x, a, t, a.xb, a.xt, k.c0), a.xt, first);
+      X pd(rows_of<T>(a.dt, a, t, a.tb, a.tt, k.c0), a.tt, first);
+      X pz(rows_of<T>(a.z ? a.z : a.x, a, t, a.zb, a.zt, k.c0), a.zt, first);
+      X py(rows_of<T>(a.dy, a, t, a.yb, a.yt, k.c0), a.yt, first);
+      X ox(rows_of<T>(a.dx, a, t, a.xb, a.xt, k.c0), a.xt, first);
+      X od(rows_of<T>(a.ddt, a, t, a.tb, a.tt, k.c0), a.tt, first);
+      X oz(rows_of<T>(a.z ? a.dz : a.dx, a, t, a.zb, a.zt, k.c0), a.zt, first);
+      // the first partner brings B, the second C
+      R pn(rows_of<T>(wi ? a.Cm : a.Bm, a, t, wi ? a.cb : a.bb, wi ? a.ct : a.bt, k.g * a.N), wi ? a.ct : a.bt, first);
+      const long row0 = (a.s.start ? t.first : (long)t.b * a.s.L) + first;
+      float* pbc = w.pbc + ((long)blockIdx.y * w.rows + row0) * 2 * P::kNP;
+      int rf = 0, rp = 0, rn = 0;
+      int nf = 0, np = 0;  // tiles fetched, prepared
+      const auto step = [](int& r) { r = (r + 1) % kBackRing; };
+      auto fetch = [&]() {
+        if (nf < tiles) {
+          const int left = nf == 0 ? end - first : kSub;
+          const long at = (seg * w.nsub + tiles - 1 - nf) * a.D + k.c0;
+          Raw& r = s.raw[rf];
+          px.copy(r.x[wi], left, k.n), px.back();
+          pd.copy(r.dt[wi], left, k.n), pd.back();
+          py.copy(r.dy[wi], left, k.n), py.back();
+          if (a.z) pz.copy(r.z[wi], left, k.n), pz.back();
+          if (wi == 0) pn.copy(r.B, left, a.N), pn.back();
+          if (wi == 1) pn.copy(r.C, left, a.N), pn.back();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] *= ATLAS_LOG2E;
-    const float Dk = a.Dk && live ? a.Dk[c] : 0.f;
-    const long row0 = a.s.start ? t.first : (long)t.b * a.s.L;
-    for (int sub = (end - t.t0 + kSub - 1) / kSub - 1; sub >= 0; --sub) {
-      const int t0 = t.t0 + sub * kSub;
-      __syncthreads();
-      load_dx<T, V, LN, kSub>(a, t, k, t0, end, sd);
-      load_states<T, LN, kSub>(a, t, k, t0, end, a.Bm, a.bb, a.bt, sB);
-      load_states<T, LN, kSub>(a, t, k, t0, end, a.Cm, a.cb, a.ct, sC);
-      load_up<T, V, LN>(a, t, k, t0, end, sg, ss, a.z ? sz : nullptr);
-      float h[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        const long at = (seg * w.nsub + sub) * a.D + c;
-        ld_states4(w.keep_h + at * a.N, n0, a.N, h);
-        if (w.split) {
-          const float cum = w.keep_dt[at];
+          for (int i = lane; i < P::kCB * LN; i += kThreads) {
+            const int ch = i / LN, n = i % LN * 4;
+            const float* q = w.keep_h + (at + ch) * a.N + n;
+            if (a.N % 4 == 0) {
+              const bool in = ch < k.n && n < a.N;
+              cp_async<16>(&r.h[wi][ch][n], in ? q : w.keep_h, in);
+            } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) h[i] += ex2(A2[i] * cum) * hs[i];
-        }
-      }
-      __syncthreads();
-      float e[kSub][4], v[kSub][4];  // a_t and a_t h_{t-1}
-#pragma unroll
-      for (int u = 0; u < kSub; ++u) {
-        const float2 d = sd[u][cl];
-        const float4 b = *reinterpret_cast<const float4*>(&sB[u][n0]);
-        const float bb[4] = {b.x, b.y, b.z, b.w}, gx = d.x * d.y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          e[u][i] = ex2(d.x * A2[i]);
-          v[u][i] = e[u][i] * h[i];
-          h[i] = v[u][i] + gx * bb[i];
-        }
-      }
-#pragma unroll
-      for (int u0 = kSub - 4; u0 >= 0; u0 -= 4) {
-        float ry[4], rs[4], rq[4];
-#pragma unroll
-        for (int uu = 3; uu >= 0; --uu) {
-          const int u = u0 + uu;
-          const float2 d = sd[u][cl];
-          const float4 b4 = *reinterpret_cast<const float4*>(&sB[u][n0]);
-          const float4 c4 = *reinterpret_cast<const float4*>(&sC[u][n0]);
-          const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-          const float gx = d.x * d.y, dyg = sg[u][cl];
-          float m[8], y = 0.f, s = 0.f, q = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float g = gp[i] + cc[i] * dyg;
-            const float ht = v[u][i] + gx * bb[i];
-            const float qt = g * v[u][i];
-            y += cc[i] * ht;
-            s += g * bb[i];
-            q += qt * A2[i];
-            dA[i] += qt * d.x;
-            m[i] = g * gx;
-            m[4 + i] = ht * dyg;
-            gp[i] = e[u][i] * g;
-          }
-          ry[uu] = y;
-          rs[uu] = s;
-          rq[uu] = q;
-          lane_sums<8, P::kCW, LN>(m, lane);
-          if (P::kCW <= 8) {
-            constexpr int NV = P::kCW <= 8 ? 8 / P::kCW : 1;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-              const int id = chl * NV + i;
-              sp[warp][u][(id >> 2) * P::kNP + n0 + (id & 3)] = m[i];
+              for (int j = 0; j < 4; ++j) {
+                const bool in = ch < k.n && n + j < a.N;
+                cp_async<4>(&r.h[wi][ch][n + j], in ? q + j : w.keep_h, in);
+              }
             }
-          } else if (chl % (P::kCW > 8 ? P::kCW / 8 : 1) == 0) {
-            const int id = chl / (P::kCW > 8 ? P::kCW / 8 : 1);
-            sp[warp][u][(id >> 2) * P::kNP + n0 + (id & 3)] = m[0];
           }
+          if (lane < P::kCB) cp_async<4>(&r.cum[wi][lane], lane < k.n ? w.keep_dt + at + lane : w.keep_dt, lane < k.n);
         }
-        lane_sums<4, LN, 1>(ry, lane);
-        lane_sums<4, LN, 1>(rs, lane);
-        lane_sums<4, LN, 1>(rq, lane);
-        constexpr int NV = LN <= 4 ? 4 / LN : 1, NR = LN > 4 ? LN / 4 : 1;
-        if (nl % NR == 0) {
+        cp_commit();
+        ++nf;
+        step(rf);
+      };
+      auto prepare = [&](int p) {
+        if (np >= tiles) return;
+        const int left = np == 0 ? end - first : kSub;
+        const Raw& r = s.raw[rp];
+        ++np;
+        step(rp);
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            const int u = u0 + (LN <= 4 ? nl * NV + i : nl / NR);
-            const float2 d = sd[u][cl];
-            const float dyg = sg[u][cl];
-            const float ddt = (rs[i] * d.y + rq[i] * (1.f / ATLAS_LOG2E)) * ss[u][cl];
-            so[0][u][cl] = rs[i] * d.x + Dk * dyg;
-            so[1][u][cl] = ddt;
-            if (a.z) so[2][u][cl] = sz[u][cl] * (ry[i] + Dk * d.y);
-            dD += dyg * d.y;
-            db += ddt;
+        for (int i = 0; i < X::kN; ++i)
+          if (X::inside(i)) {
+            const int u = X::token(i), q = X::channel(i);
+            float x[V], d[V], y[V], z[V], sl[V], sz[V];
+            ld_pack<T, V>(&r.x[wi][u][q]).unpack(x);
+            ld_pack<T, V>(&r.dt[wi][u][q]).unpack(d);
+            ld_pack<T, V>(&r.dy[wi][u][q]).unpack(y);
+            if (a.z) ld_pack<T, V>(&r.z[wi][u][q]).unpack(z);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              d[j] += bias[j];
+              sl[j] = 1.f;
+              if (a.softplus) {
+                sl[j] = sigmoidf(d[j]);
+                d[j] = softplusf(d[j]);
+              }
+              sz[j] = 0.f;
+              if (a.z) {
+                const float sg = sigmoidf(z[j]);
+                sz[j] = y[j] * silu_slope(z[j], sg);
+                y[j] *= z[j] * sg;
+              }
+              if (u >= left) d[j] = 0.f, sl[j] = 0.f;
+              x[j] *= d[j];
+            }
+            if (V == 1) {
+              s.d[p][wi][u][q] = make_float2(d[0], x[0]);
+            } else {
+#pragma unroll
+              for (int j = 0; j + 1 < V; j += 2)
+                *reinterpret_cast<float4*>(&s.d[p][wi][u][2 * turned<V>(u, (q + j) / 2)]) =
+                    make_float4(d[j], x[j], d[j + 1], x[j + 1]);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+              s.g[p][wi][u][q + j] = y[j];
+              s.slope[p][wi][u][q + j] = sl[j];
+              if (a.z) s.dz[p][wi][u][q + j] = sz[j];
+            }
+          }
+        if (wi < 2) {
+#pragma unroll
+          for (int i = lane; i < kSub * P::kNP / 4; i += kThreads) {
+            const int u = i / (P::kNP / 4), n = i % (P::kNP / 4) * 4;
+            float b[4];
+            ld_pack<T, 4>(wi ? &r.C[u][n] : &r.B[u][n]).unpack(b);
+            *reinterpret_cast<float4*>(wi ? &s.C[p][u][n] : &s.B[p][u][n]) = make_float4(b[0], b[1], b[2], b[3]);
           }
         }
-      }
+      };
+      auto finish = [&](int p, int left) {
+        const Raw& r = s.raw[rn];
+        step(rn);
+#pragma unroll
+        for (int i = 0; i < X::kN; ++i) {
+          const int u = X::token(i), q = X::channel(i);
+          if (!X::inside(i) || u >= left || q >= k.n) continue;
+          float x[V], dx[V], dd[V], dz[V];
+          ld_pack<T, V>(&r.x[wi][u][q]).unpack(x);
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float dt = s.d[p][wi][u][V == 1 ? q : 2 * turned<V>(u, (q + j) / 2) + (j & 1)].x;
+            const float dyg = s.g[p][wi][u][q + j], gB = s.sums[p][1][wi][u][q + j];
+            dx[j] = gB * dt + skip[j] * dyg;
+            dd[j] = (gB * x[j] + s.sums[p][2][wi][u][q + j] * (1.f / ATLAS_LOG2E)) * s.slope[p][wi][u][q + j];
+            dD[j] += dyg * x[j];
+            db[j] += dd[j];
+            if (a.z) dz[j] = s.dz[p][wi][u][q + j] * (s.sums[p][0][wi][u][q + j] + skip[j] * x[j]);
+          }
+          Pack<T, V> o;
+          o.pack(dx);
+          st_pack<T, V>(ox.at(i), o);
+          o.pack(dd);
+          st_pack<T, V>(od.at(i), o);
+          if (a.z) {
+            o.pack(dz);
+            st_pack<T, V>(oz.at(i), o);
+          }
+        }
+        ox.back(), od.back(), oz.back();
+        for (int i = wi * kThreads + lane; i < kSub * 2 * P::kNP; i += kWalkers * kThreads) {
+          if (i / (2 * P::kNP) >= left) continue;
+          float v = 0.f;
+#pragma unroll
+          for (int r2 = 0; r2 < kWalkers; ++r2) v += (&s.bc[p][r2][0][0])[i];
+          pbc[i] = v;
+        }
+        pbc -= kSub * 2 * P::kNP;
+      };
+      fetch();
+      fetch();
+      cp_wait<1>();
+      __syncwarp();
+      prepare(0);
       __syncthreads();
-      constexpr int CV = P::kCB / V;
-      for (int i = threadIdx.x; i < kSub * CV; i += kBackThreads) {
-        const int u = i / CV, q = (i % CV) * V;
-        if (t0 + u >= end || q >= k.n) continue;
-        Pack<T, V> o;
-#pragma unroll
-        for (int j = 0; j < V; ++j) o.set(j, so[0][u][q + j]);
-        st_pack<T, V>(reinterpret_cast<T*>(a.dx) + seq_at(a.s, t, t0 + u, a.xb, a.xt) + k.c0 + q, o);
-#pragma unroll
-        for (int j = 0; j < V; ++j) o.set(j, so[1][u][q + j]);
-        st_pack<T, V>(reinterpret_cast<T*>(a.ddt) + seq_at(a.s, t, t0 + u, a.tb, a.tt) + k.c0 + q, o);
-        if (a.z) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) o.set(j, so[2][u][q + j]);
-          st_pack<T, V>(reinterpret_cast<T*>(a.dz) + seq_at(a.s, t, t0 + u, a.zb, a.zt) + k.c0 + q, o);
-        }
+      for (int m = 0; m < tiles; ++m) {
+        fetch();
+        if (m > 0) finish((m - 1) & 1, m == 1 ? end - first : kSub);
+        cp_wait<1>();
+        __syncwarp();
+        prepare((m + 1) & 1);
+        __syncthreads();
       }
-      for (int i = threadIdx.x; i < kSub * 2 * P::kNP; i += kBackThreads) {
-        const int u = i / (2 * P::kNP), q = i % (2 * P::kNP);
-        if (t0 + u >= end) continue;
-        float s = sp[0][u][q];
+      cp_wait<0>();
+      finish((tiles - 1) & 1, tiles == 1 ? end - first : kSub);
+    }
+    // a channel's tokens lie in the lanes that share its vector
 #pragma unroll
-        for (int r = 1; r < kBackThreads / 32; ++r) s += sp[r][u][q];
-        w.pbc[((long)blockIdx.y * w.rows + row0 + t0 + u) * 2 * P::kNP + q] = s;
+    for (int j = 0; j < V; ++j) {
+#pragma unroll
+      for (int m = P::kCB / V; m < 32; m *= 2) {
+        dD[j] += __shfl_xor_sync(0xFFFFFFFFu, dD[j], m);
+        db[j] += __shfl_xor_sync(0xFFFFFFFFu, db[j], m);
+      }
+      const int ch = lane * V + j;
+      if (lane < P::kCB / V && ch < k.n) {
+        w.pD[seg * a.D + k.c0 + ch] = dD[j];
+        w.pb[seg * a.D + k.c0 + ch] = db[j];
       }
     }
+    return;
   }
-  // dD and ddt_bias lie in the lanes that owned the tokens
+
+  const int nl = lane / P::kPairs, n0 = nl * 4, cp = lane % P::kPairs;
+  pair32 A01[2], A23[2], g01[2], g23[2], dA01[2], dA23[2];
 #pragma unroll
-  for (int m = LN / 2; m; m >>= 1) {
-    dD += __shfl_xor_sync(0xFFFFFFFFu, dD, m);
-    db += __shfl_xor_sync(0xFFFFFFFFu, db, m);
+  for (int i = 0; i < 2; ++i) {
+    const int c = k.c0 + 2 * cp + i;
+    float A4[4] = {0.f, 0.f, 0.f, 0.f}, h4[4] = {0.f, 0.f, 0.f, 0.f}, g4[4] = {0.f, 0.f, 0.f, 0.f};
+    if (some && 2 * cp + i < k.n) {
+      ld_states4(a.A + (long)c * a.N, n0, a.N, A4);
+      if (w.split) {
+        ld_states4(w.seg_h + (seg * a.D + c) * a.N, n0, a.N, h4);
+        ld_states4(w.seg_g + (seg * a.D + c) * a.N, n0, a.N, g4);
+      } else if (a.dh) {
+        ld_states4(a.dh + ((long)t.b * a.D + c) * a.N, n0, a.N, g4);
+      }
+    }
+    A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
+    A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
+    // read by this lane alone
+    *reinterpret_cast<float4*>(&s.hs[wi][2 * cp + i][n0]) = make_float4(h4[0], h4[1], h4[2], h4[3]);
+    g01[i] = pair(g4[0], g4[1]);
+    g23[i] = pair(g4[2], g4[3]);
+    dA01[i] = dA23[i] = pair(0.f, 0.f);
   }
-  if (!live) return;
-  const long at = seg * a.D + c;
-  st_states4(w.pA + at * a.N, n0, a.N, dA);
-  if (nl == 0) {
-    w.pD[at] = dD;
-    w.pb[at] = db;
-  }
-  if (some && !w.split && a.dh) {
+  if (tiles > 0) __syncthreads();
+  for (int m = 0; m < tiles; ++m) {
+    const int p = m & 1;
+    pair32 h01[2][kSub + 1], h23[2][kSub + 1];  // states in front of each token
 #pragma unroll
-    for (int i = 0; i < 4; ++i) gp[i] = t.carry ? gp[i] : 0.f;
-    st_states4(a.dh + ((long)t.b * a.D + c) * a.N, n0, a.N, gp);
+    for (int i = 0; i < 2; ++i) {
+      const Raw& r = s.raw[m % kBackRing];
+      const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(&r.h[wi][2 * cp + i][n0]);
+      h01[i][0] = h.x;
+      h23[i][0] = h.y;
+      if (w.split) {
+        const ulonglong2 hs = *reinterpret_cast<const ulonglong2*>(&s.hs[wi][2 * cp + i][n0]);
+        const float cum = r.cum[wi][2 * cp + i];
+        const pair32 cc = pair(cum, cum);
+        h01[i][0] = pair_fma(pair_ex2(pair_mul(cc, A01[i])), hs.x, h.x);
+        h23[i][0] = pair_fma(pair_ex2(pair_mul(cc, A23[i])), hs.y, h.y);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
+      const float4 d = *reinterpret_cast<const float4*>(&s.d[p][wi][u][2 * turned<V>(u, cp)]);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[p][u][n0]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float dt = i ? d.z : d.x, gx = i ? d.w : d.y;
+        const pair32 dd = pair(dt, dt), gg = pair(gx, gx);
+        h01[i][u + 1] = pair_fma(pair_ex2(pair_mul(dd, A01[i])), h01[i][u], pair_mul(gg, b.x));
+        h23[i][u + 1] = pair_fma(pair_ex2(pair_mul(dd, A23[i])), h23[i][u], pair_mul(gg, b.y));
+      }
+    }
+#pragma unroll
+    for (int u0 = kSub - 4; u0 >= 0; u0 -= 4) {
+      float ry[8], rs[8], rq[8];  // four tokens x two channels
+#pragma unroll
+      for (int uu = 3; uu >= 0; --uu) {
+        const int u = u0 + uu;
+        const float4 d = *reinterpret_cast<const float4*>(&s.d[p][wi][u][2 * turned<V>(u, cp)]);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[p][u][n0]);
+        const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(&s.C[p][u][n0]);
+        const float2 dy = *reinterpret_cast<const float2*>(&s.g[p][wi][u][2 * cp]);
+        pair32 mB01, mB23, mC01, mC23;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float dt = i ? d.z : d.x, gx = i ? d.w : d.y, y = i ? dy.y : dy.x;
+          const pair32 dd = pair(dt, dt), gg = pair(gx, gx), yy = pair(y, y);
+          const pair32 e01 = pair_ex2_again(pair_mul(dd, A01[i])), e23 = pair_ex2_again(pair_mul(dd, A23[i]));
+          const pair32 G01 = pair_fma(q.x, yy, g01[i]), G23 = pair_fma(q.y, yy, g23[i]);  // dL/dh_t
+          const pair32 H01 = h01[i][u + 1], H23 = h23[i][u + 1];
+          ry[2 * uu + i] = pair_sum(pair_fma(H23, q.y, pair_mul(H01, q.x)));
+          rs[2 * uu + i] = pair_sum(pair_fma(G23, b.y, pair_mul(G01, b.x)));
+          g01[i] = pair_mul(e01, G01);
+          g23[i] = pair_mul(e23, G23);
+          const pair32 q01 = pair_mul(g01[i], h01[i][u]), q23 = pair_mul(g23[i], h23[i][u]);
+          rq[2 * uu + i] = pair_sum(pair_fma(q23, A23[i], pair_mul(q01, A01[i])));
+          dA01[i] = pair_fma(q01, dd, dA01[i]);
+          dA23[i] = pair_fma(q23, dd, dA23[i]);
+          mB01 = i ? pair_fma(G01, gg, mB01) : pair_mul(G01, gg);
+          mB23 = i ? pair_fma(G23, gg, mB23) : pair_mul(G23, gg);
+          mC01 = i ? pair_fma(H01, yy, mC01) : pair_mul(H01, yy);
+          mC23 = i ? pair_fma(H23, yy, mC23) : pair_mul(H23, yy);
+        }
+        float v[8];
+        unpair(mB01, v[0], v[1]);
+        unpair(mB23, v[2], v[3]);
+        unpair(mC01, v[4], v[5]);
+        unpair(mC23, v[6], v[7]);
+        lane_sums<8, P::kPairs, 1>(v, lane);
+        constexpr int M = P::kPairs <= 8 ? 8 / P::kPairs : 1, E = P::kPairs > 8 ? P::kPairs / 8 : 1;
+        if (cp % E == 0) {
+#pragma unroll
+          for (int i = 0; i < M; ++i) {
+            const int id = cp / E * M + i;
+            s.bc[p][wi][u][(id >> 2) * P::kNP + n0 + (id & 3)] = v[i];
+          }
+        }
+      }
+      auto put = [&](int which, float* v) {
+        lane_sums<8, LN, P::kPairs>(v, lane);
+        constexpr int M = LN <= 8 ? 8 / LN : 1, E = LN > 8 ? LN / 8 : 1;  // (token, channel) order
+        if (nl % E == 0) {
+          if constexpr (M >= 2) {
+#pragma unroll
+            for (int i = 0; i < M; i += 2)
+              *reinterpret_cast<float2*>(&s.sums[p][which][wi][u0 + (nl * M + i) / 2][2 * cp]) =
+                  make_float2(v[i], v[i + 1]);
+          } else {
+            s.sums[p][which][wi][u0 + nl / E / 2][2 * cp + nl / E % 2] = v[0];
+          }
+        }
+      };
+      if (a.z) put(0, ry);
+      put(1, rs);
+      put(2, rq);
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = k.c0 + 2 * cp + i;
+    if (2 * cp + i >= k.n) continue;
+    float v[4];
+    unpair(dA01[i], v[0], v[1]);
+    unpair(dA23[i], v[2], v[3]);
+    st_states4(w.pA + (seg * a.D + c) * a.N, n0, a.N, v);
+    if (some && !w.split && a.dh) {
+      unpair(g01[i], v[0], v[1]);
+      unpair(g23[i], v[2], v[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = t.carry ? v[j] : 0.f;
+      st_states4(a.dh + ((long)t.b * a.D + c) * a.N, n0, a.N, v);
+    }
   }
 }
 
 // Adds the partial sums: the first `nbc` blocks dB and dC, the others dA, dD and ddt_bias.
 template <typename T, int LN>
 __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int nbc) {
-  constexpr int NP = BackShape<LN>::kNP;
+  constexpr int NP = Shape<LN>::kNP;
   if ((int)blockIdx.x < nbc) {
     const int bpg = w.cb / a.G;
     long lo = 0, hi = w.rows;
@@ -459,17 +567,32 @@ __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int
   }
 }
 
+template <typename T, int V, int LN, bool NV>
+bool back_pass(const ScanArgs& a, const Back<LN>& w, cudaStream_t st) {
+  constexpr size_t smem = sizeof(BackShared<T, LN>);
+  auto* f = back_kernel<T, V, LN, NV>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return false;
+  f<<<dim3((unsigned)w.segs, w.cb), kBackThreads, smem, st>>>(a, w);
+  return true;
+}
+
 template <typename T, int V, int LN>
 int backward(const ScanArgs& a, cudaStream_t st) {
-  constexpr int VV = V < BackShape<LN>::kCB ? V : BackShape<LN>::kCB;
+  // four channels a vector: a tile of kSub tokens then has one for every lane
+  constexpr int V4 = V > 4 ? 4 : V, VV = V4 < Shape<LN>::kCB ? V4 : Shape<LN>::kCB;
   const Back<LN> w(a, a.ws);
-  if (w.cb > 65535 || a.s.B > 65535 || w.segs > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
-  const dim3 grid((unsigned)w.segs, w.cb);
-  if (w.segs > 0) keep_kernel<T, VV, LN><<<grid, kBackThreads, 0, st>>>(a, w);
-  if (w.segs > 0 && w.split)
-    join_back_kernel<LN><<<dim3((unsigned)(((long)a.D * a.N + 255) / 256), a.s.B), 256, 0, st>>>(a, w);
-  if (w.segs > 0) back_kernel<T, VV, LN><<<grid, kBackThreads, 0, st>>>(a, w);
-  const long nb = (w.rows * a.G * 2 * BackShape<LN>::kNP + 255) / 256;
+  const int by = blocks_over<Shape<LN>::kCB>(a);
+  if (by > 65535 || a.s.B > 65535 || w.segs > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
+  if (w.segs > 0) {
+    if (!segment_pass<T, V, LN, kKeep>(a, w.segments(), st)) return ATLAS_ERR_CUDA;
+    if (w.split)
+      join_back_kernel<LN><<<dim3((unsigned)(((long)a.D * a.N + 255) / 256), a.s.B), 256, 0, st>>>(a, w);
+    if (!(VV > 1 && a.wide_n ? back_pass<T, VV, LN, (VV > 1)>(a, w, st) : back_pass<T, VV, LN, false>(a, w, st)))
+      return ATLAS_ERR_CUDA;
+  }
+  const long nb = (w.rows * a.G * 2 * Shape<LN>::kNP + 255) / 256;
   const int nbc = (int)(nb < 152 * 16 ? nb : 152 * 16);
   const long na = ((long)a.D * (a.N + 2) + 255) / 256;
   finish_kernel<T, LN><<<nbc + (int)(na < 4096 ? na : 4096), 256, 0, st>>>(a, w, nbc);
