@@ -97,6 +97,27 @@ __device__ __forceinline__ void st_pack(T* p, const Pack<T, V>& v) {
   *reinterpret_cast<Pack<T, V>*>(p) = v;
 }
 
+// V neighbouring 32-bit numbers, aligned to V (at most four at a time).
+template <int V>
+__device__ __forceinline__ void ld_vec(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += (V < 4 ? V : 4)) {
+    const auto q = ld_pack<float, (V < 4 ? V : 4)>(p + i);
+#pragma unroll
+    for (int j = 0; j < (V < 4 ? V : 4); ++j) v[i + j] = q.e[j];
+  }
+}
+template <int V>
+__device__ __forceinline__ void st_vec(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < V; i += (V < 4 ? V : 4)) {
+    Pack<float, (V < 4 ? V : 4)> q;
+#pragma unroll
+    for (int j = 0; j < (V < 4 ? V : 4); ++j) q.e[j] = v[i + j];
+    st_pack<float, (V < 4 ? V : 4)>(p + i, q);
+  }
+}
+
 // Element of a type known at run time (parameters, read once per block).
 __device__ __forceinline__ float ld_any(const void* p, long i, int dtype) {
   if (dtype == ATLAS_BF16) return to_f(reinterpret_cast<const __nv_bfloat16*>(p)[i]);

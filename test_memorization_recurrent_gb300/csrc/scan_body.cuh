@@ -295,8 +295,11 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
 #pragma unroll
               for (int j = 0; j < V; ++j) y[j] *= siluf(z[j]);
             }
+            if (left < kTile) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) s.y[p][u][q + j] = u < left ? y[j] : 0.f;
+              for (int j = 0; j < V; ++j) y[j] = u < left ? y[j] : 0.f;
+            }
+            st_vec<V>(&s.y[p][u][q], y);
           }
       }
 #pragma unroll
@@ -320,8 +323,9 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
         if (!X::inside(i) || u >= left_n || q >= k.n) continue;
         float y[V], z[V];
         ld_pack<T, V>(&r.x[u][q]).unpack(y);
+        ld_vec<V>(&s.y[p][u][q], z);
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = fmaf(skip[j], y[j], s.y[p][u][q + j]);
+        for (int j = 0; j < V; ++j) y[j] = fmaf(skip[j], y[j], z[j]);
         if (a.z) {
           ld_pack<T, V>(&r.z[u][q]).unpack(z);
 #pragma unroll

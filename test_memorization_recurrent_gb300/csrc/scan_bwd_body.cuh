@@ -148,10 +148,10 @@ struct BackShared {
     alignas(16) T dy[kWalkers][kSub][P::kCB];
     alignas(16) T B[kSub][P::kNP];
     alignas(16) T C[kSub][P::kNP];
-    alignas(16) float h[kWalkers][P::kCB][P::kNP];  // the kept state, and the sum of dt there
-    alignas(16) float cum[kWalkers][P::kCB];
+    alignas(16) float h[kWalkers][2][kThreads][4];  // the kept states of each walking lane's two
+    alignas(16) float cum[kWalkers][P::kCB];        // channels, and the sum of dt there
   };
-  alignas(16) float hs[kWalkers][P::kCB][P::kNP];  // the state the segment starts from
+  alignas(16) float hs[kWalkers][2][kThreads][4];  // the states the segment starts from
   alignas(16) float2 d[2][kWalkers][kSub][P::kCB];     // dt, dt x
   alignas(16) float g[2][kWalkers][kSub][P::kCB];      // dy SiLU(z)
   alignas(16) float slope[2][kWalkers][kSub][P::kCB];  // of softplus
@@ -239,14 +239,15 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
           for (int i = lane; i < P::kCB * LN; i += kThreads) {
             const int ch = i / LN, n = i % LN * 4;
             const float* q = w.keep_h + (at + ch) * a.N + n;
+            float* o = r.h[wi][ch & 1][i % LN * P::kPairs + ch / 2];
             if (a.N % 4 == 0) {
               const bool in = ch < k.n && n < a.N;
-              cp_async<16>(&r.h[wi][ch][n], in ? q : w.keep_h, in);
+              cp_async<16>(o, in ? q : w.keep_h, in);
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const bool in = ch < k.n && n + j < a.N;
-                cp_async<4>(&r.h[wi][ch][n + j], in ? q + j : w.keep_h, in);
+                cp_async<4>(o + j, in ? q + j : w.keep_h, in);
               }
             }
           }
@@ -285,9 +286,14 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
                 sz[j] = y[j] * silu_slope(z[j], sg);
                 y[j] *= z[j] * sg;
               }
-              if (u >= left) d[j] = 0.f, sl[j] = 0.f;
-              x[j] *= d[j];
             }
+            if (left < kSub) {  // nothing behind the end
+#pragma unroll
+              for (int j = 0; j < V; ++j)
+                if (u >= left) d[j] = sl[j] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] *= d[j];
             if (V == 1) {
               s.d[p][wi][u][q] = make_float2(d[0], x[0]);
             } else {
@@ -296,12 +302,9 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
                 *reinterpret_cast<float4*>(&s.d[p][wi][u][2 * turned<V>(u, (q + j) / 2)]) =
                     make_float4(d[j], x[j], d[j + 1], x[j + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-              s.g[p][wi][u][q + j] = y[j];
-              s.slope[p][wi][u][q + j] = sl[j];
-              if (a.z) s.dz[p][wi][u][q + j] = sz[j];
-            }
+            st_vec<V>(&s.g[p][wi][u][q], y);
+            st_vec<V>(&s.slope[p][wi][u][q], sl);
+            if (a.z) st_vec<V>(&s.dz[p][wi][u][q], sz);
           }
         if (wi < 2) {
 #pragma unroll
@@ -320,17 +323,35 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
         for (int i = 0; i < X::kN; ++i) {
           const int u = X::token(i), q = X::channel(i);
           if (!X::inside(i) || u >= left || q >= k.n) continue;
-          float x[V], dx[V], dd[V], dz[V];
+          float x[V], dx[V], dd[V], dz[V], dt[V], dyg[V], gB[V], qA[V], sl[V];
           ld_pack<T, V>(&r.x[wi][u][q]).unpack(x);
+          if (V == 1) {
+            dt[0] = s.d[p][wi][u][q].x;
+          } else {
+#pragma unroll
+            for (int j = 0; j + 1 < V; j += 2) {
+              const float4 d = *reinterpret_cast<const float4*>(&s.d[p][wi][u][2 * turned<V>(u, (q + j) / 2)]);
+              dt[j] = d.x;
+              dt[j + 1] = d.z;
+            }
+          }
+          ld_vec<V>(&s.g[p][wi][u][q], dyg);
+          ld_vec<V>(&s.sums[p][1][wi][u][q], gB);
+          ld_vec<V>(&s.sums[p][2][wi][u][q], qA);
+          ld_vec<V>(&s.slope[p][wi][u][q], sl);
 #pragma unroll
           for (int j = 0; j < V; ++j) {
-            const float dt = s.d[p][wi][u][V == 1 ? q : 2 * turned<V>(u, (q + j) / 2) + (j & 1)].x;
-            const float dyg = s.g[p][wi][u][q + j], gB = s.sums[p][1][wi][u][q + j];
-            dx[j] = gB * dt + skip[j] * dyg;
-            dd[j] = (gB * x[j] + s.sums[p][2][wi][u][q + j] * (1.f / ATLAS_LOG2E)) * s.slope[p][wi][u][q + j];
-            dD[j] += dyg * x[j];
+            dx[j] = gB[j] * dt[j] + skip[j] * dyg[j];
+            dd[j] = (gB[j] * x[j] + qA[j] * (1.f / ATLAS_LOG2E)) * sl[j];
+            dD[j] += dyg[j] * x[j];
             db[j] += dd[j];
-            if (a.z) dz[j] = s.dz[p][wi][u][q + j] * (s.sums[p][0][wi][u][q + j] + skip[j] * x[j]);
+          }
+          if (a.z) {
+            float ch[V];
+            ld_vec<V>(&s.dz[p][wi][u][q], dz);
+            ld_vec<V>(&s.sums[p][0][wi][u][q], ch);
+#pragma unroll
+            for (int j = 0; j < V; ++j) dz[j] *= ch[j] + skip[j] * x[j];
           }
           Pack<T, V> o;
           o.pack(dx);
@@ -404,7 +425,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
     A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
     A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
     // read by this lane alone
-    *reinterpret_cast<float4*>(&s.hs[wi][2 * cp + i][n0]) = make_float4(h4[0], h4[1], h4[2], h4[3]);
+    *reinterpret_cast<float4*>(s.hs[wi][i][lane]) = make_float4(h4[0], h4[1], h4[2], h4[3]);
     g01[i] = pair(g4[0], g4[1]);
     g23[i] = pair(g4[2], g4[3]);
     dA01[i] = dA23[i] = pair(0.f, 0.f);
@@ -416,11 +437,11 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const Raw& r = s.raw[m % kBackRing];
-      const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(&r.h[wi][2 * cp + i][n0]);
+      const ulonglong2 h = *reinterpret_cast<const ulonglong2*>(r.h[wi][i][lane]);
       h01[i][0] = h.x;
       h23[i][0] = h.y;
       if (w.split) {
-        const ulonglong2 hs = *reinterpret_cast<const ulonglong2*>(&s.hs[wi][2 * cp + i][n0]);
+        const ulonglong2 hs = *reinterpret_cast<const ulonglong2*>(s.hs[wi][i][lane]);
         const float cum = r.cum[wi][2 * cp + i];
         const pair32 cc = pair(cum, cum);
         h01[i][0] = pair_fma(pair_ex2(pair_mul(cc, A01[i])), hs.x, h.x);
