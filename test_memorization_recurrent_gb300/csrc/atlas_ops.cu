@@ -128,9 +128,10 @@ bool conv_y_apart(const ConvArgs& a) {
   return a.s.start || a.s.B <= 1 || a.yb >= span;
 }
 
-bool conv_wide(const ConvArgs& a, const void* x, const void* y, const void* s0, const void* s1) {
-  const int v = 16 / size_of(a.dt);
-  return aligned(x, 16) && aligned(y, 16) && aligned(s0, 16) && aligned(s1, 16) && a.C % v == 0 &&
+// Whether rows, heads and states keep `bytes` (a power of two) aligned.
+bool conv_wide(const ConvArgs& a, const void* x, const void* y, const void* s0, const void* s1, int bytes) {
+  const int v = bytes / size_of(a.dt), n = bytes;
+  return aligned(x, n) && aligned(y, n) && aligned(s0, n) && aligned(s1, n) && a.C % v == 0 &&
          a.xb % v == 0 && a.xt % v == 0 && a.yb % v == 0 && a.yt % v == 0 && a.yh % v == 0 &&
          (!a.hd || a.hd % v == 0);
 }
@@ -269,7 +270,7 @@ int atlas_conv_forward(const void* x, const void* weight, const void* bias,
   a.y = y;
   a.st_in = state_in;
   a.st_out = state_out;
-  a.wide = conv_wide(a, x, y, state_in, state_out);
+  a.wide = conv_wide(a, x, y, state_in, state_out, 4 * e);  // four elements a lane
   return conv_forward_launch(a, stream_of(stream));
 }
 
@@ -305,7 +306,7 @@ int atlas_conv_backward(const void* x, const void* weight, const void* bias,
   a.dw = dw;
   a.dbias = dbias;
   a.ws = cfg->workspace;
-  a.wide = conv_wide(a, x, dy, state_in, dx);
+  a.wide = conv_wide(a, x, dy, state_in, dx, 16);  // 16-byte copies
   return conv_backward_launch(a, stream_of(stream));
 }
 

@@ -21,7 +21,7 @@ int conv_backward_launch(const ConvArgs& a, cudaStream_t st) { return conv_run(a
 size_t conv_backward_workspace(const ConvArgs& a) {
   size_t most = 0;
   for (int V : {1, 4}) {
-    const long tiles = seq_tiles(a.s, conv::tile_tokens(a, V, 152 * 16));
+    const long tiles = seq_tiles(a.s, conv::back_tile_tokens(a, V));
     const size_t n = (size_t)conv::back_blocks(a, V, tiles) * (a.W + 1) * a.C;
     most = n > most ? n : most;
   }

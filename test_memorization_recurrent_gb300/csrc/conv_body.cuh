@@ -4,9 +4,13 @@
 //   p_t = b + sum_k w_k x_{t-W+1+k},  y_t = SiLU(p_t) or p_t
 //   dp_t = dy_t SiLU'(p_t),  dx_s = sum_i w_{W-1-i} dp_{s+i},  dw_k = sum_t dp_t x_{t-W+1+k}
 //
-// Bound by memory: x is read once and y written once.  A lane owns V adjacent channels
-// (16 bytes forward, V = 4 backward) and walks the tokens of its tile with the last W - 1
-// inputs in registers, so that only the W - 1 tokens in front of a tile are read twice.
+// Bound by memory: x (and dy) are read once and y (dx) written once.  A lane owns V adjacent
+// channels and walks the tokens of its tile with the last W - 1 inputs in registers, so that
+// only the tokens in front of a tile (and, backward, those behind it) are read twice.  V is
+// four: with eight, the taps, window and loads of a lane take 202 registers, and too few
+// warps are left to cover the latency.  8 x 4096 tokens x 2048 channels of bf16, four taps:
+// 126 us with eight, 59 us with four (4.6 TB/s); 24 warps an SM, 59 us, against 91 with 20,
+// 65 with 28, 78 with 32.
 #pragma once
 #include "ops_common.cuh"
 
@@ -22,214 +26,301 @@ __device__ __forceinline__ long y_at(const ConvArgs& a, const SeqTile& t, int to
   return a.hd ? o + (long)(c / a.hd) * a.yh + c % a.hd : o + c;
 }
 
+// V channels as pairs (V = 1: one pair with an idle half).
+template <int V>
+constexpr int kPairs = V > 1 ? V / 2 : 1;
+
+template <typename T, int V>
+__device__ __forceinline__ void to_pairs(const Pack<T, V>& p, pair32* v) {
+  float f[V > 1 ? V : 2] = {};
+  p.unpack(f);
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) v[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> from_pairs(const pair32* v) {
+  float f[V > 1 ? V : 2];
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) unpair(v[i], f[2 * i], f[2 * i + 1]);
+  Pack<T, V> p;
+  p.pack(f);
+  return p;
+}
+
+// Taps and bias of V channels: the V x W taps are neighbours in memory.
+template <typename WT, int V, int W>
+__device__ __forceinline__ void load_taps_as(const ConvArgs& a, int c, pair32 (*w)[kPairs<V>], pair32* b) {
+  float f[W * V + 1], g[V + 1];
+#pragma unroll
+  for (int i = 0; i < V; ++i) g[i] = 0.f;
+  f[W * V] = g[V] = 0.f;
+  const WT* p = reinterpret_cast<const WT*>(a.w) + (long)c * W;
+  const WT* q = reinterpret_cast<const WT*>(a.bias) + c;
+  if (c >= a.C) {
+#pragma unroll
+    for (int i = 0; i < W * V; ++i) f[i] = 0.f;
+  } else if (V == 4 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(WT) - 1)) == 0) {
+#pragma unroll
+    for (int i = 0; i < W * V; i += 4) ld_pack<WT, 4>(p + i).unpack(f + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W * V; ++i) f[i] = to_f(p[i]);
+  }
+  if (a.bias && c < a.C) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) g[i] = to_f(q[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPairs<V>; ++i) {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k][i] = pair(f[2 * i * W + k], V > 1 ? f[(2 * i + (V > 1)) * W + k] : 0.f);
+    b[i] = pair(g[2 * i], V > 1 ? g[2 * i + (V > 1)] : 0.f);
+  }
+}
+template <int V, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs& a, int c, pair32 (*w)[kPairs<V>], pair32* b) {
+  if (a.wt == ATLAS_BF16)
+    load_taps_as<__nv_bfloat16, V, W>(a, c, w, b);
+  else if (a.wt == ATLAS_F16)
+    load_taps_as<__half, V, W>(a, c, w, b);
+  else
+    load_taps_as<float, V, W>(a, c, w, b);
+}
+
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kLanes * kWarps) forward_kernel(ConvArgs a, int TT, long tiles) {
+__global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kernel(ConvArgs a, int TT, long tiles) {
+  constexpr int H = W - 1, N = kPairs<V>;
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
   const long tile = (long)blockIdx.x * kWarps + threadIdx.y;
   SeqTile t;
   if (tile >= tiles || !seq_tile(a.s, tile, TT, t) || c >= a.C) return;
-  const T* x = reinterpret_cast<const T*>(a.x);
-  T* y = reinterpret_cast<T*>(a.y);
-  constexpr int H = W - 1;
-  float w[W][V], b[V], win[W][V];
+  const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
+  T* y = reinterpret_cast<T*>(a.y) + y_at(a, t, 0, c);
+  pair32 w[W][N], b[N], win[W][N];
+  load_taps<V, W>(a, c, w, b);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k][j] = ld_any(a.w, (long)(c + j) * W + k, a.wt);
-    b[j] = a.bias ? ld_any(a.bias, c + j, a.wt) : 0.f;
-  }
-  Pack<T, V> st[W];  // the last H inputs before the tile
-#pragma unroll
-  for (int k = 0; k < H; ++k) {
+  for (int k = 0; k < H; ++k) {  // the last H inputs before the tile
     const int tok = t.t0 - H + k;
+    Pack<T, V> v;
     if (tok >= 0)
-      st[k] = ld_pack<T, V>(x + seq_at(a.s, t, tok, a.xb, a.xt) + c);
+      v = ld_pack<T, V>(x + (long)tok * a.xt);
     else if (a.st_in && t.carry)  // t0 == 0: a tile is never shorter than H
-      st[k] = ld_pack<T, V>(reinterpret_cast<const T*>(a.st_in) + ((long)t.slot * H + k) * a.C + c);
+      v = ld_pack<T, V>(reinterpret_cast<const T*>(a.st_in) + ((long)t.slot * H + k) * a.C + c);
     else
-      st[k].zero();
+      v.zero();
+    to_pairs<T, V>(v, win[k]);
   }
   // the first tile alone reads the state, so it also writes the new one (the buffers may
   // be the same): the last H of (state, inputs)
   if (a.st_out && t.t0 == 0) {
+    const T* s0 = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + (long)t.slot * H * a.C + c : nullptr;
     T* o = reinterpret_cast<T*>(a.st_out) + (long)t.slot * H * a.C + c;
+    Pack<T, V> v[W];
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       const int tok = t.len - H + k;
-      Pack<T, V> v;
-      if (tok >= 0) {
-        v = ld_pack<T, V>(x + seq_at(a.s, t, tok, a.xb, a.xt) + c);
-      } else {
-        v = st[0];
-#pragma unroll
-        for (int i = 1; i < H; ++i)
-          if (i == tok + H) v = st[i];
-      }
-      st_pack<T, V>(o + (long)k * a.C, v);
+      if (tok >= 0)
+        v[k] = ld_pack<T, V>(x + (long)tok * a.xt);
+      else if (s0)
+        v[k] = ld_pack<T, V>(s0 + (long)(tok + H) * a.C);
+      else
+        v[k].zero();
     }
+#pragma unroll
+    for (int k = 0; k < H; ++k) st_pack<T, V>(o + (long)k * a.C, v[k]);
   }
-#pragma unroll
-  for (int k = 0; k < H; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) win[k][j] = st[k].get(j);
   const int t1 = min(t.t0 + TT, t.len);
   constexpr int U = 8;  // tokens loaded ahead
-  for (int t0 = t.t0; t0 < t1; t0 += U) {
+  x += (long)t.t0 * a.xt;
+  y += (long)t.t0 * a.yt;
+  for (int left = t1 - t.t0; left > 0; left -= U) {
     Pack<T, V> in[U];
-    const T* xp = x + seq_at(a.s, t, t0, a.xb, a.xt) + c;
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t0 + u < t1) in[u] = ld_pack<T, V>(xp + (long)u * a.xt);
-    T* yp = y + y_at(a, t, t0, c);
+      if (u < left) in[u] = ld_pack<T, V>(x + u * a.xt);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (t0 + u >= t1) break;
-      Pack<T, V> out;
+      if (u >= left) break;
+      to_pairs<T, V>(in[u], win[H]);
+      pair32 p[N];
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        win[H][j] = in[u].get(j);
-        float p = b[j];
+      for (int i = 0; i < N; ++i) {
+        p[i] = b[i];
 #pragma unroll
-        for (int k = 0; k < W; ++k) p += w[k][j] * win[k][j];
-        out.set(j, a.act == ATLAS_ACT_SILU ? siluf(p) : p);
+        for (int k = 0; k < W; ++k) p[i] = pair_fma(w[k][i], win[k][i], p[i]);
+        if (a.act == ATLAS_ACT_SILU) {
+          float lo, hi;
+          unpair(p[i], lo, hi);
+          p[i] = pair(siluf(lo), siluf(hi));
+        }
 #pragma unroll
-        for (int k = 0; k < H; ++k) win[k][j] = win[k + 1][j];
+        for (int k = 0; k < H; ++k) win[k][i] = win[k + 1][i];
       }
+      const Pack<T, V> out = from_pairs<T, V>(p);
       if (V == 1 || !a.hd || a.hd % V == 0) {
-        st_pack<T, V>(yp + (long)u * a.yt, out);
+        st_pack<T, V>(y + u * a.yt, out);
       } else {  // a vector crosses heads
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[y_at(a, t, t0 + u, c + j)] = out.e[j];
+        for (int j = 0; j < V; ++j)
+          reinterpret_cast<T*>(a.y)[y_at(a, t, t1 - left + u, c + j)] = out.e[j];
       }
     }
+    x += U * a.xt;
+    y += U * a.yt;
   }
 }
 
+// Rows of x and dy on their way to a worker of backward_kernel.
+constexpr int kChunk = 8, kStages = 4;
+template <typename T, int V>
+struct Ring {
+  T x[kStages][kChunk][kLanes * V];
+  T dy[kStages][kChunk][kLanes * V];
+};
+
 // A warp is a worker: it walks tiles and keeps dw and db of its channels in registers; the
 // block adds its workers in a fixed order and writes one row of partial sums
-// part[block][(W + 1)][C].  Positions before a sequence give dL/d state, into ds.
+// part[block][(W + 1)][C].  A tile is a stream of positions from t0 - H to t1 + H: the inputs
+// in front of it (the state before a sequence's first token), its own tokens, and those whose
+// dp reaches back into it; dx of a position is complete H positions later.  Positions before a
+// sequence give dL/d state, into ds.  The stream is copied to shared memory kStages - 1
+// chunks ahead.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kLanes * kWarps)
     backward_kernel(ConvArgs a, int TT, long tiles, float* part, float* ds) {
-  extern __shared__ float sm[];
+  constexpr int H = W - 1, N = kPairs<V>;
+  extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
+  Ring<T, V>& ring = reinterpret_cast<Ring<T, V>*>(smem)[threadIdx.y];
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
-  const T* x = reinterpret_cast<const T*>(a.x);
-  const T* dy = reinterpret_cast<const T*>(a.dy);
-  T* dx = reinterpret_cast<T*>(a.dx);
-  constexpr int H = W - 1;
-  float w[W][V], b[V], dw[W][V], db[V];
+  pair32 w[W][N], b[N], dw[W][N], db[N];
+  load_taps<V, W>(a, c, w, b);
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int i = 0; i < N; ++i) {
+    db[i] = pair(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      w[k][j] = c < a.C ? ld_any(a.w, (long)(c + j) * W + k, a.wt) : 0.f;
-      dw[k][j] = 0.f;
-    }
-    b[j] = a.bias && c < a.C ? ld_any(a.bias, c + j, a.wt) : 0.f;
-    db[j] = 0.f;
+    for (int k = 0; k < W; ++k) dw[k][i] = db[i];
   }
+  // copies: CL lanes a row, 16 bytes each (V = 1: one element each, at once)
+  constexpr int CV = V == 1 ? 1 : 16 / sizeof(T), CL = kLanes * V / CV, RP = kLanes / CL;
+  const int cc = (blockIdx.y * kLanes) * V + lane % CL * CV;  // the channels this lane copies
+  const bool cin = cc < a.C;
   for (long tile = (long)blockIdx.x * kWarps + threadIdx.y; tile < tiles;
        tile += (long)gridDim.x * kWarps) {
     SeqTile t;
-    if (!seq_tile(a.s, tile, TT, t) || c >= a.C) continue;
-    float win[W][V], dp[W][V];
+    if (!seq_tile(a.s, tile, TT, t)) continue;
+    const int t1 = min(t.t0 + TT, t.len), q0 = t.t0 - H, q1 = t1 + H;
+    const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + cc;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + y_at(a, t, 0, cc);
+    const T* st = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + ((long)t.b * H + H) * a.C + cc : nullptr;
+    auto fetch = [&](int stage, int base) {
 #pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const int tok = t.t0 - H + k;
-      Pack<T, V> v;
-      if (tok >= 0)
-        v = ld_pack<T, V>(x + seq_at(a.s, t, tok, a.xb, a.xt) + c);
-      else if (a.st_in && t.carry)
-        v = ld_pack<T, V>(reinterpret_cast<const T*>(a.st_in) + ((long)t.b * H + k) * a.C + c);
-      else
-        v.zero();
-#pragma unroll
-      for (int j = 0; j < V; ++j) win[k][j] = v.get(j), dp[k][j] = 0.f;
-    }
-    const int t1 = min(t.t0 + TT, t.len);
-    // dp is needed H tokens past the tile; emission runs H tokens behind
-    constexpr int U = 4;
-    for (int q0 = t.t0; q0 < t1 + H; q0 += U) {
-      Pack<T, V> in[U], up[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int tok = q0 + u;
-        if (tok < t.len && tok < t1 + H) {
-          in[u] = ld_pack<T, V>(x + seq_at(a.s, t, tok, a.xb, a.xt) + c);
-          if (V == 1 || !a.hd || a.hd % V == 0) {
-            up[u] = ld_pack<T, V>(dy + y_at(a, t, tok, c));
-          } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) up[u].e[j] = dy[y_at(a, t, tok, c + j)];
-          }
+      for (int r = 0; r < kChunk; r += RP) {
+        const int u = r + lane / CL, q = base + u;
+        const bool fx = cin && q < t.len && (q >= 0 || st), fy = cin && q >= t.t0 && q < min(t.len, q1);
+        const T* px = !fx ? reinterpret_cast<const T*>(a.w) : q >= 0 ? x + (long)q * a.xt : st + (long)q * a.C;
+        const T* py = fy ? dy + (long)q * a.yt : reinterpret_cast<const T*>(a.w);
+        T* ox = &ring.x[stage][u][lane % CL * CV];
+        T* oy = &ring.dy[stage][u][lane % CL * CV];
+        if constexpr (V > 1) {
+          cp_async<16>(ox, fx ? px : reinterpret_cast<const T*>(a.dx), fx);
+          cp_async<16>(oy, fy ? py : reinterpret_cast<const T*>(a.dx), fy);
         } else {
-          in[u].zero();
-          up[u].zero();
+          *ox = fx ? *px : from_f<T>(0.f);
+          *oy = fy ? *py : from_f<T>(0.f);
         }
       }
+    };
+    pair32 win[W][N], dp[W][N];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int tok = q0 + u;
-        if (tok >= t1 + H) break;
+    for (int k = 0; k < W; ++k)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          win[H][j] = in[u].get(j);
-          float g = up[u].get(j);
+      for (int i = 0; i < N; ++i) win[k][i] = dp[k][i] = pair(0.f, 0.f);
+    T* dx = reinterpret_cast<T*>(a.dx) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) {
+      fetch(k, q0 + k * kChunk);
+      cp_commit();
+    }
+    int stage = 0;
+    for (int base = q0; base < q1; base += kChunk) {
+      cp_wait<kStages - 2>();
+      __syncwarp();  // this chunk is there for all lanes, and the one before has been read
+      fetch(stage == 0 ? kStages - 1 : stage - 1, base + (kStages - 1) * kChunk);
+      cp_commit();
+#pragma unroll
+      for (int u = 0; u < kChunk; ++u) {
+        const int q = base + u;
+        if (q >= q1) break;
+        pair32 g[N];
+        to_pairs<T, V>(ld_pack<T, V>(&ring.x[stage][u][lane * V]), win[H]);
+        to_pairs<T, V>(ld_pack<T, V>(&ring.dy[stage][u][lane * V]), g);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
           if (a.act == ATLAS_ACT_SILU) {
-            float p = b[j];
+            pair32 p = b[i];
 #pragma unroll
-            for (int k = 0; k < W; ++k) p += w[k][j] * win[k][j];
-            g *= silu_slope(p, sigmoidf(p));
+            for (int k = 0; k < W; ++k) p = pair_fma(w[k][i], win[k][i], p);
+            float lo, hi;
+            unpair(p, lo, hi);
+            const float sl = sigmoidf(lo), sh = sigmoidf(hi);
+            g[i] = pair_mul(g[i], pair(silu_slope(lo, sl), silu_slope(hi, sh)));
           }
-          if (tok >= t.len) g = 0.f;
-          dp[H][j] = g;
-          if (tok < t1) {
-            db[j] += g;
+          if (q < t.t0 || q >= t.len) g[i] = pair(0.f, 0.f);  // also where p is not finite
+          dp[H][i] = g[i];
+          if (q < t1) {
+            db[i] = pair_add(db[i], g[i]);
 #pragma unroll
-            for (int k = 0; k < W; ++k) dw[k][j] += g * win[k][j];
+            for (int k = 0; k < W; ++k) dw[k][i] = pair_fma(g[i], win[k][i], dw[k][i]);
           }
         }
-        const int s = tok - H;  // the position whose gradient is complete
-        if (s >= t.t0 || t.t0 == 0) {
-          float o[V];
+        const int s = q - H;  // the position whose gradient is complete
+        if (c < a.C && s >= (t.t0 == 0 ? -H : t.t0)) {
+          pair32 o[N];
 #pragma unroll
-          for (int j = 0; j < V; ++j) {
-            o[j] = 0.f;
+          for (int i = 0; i < N; ++i) {
+            o[i] = pair_mul(w[H][i], dp[0][i]);
 #pragma unroll
-            for (int i = 0; i < W; ++i) o[j] += w[H - i][j] * dp[i][j];
+            for (int k = 1; k < W; ++k) o[i] = pair_fma(w[H - k][i], dp[k][i], o[i]);
           }
           const int tail = s - (t.len - H);  // row of dL/d state_out that is this position
           if (a.dstate && tail >= 0) {
+            const float* d = a.dstate + ((long)t.b * H + tail) * a.C + c;
 #pragma unroll
-            for (int j = 0; j < V; ++j) o[j] += a.dstate[((long)t.b * H + tail) * a.C + c + j];
+            for (int i = 0; i < N; ++i) o[i] = pair_add(o[i], pair(d[2 * i], V > 1 ? d[2 * i + 1] : 0.f));
           }
           if (s >= 0) {
-            Pack<T, V> v;
-#pragma unroll
-            for (int j = 0; j < V; ++j) v.set(j, o[j]);
-            st_pack<T, V>(dx + seq_at(a.s, t, s, a.xb, a.xt) + c, v);
+            st_pack<T, V>(dx + (long)s * a.xt, from_pairs<T, V>(o));
           } else if (a.dstate) {
+            float* d = ds + ((long)t.b * H + s + H) * a.C + c;
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-              ds[((long)t.b * H + s + H) * a.C + c + j] = t.carry ? o[j] : 0.f;
+            for (int i = 0; i < N; ++i) {
+              float lo, hi;
+              unpair(o[i], lo, hi);
+              d[2 * i] = t.carry ? lo : 0.f;
+              if (V > 1) d[2 * i + 1] = t.carry ? hi : 0.f;
+            }
           }
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
           for (int k = 0; k < H; ++k) {
-            win[k][j] = win[k + 1][j];
-            dp[k][j] = dp[k + 1][j];
+            win[k][i] = win[k + 1][i];
+            dp[k][i] = dp[k + 1][i];
           }
       }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
     }
+    cp_wait<0>();
   }
   // the block's workers, one after the other
-  float* acc = sm + lane * V;  // [W + 1][32 V]
+  __syncthreads();  // the rings are no longer needed
+  float* acc = reinterpret_cast<float*>(smem) + lane * V;  // [W + 1][32 V]
   for (int r = 0; r < kWarps; ++r) {
     __syncthreads();
     if (r == threadIdx.y) {
@@ -237,7 +328,9 @@ __global__ void __launch_bounds__(kLanes * kWarps)
       for (int k = 0; k <= W; ++k)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const float s = (r == 0 ? 0.f : acc[k * kLanes * V + j]) + (k < W ? dw[k < W ? k : 0][j] : db[j]);
+          float lo, hi;
+          unpair(k < W ? dw[k < W ? k : 0][j / 2] : db[j / 2], lo, hi);
+          const float s = (r == 0 ? 0.f : acc[k * kLanes * V + j]) + (j % 2 ? hi : lo);
           if (r < kWarps - 1)
             acc[k * kLanes * V + j] = s;
           else if (c < a.C)
@@ -286,29 +379,40 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Tokens per tile: long tiles read fewer tokens twice (W - 1 of each), short ones fill the
-// machine; at least H so that one tile alone touches the state.
-inline int tile_tokens(const ConvArgs& a, int V, long warps) {
-  const long lanes = (a.C + kLanes * V - 1) / (kLanes * V);
-  const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
-  int TT = 64;
-  while (TT > 8 && rows / TT * lanes < warps) TT /= 2;
-  return TT;
+inline long lane_groups(const ConvArgs& a, int V) { return (a.C + kLanes * V - 1) / (kLanes * V); }
+
+// Tokens per tile: as many tiles as warps fit (24 an SM at up to four taps), so that all run
+// at once and few tokens are read twice; at least 16, so that one tile alone touches the state.
+inline int tile_tokens(const ConvArgs& a, int V) {
+  const long n = 152 * 24 / lane_groups(a, V);
+  const long each = a.s.start ? n : n / (a.s.B < 1 ? 1 : a.s.B);  // tiles a sequence (packed: in all)
+  const long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
+  return (int)(TT < 16 ? 16 : TT);
 }
 
+// Workers of the backward pass: twelve warps an SM over the groups of channels; and as many
+// tiles as workers, none shorter than 16 tokens.
+inline long back_workers(const ConvArgs& a, int V) {
+  const long n = 152 * 12 / lane_groups(a, V) / kWarps * kWarps;
+  return n < kWarps ? kWarps : n;
+}
+inline int back_tile_tokens(const ConvArgs& a, int V) {
+  const long n = back_workers(a, V);
+  const long each = a.s.start ? n : n / (a.s.B < 1 ? 1 : a.s.B);  // tiles a sequence (packed: in all)
+  long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
+  return (int)(TT < 16 ? 16 : TT);
+}
 inline int back_blocks(const ConvArgs& a, int V, long tiles) {
-  const long lanes = (a.C + kLanes * V - 1) / (kLanes * V);
-  long n = (152 * 4 + lanes - 1) / lanes;  // four blocks an SM
-  const long need = (tiles + kWarps - 1) / kWarps;
+  const long n = back_workers(a, V) / kWarps, need = (tiles + kWarps - 1) / kWarps;
   return (int)(n < need ? n : need);
 }
 
 template <typename T, int V, int W>
 int forward(const ConvArgs& a, cudaStream_t st) {
-  const int TT = tile_tokens(a, V, 152 * 32);
+  const int TT = tile_tokens(a, V);
   const long tiles = seq_tiles(a.s, TT);
   const long bx = (tiles + kWarps - 1) / kWarps;
-  const long by = (a.C + kLanes * V - 1) / (kLanes * V);
+  const long by = lane_groups(a, V);
   if (bx > 0x7FFFFFFFL || by > 65535) return ATLAS_ERR_UNSUPPORTED;
   forward_kernel<T, V, W><<<dim3((unsigned)bx, (unsigned)by), dim3(kLanes, kWarps), 0, st>>>(a, TT, tiles);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
@@ -316,27 +420,31 @@ int forward(const ConvArgs& a, cudaStream_t st) {
 
 template <typename T, int V, int W>
 int backward(const ConvArgs& a, cudaStream_t st) {
-  const int TT = tile_tokens(a, V, 152 * 16);
+  const int TT = back_tile_tokens(a, V);
   const long tiles = seq_tiles(a.s, TT);
   const int n = back_blocks(a, V, tiles);
-  const long by = (a.C + kLanes * V - 1) / (kLanes * V);
+  const long by = lane_groups(a, V);
   if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
   float* ds = reinterpret_cast<float*>(a.ws);
   float* part = ds + (a.dstate ? (size_t)a.s.B * (W - 1) * a.C : 0);
-  const size_t smem = (size_t)(W + 1) * kLanes * V * 4;
+  constexpr size_t rings = kWarps * sizeof(Ring<T, V>), sums = (size_t)(W + 1) * kLanes * V * 4;
+  constexpr size_t smem = rings > sums ? rings : sums;
+  auto* f = backward_kernel<T, V, W>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATLAS_ERR_CUDA;
   if (n > 0)
-    backward_kernel<T, V, W><<<dim3((unsigned)n, (unsigned)by), dim3(kLanes, kWarps), smem, st>>>(
-        a, TT, tiles, part, ds);
+    f<<<dim3((unsigned)n, (unsigned)by), dim3(kLanes, kWarps), smem, st>>>(a, TT, tiles, part, ds);
   const int nsum = ((W + 1) * a.C + 31) / 32;
   const long moved = a.dstate ? ((long)a.s.B * (W - 1) * a.C + 255) / 256 : 0;
   finish_kernel<T><<<nsum + (unsigned)(moved < 1024 ? moved : 1024), 256, 0, st>>>(a, n, part, ds);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
-template <typename T, int VF, int VB>
+template <typename T, int V>
 int run(const ConvArgs& a, bool back, cudaStream_t st) {
 #define ATLAS_W(W) \
-  case W: return back ? backward<T, VB, W>(a, st) : forward<T, VF, W>(a, st);
+  case W: return back ? backward<T, V, W>(a, st) : forward<T, V, W>(a, st);
   switch (a.W) {
     ATLAS_W(1) ATLAS_W(2) ATLAS_W(3) ATLAS_W(4) ATLAS_W(5) ATLAS_W(6) ATLAS_W(7) ATLAS_W(8)
     default: return ATLAS_ERR_UNSUPPORTED;

@@ -3,6 +3,6 @@
 
 namespace atlas {
 int conv_run_f32(const ConvArgs& a, bool back, cudaStream_t st) {
-  return a.wide ? conv::run<float, 4, 4>(a, back, st) : conv::run<float, 1, 1>(a, back, st);
+  return a.wide ? conv::run<float, 4>(a, back, st) : conv::run<float, 1>(a, back, st);
 }
 }  // namespace atlas

@@ -51,7 +51,7 @@ struct ConvArgs {
   void* ws;
   int C, W, act, dt, wt, hd;
   long xb, xt, yb, yt, yh;
-  int wide;  // x, y and the states allow 16-byte accesses
+  int wide;  // x, y and the states allow accesses of four elements (backward: 16 bytes)
 };
 int conv_forward_launch(const ConvArgs& a, cudaStream_t st);
 size_t conv_backward_workspace(const ConvArgs& a);

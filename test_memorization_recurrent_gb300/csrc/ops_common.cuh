@@ -245,11 +245,20 @@ inline __host__ __device__ long seq_tiles(const SeqArgs& a, int TT) {
 // by whole warps with the same i.
 __device__ __forceinline__ bool seq_tile(const SeqArgs& a, long i, int TT, SeqTile& t) {
   if (a.start) {
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      const int s = min(max(a.start[mid], 0), a.L);
-      if ((long)s / TT + mid <= i) lo = mid; else hi = mid - 1;
+    // the last sequence whose first number is not above i, 32 candidates at a time
+    int lo = 0, n = a.B;
+    const int lane = threadIdx.x & 31;
+    while (n > 1) {
+      const int step = (n + 31) / 32, j = lane * step;
+      bool le = false;
+      if (j < n) {
+        const int s = min(max(a.start[lo + j], 0), a.L);
+        le = j == 0 || (long)s / TT + lo + j <= i;
+      }
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
+      const int last = 31 - __clz((int)m);  // of the candidates not above i (the first always counts)
+      lo += last * step;
+      n = min(step, n - last * step);
     }
     const int s = a.start[lo], e = a.start[lo + 1];
     if (s < 0 || e < s || e > a.L) return false;  // reported by seq_check
@@ -269,7 +278,7 @@ __device__ __forceinline__ bool seq_tile(const SeqArgs& a, long i, int TT, SeqTi
   t.slot = t.b;
   if (a.slot) {
     t.slot = a.slot[t.b];
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;  // (of the warp's lanes, each looks at some)
     bool bad = t.slot < 0 || t.slot >= a.n_slots;
     for (int j = lane; j < t.b; j += 32) bad |= a.slot[j] == t.slot;
     if (__any_sync(0xFFFFFFFFu, bad)) {
