@@ -247,39 +247,40 @@ __global__ void __launch_bounds__(kLanes * kWarps)
       cp_commit();
     }
     int stage = 0;
-    for (int base = q0; base < q1; base += kChunk) {
-      cp_wait<kStages - 2>();
-      __syncwarp();  // this chunk is there for all lanes, and the one before has been read
-      fetch(stage == 0 ? kStages - 1 : stage - 1, base + (kStages - 1) * kChunk);
-      cp_commit();
+    // the positions of one chunk; EDGE: some of them are not plain tokens of the tile
+    auto walk = [&](int base, auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+      T* out = dx + (long)(base - H) * a.xt;
 #pragma unroll
       for (int u = 0; u < kChunk; ++u) {
         const int q = base + u;
-        if (q >= q1) break;
+        if (EDGE && q >= q1) break;
         pair32 g[N];
         to_pairs<T, V>(ld_pack<T, V>(&ring.x[stage][u][lane * V]), win[H]);
         to_pairs<T, V>(ld_pack<T, V>(&ring.dy[stage][u][lane * V]), g);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          if (a.act == ATLAS_ACT_SILU) {
+          if (a.act == ATLAS_ACT_SILU) {  // SiLU'(p) = s (1 + p (1 - s)), s = 1 / (1 + exp(-p))
+            const pair32 one = pair(1.f, 1.f);
             pair32 p = b[i];
 #pragma unroll
             for (int k = 0; k < W; ++k) p = pair_fma(w[k][i], win[k][i], p);
+            const pair32 e = pair_add(pair_ex2(pair_mul(p, pair(-ATLAS_LOG2E, -ATLAS_LOG2E))), one);
             float lo, hi;
-            unpair(p, lo, hi);
-            const float sl = sigmoidf(lo), sh = sigmoidf(hi);
-            g[i] = pair_mul(g[i], pair(silu_slope(lo, sl), silu_slope(hi, sh)));
+            unpair(e, lo, hi);
+            const pair32 s = pair(rcp(lo), rcp(hi));
+            g[i] = pair_mul(g[i], pair_mul(s, pair_fma(p, pair_fma(s, pair(-1.f, -1.f), one), one)));
           }
-          if (q < t.t0 || q >= t.len) g[i] = pair(0.f, 0.f);  // also where p is not finite
+          if (EDGE && (q < t.t0 || q >= t.len)) g[i] = pair(0.f, 0.f);  // also where p is not finite
           dp[H][i] = g[i];
-          if (q < t1) {
+          if (!EDGE || q < t1) {
             db[i] = pair_add(db[i], g[i]);
 #pragma unroll
             for (int k = 0; k < W; ++k) dw[k][i] = pair_fma(g[i], win[k][i], dw[k][i]);
           }
         }
         const int s = q - H;  // the position whose gradient is complete
-        if (c < a.C && s >= (t.t0 == 0 ? -H : t.t0)) {
+        if (!EDGE || s >= (t.t0 == 0 ? -H : t.t0)) {
           pair32 o[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -287,25 +288,30 @@ __global__ void __launch_bounds__(kLanes * kWarps)
 #pragma unroll
             for (int k = 1; k < W; ++k) o[i] = pair_fma(w[H - k][i], dp[k][i], o[i]);
           }
-          const int tail = s - (t.len - H);  // row of dL/d state_out that is this position
-          if (a.dstate && tail >= 0) {
-            const float* d = a.dstate + ((long)t.b * H + tail) * a.C + c;
+          if (!EDGE) {
+            if (c < a.C) st_pack<T, V>(out, from_pairs<T, V>(o));
+          } else if (c < a.C) {
+            const int tail = s - (t.len - H);  // row of dL/d state_out that is this position
+            if (a.dstate && tail >= 0) {
+              const float* d = a.dstate + ((long)t.b * H + tail) * a.C + c;
 #pragma unroll
-            for (int i = 0; i < N; ++i) o[i] = pair_add(o[i], pair(d[2 * i], V > 1 ? d[2 * i + 1] : 0.f));
-          }
-          if (s >= 0) {
-            st_pack<T, V>(dx + (long)s * a.xt, from_pairs<T, V>(o));
-          } else if (a.dstate) {
-            float* d = ds + ((long)t.b * H + s + H) * a.C + c;
+              for (int i = 0; i < N; ++i) o[i] = pair_add(o[i], pair(d[2 * i], V > 1 ? d[2 * i + 1] : 0.f));
+            }
+            if (s >= 0) {
+              st_pack<T, V>(out, from_pairs<T, V>(o));
+            } else if (a.dstate) {
+              float* d = ds + ((long)t.b * H + s + H) * a.C + c;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              float lo, hi;
-              unpair(o[i], lo, hi);
-              d[2 * i] = t.carry ? lo : 0.f;
-              if (V > 1) d[2 * i + 1] = t.carry ? hi : 0.f;
+              for (int i = 0; i < N; ++i) {
+                float lo, hi;
+                unpair(o[i], lo, hi);
+                d[2 * i] = t.carry ? lo : 0.f;
+                if (V > 1) d[2 * i + 1] = t.carry ? hi : 0.f;
+              }
             }
           }
         }
+        out += a.xt;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
@@ -314,6 +320,16 @@ __global__ void __launch_bounds__(kLanes * kWarps)
             dp[k][i] = dp[k + 1][i];
           }
       }
+    };
+    for (int base = q0; base < q1; base += kChunk) {
+      cp_wait<kStages - 2>();
+      __syncwarp();  // this chunk is there for all lanes, and the one before has been read
+      fetch(stage == 0 ? kStages - 1 : stage - 1, base + (kStages - 1) * kChunk);
+      cp_commit();
+      if (base >= t.t0 + H && base + kChunk <= min(t1, t.len - H))
+        walk(base, std::false_type());
+      else
+        walk(base, std::true_type());
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
     cp_wait<0>();
