@@ -4,10 +4,14 @@
 //   h = x + r,  y = h rstd w,  rstd = 1 / sqrt(mean(h^2) + eps)
 //   dx = rstd (w dy - hat mean(w dy hat)) + dh,  dw = sum over rows of dy hat,  hat = h rstd
 //
-// Both passes are bound by memory: a row is read once into registers, reduced, and
-// written once.  A row of at most 1024 channels belongs to 8, 16 or 32 lanes of a warp
-// (keys and queries: one row is one head), a longer one to a block.  Sums run in 32
-// bits; the only roundings are those of the outputs to their types.
+// Both passes are bound by memory: a row is read once into registers, reduced, and written
+// once, so what counts is how many loads are under way.  Aligned rows are held as they lie in
+// memory, eight elements a load, all loads issued before the first conversion (the element's
+// type is known at run time, its size at compile time).  Forward, a row of up to 2048 channels
+// belongs to 8, 16 or 32 lanes of a warp and needs no barrier; a longer one, or one of a few
+// rows, to a block.  Backward, a block walks rows and keeps the sums of dw in registers, the
+// next row's loads under way.  Rows of odd widths or addresses take the element-wise kernels.
+// Sums run in 32 bits; the only roundings are those of the outputs to their types.
 #include <cuda_fp8.h>
 
 #include "ops_common.cuh"
@@ -106,7 +110,7 @@ __device__ __forceinline__ float row_max(float v, const RowGroup& g, float* red)
 }
 
 template <int V, int K>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_kernel(NormArgs a, int tpr) {
+__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArgs a, int tpr) {
   extern __shared__ float sm[];  // 32 floats, then (8-bit groups that cross lanes) the groups' maxima
   float* red = sm;
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
@@ -207,7 +211,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_kernel(NormA
 // A block walks the rows blockIdx.x * rpb + .., step gridDim.x * rpb; each thread keeps the
 // sums of dy hat of its columns over its rows, and the block writes one row of partial sums.
 template <int V, int K>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_kernel(NormArgs a, int tpr) {
+__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormArgs a, int tpr) {
   extern __shared__ float sm[];
   float* red = sm;
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
@@ -285,6 +289,291 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_kernel(Norm
   }
 }
 
+// ------------------------------------------------------- aligned rows
+
+// Eight elements as they lie in memory: BYTES each (0: none).
+template <int BYTES>
+struct Raw8 {
+  uint4 q[BYTES == 4 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, long i) {
+    if (BYTES == 0) return;
+    const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + i * BYTES);
+    q[0] = __ldcs(v);
+    if (BYTES == 4) q[BYTES == 4] = __ldcs(v + 1);
+  }
+  __device__ __forceinline__ void load_kept(const void* p, long i) {  // read again by other rows
+    if (BYTES == 0) return;
+    const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) + i * BYTES);
+    q[0] = v[0];
+    if (BYTES == 4) q[BYTES == 4] = v[1];
+  }
+  __device__ __forceinline__ void zero() { q[0] = q[BYTES == 4] = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void floats(int dtype, float* v) const {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
+    if (BYTES == 4) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[BYTES == 4 ? i : 0]);
+    } else if (BYTES == 2) {
+      if (dtype == ATLAS_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        }
+      }
+    }
+  }
+};
+
+// Eight values to an element type of 4, 2 or 1 bytes (e4m3: within +-448 by their scale).
+__device__ __forceinline__ void st8(void* p, long i, int dtype, const float* v) {
+  if (dtype == ATLAS_F32) {
+    float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i);
+    __stcs(o, make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(o + 1, make_float4(v[4], v[5], v[6], v[7]));
+  } else if (dtype == ATLAS_E4M3) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      w[k] = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k], v[4 * k + 1]), __NV_SATFINITE, __NV_E4M3) |
+             (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2], v[4 * k + 3]), __NV_SATFINITE, __NV_E4M3) << 16;
+    __stcs(reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(p) + i), make_uint2(w[0], w[1]));
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (dtype == ATLAS_BF16) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&t);
+      } else {
+        const __half2 t = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+    }
+    __stcs(reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p) + i), make_uint4(w[0], w[1], w[2], w[3]));
+  }
+}
+
+// K vectors of eight a thread, R rows at a time.  tpr threads a row: 8, 16 or 32 lanes, or the
+// whole block (R = 1).
+template <int XB, int RB, int K, int R>
+__global__ void __launch_bounds__(512) norm_forward_rows(NormArgs a, int tpr) {
+  extern __shared__ float sm[];
+  float* red = sm;
+  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
+  const int rpb = blockDim.x / tpr;
+  const long row0 = (long)blockIdx.x * rpb * R + threadIdx.x / tpr;
+  Raw8<XB> x[R][K];
+  Raw8<RB> r[R][K];
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long row = row0 + j * rpb;
+      const int c = (k * tpr + g.lane) * 8;
+      if (row < a.rows && c < a.d) {
+        x[j][k].load(a.x, row * a.sx + c);
+        if (RB) r[j][k].load(a.r, row * a.sr + c);
+      } else {
+        x[j][k].zero();
+        r[j][k].zero();
+      }
+    }
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const long row = row0 + j * rpb;
+    const bool live = row < a.rows;
+    float h[K][8], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * tpr + g.lane) * 8;
+      x[j][k].floats(a.dt, h[k]);
+      if (RB) {
+        float v[8];
+        r[j][k].floats(a.rt, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] += v[i];
+      }
+      if (a.r_out && live && c < a.d) st8(a.r_out, row * a.sr + c, a.rt, h[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
+    }
+    const float rstd = rsqrtf(row_sum(ss, g, red) / a.d + a.eps);
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * tpr + g.lane) * 8;
+      float w[8];
+      if (a.w && c < a.d) {
+        if (a.wt == ATLAS_F32) {
+          Raw8<4> q;
+          q.load_kept(a.w, c);
+          q.floats(a.wt, w);
+        } else {
+          Raw8<2> q;
+          q.load_kept(a.w, c);
+          q.floats(a.wt, w);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] *= rstd * w[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] *= rstd;
+      }
+      if (a.ot != ATLAS_E4M3) {
+        if (live && c < a.d) st8(a.y, row * a.sy + c, a.ot, h[k]);
+      } else if (a.group == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(h[k][i]));
+      } else {
+        // the group's lanes are neighbours: group / 8 of them, a power of two
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(h[k][i]));
+        for (int o = a.group >> 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float scale = fmaxf(m, kAmaxMin) * (1.f / kE4m3Max), inv = 1.f / scale;
+        if (live && c < a.d) {
+          const int ng = (a.d + a.group - 1) / a.group;
+          if (c % a.group == 0) a.scale[row * ng + c / a.group] = scale;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] *= inv;
+          st8(a.y, row * a.sy + c, a.ot, h[k]);
+        }
+      }
+    }
+    if (a.ot == ATLAS_E4M3 && a.group == 0) {
+      const float scale = fmaxf(row_max(amax, g, red), kAmaxMin) * (1.f / kE4m3Max), inv = 1.f / scale;
+      if (live && g.lane == 0) a.scale[row] = scale;
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * tpr + g.lane) * 8;
+        if (live && c < a.d) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] *= inv;
+          st8(a.y, row * a.sy + c, a.ot, h[k]);
+        }
+      }
+    }
+  }
+}
+
+// Backward: tpr threads a row as above; block b takes the rows b * rpb + .., step
+// gridDim.x * rpb.  Both sums of a row are reduced together.
+template <int HB, int DB, int GB, int K>  // bytes of h, dy, dh (0: none)
+__global__ void __launch_bounds__(512) norm_backward_rows(NormArgs a, int tpr) {
+  extern __shared__ float sm[];
+  float2* red = reinterpret_cast<float2*>(sm);  // [2][16], then the columns' sums
+  const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  const int nw = tpr >> 5;
+  float dw[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * tpr + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = 0.f, w[k][i] = 1.f;
+    if (a.w && c < a.d) {
+      if (a.wt == ATLAS_F32) {
+        Raw8<4> q;
+        q.load_kept(a.w, c);
+        q.floats(a.wt, w[k]);
+      } else {
+        Raw8<2> q;
+        q.load_kept(a.w, c);
+        q.floats(a.wt, w[k]);
+      }
+    }
+  }
+  Raw8<HB> h[K];
+  Raw8<DB> dy[K];
+  Raw8<GB> dh[K];
+  auto fetch = [&](long row) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * tpr + lane) * 8;
+      if (row < a.rows && c < a.d) {
+        h[k].load(a.x, row * a.sr + c);
+        dy[k].load(a.dy, row * a.sy + c);
+        if (GB) dh[k].load(a.r, row * a.sr + c);
+      } else {
+        h[k].zero();
+        dy[k].zero();
+        dh[k].zero();
+      }
+    }
+  };
+  long row = (long)blockIdx.x * rpb + mine;
+  fetch(row);
+  for (int odd = 0; row - mine < a.rows; row += (long)gridDim.x * rpb, odd ^= 1) {
+    float hv[K][8], dv[K][8], gv[K][8], ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      h[k].floats(a.rt, hv[k]);
+      dy[k].floats(a.dt, dv[k]);
+      if (GB) dh[k].floats(a.rt, gv[k]);
+    }
+    fetch(row + (long)gridDim.x * rpb);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss += hv[k][i] * hv[k][i];
+        dot += hv[k][i] * (w[k][i] * dv[k][i]);
+      }
+    for (int m = min(tpr, 32) >> 1; m; m >>= 1) {
+      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
+    }
+    if (nw > 1) {  // one row a block; two buffers, so that one barrier a row is enough
+      if ((threadIdx.x & 31) == 0) red[odd * 16 + (threadIdx.x >> 5)] = make_float2(ss, dot);
+      __syncthreads();
+      ss = dot = 0.f;
+      for (int i = 0; i < nw; ++i) {
+        const float2 v = red[odd * 16 + i];
+        ss += v.x;
+        dot += v.y;
+      }
+    }
+    const float rstd = rsqrtf(ss / a.d + a.eps);
+    const float mean = dot * rstd / a.d;  // mean(w dy hat)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * tpr + lane) * 8;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float hat = hv[k][i] * rstd;
+        dw[k][i] += dv[k][i] * hat;
+        o[i] = rstd * (w[k][i] * dv[k][i] - hat * mean) + (GB ? gv[k][i] : 0.f);
+      }
+      if (row < a.rows && c < a.d) st8(a.y, row * a.sr + c, a.rt, o);
+    }
+  }
+  if (!a.dw) return;
+  float* acc = sm + 64;
+  for (int r = 0; r < rpb; ++r) {  // rows of one block in a fixed order
+    __syncthreads();
+    if (r == mine) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * tpr + lane) * 8;
+        if (c < a.d) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float s = (r == 0 ? 0.f : acc[c + i]) + dw[k][i];
+            if (r == rpb - 1)
+              a.part[(long)blockIdx.x * a.d + c + i] = s;
+            else
+              acc[c + i] = s;
+          }
+        }
+      }
+    }
+  }
+}
+
 // dw[c] = sum over the blocks' partial sums; 32 columns a block, 8 threads a column.
 __global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, float* dw, int nblk, int d) {
   __shared__ float s[8][33];
@@ -303,87 +592,134 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, float* 
 }
 
 // Threads per row, vectors per thread and threads per block for rows of d channels in
-// vectors of V.  Rows up to 32 x 4 vectors: lanes of a warp; longer: a block with at most
-// `most` vectors a thread.
+// vectors of V.
 struct RowPlan {
   int tpr, k, block;
 };
-RowPlan row_plan(int d, int V, int most) {
-  const int nv = (d + V - 1) / V;
+RowPlan elem_plan(int d, int most) {
   RowPlan p;
-  if (nv <= 128) {
-    p.tpr = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
-    p.k = (nv + p.tpr - 1) / p.tpr;
+  if (d <= 128) {
+    p.tpr = d <= 8 ? 8 : d <= 16 ? 16 : 32;
+    p.k = 4;
     p.block = 256;
   } else {
     p.k = most;
-    while (p.k < 32 && (nv + p.k - 1) / p.k > (V == 8 ? 512 : 1024)) p.k *= 2;
+    while (p.k < 32 && (d + p.k - 1) / p.k > 1024) p.k *= 2;
+    p.tpr = ((d + p.k - 1) / p.k + 31) / 32 * 32;
+    p.block = p.tpr;
+    p.k = p.k <= 4 ? 4 : 32;
+  }
+  return p;
+}
+// Up to `lanes_k` vectors a lane, a row belongs to lanes of a warp; else to a block of at most
+// 512 threads.
+RowPlan rows_plan(int d, int lanes_k) {
+  const int nv = (d + 7) / 8;
+  RowPlan p;
+  if (nv <= 32 * lanes_k) {
+    p.tpr = nv <= 8 ? 8 : nv <= 16 ? 16 : 32;
+    p.k = (nv + p.tpr - 1) / p.tpr;
+    p.block = 128;
+  } else {
+    p.k = 1;
+    while ((nv + p.k - 1) / p.k > 512) p.k *= 2;
     p.tpr = ((nv + p.k - 1) / p.k + 31) / 32 * 32;
     p.block = p.tpr;
   }
-  p.k = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : p.k <= 8 ? 8 : 32;
+  p.k = p.k <= 1 ? 1 : p.k <= 2 ? 2 : p.k <= 4 ? 4 : 8;
   return p;
 }
 
 int back_blocks(const NormArgs& a, const RowPlan& p) {
   const long rpb = p.block / p.tpr;
   const long need = (a.rows + rpb - 1) / rpb;
-  const long most = 152L * (2048 / (p.block < 256 ? 256 : p.block)) / 2;
+  const long most = 152L * (1536 / (p.block < 256 ? 256 : p.block));
   return (int)(need < most ? need : most);
 }
+
+template <int XB, int RB>
+int forward_rows(const NormArgs& a, cudaStream_t st) {
+  // few rows: a block each, so that the row's loads are spread over it
+  const bool few = a.rows <= 152 * 8;
+  const RowPlan p = rows_plan(a.d, few ? 1 : 8);
+  const int rpb = p.block / p.tpr;
+  const int R = p.k == 1 && p.tpr <= 32 && !few ? 4 : 1;  // short rows: four under way
+  const long blocks = (a.rows + (long)rpb * R - 1) / ((long)rpb * R);
+  if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
+  const size_t smem = 32 * 4;
+  if (p.k == 1 && R == 4)
+    norm_forward_rows<XB, RB, 1, 4><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  else if (p.k == 1)
+    norm_forward_rows<XB, RB, 1, 1><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  else if (p.k == 2)
+    norm_forward_rows<XB, RB, 2, 1><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  else if (p.k == 4)
+    norm_forward_rows<XB, RB, 4, 1><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  else
+    norm_forward_rows<XB, RB, 8, 1><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
+
+template <int HB, int DB, int GB>
+void backward_rows(const NormArgs& a, const RowPlan& p, int blocks, cudaStream_t st) {
+  const size_t smem = (64 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
+  if (p.k == 1)
+    norm_backward_rows<HB, DB, GB, 1><<<blocks, p.block, smem, st>>>(a, p.tpr);
+  else
+    norm_backward_rows<HB, DB, GB, 2><<<blocks, p.block, smem, st>>>(a, p.tpr);
+}
+
+// Rows whose registers (h, dy, dw and the next row) the backward kernel can hold.
+bool back_wide(const NormArgs& a) { return a.wide && a.d <= 8192; }
 
 }  // namespace
 
 int norm_forward_launch(const NormArgs& a, cudaStream_t st) {
-  const int V = a.wide ? 8 : 1;
-  const RowPlan p = row_plan(a.d, V, 2);
+  // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
+  const bool lanes = a.group == 0 || (a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
+  if (a.wide && lanes) {
+    const int xb = a.dt == ATLAS_F32 ? 4 : 2, rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
+    if (xb == 2) return rb == 0 ? forward_rows<2, 0>(a, st) : rb == 2 ? forward_rows<2, 2>(a, st) : forward_rows<2, 4>(a, st);
+    return rb == 0 ? forward_rows<4, 0>(a, st) : rb == 2 ? forward_rows<4, 2>(a, st) : forward_rows<4, 4>(a, st);
+  }
+  const RowPlan p = elem_plan(a.d, 2);
   const int rpb = p.block / p.tpr;
   const long blocks = (a.rows + rpb - 1) / rpb;
   if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   const int ng = a.group ? (a.d + a.group - 1) / a.group : 0;
   const size_t smem = (32 + (size_t)rpb * ng) * 4;
-#define ATLAS_RUN(VV, KK)                                                                      \
-  do {                                                                                         \
-    if (smem > 48 * 1024 &&                                                                    \
-        cudaFuncSetAttribute(norm_forward_kernel<VV, KK>,                                      \
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=        \
-            cudaSuccess)                                                                       \
-      return ATLAS_ERR_CUDA;                                                                   \
-    norm_forward_kernel<VV, KK><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);            \
-  } while (0)
-  if (V == 8) {
-    if (p.k == 1) ATLAS_RUN(8, 1);
-    else if (p.k == 2) ATLAS_RUN(8, 2);
-    else if (p.k == 4) ATLAS_RUN(8, 4);
-    else ATLAS_RUN(8, 8);
-  } else {
-    if (p.k <= 4) ATLAS_RUN(1, 4); else ATLAS_RUN(1, 32);
-  }
-#undef ATLAS_RUN
+  auto* f = p.k <= 4 ? norm_forward_elem<1, 4> : norm_forward_elem<1, 32>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATLAS_ERR_CUDA;
+  f<<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
 size_t norm_backward_workspace(const NormArgs& a) {
-  const RowPlan p1 = row_plan(a.d, 1, 4), p8 = row_plan(a.d, 8, 2);
-  const int n1 = back_blocks(a, p1), n8 = back_blocks(a, p8);
+  const int n1 = back_blocks(a, elem_plan(a.d, 4)), n8 = back_blocks(a, rows_plan(a.d, 1));
   return (size_t)(n1 > n8 ? n1 : n8) * a.d * 4;
 }
 
 int norm_backward_launch(const NormArgs& a, cudaStream_t st) {
-  const int V = a.wide ? 8 : 1;
-  const RowPlan p = row_plan(a.d, V, V == 8 ? 2 : 4);
+  const bool wide = back_wide(a);
+  const RowPlan p = wide ? rows_plan(a.d, 1) : elem_plan(a.d, 4);
   const int blocks = back_blocks(a, p);
-  const size_t smem = (32 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
-  if (blocks > 0) {
-    if (V == 8) {
-      if (p.k == 1) norm_backward_kernel<8, 1><<<blocks, p.block, smem, st>>>(a, p.tpr);
-      else if (p.k == 2) norm_backward_kernel<8, 2><<<blocks, p.block, smem, st>>>(a, p.tpr);
-      else if (p.k == 4) norm_backward_kernel<8, 4><<<blocks, p.block, smem, st>>>(a, p.tpr);
-      else norm_backward_kernel<8, 8><<<blocks, p.block, smem, st>>>(a, p.tpr);
+  if (blocks > 0 && wide) {
+    const int hb = a.rt == ATLAS_F32 ? 4 : 2, db = a.dt == ATLAS_F32 ? 4 : 2;
+    if (hb == 2 && db == 2) {
+      if (a.r) backward_rows<2, 2, 2>(a, p, blocks, st); else backward_rows<2, 2, 0>(a, p, blocks, st);
+    } else if (hb == 2) {
+      if (a.r) backward_rows<2, 4, 2>(a, p, blocks, st); else backward_rows<2, 4, 0>(a, p, blocks, st);
+    } else if (db == 2) {
+      if (a.r) backward_rows<4, 2, 4>(a, p, blocks, st); else backward_rows<4, 2, 0>(a, p, blocks, st);
     } else {
-      if (p.k <= 4) norm_backward_kernel<1, 4><<<blocks, p.block, smem, st>>>(a, p.tpr);
-      else norm_backward_kernel<1, 32><<<blocks, p.block, smem, st>>>(a, p.tpr);
+      if (a.r) backward_rows<4, 4, 4>(a, p, blocks, st); else backward_rows<4, 4, 0>(a, p, blocks, st);
     }
+  } else if (blocks > 0) {
+    const size_t smem = (32 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
+    if (p.k <= 4) norm_backward_elem<1, 4><<<blocks, p.block, smem, st>>>(a, p.tpr);
+    else norm_backward_elem<1, 32><<<blocks, p.block, smem, st>>>(a, p.tpr);
   }
   if (a.dw) norm_dw_kernel<<<(a.d + 31) / 32, 256, 0, st>>>(a.part, a.dw, blocks, a.d);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
