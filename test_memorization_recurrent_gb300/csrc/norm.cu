@@ -83,36 +83,47 @@ struct RowGroup {
   int tpr, lane, tid;  // threads per row, lane within them
 };
 
-__device__ __forceinline__ float row_sum(float v, const RowGroup& g, float* red) {
-  for (int m = min(g.tpr, 32) >> 1; m; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+// Sum and maximum over a row's threads.  A block's warps meet in red[0 .. 31], of which the
+// words past their number are zero; the next use of the same words has to be another
+// reduction's barrier away.
+template <typename F>
+__device__ __forceinline__ float row_reduce(float v, const RowGroup& g, float* red, F f) {
+  if (g.tpr >= 32) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
+  } else {
+    for (int m = g.tpr >> 1; m; m >>= 1) v = f(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
+  }
   if (g.tpr > 32) {
-    const int nw = g.tpr >> 5;
-    __syncthreads();
     if ((g.tid & 31) == 0) red[g.tid >> 5] = v;
     __syncthreads();
+    const float4* q = reinterpret_cast<const float4*>(red);
     v = 0.f;
-    for (int i = 0; i < nw; ++i) v += red[i];
+    for (int i = 0; i < (g.tpr + 127) / 128; ++i) {
+      const float4 t = q[i];
+      v = f(v, f(f(t.x, t.y), f(t.z, t.w)));
+    }
   }
   return v;
 }
+__device__ __forceinline__ float row_sum(float v, const RowGroup& g, float* red) {
+  return row_reduce(v, g, red, [](float x, float y) { return x + y; });
+}
 // NaN stays out of a maximum (fmaxf), as it does of its scale; the element itself stays NaN.
 __device__ __forceinline__ float row_max(float v, const RowGroup& g, float* red) {
-  for (int m = min(g.tpr, 32) >> 1; m; m >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, m));
-  if (g.tpr > 32) {
-    const int nw = g.tpr >> 5;
-    __syncthreads();
-    if ((g.tid & 31) == 0) red[g.tid >> 5] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < nw; ++i) v = fmaxf(v, red[i]);
-  }
-  return v;
+  return row_reduce(v, g, red, [](float x, float y) { return fmaxf(x, y); });
+}
+// The words that reductions meet in, before their first use.
+__device__ __forceinline__ void clear_red(float* red, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) red[i] = 0.f;
+  __syncthreads();
 }
 
 template <int V, int K>
 __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArgs a, int tpr) {
-  extern __shared__ float sm[];  // 32 floats, then (8-bit groups that cross lanes) the groups' maxima
+  extern __shared__ __align__(16) float sm[];  // 64 floats, then (8-bit groups that cross lanes) the groups' maxima
   float* red = sm;
+  clear_red(red, 64);
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
   const int rpb = blockDim.x / tpr;
   const long row = (long)blockIdx.x * rpb + threadIdx.x / tpr;
@@ -137,7 +148,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArg
 #pragma unroll
     for (int j = 0; j < V; ++j) ss += h[k][j] * h[k][j];
   }
-  const float rstd = rsqrtf(row_sum(ss, g, red) / a.d + a.eps);
+  const float rstd = rsqrtf(row_sum(ss, g, red) * a.inv_d + a.eps);
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -156,7 +167,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArg
   }
   if (a.ot != ATLAS_E4M3) return;
   if (a.group == 0) {
-    const float scale = fmaxf(row_max(amax, g, red), kAmaxMin) * (1.f / kE4m3Max);
+    const float scale = fmaxf(row_max(amax, g, red + 32), kAmaxMin) * (1.f / kE4m3Max);
     const float inv = 1.f / scale;
     if (live && g.lane == 0) a.scale[row] = scale;
 #pragma unroll
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArg
   // groups of channels: maxima of non-negative floats order like their bits, so integer
   // maxima in shared memory give the same result in any order
   const int ng = (a.d + a.group - 1) / a.group;
-  unsigned* gm = reinterpret_cast<unsigned*>(sm + 32) + (threadIdx.x / tpr) * ng;
+  unsigned* gm = reinterpret_cast<unsigned*>(sm + 64) + (threadIdx.x / tpr) * ng;
   for (int i = g.lane; i < ng; i += tpr) gm[i] = 0u;
   __syncthreads();
 #pragma unroll
@@ -212,8 +223,9 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArg
 // sums of dy hat of its columns over its rows, and the block writes one row of partial sums.
 template <int V, int K>
 __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormArgs a, int tpr) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
   float* red = sm;
+  clear_red(red, 64);
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
   const int rpb = blockDim.x / tpr;
   float dw[K][V];
@@ -242,10 +254,10 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormAr
         }
       }
     }
-    ss = row_sum(ss, g, red);
-    dot = row_sum(dot, g, red);
-    const float rstd = rsqrtf(ss / a.d + a.eps);
-    const float mean = dot * rstd / a.d;  // mean(w dy hat)
+    ss = row_sum(ss, g, red);  // the other sum's barrier lies between two uses of the same words
+    dot = row_sum(dot, g, red + 32);
+    const float rstd = rsqrtf(ss * a.inv_d + a.eps);
+    const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * tpr + g.lane) * V;
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormAr
   }
   if (!a.dw) return;
   // rows of one block are added in a fixed order
-  float* acc = sm + 32;
+  float* acc = sm + 64;
   const int mine = threadIdx.x / tpr;
   for (int r = 0; r < rpb; ++r) {
     __syncthreads();
@@ -357,123 +369,14 @@ __device__ __forceinline__ void st8(void* p, long i, int dtype, const float* v) 
   }
 }
 
-// K vectors of eight a thread, R rows at a time.  tpr threads a row: 8, 16 or 32 lanes, or the
-// whole block (R = 1).
-template <int XB, int RB, int K, int R>
-__global__ void __launch_bounds__(512) norm_forward_rows(NormArgs a, int tpr) {
-  extern __shared__ float sm[];
-  float* red = sm;
-  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
-  const int rpb = blockDim.x / tpr;
-  const long row0 = (long)blockIdx.x * rpb * R + threadIdx.x / tpr;
-  Raw8<XB> x[R][K];
-  Raw8<RB> r[R][K];
-#pragma unroll
-  for (int j = 0; j < R; ++j)
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const long row = row0 + j * rpb;
-      const int c = (k * tpr + g.lane) * 8;
-      if (row < a.rows && c < a.d) {
-        x[j][k].load(a.x, row * a.sx + c);
-        if (RB) r[j][k].load(a.r, row * a.sr + c);
-      } else {
-        x[j][k].zero();
-        r[j][k].zero();
-      }
-    }
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const long row = row0 + j * rpb;
-    const bool live = row < a.rows;
-    float h[K][8], ss = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * tpr + g.lane) * 8;
-      x[j][k].floats(a.dt, h[k]);
-      if (RB) {
-        float v[8];
-        r[j][k].floats(a.rt, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] += v[i];
-      }
-      if (a.r_out && live && c < a.d) st8(a.r_out, row * a.sr + c, a.rt, h[k]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
-    }
-    const float rstd = rsqrtf(row_sum(ss, g, red) / a.d + a.eps);
-    float amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * tpr + g.lane) * 8;
-      float w[8];
-      if (a.w && c < a.d) {
-        if (a.wt == ATLAS_F32) {
-          Raw8<4> q;
-          q.load_kept(a.w, c);
-          q.floats(a.wt, w);
-        } else {
-          Raw8<2> q;
-          q.load_kept(a.w, c);
-          q.floats(a.wt, w);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] *= rstd * w[i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] *= rstd;
-      }
-      if (a.ot != ATLAS_E4M3) {
-        if (live && c < a.d) st8(a.y, row * a.sy + c, a.ot, h[k]);
-      } else if (a.group == 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(h[k][i]));
-      } else {
-        // the group's lanes are neighbours: group / 8 of them, a power of two
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(h[k][i]));
-        for (int o = a.group >> 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float scale = fmaxf(m, kAmaxMin) * (1.f / kE4m3Max), inv = 1.f / scale;
-        if (live && c < a.d) {
-          const int ng = (a.d + a.group - 1) / a.group;
-          if (c % a.group == 0) a.scale[row * ng + c / a.group] = scale;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[k][i] *= inv;
-          st8(a.y, row * a.sy + c, a.ot, h[k]);
-        }
-      }
-    }
-    if (a.ot == ATLAS_E4M3 && a.group == 0) {
-      const float scale = fmaxf(row_max(amax, g, red), kAmaxMin) * (1.f / kE4m3Max), inv = 1.f / scale;
-      if (live && g.lane == 0) a.scale[row] = scale;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = (k * tpr + g.lane) * 8;
-        if (live && c < a.d) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[k][i] *= inv;
-          st8(a.y, row * a.sy + c, a.ot, h[k]);
-        }
-      }
-    }
-  }
-}
-
-// Backward: tpr threads a row as above; block b takes the rows b * rpb + .., step
-// gridDim.x * rpb.  Both sums of a row are reduced together.
-template <int HB, int DB, int GB, int K>  // bytes of h, dy, dh (0: none)
-__global__ void __launch_bounds__(512) norm_backward_rows(NormArgs a, int tpr) {
-  extern __shared__ float sm[];
-  float2* red = reinterpret_cast<float2*>(sm);  // [2][16], then the columns' sums
-  const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
-  const int nw = tpr >> 5;
-  float dw[K][8], w[K][8];
+// This thread's weights: K vectors of eight, ones without a weight.
+template <int K>
+__device__ __forceinline__ void load_weights(const NormArgs& a, int tpr, int lane, float (*w)[8]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (k * tpr + lane) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i] = 0.f, w[k][i] = 1.f;
+    for (int i = 0; i < 8; ++i) w[k][i] = 1.f;
     if (a.w && c < a.d) {
       if (a.wt == ATLAS_F32) {
         Raw8<4> q;
@@ -486,35 +389,225 @@ __global__ void __launch_bounds__(512) norm_backward_rows(NormArgs a, int tpr) {
       }
     }
   }
-  Raw8<HB> h[K];
-  Raw8<DB> dy[K];
-  Raw8<GB> dh[K];
-  auto fetch = [&](long row) {
+}
+
+// One row from its vectors and weights: K of eight a thread.  red: 64 words, of which the next row of the
+// same threads takes another 64.
+template <int XB, int RB, int K>
+__device__ __forceinline__ void forward_row(const NormArgs& a, const RowGroup& g, float* red, long row,
+                                            bool live, const Raw8<XB>* x, const Raw8<RB>* r,
+                                            const float (*w)[8]) {
+  float h[K][8], ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * g.tpr + g.lane) * 8;
+    x[k].floats(a.dt, h[k]);
+    if (RB) {
+      float v[8];
+      r[k].floats(a.rt, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] += v[i];
+    }
+    if (a.r_out && live && c < a.d) st8(a.r_out, row * a.sr + c, a.rt, h[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
+  }
+  const float rstd = rsqrtf(row_sum(ss, g, red) * a.inv_d + a.eps);
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * g.tpr + g.lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[k][i] *= rstd * w[k][i];
+    if (a.ot != ATLAS_E4M3) {
+      if (live && c < a.d) st8(a.y, row * a.sy + c, a.ot, h[k]);
+      continue;
+    }
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(h[k][i]));
+    if (a.group == 0) {
+      amax = fmaxf(amax, m);
+      continue;
+    }
+    // the group's lanes are neighbours: group / 8 of them, a power of two
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (8 * o < a.group) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    const float scale = fmaxf(m, kAmaxMin) * (1.f / kE4m3Max), inv = rcp(scale);
+    if (live && c < a.d) {
+      if ((c & (a.group - 1)) == 0) a.scale[row * a.ng + (c >> a.gshift)] = scale;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[k][i] *= inv;
+      st8(a.y, row * a.sy + c, a.ot, h[k]);
+    }
+  }
+  if (a.ot == ATLAS_E4M3 && a.group == 0) {
+    const float scale = fmaxf(row_max(amax, g, red + 32), kAmaxMin) * (1.f / kE4m3Max), inv = rcp(scale);
+    if (live && g.lane == 0) a.scale[row] = scale;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * g.tpr + g.lane) * 8;
+      if (live && c < a.d) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] *= inv;
+        st8(a.y, row * a.sy + c, a.ot, h[k]);
+      }
+    }
+  }
+}
+
+// R rows at a time.  tpr threads a row: 8, 16 or 32 lanes, or the whole block (R = 1).
+template <int XB, int RB, int K, int R>
+__global__ void __launch_bounds__(512) norm_forward_rows(NormArgs a, int tpr) {
+  extern __shared__ __align__(16) float sm[];
+  if (tpr > 32) clear_red(sm, 64);
+  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
+  const int rpb = blockDim.x / tpr;
+  const long row0 = (long)blockIdx.x * rpb * R + threadIdx.x / tpr;
+  Raw8<XB> x[R][K];
+  Raw8<RB> r[R][K];
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long row = row0 + j * rpb;
+      const int c = (k * tpr + g.lane) * 8;
+      x[j][k].zero();
+      r[j][k].zero();
+      if (row < a.rows && c < a.d) {
+        x[j][k].load(a.x, row * a.sx + c);
+        if (RB) r[j][k].load(a.r, row * a.sr + c);
+      }
+    }
+  float w[K][8];
+  load_weights<K>(a, tpr, g.lane, w);
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    forward_row<XB, RB, K>(a, g, sm, row0 + j * rpb, row0 + j * rpb < a.rows, x[j], r[j], w);
+}
+
+// A row of n bytes (a multiple of 16) from p to shared memory by `threads` threads, neighbouring
+// lanes taking neighbouring 16 bytes (a lane that took its own eight 32-bit elements would
+// have each 32-byte sector asked for twice).
+// Q pieces a thread.
+template <int Q>
+__device__ __forceinline__ void copy_row(char* s, const void* p, long at, int n, bool live, int lane, int threads) {
+  const char* q = reinterpret_cast<const char*>(p) + (live ? at : 0);
+#pragma unroll
+  for (int k = 0; k < Q; ++k) {
+    const int i = (k * threads + lane) * 16;
+    if (i < n) cp_async<16>(s + i, live ? q + i : q, live);
+  }
+}
+
+// Many rows of a block each: a block walks rows and copies the next kStages - 1 to shared
+// memory while it computes one, so that loads are always under way.  The lanes that copy 16-bit
+// elements are those that read them; with 32-bit elements the barrier in a row's reduction also
+// hands over the next row, whose copies have been waited for before it.
+constexpr int kStages = 3;
+template <int XB, int RB, int K>
+__global__ void __launch_bounds__(512) norm_forward_ring(NormArgs a) {
+  extern __shared__ __align__(16) float sm[];  // [2][64] for the reductions, then [stage]: x, r
+  constexpr bool kOwn = XB == 2 && RB != 4;
+  clear_red(sm, 128);
+  const RowGroup g{(int)blockDim.x, (int)threadIdx.x, (int)threadIdx.x};
+  const int bytes = a.d * (XB + RB);
+  char* ring = reinterpret_cast<char*>(sm + 128);
+  auto fetch = [&](long row, int stage) {
+    char* s = ring + stage * bytes;
+    copy_row<K * XB / 2>(s, a.x, row * a.sx * XB, a.d * XB, row < a.rows, g.lane, g.tpr);
+    if (RB) copy_row<K * RB / 2>(s + a.d * XB, a.r, row * a.sr * RB, a.d * RB, row < a.rows, g.lane, g.tpr);
+    cp_commit();
+  };
+  float w[K][8];
+  if (K <= 2) load_weights<K>(a, g.tpr, g.lane, w);
+  long row = blockIdx.x;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(row + (long)i * gridDim.x, i);
+  cp_wait<kStages - 2>();
+  __syncthreads();
+  int stage = 0;
+  for (int odd = 0; row < a.rows; row += gridDim.x, odd ^= 64) {
+    fetch(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
+    if (kOwn) cp_wait<kStages - 1>();
+    Raw8<XB> x[K];
+    Raw8<RB> r[K];
+    const char* s = ring + stage * bytes;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * g.tpr + g.lane) * 8;
+      x[k].zero();
+      r[k].zero();
+      if (c < a.d) {
+        x[k].load_kept(s, c);
+        if (RB) r[k].load_kept(s + a.d * XB, c);
+      }
+    }
+    if (!kOwn) cp_wait<kStages - 2>();  // the next row's
+    if (K > 2) load_weights<K>(a, g.tpr, g.lane, w);  // (long rows: again for each, from L2)
+    forward_row<XB, RB, K>(a, g, sm + odd, row, true, x, r, w);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  cp_wait<0>();
+}
+
+// Backward: tpr threads a row as above; block b takes the rows b * rpb + .., step
+// gridDim.x * rpb.  Both sums of a row are reduced together.
+// MT: most threads; up to 320 (2560 channels), two blocks an SM without a register in memory.
+template <int HB, int DB, int GB, int K, int MT>  // bytes of h, dy, dh (0: none)
+__global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) norm_backward_rows(NormArgs a, int tpr) {
+  extern __shared__ __align__(16) float sm[];
+  float2* red = reinterpret_cast<float2*>(sm);  // [2][16], then the rows' ring
+  const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  const int nw = tpr >> 5;
+  clear_red(sm, 64);
+  float dw[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
+  load_weights<K>(a, tpr, lane, w);
+  // [stage][row of the block]: h, dy, dh
+  const int bytes = a.d * (HB + DB + GB);
+  char* ring = reinterpret_cast<char*>(sm + 64) + mine * bytes;
+  const long step = (long)gridDim.x * rpb;
+  auto fetch = [&](long row, int stage) {
+    char* s = ring + stage * rpb * bytes;
+    copy_row<K * HB / 2>(s, a.x, row * a.sr * HB, a.d * HB, row < a.rows, lane, tpr);
+    copy_row<K * DB / 2>(s + a.d * HB, a.dy, row * a.sy * DB, a.d * DB, row < a.rows, lane, tpr);
+    if (GB) copy_row<K * GB / 2>(s + a.d * (HB + DB), a.r, row * a.sr * GB, a.d * GB, row < a.rows, lane, tpr);
+    cp_commit();
+  };
+  long row = (long)blockIdx.x * rpb + mine;
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(row + i * step, i);
+  cp_wait<kStages - 2>();
+  __syncthreads();
+  int stage = 0;
+  for (int odd = 0; row - mine < a.rows; row += step, odd ^= 1) {
+    fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+    float hv[K][8], dv[K][8], gv[K][8], ss = 0.f, dot = 0.f;
+    const char* s = ring + stage * rpb * bytes;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * tpr + lane) * 8;
-      if (row < a.rows && c < a.d) {
-        h[k].load(a.x, row * a.sr + c);
-        dy[k].load(a.dy, row * a.sy + c);
-        if (GB) dh[k].load(a.r, row * a.sr + c);
-      } else {
-        h[k].zero();
-        dy[k].zero();
-        dh[k].zero();
+      Raw8<HB> h;
+      Raw8<DB> dy;
+      Raw8<GB> dh;
+      h.zero(), dy.zero(), dh.zero();
+      if (c < a.d) {
+        h.load_kept(s, c);
+        dy.load_kept(s + a.d * HB, c);
+        if (GB) dh.load_kept(s + a.d * (HB + DB), c);
       }
+      h.floats(a.rt, hv[k]);
+      dy.floats(a.dt, dv[k]);
+      if (GB) dh.floats(a.rt, gv[k]);
     }
-  };
-  long row = (long)blockIdx.x * rpb + mine;
-  fetch(row);
-  for (int odd = 0; row - mine < a.rows; row += (long)gridDim.x * rpb, odd ^= 1) {
-    float hv[K][8], dv[K][8], gv[K][8], ss = 0.f, dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      h[k].floats(a.rt, hv[k]);
-      dy[k].floats(a.dt, dv[k]);
-      if (GB) dh[k].floats(a.rt, gv[k]);
-    }
-    fetch(row + (long)gridDim.x * rpb);
+    cp_wait<kStages - 2>();  // the next row's copies, handed over by the barrier below
+    if (nw <= 1) __syncwarp();
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -530,14 +623,14 @@ __global__ void __launch_bounds__(512) norm_backward_rows(NormArgs a, int tpr) {
       if ((threadIdx.x & 31) == 0) red[odd * 16 + (threadIdx.x >> 5)] = make_float2(ss, dot);
       __syncthreads();
       ss = dot = 0.f;
-      for (int i = 0; i < nw; ++i) {
-        const float2 v = red[odd * 16 + i];
-        ss += v.x;
-        dot += v.y;
+      for (int i = 0; i < (nw + 1) / 2; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(red + odd * 16)[i];
+        ss += v.x + v.z;
+        dot += v.y + v.w;
       }
     }
-    const float rstd = rsqrtf(ss / a.d + a.eps);
-    const float mean = dot * rstd / a.d;  // mean(w dy hat)
+    const float rstd = rsqrtf(ss * a.inv_d + a.eps);
+    const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * tpr + lane) * 8;
@@ -551,8 +644,9 @@ __global__ void __launch_bounds__(512) norm_backward_rows(NormArgs a, int tpr) {
       if (row < a.rows && c < a.d) st8(a.y, row * a.sr + c, a.rt, o);
     }
   }
+  cp_wait<0>();
   if (!a.dw) return;
-  float* acc = sm + 64;
+  float* acc = sm + 64;  // over the rows' ring
   for (int r = 0; r < rpb; ++r) {  // rows of one block in a fixed order
     __syncthreads();
     if (r == mine) {
@@ -637,16 +731,40 @@ int back_blocks(const NormArgs& a, const RowPlan& p) {
   return (int)(need < most ? need : most);
 }
 
+// Blocks an SM for a kernel that needs `smem` bytes a block, at most `most`.
+int resident(size_t smem, int most) {
+  const int n = (int)((size_t)224 * 1024 / (smem + 1024));
+  return n < 1 ? 1 : n < most ? n : most;
+}
+
+template <int XB, int RB, int K>
+int forward_ring(const NormArgs& a, int threads, size_t smem, cudaStream_t st) {
+  auto* f = norm_forward_ring<XB, RB, K>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATLAS_ERR_CUDA;
+  const long most = 152L * resident(smem, 8 * 256 / threads);
+  f<<<(unsigned)(a.rows < most ? a.rows : most), threads, smem, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
+
 template <int XB, int RB>
 int forward_rows(const NormArgs& a, cudaStream_t st) {
-  // few rows: a block each, so that the row's loads are spread over it
+  // rows of up to 256 channels: lanes of a warp; longer ones: a block
   const bool few = a.rows <= 152 * 8;
-  const RowPlan p = rows_plan(a.d, few ? 1 : 8);
+  const RowPlan p = rows_plan(a.d, 1);
+  const size_t ring = 512 + (size_t)kStages * a.d * (XB + RB);
+  if (!few && p.tpr > 32 && ring <= 200 * 1024) {
+    if (p.k == 1) return forward_ring<XB, RB, 1>(a, p.block, ring, st);
+    if (p.k == 2) return forward_ring<XB, RB, 2>(a, p.block, ring, st);
+    if (p.k == 4) return forward_ring<XB, RB, 4>(a, p.block, ring, st);
+    return forward_ring<XB, RB, 8>(a, p.block, ring, st);
+  }
   const int rpb = p.block / p.tpr;
   const int R = p.k == 1 && p.tpr <= 32 && !few ? 4 : 1;  // short rows: four under way
   const long blocks = (a.rows + (long)rpb * R - 1) / ((long)rpb * R);
   if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
-  const size_t smem = 32 * 4;
+  const size_t smem = 64 * 4;
   if (p.k == 1 && R == 4)
     norm_forward_rows<XB, RB, 1, 4><<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
   else if (p.k == 1)
@@ -660,22 +778,41 @@ int forward_rows(const NormArgs& a, cudaStream_t st) {
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
+template <int HB, int DB, int GB, int K, int MT>
+int backward_rows(const NormArgs& a, const RowPlan& p, int& blocks, cudaStream_t st) {
+  const size_t ring = (size_t)kStages * (p.block / p.tpr) * a.d * (HB + DB + GB), sums = (size_t)a.d * 4;
+  const size_t smem = 256 + (ring > sums ? ring : sums);
+  auto* f = norm_backward_rows<HB, DB, GB, K, MT>;
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return ATLAS_ERR_CUDA;
+  // no more blocks than run at once
+  const int most = 152 * resident(smem, (MT == 320 ? 640 : 512) / p.block);
+  blocks = blocks < most ? blocks : most;
+  f<<<blocks, p.block, smem, st>>>(a, p.tpr);
+  return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
+}
 template <int HB, int DB, int GB>
-void backward_rows(const NormArgs& a, const RowPlan& p, int blocks, cudaStream_t st) {
-  const size_t smem = (64 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
-  if (p.k == 1)
-    norm_backward_rows<HB, DB, GB, 1><<<blocks, p.block, smem, st>>>(a, p.tpr);
-  else
-    norm_backward_rows<HB, DB, GB, 2><<<blocks, p.block, smem, st>>>(a, p.tpr);
+int backward_rows(const NormArgs& a, const RowPlan& p, int& blocks, cudaStream_t st) {
+  if (p.k == 1 && p.block <= 320) return backward_rows<HB, DB, GB, 1, 320>(a, p, blocks, st);
+  if (p.k == 1) return backward_rows<HB, DB, GB, 1, 512>(a, p, blocks, st);
+  return backward_rows<HB, DB, GB, 2, 512>(a, p, blocks, st);
 }
 
-// Rows whose registers (h, dy, dw and the next row) the backward kernel can hold.
-bool back_wide(const NormArgs& a) { return a.wide && a.d <= 8192; }
+// Rows whose registers and ring the backward kernel can hold: three rows of h, dy and dh.
+bool back_wide(const NormArgs& a) {
+  const int hb = a.rt == ATLAS_F32 ? 4 : 2, db = a.dt == ATLAS_F32 ? 4 : 2;
+  return a.wide && a.d <= 8192 && (size_t)kStages * a.d * (2 * hb + db) <= 200 * 1024;
+}
 
 }  // namespace
 
-int norm_forward_launch(const NormArgs& a, cudaStream_t st) {
+int norm_forward_launch(const NormArgs& args, cudaStream_t st) {
   // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
+  NormArgs a = args;
+  a.inv_d = 1.f / a.d;
+  a.ng = a.group ? (a.d + a.group - 1) / a.group : 1;
+  for (a.gshift = 0; (1 << a.gshift) < a.group;) ++a.gshift;
   const bool lanes = a.group == 0 || (a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
   if (a.wide && lanes) {
     const int xb = a.dt == ATLAS_F32 ? 4 : 2, rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
@@ -687,7 +824,7 @@ int norm_forward_launch(const NormArgs& a, cudaStream_t st) {
   const long blocks = (a.rows + rpb - 1) / rpb;
   if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   const int ng = a.group ? (a.d + a.group - 1) / a.group : 0;
-  const size_t smem = (32 + (size_t)rpb * ng) * 4;
+  const size_t smem = (64 + (size_t)rpb * ng) * 4;
   auto* f = p.k <= 4 ? norm_forward_elem<1, 4> : norm_forward_elem<1, 32>;
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -701,23 +838,26 @@ size_t norm_backward_workspace(const NormArgs& a) {
   return (size_t)(n1 > n8 ? n1 : n8) * a.d * 4;
 }
 
-int norm_backward_launch(const NormArgs& a, cudaStream_t st) {
+int norm_backward_launch(const NormArgs& args, cudaStream_t st) {
+  NormArgs a = args;
+  a.inv_d = 1.f / a.d;
   const bool wide = back_wide(a);
   const RowPlan p = wide ? rows_plan(a.d, 1) : elem_plan(a.d, 4);
-  const int blocks = back_blocks(a, p);
+  int blocks = back_blocks(a, p);
   if (blocks > 0 && wide) {
     const int hb = a.rt == ATLAS_F32 ? 4 : 2, db = a.dt == ATLAS_F32 ? 4 : 2;
-    if (hb == 2 && db == 2) {
-      if (a.r) backward_rows<2, 2, 2>(a, p, blocks, st); else backward_rows<2, 2, 0>(a, p, blocks, st);
-    } else if (hb == 2) {
-      if (a.r) backward_rows<2, 4, 2>(a, p, blocks, st); else backward_rows<2, 4, 0>(a, p, blocks, st);
-    } else if (db == 2) {
-      if (a.r) backward_rows<4, 2, 4>(a, p, blocks, st); else backward_rows<4, 2, 0>(a, p, blocks, st);
-    } else {
-      if (a.r) backward_rows<4, 4, 4>(a, p, blocks, st); else backward_rows<4, 4, 0>(a, p, blocks, st);
-    }
+    int rc;
+    if (hb == 2 && db == 2)
+      rc = a.r ? backward_rows<2, 2, 2>(a, p, blocks, st) : backward_rows<2, 2, 0>(a, p, blocks, st);
+    else if (hb == 2)
+      rc = a.r ? backward_rows<2, 4, 2>(a, p, blocks, st) : backward_rows<2, 4, 0>(a, p, blocks, st);
+    else if (db == 2)
+      rc = a.r ? backward_rows<4, 2, 4>(a, p, blocks, st) : backward_rows<4, 2, 0>(a, p, blocks, st);
+    else
+      rc = a.r ? backward_rows<4, 4, 4>(a, p, blocks, st) : backward_rows<4, 4, 0>(a, p, blocks, st);
+    if (rc != ATLAS_OK) return rc;
   } else if (blocks > 0) {
-    const size_t smem = (32 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
+    const size_t smem = (64 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
     if (p.k <= 4) norm_backward_elem<1, 4><<<blocks, p.block, smem, st>>>(a, p.tpr);
     else norm_backward_elem<1, 32><<<blocks, p.block, smem, st>>>(a, p.tpr);
   }

@@ -19,7 +19,8 @@ struct NormArgs {
   float* part;      // backward: [blocks, d] partial sums of dw
   long rows, sx, sr, sy;
   int d, dt, rt, wt, ot, group;
-  float eps;
+  float eps, inv_d;  // 1 / d, set at the launch
+  int ng, gshift;    // groups of a row, log2 of a group that is a power of two; set at the launch
   int wide;         // every pointer and stride allows 8-element accesses
 };
 int norm_forward_launch(const NormArgs& a, cudaStream_t st);
