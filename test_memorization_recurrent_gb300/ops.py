@@ -23,7 +23,17 @@ OPS_EXPORTS = ("atlas_norm_forward", "atlas_norm_backward", "atlas_norm_backward
 _int, _long, _vp, _size = ctypes.c_int, ctypes.c_long, ctypes.c_void_p, ctypes.c_size_t
 
 
-class AtlasNormCfg(ctypes.Structure):
+class _Cfg(ctypes.Structure):
+    """A description whose tensors' extents are worked out once, and again after a field that
+    they depend on is set."""
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name not in ("workspace", "workspace_bytes", "held", "extents"):
+            super().__setattr__("extents", None)
+
+
+class AtlasNormCfg(_Cfg):
     """Mirror of ``atlas_norm_cfg`` in include/atlas_ops.h."""
     _fields_ = [("rows", _long), ("d", _int), ("dtype", _int), ("r_dtype", _int),
                 ("w_dtype", _int), ("out_dtype", _int), ("group", _int), ("eps", ctypes.c_float),
@@ -31,7 +41,7 @@ class AtlasNormCfg(ctypes.Structure):
                 ("workspace", _vp), ("workspace_bytes", _size)]
 
 
-class AtlasConvCfg(ctypes.Structure):
+class AtlasConvCfg(_Cfg):
     """Mirror of ``atlas_conv_cfg`` in include/atlas_ops.h."""
     _fields_ = [("B", _int), ("L", _int), ("C", _int), ("W", _int), ("act", _int), ("dtype", _int),
                 ("w_dtype", _int), ("head_dim", _int), ("x_batch_stride", _long),
@@ -40,7 +50,7 @@ class AtlasConvCfg(ctypes.Structure):
                 ("carry", _vp), ("status_dev", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
 
 
-class AtlasScanCfg(ctypes.Structure):
+class AtlasScanCfg(_Cfg):
     """Mirror of ``atlas_scan_cfg`` in include/atlas_ops.h."""
     _fields_ = [("B", _int), ("L", _int), ("D", _int), ("N", _int), ("G", _int), ("dtype", _int),
                 ("softplus", _int), ("x_batch_stride", _long), ("x_token_stride", _long),
@@ -144,60 +154,59 @@ def _sequences(B, seq_start, slot, n_slots, carry):
             _checked(carry, "uint8", int(B), "carry"))
 
 
-_torch = None
-_types = None
+_types = _device = _raw_stream = _fn = None
 
 
 def _setup():
-    global _torch, _types
+    """What every call needs, looked up once."""
+    global _types, _device, _raw_stream, _fn
     import torch
+
+    from . import load_library
+    lib = load_library()
+    torch.cuda.current_device()  # initialises CUDA
     _types = (torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn)
-    _torch = torch
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _device = torch._C._cuda_getDevice
+    _fn = {name: getattr(lib, name) for name in OPS_EXPORTS}
 
 
-class _Args:
-    """Checks one call's tensors against what its description says and turns them into
-    addresses."""
-    __slots__ = ("device",)
-
-    def __init__(self):
-        if _torch is None:
-            _setup()
-        self.device = _torch.cuda.current_device()
-
-    def __call__(self, t, code, extent, name):
-        """t: tensor, address or None; extent: elements from its first to its last one."""
-        if t is None or isinstance(t, int):
-            return t
-        if t.dtype is not _types[code]:
-            raise _error(f"{name} is {t.dtype}, the description says {_types[code]}")
-        if t.get_device() != self.device:
-            raise _error(f"{name} is not on the current device (cuda:{self.device})")
-        if t.numel() < extent:  # a strided view ends further on than its elements count
-            if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent:
-                raise _error(f"{name} ends before the {extent} elements the description names")
-        return t.data_ptr()
+def _begin():
+    """The current device; before anything else of a call."""
+    if _fn is None:
+        _setup()
+    return _device()
 
 
-def _stream(stream):
+def _arg(t, code, extent, name, device):
+    """Address of one argument (a tensor, an address or None) after its checks; extent:
+    elements from the first to the last one that the description names."""
+    if t is None or type(t) is int:
+        return t
+    if t.dtype is not _types[code]:
+        raise _error(f"{name} is {t.dtype}, the description says {_types[code]}")
+    if t.get_device() != device:
+        raise _error(f"{name} is not on the current device (cuda:{device})")
+    if t.numel() < extent:  # a strided view ends further on than its elements count
+        if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent:
+            raise _error(f"{name} ends before the {extent} elements the description names")
+    return t.data_ptr()
+
+
+def _call(name, args, stream, device):
     if stream is None:
-        return _torch.cuda.current_stream().cuda_stream
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-
-
-def _raise(rc):
+        stream = _raw_stream(device)
+    elif type(stream) is not int:
+        stream = stream.cuda_stream
+    rc = _fn[name](*args, stream)
     if rc != 0:
         from . import AtlasError, atlas_mem_strerror
         raise AtlasError(rc, atlas_mem_strerror(rc))
 
 
-def _lib():
-    from . import load_library
-    return load_library()
-
-
 def _bytes(fn, cfg):
-    n = int(getattr(_lib(), fn)(ctypes.byref(cfg)))
+    from . import load_library
+    n = int(getattr(load_library(), fn)(ctypes.byref(cfg)))
     if n == 2 ** 64 - 1:
         raise _error("invalid or uncovered description")
     return n
@@ -218,18 +227,23 @@ def _rows(cfg, stride):
 
 # ------------------------------------------------------------------ norm
 
+def _norm_extents(c):
+    groups = 1 if c.group <= 0 or c.group >= c.d else -(-c.d // c.group)
+    c.extents = e = (c.dtype, c.r_dtype, c.w_dtype, c.out_dtype, c.d, _rows(c, c.x_stride), _rows(c, c.r_stride),
+                     _rows(c, c.y_stride), c.rows * groups)
+    return e
+
+
 def atlas_norm_forward(x, residual, weight, cfg: AtlasNormCfg, y, residual_out=None, scale=None,
                        stream=None) -> None:
     """y = norm(x + residual) * weight; residual_out receives x + residual, scale the scales
     of an E4M3 output.  residual, weight and residual_out may be None."""
-    p = _Args()
-    d, rows, r = cfg.d, cfg.rows, _rows(cfg, cfg.r_stride)
-    groups = 1 if cfg.group <= 0 or cfg.group >= d else -(-d // cfg.group)
-    _raise(_lib().atlas_norm_forward(
-        p(x, cfg.dtype, _rows(cfg, cfg.x_stride), "x"), p(residual, cfg.r_dtype, r, "residual"),
-        p(weight, cfg.w_dtype, d, "weight"), cfg, p(y, cfg.out_dtype, _rows(cfg, cfg.y_stride), "y"),
-        p(residual_out, cfg.r_dtype, r, "residual_out"), p(scale, F32, rows * groups, "scale"),
-        _stream(stream)))
+    dev = _begin()
+    t, r, w, o, d, nx, nr, ny, ns = cfg.extents or _norm_extents(cfg)
+    _call("atlas_norm_forward",
+          (_arg(x, t, nx, "x", dev), _arg(residual, r, nr, "residual", dev), _arg(weight, w, d, "weight", dev), cfg,
+           _arg(y, o, ny, "y", dev), _arg(residual_out, r, nr, "residual_out", dev), _arg(scale, F32, ns, "scale", dev)),
+          stream, dev)
 
 
 def atlas_norm_backward_workspace_bytes(cfg: AtlasNormCfg) -> int:
@@ -239,40 +253,41 @@ def atlas_norm_backward_workspace_bytes(cfg: AtlasNormCfg) -> int:
 def atlas_norm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, stream=None) -> None:
     """dx = dL/dh and dw = dL/d weight from dy = dL/dy and (or None) dh, the gradient that
     reaches the residual stream from later layers."""
-    p = _Args()
-    r = _rows(cfg, cfg.r_stride)
-    _raise(_lib().atlas_norm_backward(
-        p(h, cfg.r_dtype, r, "h"), p(weight, cfg.w_dtype, cfg.d, "weight"),
-        p(dy, cfg.dtype, _rows(cfg, cfg.y_stride), "dy"), p(dh, cfg.r_dtype, r, "dh"), cfg,
-        p(dx, cfg.r_dtype, r, "dx"), p(dw, F32, cfg.d, "dw"), _stream(stream)))
+    dev = _begin()
+    t, r, w, _, d, _, nr, ny, _ = cfg.extents or _norm_extents(cfg)
+    _call("atlas_norm_backward",
+          (_arg(h, r, nr, "h", dev), _arg(weight, w, d, "weight", dev), _arg(dy, t, ny, "dy", dev),
+           _arg(dh, r, nr, "dh", dev), cfg, _arg(dx, r, nr, "dx", dev), _arg(dw, F32, d, "dw", dev)), stream, dev)
 
 
 # ------------------------------------------------------------------ conv
 
-def _conv_y(cfg):
-    hd = cfg.head_dim
-    if not hd:
-        return _tokens(cfg, cfg.y_batch_stride, cfg.y_token_stride, cfg.C)
-    if cfg.L < 1 or cfg.B < 1:
-        return 0
-    if not (cfg.y_batch_stride or cfg.y_token_stride or cfg.y_head_stride):
-        return (1 if cfg.seq_start else cfg.B) * cfg.L * cfg.C
-    return ((0 if cfg.seq_start else (cfg.B - 1) * cfg.y_batch_stride)
-            + (cfg.C // hd - 1) * cfg.y_head_stride + (cfg.L - 1) * cfg.y_token_stride + hd)
+def _conv_extents(c):
+    hd, C, n = c.head_dim, c.C, c.n_slots if c.slot else c.B
+    if c.L < 1 or c.B < 1:
+        ny = 0
+    elif not hd:
+        ny = _tokens(c, c.y_batch_stride, c.y_token_stride, C)
+    elif not (c.y_batch_stride or c.y_token_stride or c.y_head_stride):
+        ny = (1 if c.seq_start else c.B) * c.L * C
+    else:
+        ny = ((0 if c.seq_start else (c.B - 1) * c.y_batch_stride) + (C // hd - 1) * c.y_head_stride
+              + (c.L - 1) * c.y_token_stride + hd)
+    c.extents = e = (c.dtype, c.w_dtype, C, C * c.W, _tokens(c, c.x_batch_stride, c.x_token_stride, C), ny,
+                     n * (c.W - 1) * C, c.B * (c.W - 1) * C)
+    return e
 
 
 def atlas_conv_forward(x, weight, bias, cfg: AtlasConvCfg, y, state_in=None, state_out=None,
                        stream=None) -> None:
     """Short causal convolution of every channel; L = 1 is the single-token form.  state_in
     and state_out ([B or n_slots, W - 1, C]) may be None or the same tensor."""
-    p = _Args()
-    C, W, t = cfg.C, cfg.W, cfg.dtype
-    n = (cfg.n_slots if cfg.slot else cfg.B) * (W - 1) * C
-    _raise(_lib().atlas_conv_forward(
-        p(x, t, _tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, C), "x"),
-        p(weight, cfg.w_dtype, C * W, "weight"), p(bias, cfg.w_dtype, C, "bias"), cfg,
-        p(y, t, _conv_y(cfg), "y"), p(state_in, t, n, "state_in"), p(state_out, t, n, "state_out"),
-        _stream(stream)))
+    dev = _begin()
+    t, w, C, nw, nx, ny, n, _ = cfg.extents or _conv_extents(cfg)
+    _call("atlas_conv_forward",
+          (_arg(x, t, nx, "x", dev), _arg(weight, w, nw, "weight", dev), _arg(bias, w, C, "bias", dev), cfg,
+           _arg(y, t, ny, "y", dev), _arg(state_in, t, n, "state_in", dev), _arg(state_out, t, n, "state_out", dev)),
+          stream, dev)
 
 
 def atlas_conv_backward_workspace_bytes(cfg: AtlasConvCfg) -> int:
@@ -283,17 +298,26 @@ def atlas_conv_backward(x, weight, bias, cfg: AtlasConvCfg, state_in, dy, dstate
                         stream=None) -> None:
     """Gradients of the convolution (see include/atlas_ops.h); dstate is dL/d state_out on
     entry and dL/d state_in on return."""
-    p = _Args()
-    C, W, t = cfg.C, cfg.W, cfg.dtype
-    n, nx = cfg.B * (W - 1) * C, _tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, C)
-    _raise(_lib().atlas_conv_backward(
-        p(x, t, nx, "x"), p(weight, cfg.w_dtype, C * W, "weight"), p(bias, cfg.w_dtype, C, "bias"),
-        cfg, p(state_in, t, n, "state_in"), p(dy, t, _conv_y(cfg), "dy"),
-        p(dstate, F32, n, "dstate"), p(dx, t, nx, "dx"), p(dw, F32, C * W, "dw"),
-        p(dbias, F32, C, "dbias"), _stream(stream)))
+    dev = _begin()
+    t, w, C, nw, nx, ny, _, n = cfg.extents or _conv_extents(cfg)
+    _call("atlas_conv_backward",
+          (_arg(x, t, nx, "x", dev), _arg(weight, w, nw, "weight", dev), _arg(bias, w, C, "bias", dev), cfg,
+           _arg(state_in, t, n, "state_in", dev), _arg(dy, t, ny, "dy", dev), _arg(dstate, F32, n, "dstate", dev),
+           _arg(dx, t, nx, "dx", dev), _arg(dw, F32, nw, "dw", dev), _arg(dbias, F32, C, "dbias", dev)), stream, dev)
 
 
 # ------------------------------------------------------------------ scan
+
+def _scan_extents(c):
+    D, gn, dn = c.D, c.G * c.N, c.D * c.N
+    c.extents = e = (c.dtype, D, dn, _tokens(c, c.x_batch_stride, c.x_token_stride, D),
+                     _tokens(c, c.dt_batch_stride, c.dt_token_stride, D),
+                     _tokens(c, c.b_batch_stride, c.b_token_stride, gn),
+                     _tokens(c, c.c_batch_stride, c.c_token_stride, gn),
+                     _tokens(c, c.z_batch_stride, c.z_token_stride, D),
+                     _tokens(c, c.y_batch_stride, c.y_token_stride, D), (c.n_slots if c.slot else c.B) * dn, c.B * dn)
+    return e
+
 
 def atlas_scan_workspace_bytes(cfg: AtlasScanCfg) -> int:
     return _bytes("atlas_scan_workspace_bytes", cfg)
@@ -303,40 +327,29 @@ def atlas_scan_backward_workspace_bytes(cfg: AtlasScanCfg) -> int:
     return _bytes("atlas_scan_backward_workspace_bytes", cfg)
 
 
-def _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg):
-    t, D, gn = cfg.dtype, cfg.D, cfg.G * cfg.N
-    n = (_tokens(cfg, cfg.x_batch_stride, cfg.x_token_stride, D),
-         _tokens(cfg, cfg.dt_batch_stride, cfg.dt_token_stride, D),
-         _tokens(cfg, cfg.b_batch_stride, cfg.b_token_stride, gn),
-         _tokens(cfg, cfg.c_batch_stride, cfg.c_token_stride, gn),
-         _tokens(cfg, cfg.z_batch_stride, cfg.z_token_stride, D),
-         _tokens(cfg, cfg.y_batch_stride, cfg.y_token_stride, D))
-    return n, (p(x, t, n[0], "x"), p(dt, t, n[1], "dt"), p(A, F32, D * cfg.N, "A"),
-               p(Bm, t, n[2], "B"), p(Cm, t, n[3], "C"), p(Dskip, F32, D, "Dskip"),
-               p(z, t, n[4], "z"), p(dt_bias, F32, D, "dt_bias"))
-
-
 def atlas_scan_forward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, y, h_in=None,
                        h_out=None, stream=None) -> None:
     """Selective scan; L = 1 is the single-token form.  Dskip, z, dt_bias, h_in and h_out
     may be None; h_in and h_out ([B or n_slots, D, N]) may be the same tensor."""
-    p = _Args()
-    n, inputs = _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg)
-    s = (cfg.n_slots if cfg.slot else cfg.B) * cfg.D * cfg.N
-    _raise(_lib().atlas_scan_forward(*inputs, cfg, p(y, cfg.dtype, n[5], "y"),
-                                     p(h_in, F32, s, "h_in"), p(h_out, F32, s, "h_out"),
-                                     _stream(stream)))
+    dev = _begin()
+    t, D, dn, nx, nt, nb, nc, nz, ny, n, _ = cfg.extents or _scan_extents(cfg)
+    _call("atlas_scan_forward",
+          (_arg(x, t, nx, "x", dev), _arg(dt, t, nt, "dt", dev), _arg(A, F32, dn, "A", dev), _arg(Bm, t, nb, "B", dev),
+           _arg(Cm, t, nc, "C", dev), _arg(Dskip, F32, D, "Dskip", dev), _arg(z, t, nz, "z", dev),
+           _arg(dt_bias, F32, D, "dt_bias", dev), cfg, _arg(y, t, ny, "y", dev), _arg(h_in, F32, n, "h_in", dev),
+           _arg(h_out, F32, n, "h_out", dev)), stream, dev)
 
 
 def atlas_scan_backward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, h_in, dy, dh, dx,
                         ddt, dA, dB, dC, dD, dz, ddt_bias, stream=None) -> None:
     """Gradients of the scan (see include/atlas_ops.h); dh is dL/d h_out on entry and
     dL/d h_in on return."""
-    p = _Args()
-    n, inputs = _scan_inputs(p, x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg)
-    t, D, s = cfg.dtype, cfg.D, cfg.B * cfg.D * cfg.N
-    _raise(_lib().atlas_scan_backward(
-        *inputs, cfg, p(h_in, F32, s, "h_in"), p(dy, t, n[5], "dy"), p(dh, F32, s, "dh"),
-        p(dx, t, n[0], "dx"), p(ddt, t, n[1], "ddt"), p(dA, F32, D * cfg.N, "dA"),
-        p(dB, t, n[2], "dB"), p(dC, t, n[3], "dC"), p(dD, F32, D, "dD"), p(dz, t, n[4], "dz"),
-        p(ddt_bias, F32, D, "ddt_bias"), _stream(stream)))
+    dev = _begin()
+    t, D, dn, nx, nt, nb, nc, nz, ny, _, n = cfg.extents or _scan_extents(cfg)
+    _call("atlas_scan_backward",
+          (_arg(x, t, nx, "x", dev), _arg(dt, t, nt, "dt", dev), _arg(A, F32, dn, "A", dev), _arg(Bm, t, nb, "B", dev),
+           _arg(Cm, t, nc, "C", dev), _arg(Dskip, F32, D, "Dskip", dev), _arg(z, t, nz, "z", dev),
+           _arg(dt_bias, F32, D, "dt_bias", dev), cfg, _arg(h_in, F32, n, "h_in", dev), _arg(dy, t, ny, "dy", dev),
+           _arg(dh, F32, n, "dh", dev), _arg(dx, t, nx, "dx", dev), _arg(ddt, t, nt, "ddt", dev),
+           _arg(dA, F32, dn, "dA", dev), _arg(dB, t, nb, "dB", dev), _arg(dC, t, nc, "dC", dev),
+           _arg(dD, F32, D, "dD", dev), _arg(dz, t, nz, "dz", dev), _arg(ddt_bias, F32, D, "ddt_bias", dev)), stream, dev)
