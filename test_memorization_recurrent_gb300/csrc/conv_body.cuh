@@ -400,8 +400,9 @@ inline long lane_groups(const ConvArgs& a, int V) { return (a.C + kLanes * V - 1
 // Tokens per tile: as many tiles as warps fit (24 an SM at up to four taps), so that all run
 // at once and few tokens are read twice; at least 16, so that one tile alone touches the state.
 inline int tile_tokens(const ConvArgs& a, int V) {
-  const long n = 152 * 24 / lane_groups(a, V);
-  const long each = a.s.start ? n : n / (a.s.B < 1 ? 1 : a.s.B);  // tiles a sequence (packed: in all)
+  const long n = 152 * 24 / lane_groups(a, V) / kWarps * kWarps;
+  // tiles a sequence; packed: in all, with one more for the end of each sequence
+  const long each = a.s.start ? n - a.s.B : n / (a.s.B < 1 ? 1 : a.s.B);
   const long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
   return (int)(TT < 16 ? 16 : TT);
 }
@@ -414,7 +415,7 @@ inline long back_workers(const ConvArgs& a, int V) {
 }
 inline int back_tile_tokens(const ConvArgs& a, int V) {
   const long n = back_workers(a, V);
-  const long each = a.s.start ? n : n / (a.s.B < 1 ? 1 : a.s.B);  // tiles a sequence (packed: in all)
+  const long each = a.s.start ? n - a.s.B : n / (a.s.B < 1 ? 1 : a.s.B);
   long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
   return (int)(TT < 16 ? 16 : TT);
 }

@@ -15,8 +15,8 @@
 //
 // When sequences times channels do not fill the machine, the tokens are split into
 // segments: a first pass finds each segment's end state from a zero start (with the sum of
-// its dt: the decay over a segment is exp(A sum dt)), a second one joins them into start
-// states, the third computes the outputs.
+// its dt: the decay over a segment is exp(A sum dt)); the second computes the outputs, each
+// segment from the start state that it joins from those in front of it.
 #pragma once
 #include "ops_common.cuh"
 
@@ -145,10 +145,11 @@ __device__ __forceinline__ int turned(int u, int p) {
   return V > 2 ? p ^ (u & (V / 2 - 1)) : p;
 }
 
-// What a walk over a segment is for: kOut, its outputs; kEnds, its end state from a zero
+// What a walk over a segment is for: kOut, its outputs (kJoin: with several segments a sequence,
+// a kernel of its own, whose start would cost kOut's loop registers); kEnds, its end state from a zero
 // start; kKeep, for the backward pass: the state in front of every kSub tokens too, and what
 // the segment's own tokens add to the adjoint in front of it.
-enum Mode { kOut, kEnds, kKeep };
+enum Mode { kOut, kEnds, kKeep, kJoin };
 constexpr int kSub = 8;
 
 // Shared memory of segment_kernel.
@@ -173,7 +174,7 @@ struct SegmentShared {
   int swap;
 };
 
-// Where the segments' states go: seg_h and seg_dt of kEnds and kKeep (kOut reads seg_h), the
+// Where the segments' states go: h and dt of kEnds and kKeep (kJoin reads them), the
 // rest of kKeep.
 struct Segments {
   int S;                          // tokens of a segment
@@ -182,12 +183,13 @@ struct Segments {
   int nsub;
 };
 
-// kOut starts from seg.h (or, with one segment a sequence, from the sequence's state).  kEnds
-// leaves a sequence's last segment out.  kKeep with seg.h starts from zeros, else from the
+// kOut starts from the sequence's state, kJoin from the segments in front, seg.h.  kEnds starts a sequence's first segment from its state, which the last
+// segment's place receives too (kJoin may be overwriting it with the final one), and leaves the
+// last segment out.  kKeep with seg.h starts from zeros, else from the
 // sequence's state, and then leaves the adjoint out.  NV: B and C are copied in vectors too.
 template <typename T, int V, int LN, Mode MODE, bool NV>
 __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Segments sg) {
-  constexpr bool ENDS = MODE == kEnds, KEEP = MODE == kKeep, OUT = MODE == kOut;
+  constexpr bool ENDS = MODE == kEnds, KEEP = MODE == kKeep, JOIN = MODE == kJoin, OUT = MODE == kOut || JOIN;
   using P = Shape<LN>;
   using X = Tile<T, V, P::kCB>;
   constexpr int VN = !NV ? 1 : 16 / sizeof(T) < P::kNP ? 16 / sizeof(T) : P::kNP;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
   SeqTile t;
   if (!seq_tile(a.s, seg, sg.S, t)) return;
   const int end = min(t.t0 + sg.S, t.len);
-  if (ENDS && end == t.len) return;
+  if (ENDS && end == t.len) return;  // (the last segment, or the only one)
   const Channels k = channels_at<P::kCB>(a, blockIdx.y);
   const int tiles = (end - t.t0 + kTile - 1) / kTile;
   const int lane = threadIdx.x & 31;
@@ -373,10 +375,37 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
     for (int j = 0; j < 4; ++j) h4[j] = 0.f;
     if (2 * cp + i < k.n) {
       ld_states4(a.A + (long)c * a.N, n0, a.N, A4);
-      if (OUT && sg.h)
-        ld_states4(sg.h + (seg * a.D + c) * a.N, n0, a.N, h4);
-      else if (!ENDS && !sg.h && a.h_in && t.carry)
+      const long first = seg - t.t0 / sg.S, last = first + seq_tiles_of(t.len, sg.S) - 1;
+      if (JOIN && last > first) {
+        // the sequence's state, then the segments in front, four under way at a time
+        if (seg == first) {
+          ld_states4(sg.h + (last * a.D + c) * a.N, n0, a.N, h4);
+        } else {
+#pragma unroll 1
+          for (long q0 = first; q0 < seg; q0 += 4) {
+            float own[4][4], d[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              d[q] = 0.f;
+              own[q][0] = own[q][1] = own[q][2] = own[q][3] = 0.f;
+              if (q0 + q < seg) {
+                ld_states4(sg.h + ((q0 + q) * a.D + c) * a.N, n0, a.N, own[q]);
+                d[q] = sg.dt[(q0 + q) * a.D + c];
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                h4[j] = ex2(A4[j] * ATLAS_LOG2E * d[q]) * h4[j] + own[q][j];
+          }
+        }
+      } else if (!KEEP && (!ENDS || seg == first) && a.h_in && t.carry) {
         ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
+      } else if (KEEP && !sg.h && a.h_in && t.carry) {
+        ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h4);
+      }
+      if (ENDS && seg == first) st_states4(sg.h + (last * a.D + c) * a.N, n0, a.N, h4);
     }
     A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
     A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
@@ -492,78 +521,69 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
   }
 }
 
-// Joins the segments of each sequence: seg_h becomes the state each segment starts from.
-// One thread per (sequence, channel, state).
-static __global__ void __launch_bounds__(256)
-    join_kernel(ScanArgs a, int S, float* seg_h, const float* seg_dt) {
-  const long dn = (long)a.D * a.N;
-  const int b = blockIdx.y;
-  const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  long seg;
-  if (a.s.start) {
-    const int s = a.s.start[b], e = a.s.start[b + 1];
-    if (s < 0 || e < s || e > a.s.L) return;
-    seg = (long)s / S + b;
-  } else {
-    seg = (long)b * seq_tiles_of(a.s.L, S);
-  }
-  SeqTile t;
-  if (!seq_tile(a.s, seg, S, t) || i >= dn) return;
-  const int c = (int)(i / a.N);
-  const float A2 = a.A[i] * ATLAS_LOG2E;
-  float h = a.h_in && t.carry ? a.h_in[(long)t.slot * dn + i] : 0.f;
-  const int n = seq_tiles_of(t.len, S);
-  constexpr int U = 8;  // segments whose values are under way at a time
-  for (int k0 = 0; k0 < n; k0 += U) {
-    float own[U], d[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      own[j] = k0 + j + 1 < n ? seg_h[(seg + k0 + j) * dn + i] : 0.f;
-      d[j] = k0 + j + 1 < n ? seg_dt[(seg + k0 + j) * a.D + c] : 0.f;
-    }
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (k0 + j < n) seg_h[(seg + k0 + j) * dn + i] = h;
-      h = ex2(A2 * d[j]) * h + own[j];
-    }
-  }
-}
-
-// One token a sequence: every lane takes four states of a channel, loads and stores them
-// once.  Bound by the state's traffic.
-constexpr int kTokenThreads = 128;
+// One token a sequence: a lane takes four states of kTokenU channels, loads and stores them
+// once.  Bound by the state's traffic, and for few sequences by latency: what does not depend
+// on the sequence's slot is under way before the slot is looked up.
+constexpr int kTokenThreads = 128, kTokenU = 2;
 template <typename T, int LN>
 __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
-  SeqTile t;
+  constexpr int CB = kTokenThreads / LN;  // channels of a block at a time
   const int b = blockIdx.x;
-  if (!seq_tile(a.s, b, 1, t)) return;
   const int lane = threadIdx.x & 31, nl = lane % LN, n0 = nl * 4;
-  const int c = (blockIdx.y * kTokenThreads + (int)threadIdx.x) / LN;
-  const bool live = c < a.D;
-  float y = 0.f, x = 0.f;
-  if (live) {
-    float A[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-    ld_states4(a.A + (long)c * a.N, n0, a.N, A);
-    if (a.h_in && t.carry) ld_states4(a.h_in + ((long)t.slot * a.D + c) * a.N, n0, a.N, h);
-    x = to_f(reinterpret_cast<const T*>(a.x)[b * a.xb + c]);
-    float d = to_f(reinterpret_cast<const T*>(a.dt)[b * a.tb + c]) + (a.bias ? a.bias[c] : 0.f);
-    if (a.softplus) d = softplusf(d);
-    const long g = (long)(c / (a.D / a.G)) * a.N;
-    const T* B = reinterpret_cast<const T*>(a.Bm) + b * a.bb + g;
-    const T* C = reinterpret_cast<const T*>(a.Cm) + b * a.cb + g;
+  const int c0 = blockIdx.y * kTokenU * CB + (int)threadIdx.x / LN;
+  float A[kTokenU][4], h[kTokenU][4], B[kTokenU][4], C[kTokenU][4];
+  float x[kTokenU], d[kTokenU], z[kTokenU], skip[kTokenU];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < a.N) {
-        h[i] = ex2(d * (A[i] * ATLAS_LOG2E)) * h[i] + d * x * to_f(B[n0 + i]);
-        y += h[i] * to_f(C[n0 + i]);
+  for (int i = 0; i < kTokenU; ++i) {
+    const int c = c0 + i * CB;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A[i][j] = h[i][j] = B[i][j] = C[i][j] = 0.f;
+    x[i] = d[i] = z[i] = skip[i] = 0.f;
+    if (c >= a.D) continue;
+    ld_states4(a.A + (long)c * a.N, n0, a.N, A[i]);
+    x[i] = to_f(reinterpret_cast<const T*>(a.x)[b * a.xb + c]);
+    d[i] = to_f(reinterpret_cast<const T*>(a.dt)[b * a.tb + c]) + (a.bias ? a.bias[c] : 0.f);
+    if (a.z) z[i] = to_f(reinterpret_cast<const T*>(a.z)[b * a.zb + c]);
+    if (a.Dk) skip[i] = a.Dk[c];
+    const long g = (long)(c / (a.D / a.G)) * a.N;
+    const T* pB = reinterpret_cast<const T*>(a.Bm) + b * a.bb + g;
+    const T* pC = reinterpret_cast<const T*>(a.Cm) + b * a.cb + g;
+    if (a.wide_n) {
+      if (n0 < a.N) {
+        ld_pack<T, 4>(pB + n0).unpack(B[i]);
+        ld_pack<T, 4>(pC + n0).unpack(C[i]);
       }
-    if (a.h_out) st_states4(a.h_out + ((long)t.slot * a.D + c) * a.N, n0, a.N, h);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n0 + j < a.N) B[i][j] = to_f(pB[n0 + j]), C[i][j] = to_f(pC[n0 + j]);
+    }
   }
-  lane_sums<1, LN, 1>(&y, lane);
-  if (live && nl == 0) {
-    if (a.Dk) y += a.Dk[c] * x;
-    if (a.z) y *= siluf(to_f(reinterpret_cast<const T*>(a.z)[b * a.zb + c]));
-    reinterpret_cast<T*>(a.y)[b * a.yb + c] = from_f<T>(y);
+  SeqTile t;
+  if (!seq_tile(a.s, b, 1, t)) return;
+  if (a.h_in && t.carry) {
+#pragma unroll
+    for (int i = 0; i < kTokenU; ++i)
+      if (c0 + i * CB < a.D) ld_states4(a.h_in + ((long)t.slot * a.D + c0 + i * CB) * a.N, n0, a.N, h[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kTokenU; ++i) {
+    const int c = c0 + i * CB;
+    const float dt = a.softplus ? softplusf(d[i]) : d[i];
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[i][j] = ex2(dt * (A[i][j] * ATLAS_LOG2E)) * h[i][j] + dt * x[i] * B[i][j];
+      y += h[i][j] * C[i][j];
+    }
+    lane_sums<1, LN, 1>(&y, lane);
+    if (c >= a.D) continue;
+    if (a.h_out) st_states4(a.h_out + ((long)t.slot * a.D + c) * a.N, n0, a.N, h[i]);
+    if (nl == 0) {
+      y += skip[i] * x[i];
+      if (a.z) y *= siluf(z[i]);
+      reinterpret_cast<T*>(a.y)[b * a.yb + c] = from_f<T>(y);
+    }
   }
 }
 
@@ -609,7 +629,7 @@ int forward(const ScanArgs& a, cudaStream_t st) {
   const int by = blocks_over<Shape<LN>::kCB>(a);
   if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
   if (!a.s.start && a.s.L == 1) {
-    const long rows = ((long)a.D * LN + kTokenThreads - 1) / kTokenThreads;
+    const long rows = ((long)a.D * LN + kTokenThreads * kTokenU - 1) / (kTokenThreads * kTokenU);
     if (rows > 65535) return ATLAS_ERR_UNSUPPORTED;
     token_kernel<T, LN><<<dim3(a.s.B, (unsigned)rows), kTokenThreads, 0, st>>>(a);
     return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
@@ -619,13 +639,12 @@ int forward(const ScanArgs& a, cudaStream_t st) {
   if (sg.S) {
     sg.h = reinterpret_cast<float*>(a.ws);
     sg.dt = sg.h + (size_t)seq_tiles(a.s, sg.S) * a.D * a.N;
-    if (!segment_pass<T, V, LN, kEnds>(a, sg, st)) return ATLAS_ERR_CUDA;
-    const long dn = (long)a.D * a.N;
-    join_kernel<<<dim3((unsigned)((dn + 255) / 256), a.s.B), 256, 0, st>>>(a, sg.S, sg.h, sg.dt);
+    if (!segment_pass<T, V, LN, kEnds>(a, sg, st) || !segment_pass<T, V, LN, kJoin>(a, sg, st))
+      return ATLAS_ERR_CUDA;
   } else {
     sg.S = a.s.L > 0 ? a.s.L : 1;
+    if (!segment_pass<T, V, LN, kOut>(a, sg, st)) return ATLAS_ERR_CUDA;
   }
-  if (!segment_pass<T, V, LN, kOut>(a, sg, st)) return ATLAS_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 

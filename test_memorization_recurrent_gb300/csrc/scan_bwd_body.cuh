@@ -34,9 +34,6 @@ inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
   const long want = 152 * 2 * 6;
   const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
   long S = rows * blocks_per_seq / want / kTile * kTile;
-#ifdef BS
-  S = BS;
-#endif
   if (S < 128) S = 128;
   if (S >= a.s.L) return 0;
   return (int)S;
@@ -562,6 +559,7 @@ __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int
       const long r = i / (2 * NP) / a.G;
       if (q % NP >= a.N || r < lo || r >= hi) continue;
       float s = 0.f;
+#pragma unroll 8
       for (int k = 0; k < bpg; ++k)
         s += w.pbc[((long)(g * bpg + k) * w.rows + r) * 2 * NP + q];
       const bool isC = q >= NP;
@@ -577,6 +575,7 @@ __global__ void __launch_bounds__(256) finish_kernel(ScanArgs a, Back<LN> w, int
     const float* p = i < dn ? w.pA + i : i < dn + a.D ? w.pD + (i - dn) : w.pb + (i - dn - a.D);
     const long step = i < dn ? dn : a.D;
     float s = 0.f;
+#pragma unroll 8
     for (long k = 0; k < w.segs; ++k) s += p[k * step];
     if (i < dn)
       a.dA[i] = s;
