@@ -4,7 +4,8 @@ Like the binding of the memory update it only marshals: ``make_*_cfg`` fills a C
 description, the calls turn torch tensors into device pointers, enqueue on a stream and
 raise ``AtlasError`` on a non-zero status.  Tensor arguments are checked before the call:
 an element type other than the description's, a tensor that is not on the current CUDA
-device, or one that ends before the elements the description names raises
+device, one that ends before the elements the description names, or one that is not
+contiguous where the description has no strides of its own for it, raises
 ``AtlasError(ERR_INVALID)``.  Raw device pointers (ints) are passed on as they are.
 """
 from __future__ import annotations
@@ -89,7 +90,7 @@ def make_norm_cfg(rows, d, dtype=BF16, r_dtype=None, w_dtype=None, out_dtype=Non
         return int(dtype if t is None else t)
     cfg = AtlasNormCfg(int(rows), int(d), int(dtype), or_dtype(r_dtype), or_dtype(w_dtype),
                        or_dtype(out_dtype), int(group), float(eps), int(x_stride), int(r_stride),
-                       int(y_stride), _addr(workspace), int(workspace_bytes))
+                       int(y_stride), _space(workspace, workspace_bytes), int(workspace_bytes))
     cfg.held = workspace
     return cfg
 
@@ -105,7 +106,7 @@ def make_conv_cfg(B, L, C, W, act=ACT_SILU, dtype=BF16, w_dtype=None, head_dim=0
     cfg = AtlasConvCfg(int(B), int(L), int(C), int(W), int(act), int(dtype),
                        int(dtype if w_dtype is None else w_dtype), int(head_dim), int(xb), int(xt),
                        int(yb), int(yt), int(yh), *_sequences(B, seq_start, slot, n_slots, carry),
-                       _checked(status_dev, "int32", 1, "status_dev"), _addr(workspace),
+                       _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
                        int(workspace_bytes))
     cfg.held = (seq_start, slot, carry, status_dev, workspace)  # as long as the description
     return cfg
@@ -121,7 +122,7 @@ def make_scan_cfg(B, L, D, N, G=1, dtype=BF16, softplus=True, x_strides=(0, 0),
          for v in p]
     cfg = AtlasScanCfg(int(B), int(L), int(D), int(N), int(G), int(dtype), int(bool(softplus)),
                        *s, *_sequences(B, seq_start, slot, n_slots, carry),
-                       _checked(status_dev, "int32", 1, "status_dev"), _addr(workspace),
+                       _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
                        int(workspace_bytes))
     cfg.held = (seq_start, slot, carry, status_dev, workspace)
     return cfg
@@ -134,8 +135,13 @@ def _error(msg):
     return AtlasError(ERR_INVALID, msg)
 
 
-def _addr(t):
-    return None if t is None else t if isinstance(t, int) else t.data_ptr()
+def _space(t, nbytes):
+    """Address of a workspace tensor that holds nbytes."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise _error(f"workspace must be a contiguous CUDA tensor of at least {nbytes} bytes")
+    return t.data_ptr()
 
 
 def _checked(t, dtype, n, name):
@@ -179,17 +185,23 @@ def _begin():
 
 
 def _arg(t, code, extent, name, device):
-    """Address of one argument (a tensor, an address or None) after its checks; extent:
-    elements from the first to the last one that the description names."""
+    """Address of one argument (a tensor, an address or None) after its checks.  extent: twice
+    the elements from the first to the last one that the description names, plus one where
+    they have to be contiguous."""
     if t is None or type(t) is int:
         return t
     if t.dtype is not _types[code]:
         raise _error(f"{name} is {t.dtype}, the description says {_types[code]}")
     if t.get_device() != device:
         raise _error(f"{name} is not on the current device (cuda:{device})")
-    if t.numel() < extent:  # a strided view ends further on than its elements count
-        if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent:
-            raise _error(f"{name} ends before the {extent} elements the description names")
+    if extent & 1:
+        if not t.is_contiguous():
+            raise _error(f"{name} is not contiguous")
+        if t.numel() < extent >> 1:
+            raise _error(f"{name} has fewer than the {extent >> 1} elements the description names")
+    elif t.numel() < extent >> 1:  # a strided view ends further on than its elements count
+        if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent >> 1:
+            raise _error(f"{name} ends before the {extent >> 1} elements the description names")
     return t.data_ptr()
 
 
@@ -212,25 +224,31 @@ def _bytes(fn, cfg):
     return n
 
 
+def _dense(n):
+    return 2 * n + 1
+
+
 def _tokens(cfg, sb, st, width):
-    """Elements from the first to the last one of a [B, L, width] tensor (packed: [L, width])."""
+    """Extent of a [B, L, width] tensor (packed: [L, width])."""
     if cfg.L < 1 or cfg.B < 1:
         return 0
     if not sb and not st:
-        return (1 if cfg.seq_start else cfg.B) * cfg.L * width
-    return (0 if cfg.seq_start else (cfg.B - 1) * sb) + (cfg.L - 1) * st + width
+        return _dense((1 if cfg.seq_start else cfg.B) * cfg.L * width)
+    return 2 * ((0 if cfg.seq_start else (cfg.B - 1) * sb) + (cfg.L - 1) * st + width)
 
 
 def _rows(cfg, stride):
-    return (cfg.rows - 1) * (stride or cfg.d) + cfg.d if cfg.rows > 0 else 0
+    if cfg.rows < 1:
+        return 0
+    return 2 * ((cfg.rows - 1) * stride + cfg.d) if stride else _dense(cfg.rows * cfg.d)
 
 
 # ------------------------------------------------------------------ norm
 
 def _norm_extents(c):
     groups = 1 if c.group <= 0 or c.group >= c.d else -(-c.d // c.group)
-    c.extents = e = (c.dtype, c.r_dtype, c.w_dtype, c.out_dtype, c.d, _rows(c, c.x_stride), _rows(c, c.r_stride),
-                     _rows(c, c.y_stride), c.rows * groups)
+    c.extents = e = (c.dtype, c.r_dtype, c.w_dtype, c.out_dtype, _dense(c.d), _rows(c, c.x_stride), _rows(c, c.r_stride),
+                     _rows(c, c.y_stride), _dense(c.rows * groups))
     return e
 
 
@@ -269,12 +287,12 @@ def _conv_extents(c):
     elif not hd:
         ny = _tokens(c, c.y_batch_stride, c.y_token_stride, C)
     elif not (c.y_batch_stride or c.y_token_stride or c.y_head_stride):
-        ny = (1 if c.seq_start else c.B) * c.L * C
+        ny = _dense((1 if c.seq_start else c.B) * c.L * C)
     else:
-        ny = ((0 if c.seq_start else (c.B - 1) * c.y_batch_stride) + (C // hd - 1) * c.y_head_stride
-              + (c.L - 1) * c.y_token_stride + hd)
-    c.extents = e = (c.dtype, c.w_dtype, C, C * c.W, _tokens(c, c.x_batch_stride, c.x_token_stride, C), ny,
-                     n * (c.W - 1) * C, c.B * (c.W - 1) * C)
+        ny = 2 * ((0 if c.seq_start else (c.B - 1) * c.y_batch_stride) + (C // hd - 1) * c.y_head_stride
+                  + (c.L - 1) * c.y_token_stride + hd)
+    c.extents = e = (c.dtype, c.w_dtype, _dense(C), _dense(C * c.W), _tokens(c, c.x_batch_stride, c.x_token_stride, C),
+                     ny, _dense(n * (c.W - 1) * C), _dense(c.B * (c.W - 1) * C))
     return e
 
 
@@ -310,12 +328,13 @@ def atlas_conv_backward(x, weight, bias, cfg: AtlasConvCfg, state_in, dy, dstate
 
 def _scan_extents(c):
     D, gn, dn = c.D, c.G * c.N, c.D * c.N
-    c.extents = e = (c.dtype, D, dn, _tokens(c, c.x_batch_stride, c.x_token_stride, D),
+    c.extents = e = (c.dtype, _dense(D), _dense(dn), _tokens(c, c.x_batch_stride, c.x_token_stride, D),
                      _tokens(c, c.dt_batch_stride, c.dt_token_stride, D),
                      _tokens(c, c.b_batch_stride, c.b_token_stride, gn),
                      _tokens(c, c.c_batch_stride, c.c_token_stride, gn),
                      _tokens(c, c.z_batch_stride, c.z_token_stride, D),
-                     _tokens(c, c.y_batch_stride, c.y_token_stride, D), (c.n_slots if c.slot else c.B) * dn, c.B * dn)
+                     _tokens(c, c.y_batch_stride, c.y_token_stride, D), _dense((c.n_slots if c.slot else c.B) * dn),
+                     _dense(c.B * dn))
     return e
 
 

@@ -691,6 +691,42 @@ def test_conv_rows_past_32_bits():
     assert torch.equal(y[:, -20:], one) and torch.equal(s, s1) and not y[0, :-20:997].any()
 
 
+def test_scan_rows_past_32_bits():
+    """More than 2^32 elements in one sequence of many segments: zeros up to the last 20 tokens,
+    which are as they are alone."""
+    D, N = 2048, 4
+    L = (1 << 32) // D + 21
+    r = rng(22)
+    d = Scan(r, 1, 20, D, N, 1, "bf16", gate=False)
+    big = [torch.zeros(1, L, *t.shape[2:], dtype=t.dtype, device="cuda") for t in (d.x, d.dt, d.Bm, d.Cm)]
+    for t, s in zip(big, (d.x, d.dt, d.Bm, d.Cm)):
+        t[:, -20:] = s
+    y, h, one, h1 = torch.empty_like(big[0]), torch.empty(1, D, N, device="cuda"), torch.empty_like(d.x), torch.empty(1, D, N, device="cuda")
+    for x, dt, Bm, Cm, n, out, state in ((*big, L, y, h), (d.x, d.dt, d.Bm, d.Cm, 20, one, h1)):
+        cfg = A.make_scan_cfg(1, n, D, N)
+        space(cfg, A.atlas_scan_workspace_bytes(cfg))
+        A.atlas_scan_forward(x, dt, d.A, Bm, Cm, d.Dk, None, d.bias, cfg, out, None, state)
+        torch.cuda.synchronize()
+    assert torch.equal(y[:, -20:], one) and torch.equal(h, h1) and not y[0, :-20:997].any()
+
+
+def test_arguments_that_have_to_be_contiguous():
+    """A transposed weight, state or default-stride input has the right number of elements in the
+    wrong order."""
+    x, w = torch.zeros(2, 16, 8, device="cuda"), torch.zeros(4, 8, device="cuda").t()
+    cfg, y, st = A.make_conv_cfg(2, 16, 8, 4, dtype=A.F32), torch.zeros(2, 16, 8, device="cuda"), torch.zeros(2, 8, 3, device="cuda").transpose(1, 2)
+    good = w.contiguous()
+    for args in ((x, w, None, cfg, y), (x.transpose(0, 1).contiguous().transpose(0, 1), good, None, cfg, y), (x, good, None, cfg, y, st)):
+        with pytest.raises(A.AtlasError):
+            A.atlas_conv_forward(*args)
+    A.atlas_conv_forward(x, good, None, cfg, y, st.contiguous())
+    with pytest.raises(A.AtlasError):  # a workspace smaller than it is said to be
+        A.make_scan_cfg(1, 4, 8, 4, workspace=torch.zeros(16, device="cuda"), workspace_bytes=65)
+    with pytest.raises(A.AtlasError):  # a dimension changed after the description was used
+        cfg.L = 17
+        A.atlas_conv_forward(x, good, None, cfg, y)
+
+
 # ------------------------------------------------------- a layer around the memory
 
 def test_layer_around_the_memory_update():
