@@ -22,62 +22,6 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr float kAmaxMin = 1e-30f;
 
-// V consecutive elements (1 or 8) of a type known at run time.
-template <int V>
-__device__ __forceinline__ void ld_row(const void* p, long i, int dtype, float* v) {
-  if (V == 1) {
-    v[0] = ld_any(p, i, dtype);
-    return;
-  }
-  if (dtype == ATLAS_F32) {
-    const auto* q = reinterpret_cast<const float*>(p) + i;
-    const auto a = ld_pack<float, 4>(q), b = ld_pack<float, 4>(q + 4);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = a.e[k], v[4 + k] = b.e[k];
-  } else if (dtype == ATLAS_BF16) {
-    const auto a = ld_pack<__nv_bfloat16, 8>(reinterpret_cast<const __nv_bfloat16*>(p) + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = a.get(k);
-  } else {
-    const auto a = ld_pack<__half, 8>(reinterpret_cast<const __half*>(p) + i);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = a.get(k);
-  }
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void st_as(void* p, long i, const float* v) {
-  Pack<T, V> a;
-#pragma unroll
-  for (int k = 0; k < V; ++k) a.set(k, v[k]);
-  st_pack<T, V>(reinterpret_cast<T*>(p) + i, a);
-}
-
-template <int V>
-__device__ __forceinline__ void st_row(void* p, long i, int dtype, const float* v) {
-  if (dtype == ATLAS_F32) {
-    if (V == 1) {
-      reinterpret_cast<float*>(p)[i] = v[0];
-    } else {
-      st_as<float, 4>(p, i, v);
-      st_as<float, 4>(p, i + 4, v + 4);
-    }
-  } else if (dtype == ATLAS_BF16) {
-    st_as<__nv_bfloat16, V>(p, i, v);
-  } else if (dtype == ATLAS_F16) {
-    st_as<__half, V>(p, i, v);
-  } else {  // e4m3, to nearest even; the values are within +-448 by their scale
-    alignas(8) __nv_fp8_storage_t q[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) q[k] = __nv_cvt_float_to_fp8(v[k], __NV_SATFINITE, __NV_E4M3);
-    auto* o = reinterpret_cast<__nv_fp8_storage_t*>(p) + i;
-    if (V == 8)
-      *reinterpret_cast<uint2*>(o) = *reinterpret_cast<const uint2*>(q);
-    else
-      o[0] = q[0];
-  }
-}
-
 // The threads that share a row: TPR lanes of a warp (TPR <= 32), or the whole block.
 struct RowGroup {
   int tpr, lane, tid;  // threads per row, lane within them
@@ -119,99 +63,98 @@ __device__ __forceinline__ void clear_red(float* red, int n) {
   __syncthreads();
 }
 
-template <int V, int K>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArgs a, int tpr) {
-  extern __shared__ __align__(16) float sm[];  // 64 floats, then (8-bit groups that cross lanes) the groups' maxima
+// One element as it lies in memory: BYTES (0: none), so that all of a row's loads can be
+// issued before the first conversion.
+template <int BYTES>
+__device__ __forceinline__ uint32_t ld_raw(const void* p, long i) {
+  if (BYTES == 2) return reinterpret_cast<const uint16_t*>(p)[i];
+  if (BYTES == 4) return reinterpret_cast<const uint32_t*>(p)[i];
+  return 0;
+}
+template <int BYTES>
+__device__ __forceinline__ float raw_float(uint32_t v, int dtype) {
+  if (BYTES == 4) return __uint_as_float(v);
+  if (dtype == ATLAS_BF16) return __uint_as_float(v << 16);
+  return __half2float(__ushort_as_half((unsigned short)v));
+}
+__device__ __forceinline__ void st_elem(void* p, long i, int dtype, float v) {
+  if (dtype == ATLAS_F32)
+    reinterpret_cast<float*>(p)[i] = v;
+  else if (dtype == ATLAS_BF16)
+    reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else if (dtype == ATLAS_F16)
+    reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
+  else  // e4m3, to nearest even; the values are within +-448 by their scale
+    reinterpret_cast<__nv_fp8_storage_t*>(p)[i] = __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// Rows of any width and alignment, K elements a thread.
+template <int XB, int RB, int K>
+__global__ void __launch_bounds__(1024) norm_forward_elem(NormArgs a, int tpr) {
+  extern __shared__ __align__(16) float sm[];  // 64 floats, then the groups' maxima of an 8-bit output
   float* red = sm;
   clear_red(red, 64);
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
   const int rpb = blockDim.x / tpr;
   const long row = (long)blockIdx.x * rpb + threadIdx.x / tpr;
   const bool live = row < a.rows;
-  float h[K][V];
-  float ss = 0.f;
+  uint32_t x[K], r[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * tpr + g.lane) * V;
+    const int c = k * tpr + g.lane;
+    const bool in = live && c < a.d;
+    x[k] = in ? ld_raw<XB>(a.x, row * a.sx + c) : 0u;
+    r[k] = RB && in ? ld_raw<RB>(a.r, row * a.sr + c) : 0u;
+  }
+  float h[K], ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) h[k][j] = 0.f;
-    if (live && c < a.d) {
-      ld_row<V>(a.x, row * a.sx + c, a.dt, h[k]);
-      if (a.r) {
-        float r[V];
-        ld_row<V>(a.r, row * a.sr + c, a.rt, r);
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[k][j] += r[j];
-      }
-      if (a.r_out) st_row<V>(a.r_out, row * a.sr + c, a.rt, h[k]);
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) ss += h[k][j] * h[k][j];
+  for (int k = 0; k < K; ++k) {
+    const int c = k * tpr + g.lane;
+    h[k] = raw_float<XB>(x[k], a.dt) + (RB ? raw_float<RB>(r[k], a.rt) : 0.f);
+    if (a.r_out && live && c < a.d) st_elem(a.r_out, row * a.sr + c, a.rt, h[k]);
+    ss += h[k] * h[k];
   }
   const float rstd = rsqrtf(row_sum(ss, g, red) * a.inv_d + a.eps);
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * tpr + g.lane) * V;
+    const int c = k * tpr + g.lane;
     if (c < a.d) {
-      float w[V];
-      if (a.w) ld_row<V>(a.w, c, a.wt, w);
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        h[k][j] *= rstd;
-        if (a.w) h[k][j] *= w[j];
-        amax = fmaxf(amax, fabsf(h[k][j]));
-      }
-      if (live && a.ot != ATLAS_E4M3) st_row<V>(a.y, row * a.sy + c, a.ot, h[k]);
+      h[k] *= rstd;
+      if (a.w) h[k] *= ld_any(a.w, c, a.wt);
+      amax = fmaxf(amax, fabsf(h[k]));
+      if (live && a.ot != ATLAS_E4M3) st_elem(a.y, row * a.sy + c, a.ot, h[k]);
     }
   }
   if (a.ot != ATLAS_E4M3) return;
   if (a.group == 0) {
-    const float scale = fmaxf(row_max(amax, g, red + 32), kAmaxMin) * (1.f / kE4m3Max);
-    const float inv = 1.f / scale;
+    const float scale = fmaxf(row_max(amax, g, red + 32), kAmaxMin) * (1.f / kE4m3Max), inv = rcp(scale);
     if (live && g.lane == 0) a.scale[row] = scale;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * tpr + g.lane) * V;
-      if (live && c < a.d) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[k][j] *= inv;
-        st_row<V>(a.y, row * a.sy + c, a.ot, h[k]);
-      }
+      const int c = k * tpr + g.lane;
+      if (live && c < a.d) st_elem(a.y, row * a.sy + c, a.ot, h[k] * inv);
     }
     return;
   }
   // groups of channels: maxima of non-negative floats order like their bits, so integer
   // maxima in shared memory give the same result in any order
-  const int ng = (a.d + a.group - 1) / a.group;
+  const int ng = a.ng;
   unsigned* gm = reinterpret_cast<unsigned*>(sm + 64) + (threadIdx.x / tpr) * ng;
   for (int i = g.lane; i < ng; i += tpr) gm[i] = 0u;
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * tpr + g.lane) * V;
-    if (c < a.d) {
-      if (V == 1 || a.group % V == 0) {
-        float m = 0.f;
-#pragma unroll
-        for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(h[k][j]));
-        atomicMax(&gm[c / a.group], __float_as_uint(m));
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          atomicMax(&gm[(c + j) / a.group], __float_as_uint(fmaxf(0.f, fabsf(h[k][j]))));
-      }
-    }
+    const int c = k * tpr + g.lane;
+    if (c < a.d) atomicMax(&gm[c / a.group], __float_as_uint(fmaxf(0.f, fabsf(h[k]))));
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * tpr + g.lane) * V;
+    const int c = k * tpr + g.lane;
     if (live && c < a.d) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        h[k][j] *= 1.f / (fmaxf(__uint_as_float(gm[(c + j) / a.group]), kAmaxMin) * (1.f / kE4m3Max));
-      st_row<V>(a.y, row * a.sy + c, a.ot, h[k]);
+      const float scale = fmaxf(__uint_as_float(gm[c / a.group]), kAmaxMin) * (1.f / kE4m3Max);
+      st_elem(a.y, row * a.sy + c, a.ot, h[k] * rcp(scale));
     }
   }
   if (live)
@@ -219,40 +162,48 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_forward_elem(NormArg
       a.scale[row * ng + i] = fmaxf(__uint_as_float(gm[i]), kAmaxMin) * (1.f / kE4m3Max);
 }
 
-// A block walks the rows blockIdx.x * rpb + .., step gridDim.x * rpb; each thread keeps the
-// sums of dy hat of its columns over its rows, and the block writes one row of partial sums.
-template <int V, int K>
-__global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormArgs a, int tpr) {
+// A block walks the rows blockIdx.x * rpb + .., step gridDim.x * rpb, the next row's loads under
+// way; each thread keeps the sums of dy hat of its columns over its rows, and the block writes
+// one row of partial sums.
+template <int HB, int DB, int K>
+__global__ void __launch_bounds__(1024) norm_backward_elem(NormArgs a, int tpr) {
   extern __shared__ __align__(16) float sm[];
   float* red = sm;
   clear_red(red, 64);
   const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
-  const int rpb = blockDim.x / tpr;
-  float dw[K][V];
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int j = 0; j < V; ++j) dw[k][j] = 0.f;
-  for (long row0 = (long)blockIdx.x * rpb; row0 < a.rows; row0 += (long)gridDim.x * rpb) {
-    const long row = row0 + threadIdx.x / tpr;
-    const bool live = row < a.rows;
-    float h[K][V], dy[K][V], ss = 0.f, dot = 0.f;
+  const int rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  float dw[K];
+  uint32_t h[K], dy[K];
+  auto fetch = [&](long row) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * tpr + g.lane) * V;
+      const int c = k * tpr + g.lane;
+      const bool in = row < a.rows && c < a.d;
+      h[k] = in ? ld_raw<HB>(a.x, row * a.sr + c) : 0u;
+      dy[k] = in ? ld_raw<DB>(a.dy, row * a.sy + c) : 0u;
+    }
+  };
 #pragma unroll
-      for (int j = 0; j < V; ++j) h[k][j] = dy[k][j] = 0.f;
-      if (live && c < a.d) {
-        ld_row<V>(a.x, row * a.sr + c, a.rt, h[k]);
-        ld_row<V>(a.dy, row * a.sy + c, a.dt, dy[k]);
-        float w[V];
-        if (a.w) ld_row<V>(a.w, c, a.wt, w);
+  for (int k = 0; k < K; ++k) dw[k] = 0.f;
+  long row = (long)blockIdx.x * rpb + mine;
+  fetch(row);
+  for (; row - mine < a.rows; row += (long)gridDim.x * rpb) {
+    const bool live = row < a.rows;
+    float hv[K], dv[K], ss = 0.f, dot = 0.f;
+    uint32_t up[K];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          ss += h[k][j] * h[k][j];
-          dot += h[k][j] * (a.w ? w[j] * dy[k][j] : dy[k][j]);
-        }
-      }
+    for (int k = 0; k < K; ++k) {
+      const int c = k * tpr + g.lane;
+      hv[k] = raw_float<HB>(h[k], a.rt);
+      dv[k] = raw_float<DB>(dy[k], a.dt);
+      up[k] = a.r && live && c < a.d ? ld_raw<HB>(a.r, row * a.sr + c) : 0u;
+    }
+    fetch(row + (long)gridDim.x * rpb);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = k * tpr + g.lane;
+      ss += hv[k] * hv[k];
+      dot += hv[k] * (a.w && c < a.d ? ld_any(a.w, c, a.wt) * dv[k] : dv[k]);
     }
     ss = row_sum(ss, g, red);  // the other sum's barrier lies between two uses of the same words
     dot = row_sum(dot, g, red + 32);
@@ -260,41 +211,28 @@ __global__ void __launch_bounds__(V == 8 ? 512 : 1024) norm_backward_elem(NormAr
     const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * tpr + g.lane) * V;
+      const int c = k * tpr + g.lane;
       if (live && c < a.d) {
-        float w[V], o[V];
-        if (a.w) ld_row<V>(a.w, c, a.wt, w);
-        if (a.r) ld_row<V>(a.r, row * a.sr + c, a.rt, o);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          const float hat = h[k][j] * rstd;
-          const float wdy = a.w ? w[j] * dy[k][j] : dy[k][j];
-          dw[k][j] += dy[k][j] * hat;
-          o[j] = rstd * (wdy - hat * mean) + (a.r ? o[j] : 0.f);
-        }
-        st_row<V>(a.y, row * a.sr + c, a.rt, o);
+        const float hat = hv[k] * rstd, wdy = a.w ? ld_any(a.w, c, a.wt) * dv[k] : dv[k];
+        dw[k] += dv[k] * hat;
+        st_elem(a.y, row * a.sr + c, a.rt, rstd * (wdy - hat * mean) + raw_float<HB>(up[k], a.rt));
       }
     }
   }
   if (!a.dw) return;
-  // rows of one block are added in a fixed order
   float* acc = sm + 64;
-  const int mine = threadIdx.x / tpr;
-  for (int r = 0; r < rpb; ++r) {
+  for (int r = 0; r < rpb; ++r) {  // rows of one block in a fixed order
     __syncthreads();
     if (r == mine) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = (k * tpr + g.lane) * V;
+        const int c = k * tpr + g.lane;
         if (c < a.d) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float s = (r == 0 ? 0.f : acc[c + j]) + dw[k][j];
-            if (r == rpb - 1)
-              a.part[(long)blockIdx.x * a.d + c + j] = s;
-            else
-              acc[c + j] = s;
-          }
+          const float s = (r == 0 ? 0.f : acc[c]) + dw[k];
+          if (r == rpb - 1)
+            a.part[(long)blockIdx.x * a.d + c] = s;
+          else
+            acc[c] = s;
         }
       }
     }
@@ -690,18 +628,15 @@ __global__ void __launch_bounds__(256) norm_dw_kernel(const float* part, float* 
 struct RowPlan {
   int tpr, k, block;
 };
-RowPlan elem_plan(int d, int most) {
+RowPlan elem_plan(int d) {
   RowPlan p;
-  if (d <= 128) {
-    p.tpr = d <= 8 ? 8 : d <= 16 ? 16 : 32;
-    p.k = 4;
+  p.k = d <= 8192 ? 8 : 32;
+  if (d <= 256) {
+    p.tpr = d <= 64 ? 8 : d <= 128 ? 16 : 32;
     p.block = 256;
   } else {
-    p.k = most;
-    while (p.k < 32 && (d + p.k - 1) / p.k > 1024) p.k *= 2;
     p.tpr = ((d + p.k - 1) / p.k + 31) / 32 * 32;
     p.block = p.tpr;
-    p.k = p.k <= 4 ? 4 : 32;
   }
   return p;
 }
@@ -819,13 +754,19 @@ int norm_forward_launch(const NormArgs& args, cudaStream_t st) {
     if (xb == 2) return rb == 0 ? forward_rows<2, 0>(a, st) : rb == 2 ? forward_rows<2, 2>(a, st) : forward_rows<2, 4>(a, st);
     return rb == 0 ? forward_rows<4, 0>(a, st) : rb == 2 ? forward_rows<4, 2>(a, st) : forward_rows<4, 4>(a, st);
   }
-  const RowPlan p = elem_plan(a.d, 2);
+  const RowPlan p = elem_plan(a.d);
   const int rpb = p.block / p.tpr;
   const long blocks = (a.rows + rpb - 1) / rpb;
   if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   const int ng = a.group ? (a.d + a.group - 1) / a.group : 0;
   const size_t smem = (64 + (size_t)rpb * ng) * 4;
-  auto* f = p.k <= 4 ? norm_forward_elem<1, 4> : norm_forward_elem<1, 32>;
+  const int xb = a.dt == ATLAS_F32 ? 4 : 2, rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
+  auto pick = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+    if (xb == 2) return rb == 0 ? norm_forward_elem<2, 0, K> : rb == 2 ? norm_forward_elem<2, 2, K> : norm_forward_elem<2, 4, K>;
+    return rb == 0 ? norm_forward_elem<4, 0, K> : rb == 2 ? norm_forward_elem<4, 2, K> : norm_forward_elem<4, 4, K>;
+  };
+  auto* f = p.k == 8 ? pick(std::integral_constant<int, 8>()) : pick(std::integral_constant<int, 32>());
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATLAS_ERR_CUDA;
@@ -834,7 +775,7 @@ int norm_forward_launch(const NormArgs& args, cudaStream_t st) {
 }
 
 size_t norm_backward_workspace(const NormArgs& a) {
-  const int n1 = back_blocks(a, elem_plan(a.d, 4)), n8 = back_blocks(a, rows_plan(a.d, 1));
+  const int n1 = back_blocks(a, elem_plan(a.d)), n8 = back_blocks(a, rows_plan(a.d, 1));
   return (size_t)(n1 > n8 ? n1 : n8) * a.d * 4;
 }
 
@@ -842,7 +783,7 @@ int norm_backward_launch(const NormArgs& args, cudaStream_t st) {
   NormArgs a = args;
   a.inv_d = 1.f / a.d;
   const bool wide = back_wide(a);
-  const RowPlan p = wide ? rows_plan(a.d, 1) : elem_plan(a.d, 4);
+  const RowPlan p = wide ? rows_plan(a.d, 1) : elem_plan(a.d);
   int blocks = back_blocks(a, p);
   if (blocks > 0 && wide) {
     const int hb = a.rt == ATLAS_F32 ? 4 : 2, db = a.dt == ATLAS_F32 ? 4 : 2;
@@ -858,8 +799,14 @@ int norm_backward_launch(const NormArgs& args, cudaStream_t st) {
     if (rc != ATLAS_OK) return rc;
   } else if (blocks > 0) {
     const size_t smem = (64 + (size_t)(p.block > p.tpr ? a.d : 0)) * 4;
-    if (p.k <= 4) norm_backward_elem<1, 4><<<blocks, p.block, smem, st>>>(a, p.tpr);
-    else norm_backward_elem<1, 32><<<blocks, p.block, smem, st>>>(a, p.tpr);
+    const int hb = a.rt == ATLAS_F32 ? 4 : 2, db = a.dt == ATLAS_F32 ? 4 : 2;
+    auto pick = [&](auto k) {
+      constexpr int K = decltype(k)::value;
+      if (hb == 2) return db == 2 ? norm_backward_elem<2, 2, K> : norm_backward_elem<2, 4, K>;
+      return db == 2 ? norm_backward_elem<4, 2, K> : norm_backward_elem<4, 4, K>;
+    };
+    auto* f = p.k == 8 ? pick(std::integral_constant<int, 8>()) : pick(std::integral_constant<int, 32>());
+    f<<<blocks, p.block, smem, st>>>(a, p.tpr);
   }
   if (a.dw) norm_dw_kernel<<<(a.d + 31) / 32, 256, 0, st>>>(a.part, a.dw, blocks, a.d);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;

@@ -85,6 +85,10 @@ struct Tile {
   }
   __device__ __forceinline__ void next() { p += TT * row; }
   __device__ __forceinline__ void back() { p -= TT * row; }
+  // Asynchronous copies take at least four bytes; smaller elements come through registers,
+  // loaded by copy() and stored by put(), with other work in between.
+  static constexpr bool kAsync = V * sizeof(T) >= 4;
+  T held[kAsync ? 1 : kN];
   // this tile into s; zeros from token `left` on and past element n
   __device__ __forceinline__ void copy(T (*s)[W], int left, int n) {
 #pragma unroll
@@ -92,11 +96,18 @@ struct Tile {
       if (!inside(i)) continue;
       const int u = token(i), c = channel(i);
       const bool some = u < left && c < n;
-      if constexpr (V * sizeof(T) >= 4) {
+      if constexpr (kAsync) {
         cp_async<V * sizeof(T)>(&s[u][c], some ? at(i) : p, some);
       } else {
-        s[u][c] = some ? *at(i) : from_f<T>(0.f);
+        held[i] = some ? *at(i) : from_f<T>(0.f);
       }
+    }
+  }
+  __device__ __forceinline__ void put(T (*s)[W]) {
+    if constexpr (!kAsync) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (inside(i)) s[token(i)][channel(i)] = held[i];
     }
   }
 };
@@ -254,6 +265,19 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
         }
       }
       cp_commit();
+    };
+    auto put = [&]() {
+      if (left_f > 0) {
+        Raw& r = s.raw[rf];
+        px.put(r.x);
+        pd.put(r.dt);
+        pB.put(r.B);
+        if (!ENDS) {
+          if (a.z) pz.put(r.z);
+          pC.put(r.C);
+        }
+        if (KEEP) pg.put(r.dy[0]);
+      }
       left_f -= kTile;
       step(rf);
     };
@@ -341,9 +365,10 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
       left_n -= kTile;
       step(rn);
     };
-    fetch();
-    fetch();
-    fetch();
+    for (int i = 0; i < 3; ++i) {
+      fetch();
+      put();
+    }
     cp_wait<2>();
     __syncwarp();
     prepare(0);
@@ -354,6 +379,7 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
       cp_wait<2>();
       __syncwarp();
       prepare((m + 1) & 1);
+      put();
       __syncthreads();
     }
     cp_wait<0>();
@@ -620,8 +646,8 @@ bool segment_pass(const ScanArgs& a, const Segments& sg, cudaStream_t st) {
 template <typename T, int V, int LN, Mode MODE>
 bool segment_pass(const ScanArgs& a, const Segments& sg, cudaStream_t st) {
   constexpr int VV = V < Shape<LN>::kCB ? V : Shape<LN>::kCB;
-  return VV > 1 && a.wide_n ? segment_pass<T, VV, LN, MODE, (VV > 1)>(a, sg, st)
-                            : segment_pass<T, VV, LN, MODE, false>(a, sg, st);
+  return a.wide_n ? segment_pass<T, VV, LN, MODE, true>(a, sg, st)
+                  : segment_pass<T, VV, LN, MODE, false>(a, sg, st);
 }
 
 template <typename T, int V, int LN>

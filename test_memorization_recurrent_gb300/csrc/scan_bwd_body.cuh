@@ -251,6 +251,17 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
           if (lane < P::kCB) cp_async<4>(&r.cum[wi][lane], lane < k.n ? w.keep_dt + at + lane : w.keep_dt, lane < k.n);
         }
         cp_commit();
+      };
+      auto put = [&]() {
+        if (nf < tiles) {
+          Raw& r = s.raw[rf];
+          px.put(r.x[wi]);
+          pd.put(r.dt[wi]);
+          py.put(r.dy[wi]);
+          if (a.z) pz.put(r.z[wi]);
+          if (wi == 0) pn.put(r.B);
+          if (wi == 1) pn.put(r.C);
+        }
         ++nf;
         step(rf);
       };
@@ -370,8 +381,10 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
         }
         pbc -= kSub * 2 * P::kNP;
       };
-      fetch();
-      fetch();
+      for (int i = 0; i < 2; ++i) {
+        fetch();
+        put();
+      }
       cp_wait<1>();
       __syncwarp();
       prepare(0);
@@ -382,6 +395,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
         cp_wait<1>();
         __syncwarp();
         prepare((m + 1) & 1);
+        put();
         __syncthreads();
       }
       cp_wait<0>();
@@ -609,7 +623,7 @@ int backward(const ScanArgs& a, cudaStream_t st) {
     if (!segment_pass<T, V, LN, kKeep>(a, w.segments(), st)) return ATLAS_ERR_CUDA;
     if (w.split)
       join_back_kernel<LN><<<dim3((unsigned)(((long)a.D * a.N + 255) / 256), a.s.B), 256, 0, st>>>(a, w);
-    if (!(VV > 1 && a.wide_n ? back_pass<T, VV, LN, (VV > 1)>(a, w, st) : back_pass<T, VV, LN, false>(a, w, st)))
+    if (!(a.wide_n ? back_pass<T, VV, LN, true>(a, w, st) : back_pass<T, VV, LN, false>(a, w, st)))
       return ATLAS_ERR_CUDA;
   }
   const long nb = (w.rows * a.G * 2 * Shape<LN>::kNP + 255) / 256;
