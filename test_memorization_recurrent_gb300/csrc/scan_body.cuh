@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
     d[i] = to_f(reinterpret_cast<const T*>(a.dt)[b * a.tb + c]) + (a.bias ? a.bias[c] : 0.f);
     if (a.z) z[i] = to_f(reinterpret_cast<const T*>(a.z)[b * a.zb + c]);
     if (a.Dk) skip[i] = a.Dk[c];
-    const long g = (long)(c / (a.D / a.G)) * a.N;
+    const long g = a.G == 1 ? 0 : (long)(c / (a.D / a.G)) * a.N;
     const T* pB = reinterpret_cast<const T*>(a.Bm) + b * a.bb + g;
     const T* pC = reinterpret_cast<const T*>(a.Cm) + b * a.cb + g;
     if (a.wide_n) {

@@ -220,11 +220,23 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
       float* pbc = w.pbc + ((long)blockIdx.y * w.rows + row0) * 2 * P::kNP;
       int rf = 0, rp = 0, rn = 0;
       int nf = 0, np = 0;  // tiles fetched, prepared
+      constexpr int KN = P::kCB * LN / kThreads;
+      static_assert(P::kCB * LN % kThreads == 0, "every lane has the same number of pieces");
+      int kept_to[KN], kept_from[KN], kept_n[KN];  // places in the ring, offsets, states (of four)
+      const long at = (seg * w.nsub + tiles - 1) * a.D;
+#pragma unroll
+      for (int i = 0; i < KN; ++i) {
+        const int q = i * kThreads + lane, ch = q / LN, n = q % LN * 4;
+        kept_to[i] = ((ch & 1) * kThreads + q % LN * P::kPairs + ch / 2) * 4;
+        kept_n[i] = ch < k.n ? max(0, min(4, a.N - n)) : 0;
+        kept_from[i] = kept_n[i] > 0 ? (k.c0 + ch) * a.N + n : 0;
+      }
+      const float* kept = w.keep_h + at * a.N;
+      const float* cum = w.keep_dt + at + (lane < k.n ? k.c0 + lane : 0);
       const auto step = [](int& r) { r = (r + 1) % kBackRing; };
       auto fetch = [&]() {
         if (nf < tiles) {
           const int left = nf == 0 ? end - first : kSub;
-          const long at = (seg * w.nsub + tiles - 1 - nf) * a.D + k.c0;
           Raw& r = s.raw[rf];
           px.copy(r.x[wi], left, k.n), px.back();
           pd.copy(r.dt[wi], left, k.n), pd.back();
@@ -232,23 +244,20 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
           if (a.z) pz.copy(r.z[wi], left, k.n), pz.back();
           if (wi == 0) pn.copy(r.B, left, a.N), pn.back();
           if (wi == 1) pn.copy(r.C, left, a.N), pn.back();
+          // each lane's pieces of the kept states: where they go and come from stays but for the tile
 #pragma unroll
-          for (int i = lane; i < P::kCB * LN; i += kThreads) {
-            const int ch = i / LN, n = i % LN * 4;
-            const float* q = w.keep_h + (at + ch) * a.N + n;
-            float* o = r.h[wi][ch & 1][i % LN * P::kPairs + ch / 2];
+          for (int i = 0; i < KN; ++i) {
+            float* o = r.h[wi][0][0] + kept_to[i];
             if (a.N % 4 == 0) {
-              const bool in = ch < k.n && n < a.N;
-              cp_async<16>(o, in ? q : w.keep_h, in);
+              cp_async<16>(o, kept + kept_from[i], kept_n[i] > 0);
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool in = ch < k.n && n + j < a.N;
-                cp_async<4>(o + j, in ? q + j : w.keep_h, in);
-              }
+              for (int j = 0; j < 4; ++j) cp_async<4>(o + j, kept + kept_from[i] + (j < kept_n[i] ? j : 0), j < kept_n[i]);
             }
           }
-          if (lane < P::kCB) cp_async<4>(&r.cum[wi][lane], lane < k.n ? w.keep_dt + at + lane : w.keep_dt, lane < k.n);
+          kept -= (long)a.D * a.N;
+          if (lane < P::kCB) cp_async<4>(&r.cum[wi][lane], cum, lane < k.n);
+          cum -= a.D;
         }
         cp_commit();
       };
