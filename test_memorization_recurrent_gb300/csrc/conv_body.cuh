@@ -10,7 +10,8 @@
 // four: with eight, the taps, window and loads of a lane take 202 registers, and too few
 // warps are left to cover the latency.  8 x 4096 tokens x 2048 channels of bf16, four taps:
 // 126 us with eight, 59 us with four (4.6 TB/s); 24 warps an SM, 59 us, against 91 with 20,
-// 65 with 28, 78 with 32.
+// 65 with 28, 78 with 32.  Backward: 104 us (3.9 TB/s; 672 with loads in the worker's turn, 150
+// with the ring but the edges' conditions at every token).
 #pragma once
 #include "ops_common.cuh"
 
@@ -172,12 +173,15 @@ __global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kerne
   }
 }
 
-// Rows of x and dy on their way to a worker of backward_kernel.
-constexpr int kChunk = 8, kStages = 4;
+// Rows of x and dy on their way to a worker of backward_kernel.  32-bit elements have two
+// stages, so that three blocks fit an SM all the same.
+constexpr int kChunk = 8;
+template <typename T>
+constexpr int kStages = sizeof(T) == 4 ? 2 : 4;
 template <typename T, int V>
 struct Ring {
-  T x[kStages][kChunk][kLanes * V];
-  T dy[kStages][kChunk][kLanes * V];
+  T x[kStages<T>][kChunk][kLanes * V];
+  T dy[kStages<T>][kChunk][kLanes * V];
 };
 
 // A warp is a worker: it walks tiles and keeps dw and db of its channels in registers; the
@@ -190,7 +194,7 @@ struct Ring {
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kLanes * kWarps)
     backward_kernel(ConvArgs a, int TT, long tiles, float* part, float* ds) {
-  constexpr int H = W - 1, N = kPairs<V>;
+  constexpr int H = W - 1, N = kPairs<V>, S = kStages<T>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
   Ring<T, V>& ring = reinterpret_cast<Ring<T, V>*>(smem)[threadIdx.y];
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kLanes * kWarps)
     T* dx = reinterpret_cast<T*>(a.dx) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) {
+    for (int k = 0; k < S - 1; ++k) {
       fetch(k, q0 + k * kChunk);
       cp_commit();
     }
@@ -322,15 +326,15 @@ __global__ void __launch_bounds__(kLanes * kWarps)
       }
     };
     for (int base = q0; base < q1; base += kChunk) {
-      cp_wait<kStages - 2>();
+      cp_wait<S - 2>();
       __syncwarp();  // this chunk is there for all lanes, and the one before has been read
-      fetch(stage == 0 ? kStages - 1 : stage - 1, base + (kStages - 1) * kChunk);
+      fetch(stage == 0 ? S - 1 : stage - 1, base + (S - 1) * kChunk);
       cp_commit();
       if (base >= t.t0 + H && base + kChunk <= min(t1, t.len - H))
         walk(base, std::false_type());
       else
         walk(base, std::true_type());
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      stage = stage + 1 == S ? 0 : stage + 1;
     }
     cp_wait<0>();
   }

@@ -4,14 +4,18 @@
 //   h = x + r,  y = h rstd w,  rstd = 1 / sqrt(mean(h^2) + eps)
 //   dx = rstd (w dy - hat mean(w dy hat)) + dh,  dw = sum over rows of dy hat,  hat = h rstd
 //
-// Both passes are bound by memory: a row is read once into registers, reduced, and written
-// once, so what counts is how many loads are under way.  Aligned rows are held as they lie in
-// memory, eight elements a load, all loads issued before the first conversion (the element's
-// type is known at run time, its size at compile time).  Forward, a row of up to 2048 channels
-// belongs to 8, 16 or 32 lanes of a warp and needs no barrier; a longer one, or one of a few
-// rows, to a block.  Backward, a block walks rows and keeps the sums of dw in registers, the
-// next row's loads under way.  Rows of odd widths or addresses take the element-wise kernels.
-// Sums run in 32 bits; the only roundings are those of the outputs to their types.
+// Both passes are bound by memory, so what counts is how many loads are under way and that
+// instructions do not get in their way.  Aligned rows are held as they lie in memory, eight
+// elements a load (the element's type is known at run time, its size at compile time).  A row
+// of up to 256 channels belongs to 8, 16 or 32 lanes of a warp, four rows under way; a longer
+// one to a block, which walks rows with the next two on their way through shared memory (a few
+// rows: a block each).  Rows of odd widths or addresses take the element-wise kernels.  Sums
+// run in 32 bits; the only roundings are those of the outputs to their types.
+//
+// Measured (copy rate 6.78 TB/s): 32768 x 2048 bf16 + residual to e4m3 with scales of 128: 80 us,
+// 87% (a warp a row, loads in its turn: 123 us; divisions and a loop over the warps' sums: 96);
+// 524288 x 128 bf16: 51 us, 77%; backward, 16384 x 2560, 32-bit stream: 99 us, 88% (one row's
+// loads ahead in registers: 134); 20000 x 1371 bf16 element by element: 119 and 329 us.
 #include <cuda_fp8.h>
 
 #include "ops_common.cuh"

@@ -15,6 +15,13 @@
 // over states and over channels are taken by halving over lanes; every block writes
 // partial sums of dB, dC (per token) and dA, dD, ddt_bias (per segment), which the last
 // kernel adds in a fixed order.
+//
+// What bounds it: instruction issue in the main pass, 26 for 32 updates (17 of them in the
+// walking warps: the decay and state twice, the adjoint, seven products, and the two kinds of
+// sums).  Holding a tile's decays instead of taking them again costs 64 registers and with
+// them half the warps.  4 x 2048 tokens x 2048 channels x 16 states, bf16, gated: 514 us =
+// 126 kept states + 20 join + 333 main pass (55% of the issue slots) + 20 sums; the first
+// kernels, with one channel x four states a lane and loads in every warp's turn, took 1822.
 #pragma once
 #include "scan_body.cuh"
 

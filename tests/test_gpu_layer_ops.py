@@ -502,6 +502,17 @@ def test_scan_backward(B, L, D, N, G, dtype):
     check_grads(d, o, torch.zeros_like(d.dh), [((b,), 0 * d.h_h[b], False) for b in range(B)])
 
 
+def test_no_sequences():
+    """B = 0, in rows and packed: no gradient, sums of nothing are zero, nothing else is touched."""
+    for start in (None, torch.zeros(1, dtype=torch.int32, device="cuda")):
+        d = Scan(rng(23), 1, 0, 16, 16, 1, "fp32", packed_rows=8)
+        cfg = A.make_scan_cfg(0, 8, 16, 16, dtype=A.F32, seq_start=start)
+        o = d.backward(cfg, None, None)
+        assert not o["dA"].any() and not o["dD"].any() and not o["ddt_bias"].any()
+        assert all((o[k] == 77).all() for k in ("dx", "ddt", "dB", "dC", "dz"))
+        assert (run_scan(d, cfg, None, None) == 77).all()
+
+
 def test_scan_against_differences():
     """The forward's own differences, in 32 bits: L(x + e d) - L(x - e d) over 2e is g.d to e^2 and
     to the rounding of the losses, |L| 2^-20 / e."""
