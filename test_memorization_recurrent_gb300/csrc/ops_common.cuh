@@ -204,20 +204,14 @@ __device__ __forceinline__ float pair_sum(pair32 a) {
 // P fitted to log(1 + e) / e on [0, 1] by reweighted least squares at Chebyshev nodes
 // (relative error 5e-9; 1.5e-7 with the roundings of its evaluation).
 __device__ __forceinline__ float softplusf(float x) {
+  constexpr float k[10] = {1.f, -0.49999902f, 0.33329964f, -0.24954133f, 0.19675931f,
+                           -0.1530557f, 0.10603617f, -0.05695916f, 0.019851262f, -0.0032439807f};
   const float e = ex2(-ATLAS_LOG2E * fabsf(x));
-  float p = -0.0032439807f;
-  p = fmaf(p, e, 0.019851262f);
-  p = fmaf(p, e, -0.05695916f);
-  p = fmaf(p, e, 0.10603617f);
-  p = fmaf(p, e, -0.1530557f);
-  p = fmaf(p, e, 0.19675931f);
-  p = fmaf(p, e, -0.24954133f);
-  p = fmaf(p, e, 0.33329964f);
-  p = fmaf(p, e, -0.49999902f);
-  p = fmaf(p, e, 1.f);
+  float p = k[9];
+#pragma unroll
+  for (int i = 8; i >= 0; --i) p = fmaf(p, e, k[i]);
   return fmaf(p, e, fmaxf(x, 0.f));
 }
-
 // ------------------------------------------------------------------ sequences
 
 // Tiles of TT tokens.  With seq_start, tile numbers are handed out so that a tile

@@ -26,7 +26,7 @@
 // segments: a first pass finds each segment's end state from a zero start (with the sum of
 // its dt: the decay over a segment is exp(A sum dt)); the second computes the outputs, each
 // segment from the start state that it joins from those in front of it.  Three packed prompts of
-// 16384 tokens x 1024 channels: 174 us (68 + 105) in 17 segments.
+// 16384 tokens x 1024 channels: 150 us.
 #pragma once
 #include "ops_common.cuh"
 
@@ -623,12 +623,16 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
   }
 }
 
-// Segment length, 0 for one segment a sequence.  One segment when the sequences alone give
-// six blocks an SM; otherwise segments for that many, but none below 256 tokens.
+// Segment length, 0 for one segment a sequence.  The blocks of an SM share its throughput from
+// about two of them on, and a second walk over the tokens costs two thirds of the first: one
+// segment from 250 blocks on (4 x 4096 tokens x 1024 channels: 144 us, in segments 150 to 168;
+// twice the sequences: 199 against 330).  Below, segments for seven blocks an SM, as many as run
+// at once (three packed prompts of 16384 tokens x 1024: 170 us with six, 150 with seven, 183 with
+// eight), but none below 256 tokens.
 inline int segment_tokens(const ScanArgs& a, long blocks_per_seq) {
-  const long want = 152 * 6;
+  const long want = 152 * 7;
   const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
-  if (!a.s.start && a.s.B * blocks_per_seq >= want) return 0;
+  if (!a.s.start && a.s.B * blocks_per_seq >= 250) return 0;
   if (a.s.L <= 256) return 0;
   long S = rows * blocks_per_seq / want / kTile * kTile;
   if (S < 256) S = 256;
