@@ -19,8 +19,8 @@
 // What bounds it: instruction issue in the main pass, 26 for 32 updates (17 of them in the
 // walking warps: the decay and state twice, the adjoint, seven products, and the two kinds of
 // sums).  Holding a tile's decays instead of taking them again costs 64 registers and with
-// them half the warps.  4 x 2048 tokens x 2048 channels x 16 states, bf16, gated: 514 us =
-// 126 kept states + 20 join + 333 main pass (55% of the issue slots) + 20 sums; the first
+// them half the warps.  4 x 2048 tokens x 2048 channels x 16 states, bf16, gated: 490 us, of
+// which the main pass takes two thirds (55% of the issue slots) and the kept states a quarter; the first
 // kernels, with one channel x four states a lane and loads in every warp's turn, took 1822.
 #pragma once
 #include "scan_body.cuh"
@@ -35,15 +35,28 @@ constexpr int kBackRing = 4;  // tiles as they lie in memory: finished, walked, 
 template <int LN>
 constexpr int kBackCB = kWalkers * Shape<LN>::kCB;  // channels of a block
 
-// Segment length, 0 for one segment a sequence.  Every pass but the join costs the same for
-// short segments; two blocks an SM, and some more so that the last ones do not stand alone.
+// Segment length, 0 for one segment a sequence.  The main pass runs n blocks, two an SM at a
+// time, for a little over S tokens each (30 more for a block's start): one round of blocks takes
+// that long, several about half a round more than their share.  The shortest of the lengths
+// from 128 on is taken (4 x 2048 tokens x 2048 channels: 478 us with 256, 501 with 128, 516 with
+// 512, 624 with 2048; 8 x 512 x 2048: 252 with 512, 279 with 256).
 inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
-  const long want = 152 * 2 * 6;
-  const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
-  long S = rows * blocks_per_seq / want / kTile * kTile;
-  if (S < 128) S = 128;
-  if (S >= a.s.L) return 0;
-  return (int)S;
+  const long L = a.s.L, B = a.s.start ? 1 : a.s.B, more = a.s.start ? a.s.B : 0;
+  int best = 0;
+  double least = 0;
+  for (long c = 128;; c = c % 3 ? c / 2 * 3 : c / 3 * 4) {  // 128, 192, 256, 384, ..
+    const bool whole = c >= L;
+    const long m = whole ? 1 : (L + c - 1) / c;  // segments a sequence
+    const long S = whole ? L : ((L + m - 1) / m + kTile - 1) / kTile * kTile;
+    const double n = (double)(B * m + more) * blocks_per_seq / (152 * 2);
+    const double cost = n <= 1 ? 1.05 * S + 30 : (n + 0.5) * S + n * 30;
+    if (best == 0 || cost < least) {
+      best = whole ? -1 : (int)S;
+      least = cost;
+    }
+    if (whole) break;
+  }
+  return best < 0 || best >= L ? 0 : best;
 }
 
 // Sizes and workspace of a backward call.
