@@ -119,7 +119,7 @@ def test_norm_in_8_bits(rows, d, group):
 
 @pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32")])
 @pytest.mark.parametrize("rows,d,stride,shift", [(0, 16, 0, 0), (1, 1, 0, 0), (3, 7, 0, 0), (700, 64, 72, 0), (5000, 128, 0, 0), (9, 130, 0, 1),
-                                                 (7, 1000, 0, 0), (1000, 1032, 0, 0), (6, 2050, 0, 0), (700, 2560, 0, 0), (2, 20000, 0, 0), (2, 32767, 0, 0)])
+                                                 (7, 1000, 0, 0), (1000, 1032, 0, 0), (6, 2050, 0, 0), (700, 2560, 0, 0), (1500, 5000, 0, 0), (900, 3000, 0, 0), (2, 20000, 0, 0), (2, 32767, 0, 0)])
 def test_norm_backward(rows, d, stride, shift, dtype, r_dtype):
     r = rng(3, rows, d)
     h, hh = strided(r, rows, d, r_dtype, stride, shift, 2.0)
@@ -140,6 +140,29 @@ def test_norm_backward(rows, d, stride, shift, dtype, r_dtype):
             want = mag = (None, np.zeros(d))
         if weight:
             close(dw, want[1], mag[1], "fp32", rows / 32, "dw")
+
+
+@pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,d,group", [(1300, 264, 0), (2600, 2048, 128), (1250, 4104, 0), (1230, 8200, 256), (1220, 17000, 64)])
+def test_norm_many_long_rows(rows, d, group, dtype, r_dtype):
+    """Rows enough for blocks that walk several, one to eight vectors a thread; in place, and with an
+    8-bit output too."""
+    r = rng(24, rows, d)
+    x, xh = draw(r, (rows, d), dtype)
+    res, rh = draw(r, (rows, d), r_dtype, 2.0)
+    w, wh = draw(r, d, dtype)
+    h, want = R.norm(xh, rh, wh, 1e-6)
+    keep, y = res.clone(), torch.empty_like(x)
+    A.atlas_norm_forward(x, res, w, A.make_norm_cfg(rows, d, dtype=CODE[dtype], r_dtype=CODE[r_dtype]), y, res)
+    close(y, want, np.abs(want), dtype, 0, "y")
+    close(res, h, np.abs(xh) + np.abs(rh), r_dtype, 0, "residual")
+    g = group or d
+    q, scale = torch.empty(rows, d, dtype=DT["e4m3"], device="cuda"), torch.empty(rows, -(-d // g), device="cuda")
+    A.atlas_norm_forward(x, keep, w, A.make_norm_cfg(rows, d, dtype=CODE[dtype], r_dtype=CODE[r_dtype], out_dtype=A.E4M3, group=group), q, None, scale)
+    ref = np.maximum(np.stack([np.abs(want[:, i:i + g]).max(1) for i in range(0, d, g)], 1), 1e-30) / 448
+    assert (np.abs(host(scale) - ref) <= 2.0 ** -18 * ref).all()
+    v = want / np.repeat(ref, g, 1)[:, :d]
+    close(q, v, np.abs(v), "e4m3", 0, "q")
 
 
 def test_norm_rows_past_32_bits():
@@ -288,6 +311,30 @@ def test_conv_packed(lens, dtype, C, W):
     assert (host(dx)[:2] == 77).all() and (host(dx)[-3:] == 77).all()
 
 
+def test_many_packed_sequences():
+    """Some 1500 sequences of 0 to 5 tokens: every one finds its rows, its slot and its state."""
+    r = rng(25)
+    B, C, N, W = 1531, 24, 16, 4
+    lens = [int(n) for n in r.integers(0, 6, B)]
+    start, T, at = packed(lens)
+    slots = r.permutation(B + 7)[:B]
+    slot = torch.tensor(slots, dtype=torch.int32, device="cuda")
+    st = status()
+    c = Conv(r, B, 0, C, W, "fp32", n=B + 7, packed_rows=T)
+    y, new = torch.full_like(c.x, 77.0), c.s.clone()
+    A.atlas_conv_forward(c.x, c.w, c.b, A.make_conv_cfg(B, T, C, W, dtype=A.F32, seq_start=start, slot=slot, n_slots=B + 7, status_dev=st), y, new, new)
+    d = Scan(r, B, 0, C, N, 1, "fp32", n=B + 7, packed_rows=T)
+    h = d.h.clone()
+    z = run_scan(d, A.make_scan_cfg(B, T, C, N, dtype=A.F32, seq_start=start, slot=slot, n_slots=B + 7, status_dev=st), h, h)
+    assert int(st) == 0 and (y[-3:] == 77).all() and (z[-3:] == 77).all()
+    y, new, z, h = host(y), host(new), host(z), host(h)
+    for b, n in enumerate(lens):
+        rows, s = slice(at[b], at[b] + n), slots[b]
+        c.check(y[rows], None, rows, c.sh[s], "fp32", f"sequence {b}")
+        assert (new[s] == R.conv(c.xh[rows], c.wh, c.bh, True, c.sh[s])[1]).all()
+        d.check(z[rows], h[s], rows, d.h_h[s], f"sequence {b}")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("B,L,C,W,act", [(2, 5, 8, 4, True), (1, 1, 3, 4, True), (2, 2, 40, 4, False), (1, 65, 264, 1, True), (3, 300, 33, 3, True),
                                          (2, 9, 16, 8, True), (1, 3, 16, 8, True), (2, 200, 520, 5, True), (2, 0, 8, 4, True), (0, 5, 8, 4, True)])
@@ -386,6 +433,23 @@ def test_scan(B, L, D, N, G, dtype):
     y = run_scan(d, cfg, None, None)
     for b in range(B):
         d.check(y[b], None, (b,), 0 * d.h_h[b], f"sequence {b} from zeros")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,L,D,N,G", [(1, 600, 64, 32, 1), (2, 700, 20, 40, 1), (1, 530, 6, 128, 2), (1, 900, 70, 30, 1), (1, 1030, 128, 8, 2)])
+def test_scan_segments_of_every_width(B, L, D, N, G, dtype):
+    """Several segments a sequence, forward and backward, for each number of lanes a channel."""
+    r = rng(26, B, L, D, N)
+    d = Scan(r, B, L, D, N, G, dtype)
+    cfg = A.make_scan_cfg(B, L, D, N, G, dtype=CODE[dtype])
+    assert A.atlas_scan_workspace_bytes(cfg) > 0  # segments
+    h = d.h.clone()
+    y = run_scan(d, cfg, h, h)
+    for b in range(B):
+        d.check(y[b], h[b], (b,), d.h_h[b], f"sequence {b}")
+    dh = d.dh.clone()
+    o = d.backward(A.make_scan_cfg(B, L, D, N, G, dtype=CODE[dtype]), d.h, dh)
+    check_grads(d, o, dh, [((b,), d.h_h[b], True) for b in range(B)])
 
 
 def test_scan_without_softplus_and_large_steps():
