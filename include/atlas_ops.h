@@ -59,7 +59,8 @@ extern "C" {
  * An 8-bit output is stored with one scale per group of `group` channels (the last
  * group of a row may be shorter; group = 0: the whole row):
  *   scale = max(max |y| over the group, 1e-30) / 448,   q = e4m3(y / scale)
- * rounded to nearest even, so that y = q * scale.  A row of zeros gives q = 0.
+ * rounded to nearest even (the quotient in 32 bits, as y times 1 / scale), so that
+ * y = q * scale.  A row of zeros gives q = 0.
  * With a row of keys or queries (d = the head's width) and weight = 1 / sqrt(d)
  * this is the l2 normalisation that the memory update expects of K and Q. */
 typedef struct atlas_norm_cfg {
