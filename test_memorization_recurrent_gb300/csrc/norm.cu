@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) norm_backward_rows(Norm
         dot += v.y + v.w;
       }
     }
-    const float rstd = rsqrtf(ss * a.inv_d + a.eps);
+    // a place of the block without a row holds zeros: without eps its rstd would be infinite, and 0 rstd in dw
+    const float rstd = row < a.rows ? rsqrtf(ss * a.inv_d + a.eps) : 0.f;
     const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {

@@ -31,3 +31,21 @@ def test_8_bits_are_the_32_bit_rows_rounded(rows, d, group):
     assert torch.equal(q.float(), want.float()), int((q.float() != want.float()).sum())
 
 
+@pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("rows", [1, 5, 9, 701])
+@pytest.mark.parametrize("d", [64, 128, 256, 130, 520])
+def test_norm_backward_without_eps(d, rows, dtype, r_dtype):
+    """Rows that do not fill their block's places, eps = 0: dw is the sum over the rows there are."""
+    r = rng(31, rows, d)
+    h, hh = draw(r, (rows, d), r_dtype, 2.0)
+    dy, dyh = draw(r, (rows, d), dtype)
+    w, wh = draw(r, d, dtype)
+    cfg = A.make_norm_cfg(rows, d, dtype=CODE[dtype], r_dtype=CODE[r_dtype], eps=0.0)
+    space(cfg, A.atlas_norm_backward_workspace_bytes(cfg))
+    dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
+    A.atlas_norm_backward(h, w, dy, None, cfg, dx, dw)
+    want, mag = (R.norm_back(hh, wh, dyh, None, 0.0, mag=m) for m in (False, True))
+    close(dx, want[0], mag[0], r_dtype, 0, "dx")
+    close(dw, want[1], mag[1], "fp32", rows / 32, "dw")
+
+
