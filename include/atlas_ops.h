@@ -60,7 +60,9 @@ extern "C" {
  * group of a row may be shorter; group = 0: the whole row):
  *   scale = max(max |y| over the group, 1e-30) / 448,   q = e4m3(y / scale)
  * rounded to nearest even (the quotient in 32 bits, as y times 1 / scale), so that
- * y = q * scale.  A row of zeros gives q = 0.
+ * y = q * scale.  A row of zeros gives zeros, with eps = 0 too (its dx is then dh, and it
+ * adds nothing to dw).  h^2 and its mean are taken in 32 bits: with eps = 0 a row that is
+ * not zero but whose mean of squares is below 2^-149 is not normalised.
  * With a row of keys or queries (d = the head's width) and weight = 1 / sqrt(d)
  * this is the l2 normalisation that the memory update expects of K and Q. */
 typedef struct atlas_norm_cfg {

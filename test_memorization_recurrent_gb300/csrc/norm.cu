@@ -18,6 +18,8 @@
 // loads ahead in registers: 134); 20000 x 1371 bf16 element by element: 119 and 329 us.
 #include <cuda_fp8.h>
 
+#include <limits>
+
 #include "ops_common.cuh"
 
 namespace atlas {
@@ -35,6 +37,15 @@ __device__ __forceinline__ float scale_of(float m) { return fmaxf(m, kAmaxMin) *
 __device__ __forceinline__ float inverse(float scale) {
   const float i = rcp(scale);  // 0 for an infinite scale, and so the result
   return fmaf(fmaf(-fminf(scale, 3.4e38f), i, 1.f), i, i);
+}
+
+// 1 / sqrt(mean of squares + eps).  eps = 0 and a row of zeros: the outputs are zeros, and so is the
+// norm's part of the gradients.  Forward the launch takes the least number for eps = 0, so that 0 rstd is 0
+// without a word for it in the kernels (a select cost the rows of 128 channels 2%).
+__device__ __forceinline__ float rstd_of(float sum, const NormArgs& a) { return rsqrtf(sum * a.inv_d + a.eps); }
+__device__ __forceinline__ float back_rstd_of(float sum, const NormArgs& a) {
+  const float v = sum * a.inv_d + a.eps;
+  return v == 0.f ? 0.f : rsqrtf(v);
 }
 
 // The threads that share a row: TPR lanes of a warp (TPR <= 32), or the whole block.
@@ -129,7 +140,7 @@ __global__ void __launch_bounds__(1024) norm_forward_elem(NormArgs a, int tpr) {
     if (a.r_out && live && c < a.d) st_elem(a.r_out, row * a.sr + c, a.rt, h[k]);
     ss += h[k] * h[k];
   }
-  const float rstd = rsqrtf(row_sum(ss, g, red) * a.inv_d + a.eps);
+  const float rstd = rstd_of(row_sum(ss, g, red), a);
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(1024) norm_backward_elem(NormArgs a, int tpr) 
     }
     ss = row_sum(ss, g, red);  // the other sum's barrier lies between two uses of the same words
     dot = row_sum(dot, g, red + 32);
-    const float rstd = rsqrtf(ss * a.inv_d + a.eps);
+    const float rstd = back_rstd_of(ss, a);
     const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -365,7 +376,7 @@ __device__ __forceinline__ void forward_row(const NormArgs& a, const RowGroup& g
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss += h[k][i] * h[k][i];
   }
-  const float rstd = rsqrtf(row_sum(ss, g, red) * a.inv_d + a.eps);
+  const float rstd = rstd_of(row_sum(ss, g, red), a);
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -582,8 +593,7 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) norm_backward_rows(Norm
         dot += v.y + v.w;
       }
     }
-    // a place of the block without a row holds zeros: without eps its rstd would be infinite, and 0 rstd in dw
-    const float rstd = row < a.rows ? rsqrtf(ss * a.inv_d + a.eps) : 0.f;
+    const float rstd = back_rstd_of(ss, a);  // (a place of the block without a row holds zeros)
     const float mean = dot * rstd * a.inv_d;  // mean(w dy hat)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -762,6 +772,7 @@ int norm_forward_launch(const NormArgs& args, cudaStream_t st) {
   // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
   NormArgs a = args;
   a.inv_d = 1.f / a.d;
+  if (a.eps == 0.f) a.eps = std::numeric_limits<float>::denorm_min();  // 2^-149, nothing beside a row's own mean
   a.ng = a.group ? (a.d + a.group - 1) / a.group : 1;
   for (a.gshift = 0; (1 << a.gshift) < a.group;) ++a.gshift;
   const bool lanes = a.group == 0 || (a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);

@@ -49,3 +49,43 @@ def test_norm_backward_without_eps(d, rows, dtype, r_dtype):
     close(dw, want[1], mag[1], "fp32", rows / 32, "dw")
 
 
+@pytest.mark.parametrize("dtype,r_dtype", [("bf16", "bf16"), ("fp16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("rows,d", [(6, 128), (1500, 128), (6, 1000), (1300, 1032), (6, 37), (1300, 1371), (3, 8200), (1, 1)])
+def test_rows_of_zeros_without_eps(rows, d, dtype, r_dtype):
+    """eps = 0: a row of zeros gives zeros in every output type, and its gradient is what reaches the
+    residual stream; it adds nothing to dw."""
+    r = rng(32, rows, d)
+    x, res, w = draw(r, (rows, d), dtype)[0], draw(r, (rows, d), r_dtype, 2.0)[0], draw(r, d, dtype)[0]
+    zero = np.arange(rows) % 3 == 0
+    x[torch.from_numpy(zero).cuda()] = 0
+    res[torch.from_numpy(zero).cuda()] = 0
+    kw = dict(dtype=CODE[dtype], r_dtype=CODE[r_dtype], w_dtype=CODE[dtype], eps=0.0)
+    some = np.where(zero[:, None], 1.0, host(x) + host(res))  # (any finite row in the place of zeros)
+    want = np.where(zero[:, None], 0.0, R.norm(some, None, host(w), 0.0)[1])
+    for out in (dtype, "fp32"):
+        y = torch.empty(rows, d, dtype=DT[out], device="cuda")
+        A.atlas_norm_forward(x, res, w, A.make_norm_cfg(rows, d, out_dtype=CODE[out], **kw), y)
+        close(y, want, np.abs(want), out, 0, out)
+    for group in (0, 32):
+        g = group if 0 < group < d else d
+        q, scale = torch.empty(rows, d, dtype=DT["e4m3"], device="cuda"), torch.empty(rows, -(-d // g), device="cuda")
+        A.atlas_norm_forward(x, res, w, A.make_norm_cfg(rows, d, out_dtype=A.E4M3, group=group, **kw), q, None, scale)
+        ref = np.maximum(np.stack([np.abs(want[:, i:i + g]).max(1) for i in range(0, d, g)], 1), 1e-30) / 448
+        assert (np.abs(host(scale) - ref) <= 2.0 ** -18 * ref).all()
+        v = want / np.repeat(ref, g, 1)[:, :d]
+        close(q, v, np.abs(v), "e4m3", 0, "q")
+    h = dev(host(x) + host(res), r_dtype)
+    dy, dh = draw(r, (rows, d), dtype)[0], draw(r, (rows, d), r_dtype)[0]
+    hh = np.where(zero[:, None], 1.0, host(h))
+    for up in (dh, None):
+        cfg = A.make_norm_cfg(rows, d, **kw)
+        space(cfg, A.atlas_norm_backward_workspace_bytes(cfg))
+        dx, dw = torch.empty_like(h), torch.empty(d, device="cuda")
+        A.atlas_norm_backward(h, w, dy, up, cfg, dx, dw)
+        uph = np.zeros((rows, d)) if up is None else host(up)
+        ref, mag = (R.norm_back(hh, host(w), host(dy), uph, 0.0, mag=m)[0] for m in (False, True))
+        close(dx, np.where(zero[:, None], uph, ref), mag, r_dtype, 0, "dx")
+        ref, mag = (R.norm_back(hh[~zero], host(w), host(dy)[~zero], None, 0.0, mag=m)[1] if (~zero).any() else np.zeros(d) for m in (False, True))
+        close(dw, ref, mag, "fp32", rows / 32, "dw")
+
+
