@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kLanes * kWarps)
           }
           if (EDGE && (q < t.t0 || q >= t.len)) g[i] = pair(0.f, 0.f);  // also where p is not finite
           dp[H][i] = g[i];
-          if (!EDGE || q < t1) {
+          if (!EDGE || (q >= t.t0 && q < t1)) {  // (zero times a state that is not finite is not zero)
             db[i] = pair_add(db[i], g[i]);
 #pragma unroll
             for (int k = 0; k < W; ++k) dw[k][i] = pair_fma(g[i], win[k][i], dw[k][i]);

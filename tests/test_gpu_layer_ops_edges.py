@@ -89,3 +89,27 @@ def test_rows_of_zeros_without_eps(rows, d, dtype, r_dtype):
         close(dw, ref, mag, "fp32", rows / 32, "dw")
 
 
+@pytest.mark.parametrize("dtype,C", [("bf16", 72), ("fp32", 5)])
+def test_conv_gradient_of_states_that_are_not_finite(dtype, C):
+    """An empty sequence has no term of dw, whatever its state holds; and the tap of the current token has
+    none of any state."""
+    r, W = rng(33, C), 4
+    start = torch.tensor([0, 20, 20, 29], dtype=torch.int32, device="cuda")
+    d = Conv(r, 3, 0, C, W, dtype, act=False, packed_rows=29)
+    cfg = A.make_conv_cfg(3, 29, C, W, act=A.ACT_NONE, dtype=CODE[dtype], seq_start=start)
+    space(cfg, A.atlas_conv_backward_workspace_bytes(cfg))
+    out = []
+    for bad in (None, 1, 0):
+        s = d.s.clone()
+        if bad is not None:
+            s[bad] = float("nan")
+        o = [torch.zeros_like(d.x), torch.zeros(C, W, device="cuda"), torch.zeros(C, device="cuda"), d.ds.clone()]
+        A.atlas_conv_backward(d.x, d.w, d.b, cfg, s, d.dy, o[3], *o[:3])
+        out.append(o)
+        torch.cuda.synchronize()
+    plain, empty, first = out
+    assert all(torch.equal(p, q) for p, q in zip(plain, empty))
+    assert torch.equal(empty[3][1], d.ds[1])
+    assert torch.equal(plain[1][:, W - 1], first[1][:, W - 1]) and torch.isnan(first[1][:, :W - 1]).all()
+
+
