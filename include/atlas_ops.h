@@ -123,9 +123,11 @@ int atlas_norm_backward(const void* h, const void* weight, const void* dy, const
  * The arrays on the device cannot be checked before the launch.  The kernels check
  * them: a sequence whose rows are not 0 <= seq_start[b] <= seq_start[b + 1] <= L, whose
  * slot is >= n_slots, or whose slot an earlier sequence has too, is left out like padding, and
- * *status_dev (when given) is set to ATLAS_ERR_INVALID.  (Slots have to differ because two
- * sequences with one state would race.  A backward call with a bad seq_start reports it and
- * stays inside its tensors; its outputs are then not defined.) */
+ * so is every sequence from the first fall of seq_start on (seq_start[b + 1] < seq_start[b]),
+ * behind which rows could belong to two; *status_dev (when given) is set to
+ * ATLAS_ERR_INVALID.  (Slots have to differ because two sequences with one state would
+ * race.  A backward call with a bad seq_start reports it and stays inside its tensors; its
+ * outputs are then not defined.) */
 
 /* ------------------------------------------------------------------ conv
  *   p_t[c] = bias[c] + sum_{k < W} weight[c][k] x_{t - W + 1 + k}[c],   y = SiLU(p) or p

@@ -94,9 +94,10 @@ __global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kerne
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
+  const int rising = seq_rising(a.s);
   const long tile = (long)blockIdx.x * kWarps + threadIdx.y;
   SeqTile t;
-  if (tile >= tiles || !seq_tile(a.s, tile, TT, t) || c >= a.C) return;
+  if (tile >= tiles || !seq_tile(a.s, rising, tile, TT, t) || c >= a.C) return;
   const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
   T* y = reinterpret_cast<T*>(a.y) + y_at(a, t, 0, c);
   pair32 w[W][N], b[N], win[W][N];
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(kLanes * kWarps)
   Ring<T, V>& ring = reinterpret_cast<Ring<T, V>*>(smem)[threadIdx.y];
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
+  const int rising = seq_rising(a.s);
   pair32 w[W][N], b[N], dw[W][N], db[N];
   load_taps<V, W>(a, c, w, b);
 #pragma unroll
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kLanes * kWarps)
   for (long tile = (long)blockIdx.x * kWarps + threadIdx.y; tile < tiles;
        tile += (long)gridDim.x * kWarps) {
     SeqTile t;
-    if (!seq_tile(a.s, tile, TT, t)) continue;
+    if (!seq_tile(a.s, rising, tile, TT, t)) continue;
     const int t1 = min(t.t0 + TT, t.len), q0 = t.t0 - H, q1 = t1 + H;
     const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + cc;
     const T* dy = reinterpret_cast<const T*>(a.dy) + y_at(a, t, 0, cc);
@@ -387,12 +389,13 @@ __global__ void __launch_bounds__(256)
     }
   } else if (a.dstate) {
     const long n = (long)a.s.B * (W - 1) * a.C;
+    const int rising = seq_rising(a.s);
     for (long i = (long)(blockIdx.x - nsum) * 256 + threadIdx.x; i < n;
          i += (long)(gridDim.x - nsum) * 256) {
       if (a.s.start) {  // sequences that are left out keep what they had
         const int b = (int)(i / ((long)(W - 1) * a.C));
         const int st = a.s.start[b], e = a.s.start[b + 1];
-        if (st < 0 || e < st || e > a.s.L) continue;
+        if (b >= rising || st < 0 || e > a.s.L) continue;
       }
       a.dstate[i] = ds[i];
     }

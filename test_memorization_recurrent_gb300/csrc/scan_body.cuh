@@ -202,6 +202,7 @@ struct Segments {
   float *h, *dt;                  // [segments][D][N], [segments][D]
   float *g, *keep_h, *keep_dt;    // [segments][D][N], [segments][nsub][D][N], [segments][nsub][D]
   int nsub;
+  int* rising;                    // seq_rising, from kEnds and kKeep for the kernels behind them
 };
 
 // kOut starts from the sequence's state, kJoin from the segments in front, seg.h.  kEnds starts a sequence's first segment from its state, which the last
@@ -221,8 +222,10 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
   Shared& s = *reinterpret_cast<Shared*>(smem);
   if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, 2 * kThreads);
   const long seg = blockIdx.x;
+  const int rising = !JOIN || !a.s.start ? seq_rising(a.s) : *sg.rising;
+  if ((ENDS || KEEP) && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *sg.rising = rising;
   SeqTile t;
-  if (!seq_tile(a.s, seg, sg.S, t)) return;
+  if (!seq_tile(a.s, rising, seg, sg.S, t)) return;
   const int end = min(t.t0 + sg.S, t.len);
   if (ENDS && end == t.len) return;  // (the last segment, or the only one)
   const Channels k = channels_at<P::kCB>(a, blockIdx.y);
@@ -596,7 +599,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
     }
   }
   SeqTile t;
-  if (!seq_tile(a.s, b, 1, t)) return;
+  if (!seq_tile(a.s, a.s.B, b, 1, t)) return;
   if (a.h_in && t.carry) {
 #pragma unroll
     for (int i = 0; i < kTokenU; ++i)
@@ -640,10 +643,12 @@ inline int segment_tokens(const ScanArgs& a, long blocks_per_seq) {
   return (int)S;
 }
 
+constexpr size_t kRisingBytes = 16;  // at the workspace's start; a word, the rest for alignment
+
 template <int LN>
 size_t workspace(const ScanArgs& a) {
   const int S = segment_tokens(a, blocks_over<Shape<LN>::kCB>(a));
-  return S ? (size_t)seq_tiles(a.s, S) * a.D * (a.N + 1) * 4 : 0;
+  return S ? kRisingBytes + (size_t)seq_tiles(a.s, S) * a.D * (a.N + 1) * 4 : 0;
 }
 
 template <typename T, int V, int LN, Mode MODE, bool NV>
@@ -677,7 +682,8 @@ int forward(const ScanArgs& a, cudaStream_t st) {
   Segments sg = {};
   sg.S = segment_tokens(a, by);
   if (sg.S) {
-    sg.h = reinterpret_cast<float*>(a.ws);
+    sg.rising = reinterpret_cast<int*>(a.ws);
+    sg.h = reinterpret_cast<float*>(a.ws) + kRisingBytes / 4;
     sg.dt = sg.h + (size_t)seq_tiles(a.s, sg.S) * a.D * a.N;
     if (!segment_pass<T, V, LN, kEnds>(a, sg, st) || !segment_pass<T, V, LN, kJoin>(a, sg, st))
       return ATLAS_ERR_CUDA;

@@ -69,6 +69,7 @@ struct Back {
   float *seg_h, *seg_g, *seg_dt;  // [segs][D][N] (start state; adjoint behind the end), [segs][D]
   float *pA, *pD, *pb;      // [segs][D][N], [segs][D] twice
   float* pbc;               // [cb][rows][2][NP]
+  float* rising;            // a word, as an int: seq_rising
   size_t bytes;
   Back(const ScanArgs& a, void* ws) {
     cb = blocks_over<kBackCB<LN>>(a);
@@ -85,6 +86,7 @@ struct Back {
       q = p ? p + bytes : nullptr;
       bytes += (n + 3) / 4 * 4;
     };
+    take(rising, kRisingBytes / 4);
     take(keep_h, (size_t)segs * nsub * DN);
     take(keep_dt, (size_t)segs * nsub * D);
     take(seg_h, split ? segs * DN : 0);
@@ -96,8 +98,10 @@ struct Back {
     take(pbc, (size_t)cb * rows * 2 * Shape<LN>::kNP);
     bytes *= 4;
   }
+  // in the kernels behind the first
+  __device__ int rising_of(const SeqArgs& a) const { return a.start ? *reinterpret_cast<const int*>(rising) : a.B; }
   Segments segments() const {
-    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub};
+    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub, reinterpret_cast<int*>(rising)};
   }
 };
 
@@ -109,15 +113,16 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
   const int b = blockIdx.y;
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   long seg;
+  const int rising = w.rising_of(a.s);
   if (a.s.start) {
-    const int s = a.s.start[b], e = a.s.start[b + 1];
-    if (s < 0 || e < s || e > a.s.L) return;
+    const int s = a.s.start[b];
+    if (b >= rising || s < 0) return;
     seg = (long)s / w.S + b;
   } else {
     seg = (long)b * seq_tiles_of(a.s.L, w.S);
   }
   SeqTile t;
-  if (!seq_tile(a.s, seg, w.S, t) || i >= dn) return;
+  if (!seq_tile(a.s, rising, seg, w.S, t) || i >= dn) return;
   const int c = (int)(i / a.N);
   const float A2 = a.A[i] * ATLAS_LOG2E;
   const int n = seq_tiles_of(t.len, w.S);
@@ -210,8 +215,9 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
   Channels k = kb;  // this warp's
   k.c0 += wi * P::kCB;
   k.n = max(0, min(P::kCB, kb.n - wi * P::kCB));
+  const int rising = w.rising_of(a.s);
   SeqTile t;
-  const bool some = seq_tile(a.s, seg, w.S, t);
+  const bool some = seq_tile(a.s, rising, seg, w.S, t);
   const int end = some ? min(t.t0 + w.S, t.len) : 0;
   const int tiles = some ? (end - t.t0 + kSub - 1) / kSub : 0;
   const int first = tiles > 0 ? t.t0 + (tiles - 1) * kSub : 0;  // the last tile comes first

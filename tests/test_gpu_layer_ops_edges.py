@@ -113,3 +113,57 @@ def test_conv_gradient_of_states_that_are_not_finite(dtype, C):
     assert torch.equal(plain[1][:, W - 1], first[1][:, W - 1]) and torch.isnan(first[1][:, :W - 1]).all()
 
 
+STARTS = [[0, 1000, 200, 1200], [0, 700, 900, 400, 1300], [-3, 600, 1200], [0, 600, 5000], [0, 600, 5000, 900], [5, 3, 1300], [0, 0, 1300, 1299, 1300],
+          [4 * i for i in range(200)] + [796, 3] + [5 * i for i in range(120)]]
+
+
+@pytest.mark.parametrize("start", STARTS)
+@pytest.mark.parametrize("dtype,C,N", [("fp32", 5, 7), ("bf16", 72, 16)])
+def test_starts_that_fall(start, dtype, C, N):
+    """Sequences of several tiles and segments: those in front of the first fall whose rows are there are
+    computed, state too; rows and states of the others stay as they are."""
+    T, B, W = 1300, len(start) - 1, 4
+    fall = next((b for b in range(B) if start[b + 1] < start[b]), B)
+    good = [b for b in range(fall) if start[b] >= 0 and start[b + 1] <= T]
+    r = rng(36, B, C)
+    slots = r.permutation(B + 3)[:B]
+    slot, t = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in (slots, start))
+    used, kept = np.zeros(T, bool), np.ones(B + 3, bool)
+    for b in good:
+        used[start[b]:start[b + 1]], kept[slots[b]] = True, False
+    st, d = status(), Scan(r, B, 0, C, N, 1, dtype, n=B + 3, packed_rows=T)
+    cfg = A.make_scan_cfg(B, T, C, N, dtype=CODE[dtype], seq_start=t, slot=slot, n_slots=B + 3, status_dev=st)
+    assert A.atlas_scan_workspace_bytes(cfg) > 0  # segments
+    h = d.h.clone()
+    y = run_scan(d, cfg, h, h)
+    assert int(st) == A.ERR_INVALID
+    for b in good:
+        rows = slice(start[b], start[b + 1])
+        d.check(y[rows], h[slots[b]], rows, d.h_h[slots[b]], f"sequence {b}")
+    assert (host(y)[~used] == 77).all() and (host(h)[kept] == d.h_h[kept]).all()
+    st.zero_()
+    c = Conv(r, B, 0, C, W, dtype, n=B + 3, packed_rows=T)
+    cfg = A.make_conv_cfg(B, T, C, W, dtype=CODE[dtype], seq_start=t, slot=slot, n_slots=B + 3, status_dev=st)
+    y, new = torch.full_like(c.x, 77.0), c.s.clone()
+    A.atlas_conv_forward(c.x, c.w, c.b, cfg, y, new, new)
+    assert int(st) == A.ERR_INVALID
+    for b in good:
+        rows = slice(start[b], start[b + 1])
+        c.check(y[rows], new[slots[b]], rows, c.sh[slots[b]], dtype, f"sequence {b}")
+    assert (host(y)[~used] == 77).all() and (host(new)[kept] == c.sh[kept]).all()
+    # backward: reported, and nothing outside the rows is written
+    st.zero_()
+    cfg = A.make_conv_cfg(B, T, C, W, dtype=CODE[dtype], seq_start=t, status_dev=st)
+    space(cfg, A.atlas_conv_backward_workspace_bytes(cfg))
+    dx, ds = torch.full_like(c.x, 77.0), c.ds.clone()
+    A.atlas_conv_backward(c.x, c.w, c.b, cfg, c.s[:B].contiguous(), c.dy, ds, dx, torch.zeros(C, W, device="cuda"), torch.zeros(C, device="cuda"))
+    assert int(st) == A.ERR_INVALID and (host(dx)[~used] == 77).all()
+    assert all((host(ds)[b] == c.dsh[b]).all() for b in range(B) if b not in good)
+    st.zero_()
+    cfg = A.make_scan_cfg(B, T, C, N, dtype=CODE[dtype], seq_start=t, status_dev=st)
+    dh = d.dh.clone()
+    o = d.backward(cfg, d.h[:B].contiguous(), dh)
+    assert int(st) == A.ERR_INVALID and (host(o["dx"])[~used] == 77).all()
+    assert all((host(dh)[b] == d.dh_h[b]).all() for b in range(B) if b not in good)
+
+
