@@ -161,13 +161,7 @@ __global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kerne
         for (int k = 0; k < H; ++k) win[k][i] = win[k + 1][i];
       }
       const Pack<T, V> out = from_pairs<T, V>(p);
-      if (V == 1 || !a.hd || a.hd % V == 0) {
-        st_pack<T, V>(y + u * a.yt, out);
-      } else {  // a vector crosses heads
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-          reinterpret_cast<T*>(a.y)[y_at(a, t, t1 - left + u, c + j)] = out.e[j];
-      }
+      st_pack<T, V>(y + u * a.yt, out);  // (heads hold whole vectors: else V is 1)
     }
     x += U * a.xt;
     y += U * a.yt;
