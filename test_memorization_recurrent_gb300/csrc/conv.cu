@@ -21,8 +21,8 @@ int conv_backward_launch(const ConvArgs& a, cudaStream_t st) { return conv_run(a
 size_t conv_backward_workspace(const ConvArgs& a) {
   size_t most = 0;
   for (int V : {1, 4}) {
-    const long tiles = seq_tiles(a.s, conv::back_tile_tokens(a, V));
-    const size_t n = (size_t)conv::back_blocks(a, V, tiles) * (a.W + 1) * a.C;
+    const long share = seq_share(a.s, conv::workers(a, V, conv::kBackWarps), 1);
+    const size_t n = (size_t)conv::blocks_of(a, share) * (a.W + 1) * a.C;
     most = n > most ? n : most;
   }
   return (most + (size_t)a.s.B * (a.W - 1) * a.C) * 4;

@@ -5,13 +5,16 @@
 //   dp_t = dy_t SiLU'(p_t),  dx_s = sum_i w_{W-1-i} dp_{s+i},  dw_k = sum_t dp_t x_{t-W+1+k}
 //
 // Bound by memory: x (and dy) are read once and y (dx) written once.  A lane owns V adjacent
-// channels and walks the tokens of its tile with the last W - 1 inputs in registers, so that
-// only the tokens in front of a tile (and, backward, those behind it) are read twice.  V is
+// channels and walks the tokens of its worker's pieces of the sequences with the last W - 1 inputs in
+// registers, so that only the tokens in front of a piece (and, backward, those behind it) are read
+// twice.  Workers have equal shares of the rows: 65536 rows x 2048 channels take 102 us in eight
+// sequences, 104 in 256 equal ones, 105 with half of the rows in one of 256 (backward 182, 195, 196; with
+// tiles of a length that went by the number of sequences 6385 and 6223 us for the last).  V is
 // four: with eight, the taps, window and loads of a lane take 202 registers, and too few
 // warps are left to cover the latency.  8 x 4096 tokens x 2048 channels of bf16, four taps:
-// 126 us with eight, 59 us with four (4.6 TB/s); 24 warps an SM, 59 us, against 91 with 20,
-// 65 with 28, 78 with 32.  Backward: 104 us (3.9 TB/s; 672 with loads in the worker's turn, 150
-// with the ring but the edges' conditions at every token).
+// 126 us with eight, 59 with four, 53 (5.0 TB/s) without a second way to store, which spilled; 24
+// warps an SM, against 91 us with 20, 65 with 28, 78 with 32 where 24 took 59.  Backward: 103 us (3.9
+// TB/s; 672 with loads in the worker's turn, 150 with the ring but the edges' conditions at every token).
 #pragma once
 #include "ops_common.cuh"
 
@@ -19,7 +22,9 @@ namespace atlas {
 namespace conv {
 
 constexpr int kLanes = 32;  // channel vectors of a warp
-constexpr int kWarps = 4;   // tiles (forward) or workers (backward) of a block
+constexpr int kWarps = 4;   // workers of a block
+
+__device__ __forceinline__ long worker() { return (long)blockIdx.x * kWarps + threadIdx.y; }
 
 // Offset of channel c of token tok in y's layout.
 __device__ __forceinline__ long y_at(const ConvArgs& a, const SeqTile& t, int tok, int c) {
@@ -89,82 +94,83 @@ __device__ __forceinline__ void load_taps(const ConvArgs& a, int c, pair32 (*w)[
 }
 
 template <typename T, int V, int W>
-__global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kernel(ConvArgs a, int TT, long tiles) {
+__global__ void __launch_bounds__(kLanes * kWarps, W <= 4 ? 6 : 4) forward_kernel(ConvArgs a, long share) {
   constexpr int H = W - 1, N = kPairs<V>;
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
-  const int rising = seq_rising(a.s);
-  const long tile = (long)blockIdx.x * kWarps + threadIdx.y;
-  SeqTile t;
-  if (tile >= tiles || !seq_tile(a.s, rising, tile, TT, t) || c >= a.C) return;
-  const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
-  T* y = reinterpret_cast<T*>(a.y) + y_at(a, t, 0, c);
   pair32 w[W][N], b[N], win[W][N];
   load_taps<V, W>(a, c, w, b);
+  SeqWalk walk = seq_walk(a.s, seq_rising(a.s), worker(), share);
+  SeqTile t;
+  int t1;
+  while (seq_piece(a.s, walk, worker(), share, t, t1)) {
+    if (c >= a.C) continue;
+    const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
+    T* y = reinterpret_cast<T*>(a.y) + y_at(a, t, 0, c);
 #pragma unroll
-  for (int k = 0; k < H; ++k) {  // the last H inputs before the tile
-    const int tok = t.t0 - H + k;
-    Pack<T, V> v;
-    if (tok >= 0)
-      v = ld_pack<T, V>(x + (long)tok * a.xt);
-    else if (a.st_in && t.carry)  // t0 == 0: a tile is never shorter than H
-      v = ld_pack<T, V>(reinterpret_cast<const T*>(a.st_in) + ((long)t.slot * H + k) * a.C + c);
-    else
-      v.zero();
-    to_pairs<T, V>(v, win[k]);
-  }
-  // the first tile alone reads the state, so it also writes the new one (the buffers may
-  // be the same): the last H of (state, inputs)
-  if (a.st_out && t.t0 == 0) {
-    const T* s0 = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + (long)t.slot * H * a.C + c : nullptr;
-    T* o = reinterpret_cast<T*>(a.st_out) + (long)t.slot * H * a.C + c;
-    Pack<T, V> v[W];
-#pragma unroll
-    for (int k = 0; k < H; ++k) {
-      const int tok = t.len - H + k;
+    for (int k = 0; k < H; ++k) {  // the last H inputs before the piece
+      const int tok = t.t0 - H + k;
+      Pack<T, V> v;
       if (tok >= 0)
-        v[k] = ld_pack<T, V>(x + (long)tok * a.xt);
-      else if (s0)
-        v[k] = ld_pack<T, V>(s0 + (long)(tok + H) * a.C);
+        v = ld_pack<T, V>(x + (long)tok * a.xt);
+      else if (a.st_in && t.carry)  // t0 == 0: a later piece begins kLead rows or more into its sequence
+        v = ld_pack<T, V>(reinterpret_cast<const T*>(a.st_in) + ((long)t.slot * H + k) * a.C + c);
       else
-        v[k].zero();
+        v.zero();
+      to_pairs<T, V>(v, win[k]);
     }
+    // the first piece alone reads the state, so it also writes the new one (the buffers may
+    // be the same): the last H of (state, inputs)
+    if (a.st_out && t.t0 == 0) {
+      const T* s0 = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + (long)t.slot * H * a.C + c : nullptr;
+      T* o = reinterpret_cast<T*>(a.st_out) + (long)t.slot * H * a.C + c;
+      Pack<T, V> v[W];
 #pragma unroll
-    for (int k = 0; k < H; ++k) st_pack<T, V>(o + (long)k * a.C, v[k]);
-  }
-  const int t1 = min(t.t0 + TT, t.len);
-  constexpr int U = 8;  // tokens loaded ahead
-  x += (long)t.t0 * a.xt;
-  y += (long)t.t0 * a.yt;
-  for (int left = t1 - t.t0; left > 0; left -= U) {
-    Pack<T, V> in[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u < left) in[u] = ld_pack<T, V>(x + u * a.xt);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (u >= left) break;
-      to_pairs<T, V>(in[u], win[H]);
-      pair32 p[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[i] = b[i];
-#pragma unroll
-        for (int k = 0; k < W; ++k) p[i] = pair_fma(w[k][i], win[k][i], p[i]);
-        if (a.act == ATLAS_ACT_SILU) {
-          float lo, hi;
-          unpair(p[i], lo, hi);
-          p[i] = pair(siluf(lo), siluf(hi));
-        }
-#pragma unroll
-        for (int k = 0; k < H; ++k) win[k][i] = win[k + 1][i];
+      for (int k = 0; k < H; ++k) {
+        const int tok = t.len - H + k;
+        if (tok >= 0)
+          v[k] = ld_pack<T, V>(x + (long)tok * a.xt);
+        else if (s0)
+          v[k] = ld_pack<T, V>(s0 + (long)(tok + H) * a.C);
+        else
+          v[k].zero();
       }
-      const Pack<T, V> out = from_pairs<T, V>(p);
-      st_pack<T, V>(y + u * a.yt, out);  // (heads hold whole vectors: else V is 1)
+#pragma unroll
+      for (int k = 0; k < H; ++k) st_pack<T, V>(o + (long)k * a.C, v[k]);
     }
-    x += U * a.xt;
-    y += U * a.yt;
+    constexpr int U = 8;  // tokens loaded ahead
+    x += (long)t.t0 * a.xt;
+    y += (long)t.t0 * a.yt;
+    for (int left = t1 - t.t0; left > 0; left -= U) {
+      Pack<T, V> in[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u < left) in[u] = ld_pack<T, V>(x + u * a.xt);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u >= left) break;
+        to_pairs<T, V>(in[u], win[H]);
+        pair32 p[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          p[i] = b[i];
+#pragma unroll
+          for (int k = 0; k < W; ++k) p[i] = pair_fma(w[k][i], win[k][i], p[i]);
+          if (a.act == ATLAS_ACT_SILU) {
+            float lo, hi;
+            unpair(p[i], lo, hi);
+            p[i] = pair(siluf(lo), siluf(hi));
+          }
+#pragma unroll
+          for (int k = 0; k < H; ++k) win[k][i] = win[k + 1][i];
+        }
+        const Pack<T, V> out = from_pairs<T, V>(p);
+        st_pack<T, V>(y + u * a.yt, out);  // (heads hold whole vectors: else V is 1)
+      }
+      x += U * a.xt;
+      y += U * a.yt;
+    }
   }
 }
 
@@ -179,23 +185,22 @@ struct Ring {
   T dy[kStages<T>][kChunk][kLanes * V];
 };
 
-// A warp is a worker: it walks tiles and keeps dw and db of its channels in registers; the
+// A warp is a worker: it walks its pieces and keeps dw and db of its channels in registers; the
 // block adds its workers in a fixed order and writes one row of partial sums
-// part[block][(W + 1)][C].  A tile is a stream of positions from t0 - H to t1 + H: the inputs
-// in front of it (the state before a sequence's first token), its own tokens, and those whose
-// dp reaches back into it; dx of a position is complete H positions later.  Positions before a
-// sequence give dL/d state, into ds.  The stream is copied to shared memory kStages - 1
-// chunks ahead.
+// part[block][(W + 1)][C].  A piece of n tokens is a stream of positions from -H to n + H, counted from
+// its first token: the inputs in front of it (the state before a sequence's first token), its own
+// tokens, and those whose dp reaches back into it; dx of a position is complete H positions later.
+// Positions before a sequence give dL/d state, into ds.  The stream is copied to shared memory
+// kStages - 1 chunks ahead.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kLanes * kWarps)
-    backward_kernel(ConvArgs a, int TT, long tiles, float* part, float* ds) {
+    backward_kernel(ConvArgs a, long share, float* part, float* ds) {
   constexpr int H = W - 1, N = kPairs<V>, S = kStages<T>;
   extern __shared__ __align__(16) unsigned char smem[];
   const int lane = threadIdx.x, c = (blockIdx.y * kLanes + lane) * V;
   Ring<T, V>& ring = reinterpret_cast<Ring<T, V>*>(smem)[threadIdx.y];
   if (blockIdx.x == 0 && blockIdx.y == 0)
     seq_check(a.s, threadIdx.y * kLanes + lane, kLanes * kWarps);
-  const int rising = seq_rising(a.s);
   pair32 w[W][N], b[N], dw[W][N], db[N];
   load_taps<V, W>(a, c, w, b);
 #pragma unroll
@@ -208,20 +213,22 @@ __global__ void __launch_bounds__(kLanes * kWarps)
   constexpr int CV = V == 1 ? 1 : 16 / sizeof(T), CL = kLanes * V / CV, RP = kLanes / CL;
   const int cc = (blockIdx.y * kLanes) * V + lane % CL * CV;  // the channels this lane copies
   const bool cin = cc < a.C;
-  for (long tile = (long)blockIdx.x * kWarps + threadIdx.y; tile < tiles;
-       tile += (long)gridDim.x * kWarps) {
-    SeqTile t;
-    if (!seq_tile(a.s, rising, tile, TT, t)) continue;
-    const int t1 = min(t.t0 + TT, t.len), q0 = t.t0 - H, q1 = t1 + H;
-    const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, 0, a.xb, a.xt) + cc;
-    const T* dy = reinterpret_cast<const T*>(a.dy) + y_at(a, t, 0, cc);
+  SeqWalk walk = seq_walk(a.s, seq_rising(a.s), worker(), share);
+  SeqTile t;
+  int t1;
+  while (seq_piece(a.s, walk, worker(), share, t, t1)) {
+    const int n = t1 - t.t0, rest = t.len - t.t0;  // its tokens, those to the sequence's end
+    const bool first = t.t0 == 0;  // (else the positions in front of it are tokens)
+    const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, t.t0, a.xb, a.xt) + cc;
+    const T* dy = reinterpret_cast<const T*>(a.dy) + y_at(a, t, t.t0, cc);
     const T* st = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + ((long)t.b * H + H) * a.C + cc : nullptr;
     auto fetch = [&](int stage, int base) {
 #pragma unroll
       for (int r = 0; r < kChunk; r += RP) {
         const int u = r + lane / CL, q = base + u;
-        const bool fx = cin && q < t.len && (q >= 0 || st), fy = cin && q >= t.t0 && q < min(t.len, q1);
-        const T* px = !fx ? reinterpret_cast<const T*>(a.w) : q >= 0 ? x + (long)q * a.xt : st + (long)q * a.C;
+        const bool token = q >= 0 || !first;
+        const bool fx = cin && q < rest && (token || st), fy = cin && q >= 0 && q < min(rest, n + H);
+        const T* px = !fx ? reinterpret_cast<const T*>(a.w) : token ? x + (long)q * a.xt : st + (long)q * a.C;
         const T* py = fy ? dy + (long)q * a.yt : reinterpret_cast<const T*>(a.w);
         T* ox = &ring.x[stage][u][lane % CL * CV];
         T* oy = &ring.dy[stage][u][lane % CL * CV];
@@ -239,22 +246,22 @@ __global__ void __launch_bounds__(kLanes * kWarps)
     for (int k = 0; k < W; ++k)
 #pragma unroll
       for (int i = 0; i < N; ++i) win[k][i] = dp[k][i] = pair(0.f, 0.f);
-    T* dx = reinterpret_cast<T*>(a.dx) + seq_at(a.s, t, 0, a.xb, a.xt) + c;
+    T* dx = reinterpret_cast<T*>(a.dx) + seq_at(a.s, t, t.t0, a.xb, a.xt) + c;
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) {
-      fetch(k, q0 + k * kChunk);
+      fetch(k, k * kChunk - H);
       cp_commit();
     }
     int stage = 0;
-    // the positions of one chunk; EDGE: some of them are not plain tokens of the tile
+    // the positions of one chunk; EDGE: some of them are not plain tokens of the piece
     auto walk = [&](int base, auto edge) {
       constexpr bool EDGE = decltype(edge)::value;
       T* out = dx + (long)(base - H) * a.xt;
 #pragma unroll
       for (int u = 0; u < kChunk; ++u) {
         const int q = base + u;
-        if (EDGE && q >= q1) break;
+        if (EDGE && q >= n + H) break;
         pair32 g[N];
         to_pairs<T, V>(ld_pack<T, V>(&ring.x[stage][u][lane * V]), win[H]);
         to_pairs<T, V>(ld_pack<T, V>(&ring.dy[stage][u][lane * V]), g);
@@ -271,16 +278,16 @@ __global__ void __launch_bounds__(kLanes * kWarps)
             const pair32 s = pair(rcp(lo), rcp(hi));
             g[i] = pair_mul(g[i], pair_mul(s, pair_fma(p, pair_fma(s, pair(-1.f, -1.f), one), one)));
           }
-          if (EDGE && (q < t.t0 || q >= t.len)) g[i] = pair(0.f, 0.f);  // also where p is not finite
+          if (EDGE && (q < 0 || q >= rest)) g[i] = pair(0.f, 0.f);  // also where p is not finite
           dp[H][i] = g[i];
-          if (!EDGE || (q >= t.t0 && q < t1)) {  // (zero times a state that is not finite is not zero)
+          if (!EDGE || (q >= 0 && q < n)) {  // (zero times a state that is not finite is not zero)
             db[i] = pair_add(db[i], g[i]);
 #pragma unroll
             for (int k = 0; k < W; ++k) dw[k][i] = pair_fma(g[i], win[k][i], dw[k][i]);
           }
         }
         const int s = q - H;  // the position whose gradient is complete
-        if (!EDGE || s >= (t.t0 == 0 ? -H : t.t0)) {
+        if (!EDGE || s >= (first ? -H : 0)) {
           pair32 o[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -291,7 +298,7 @@ __global__ void __launch_bounds__(kLanes * kWarps)
           if (!EDGE) {
             if (c < a.C) st_pack<T, V>(out, from_pairs<T, V>(o));
           } else if (c < a.C) {
-            const int tail = s - (t.len - H);  // row of dL/d state_out that is this position
+            const int tail = s - (rest - H);  // row of dL/d state_out that is this position
             if (a.dstate && tail >= 0) {
               const float* d = a.dstate + ((long)t.b * H + tail) * a.C + c;
 #pragma unroll
@@ -321,12 +328,12 @@ __global__ void __launch_bounds__(kLanes * kWarps)
           }
       }
     };
-    for (int base = q0; base < q1; base += kChunk) {
+    for (int base = -H; base < n + H; base += kChunk) {
       cp_wait<S - 2>();
       __syncwarp();  // this chunk is there for all lanes, and the one before has been read
       fetch(stage == 0 ? S - 1 : stage - 1, base + (S - 1) * kChunk);
       cp_commit();
-      if (base >= t.t0 + H && base + kChunk <= min(t1, t.len - H))
+      if (base >= H && base + kChunk <= min(n, rest - H))
         walk(base, std::false_type());
       else
         walk(base, std::true_type());
@@ -398,49 +405,33 @@ __global__ void __launch_bounds__(256)
 
 inline long lane_groups(const ConvArgs& a, int V) { return (a.C + kLanes * V - 1) / (kLanes * V); }
 
-// Tokens per tile: as many tiles as warps fit (24 an SM at up to four taps), so that all run
-// at once and few tokens are read twice; at least 16, so that one tile alone touches the state.
-inline int tile_tokens(const ConvArgs& a, int V) {
-  const long n = 152 * 24 / lane_groups(a, V) / kWarps * kWarps;
-  // tiles a sequence; packed: in all, with one more for the end of each sequence
-  const long each = a.s.start ? n - a.s.B : n / (a.s.B < 1 ? 1 : a.s.B);
-  const long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
-  return (int)(TT < 16 ? 16 : TT);
-}
-
-// Workers of the backward pass: twelve warps an SM over the groups of channels; and as many
-// tiles as workers, none shorter than 16 tokens.
-inline long back_workers(const ConvArgs& a, int V) {
-  const long n = 152 * 12 / lane_groups(a, V) / kWarps * kWarps;
+// Workers over the groups of channels: as many warps as run at once, so that few tokens are read twice
+// (forward 24 an SM at up to four taps, backward twelve).
+inline long workers(const ConvArgs& a, int V, int an_sm) {
+  const long n = 152 * an_sm / lane_groups(a, V) / kWarps * kWarps;
   return n < kWarps ? kWarps : n;
 }
-inline int back_tile_tokens(const ConvArgs& a, int V) {
-  const long n = back_workers(a, V);
-  const long each = a.s.start ? n - a.s.B : n / (a.s.B < 1 ? 1 : a.s.B);
-  long TT = each > 1 ? (a.s.L + each - 1) / each : a.s.L;
-  return (int)(TT < 16 ? 16 : TT);
-}
-inline int back_blocks(const ConvArgs& a, int V, long tiles) {
-  const long n = back_workers(a, V) / kWarps, need = (tiles + kWarps - 1) / kWarps;
-  return (int)(n < need ? n : need);
+constexpr int kForwardWarps = 24, kBackWarps = 12;
+// Blocks for a share of units.
+inline long blocks_of(const ConvArgs& a, long share) {
+  const long n = (seq_units(a.s) + share - 1) / share;
+  return (n + kWarps - 1) / kWarps;
 }
 
 template <typename T, int V, int W>
 int forward(const ConvArgs& a, cudaStream_t st) {
-  const int TT = tile_tokens(a, V);
-  const long tiles = seq_tiles(a.s, TT);
-  const long bx = (tiles + kWarps - 1) / kWarps;
+  const long share = seq_share(a.s, workers(a, V, kForwardWarps), 4);
+  const long bx = blocks_of(a, share);
   const long by = lane_groups(a, V);
-  if (bx > 0x7FFFFFFFL || by > 65535) return ATLAS_ERR_UNSUPPORTED;
-  forward_kernel<T, V, W><<<dim3((unsigned)bx, (unsigned)by), dim3(kLanes, kWarps), 0, st>>>(a, TT, tiles);
+  if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
+  forward_kernel<T, V, W><<<dim3((unsigned)bx, (unsigned)by), dim3(kLanes, kWarps), 0, st>>>(a, share);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
 
 template <typename T, int V, int W>
 int backward(const ConvArgs& a, cudaStream_t st) {
-  const int TT = back_tile_tokens(a, V);
-  const long tiles = seq_tiles(a.s, TT);
-  const int n = back_blocks(a, V, tiles);
+  const long share = seq_share(a.s, workers(a, V, kBackWarps), 1);
+  const int n = (int)blocks_of(a, share);
   const long by = lane_groups(a, V);
   if (by > 65535) return ATLAS_ERR_UNSUPPORTED;
   float* ds = reinterpret_cast<float*>(a.ws);
@@ -452,7 +443,7 @@ int backward(const ConvArgs& a, cudaStream_t st) {
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATLAS_ERR_CUDA;
   if (n > 0)
-    f<<<dim3((unsigned)n, (unsigned)by), dim3(kLanes, kWarps), smem, st>>>(a, TT, tiles, part, ds);
+    f<<<dim3((unsigned)n, (unsigned)by), dim3(kLanes, kWarps), smem, st>>>(a, share, part, ds);
   const int nsum = ((W + 1) * a.C + 31) / 32;
   const long moved = a.dstate ? ((long)a.s.B * (W - 1) * a.C + 255) / 256 : 0;
   finish_kernel<T><<<nsum + (unsigned)(moved < 1024 ? moved : 1024), 256, 0, st>>>(a, n, part, ds);

@@ -250,26 +250,48 @@ __device__ __forceinline__ int seq_rising(const SeqArgs& a) {
   return first;
 }
 
-// Which tile number `i` is; false when it is none (or its sequence is left out).  rising: what
-// seq_rising gave (0: the first sequence falls, and the search ends there).  Called by whole warps with
-// the same i.
+// The last sequence whose first tile number is not above i, of the first `rising` (0: the first sequence
+// falls, and the search ends there).  32 candidates at a time, by a whole warp.  Sequence b's first number is clamp(start[b]) / TT + b * each.
+__device__ __forceinline__ int seq_search(const SeqArgs& a, int rising, long i, int TT, int each) {
+  int lo = 0, n = a.B;  // (not `rising`, whose load may be under way)
+  const int lane = threadIdx.x & 31;
+  while (n > 1) {
+    const int step = (n + 31) / 32, j = lane * step;
+    bool le = false;
+    if (j < n) {
+      const int s = min(max(a.start[lo + j], 0), a.L);
+      le = j == 0 || (lo + j < rising && (long)s / TT + (long)(lo + j) * each <= i);
+    }
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
+    const int last = 31 - __clz((int)m);  // of the candidates not above i (the first always counts)
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+// The state of sequence t.b; false when it has none of its own and is left out.  By a whole warp.
+__device__ __forceinline__ bool seq_state(const SeqArgs& a, SeqTile& t) {
+  t.slot = t.b;
+  if (a.slot) {
+    t.slot = a.slot[t.b];
+    const int lane = threadIdx.x & 31;  // (of the warp's lanes, each looks at some)
+    bool bad = t.slot < 0 || t.slot >= a.n_slots;
+    for (int j = lane; j < t.b; j += 32) bad |= a.slot[j] == t.slot;
+    if (__any_sync(0xFFFFFFFFu, bad)) {
+      if (a.status && t.slot >= 0 && t.t0 == 0 && lane == 0) *a.status = ATLAS_ERR_INVALID;
+      return false;
+    }
+  }
+  t.carry = a.carry ? a.carry[t.b] != 0 : true;
+  return true;
+}
+
+// Which tile number `i` is; false when it is none (or its sequence is left out).  Called by whole
+// warps with the same i.
 __device__ __forceinline__ bool seq_tile(const SeqArgs& a, int rising, long i, int TT, SeqTile& t) {
   if (a.start) {
-    // the last sequence whose first number is not above i, 32 candidates at a time
-    int lo = 0, n = max(rising, 1);
-    const int lane = threadIdx.x & 31;
-    while (n > 1) {
-      const int step = (n + 31) / 32, j = lane * step;
-      bool le = false;
-      if (j < n) {
-        const int s = min(max(a.start[lo + j], 0), a.L);
-        le = j == 0 || (long)s / TT + lo + j <= i;
-      }
-      const unsigned m = __ballot_sync(0xFFFFFFFFu, le);
-      const int last = 31 - __clz((int)m);  // of the candidates not above i (the first always counts)
-      lo += last * step;
-      n = min(step, n - last * step);
-    }
+    const int lo = seq_search(a, rising, i, TT, 1);
     const int s = a.start[lo], e = a.start[lo + 1];
     if (s < 0 || e < s || e > a.L) return false;  // reported by seq_check
     t.b = lo;
@@ -285,19 +307,77 @@ __device__ __forceinline__ bool seq_tile(const SeqArgs& a, int rising, long i, i
     t.first = 0;
     t.len = a.L;
   }
-  t.slot = t.b;
-  if (a.slot) {
-    t.slot = a.slot[t.b];
-    const int lane = threadIdx.x & 31;  // (of the warp's lanes, each looks at some)
-    bool bad = t.slot < 0 || t.slot >= a.n_slots;
-    for (int j = lane; j < t.b; j += 32) bad |= a.slot[j] == t.slot;
-    if (__any_sync(0xFFFFFFFFu, bad)) {
-      if (a.status && t.slot >= 0 && t.t0 == 0 && lane == 0) *a.status = ATLAS_ERR_INVALID;
-      return false;
+  return seq_state(a, t);
+}
+
+// Rows dealt to workers in equal shares, whatever the sequences' lengths.  Sequence b has the units from
+// clamp(start[b]) + b kStart on: kStart for its start (what a worker needs to begin with a sequence takes
+// about as long as that many rows) and one a row; worker w takes the units w * share .., and walks
+// what they hold of one sequence after the other.  A cut among a sequence's first kLead rows moves to the
+// nearer end of them, so a piece that begins later has no state in its reach (moved to the start, and
+// from 16 rows, they made some workers half as long again).
+constexpr int kStart = 16, kLead = 8;
+static_assert(ATLAS_CONV_MAX_W - 1 <= kLead, "a state reaches kLead rows");
+inline long seq_units(const SeqArgs& a) {
+  return a.B == 0 ? 0 : (a.start ? (long)a.L : (long)a.B * a.L) + (long)a.B * kStart;
+}
+// Units a worker for at most n workers, 16 at least; short sequences (single tokens) have a worker each
+// for up to `rounds` times n of them.
+inline long seq_share(const SeqArgs& a, long n, int rounds) {
+  if (a.B < 1) return 1;
+  const long u = seq_units(a), B = a.B, one = (u + B - 1) / B;
+  if (one <= kStart + 16 && B <= rounds * n) return one;
+  const long even = (u + n - 1) / n;
+  return even > 16 ? even : 16;
+}
+
+struct SeqWalk {
+  int b, end;  // the next sequence to look at, the number of sequences
+};
+
+// A worker's walk; rising as above.  Called by whole warps.
+__device__ __forceinline__ SeqWalk seq_walk(const SeqArgs& a, int rising, long worker, long share) {
+  const long u0 = worker * share;
+  if (a.start) return SeqWalk{seq_search(a, rising, u0, 1, kStart), rising};
+  const unsigned each = (unsigned)a.L + kStart;
+  return SeqWalk{(int)min(u0 >> 32 ? u0 / each : (long)((unsigned)u0 / each), (long)a.B), a.B};
+}
+
+// The next piece: tokens t.t0 .. t1 of a sequence (none of an empty one), its start and state with it when
+// t0 is 0.  False behind the last.
+__device__ __forceinline__ bool seq_piece(const SeqArgs& a, SeqWalk& w, long worker, long share, SeqTile& t,
+                                          int& t1) {
+  const long u0 = worker * share, u1 = u0 + share;
+  while (w.b < w.end) {
+    t.b = w.b++;
+    long unit;
+    bool ok = true;
+    if (a.start) {
+      const int s = a.start[t.b], e = a.start[t.b + 1];
+      unit = (long)min(max(s, 0), a.L) + (long)t.b * kStart;
+      t.first = s;
+      t.len = e - s;
+      ok = s >= 0 && e <= a.L;  // else reported by seq_check
+    } else {
+      unit = t.b * ((long)a.L + kStart);
+      t.first = 0;
+      t.len = a.L;
     }
+    if (unit >= u1) break;
+    if (!ok) continue;
+    const auto cut = [&](long v) {  // the token in front of which unit v cuts; behind the last: len + 1
+      const long r = v - kStart;
+      return r >= t.len ? t.len + 1L : r >= kLead ? r : r >= kLead / 2 ? (long)kLead : 0L;
+    };
+    const long from = cut(u0 - unit), to = cut(u1 - unit);
+    if (from >= to) continue;
+    t.t0 = (int)from;
+    t1 = (int)min(to, (long)t.len);
+    if (unit + kStart + t.len >= u1) w.b = w.end;  // the worker's last
+    if (seq_state(a, t)) return true;
   }
-  t.carry = a.carry ? a.carry[t.b] != 0 : true;
-  return true;
+  w.b = w.end;
+  return false;
 }
 
 // Report a bad seq_start: called by the threads of one block of the grid.

@@ -202,7 +202,8 @@ struct Segments {
   float *h, *dt;                  // [segments][D][N], [segments][D]
   float *g, *keep_h, *keep_dt;    // [segments][D][N], [segments][nsub][D][N], [segments][nsub][D]
   int nsub;
-  int* rising;                    // seq_rising, from kEnds and kKeep for the kernels behind them
+  int* rising;                    // how many sequences count, for the kernels behind the one that finds it
+  int known;                      // whether it is there already
 };
 
 // kOut starts from the sequence's state, kJoin from the segments in front, seg.h.  kEnds starts a sequence's first segment from its state, which the last
@@ -222,8 +223,8 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
   Shared& s = *reinterpret_cast<Shared*>(smem);
   if (blockIdx.x == 0 && blockIdx.y == 0) seq_check(a.s, threadIdx.x, 2 * kThreads);
   const long seg = blockIdx.x;
-  const int rising = !JOIN || !a.s.start ? seq_rising(a.s) : *sg.rising;
-  if ((ENDS || KEEP) && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *sg.rising = rising;
+  const int rising = !a.s.start ? a.s.B : sg.known ? *sg.rising : seq_rising(a.s);
+  if ((ENDS || KEEP) && !sg.known && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *sg.rising = rising;
   SeqTile t;
   if (!seq_tile(a.s, rising, seg, sg.S, t)) return;
   const int end = min(t.t0 + sg.S, t.len);
@@ -651,6 +652,19 @@ size_t workspace(const ScanArgs& a) {
   return S ? kRisingBytes + (size_t)seq_tiles(a.s, S) * a.D * (a.N + 1) * 4 : 0;
 }
 
+// How many sequences of a packed batch count, ahead of the first pass when they are many: its blocks
+// would each look at all of them (4000 short sequences x 512 channels: 845 us, 678 so).
+template <typename T>
+__global__ void __launch_bounds__(1024) rising_kernel(SeqArgs a, int* out) {
+  const int rising = seq_rising(a);
+  if (threadIdx.x == 0) *out = rising;
+}
+template <typename T>
+void find_rising(const ScanArgs& a, Segments& sg, cudaStream_t st) {
+  sg.known = a.s.start && a.s.B > 2 * kThreads;
+  if (sg.known) rising_kernel<T><<<1, 1024, 0, st>>>(a.s, sg.rising);
+}
+
 template <typename T, int V, int LN, Mode MODE, bool NV>
 bool segment_pass(const ScanArgs& a, const Segments& sg, cudaStream_t st) {
   const dim3 grid((unsigned)seq_tiles(a.s, sg.S), blocks_over<Shape<LN>::kCB>(a));
@@ -685,8 +699,10 @@ int forward(const ScanArgs& a, cudaStream_t st) {
     sg.rising = reinterpret_cast<int*>(a.ws);
     sg.h = reinterpret_cast<float*>(a.ws) + kRisingBytes / 4;
     sg.dt = sg.h + (size_t)seq_tiles(a.s, sg.S) * a.D * a.N;
-    if (!segment_pass<T, V, LN, kEnds>(a, sg, st) || !segment_pass<T, V, LN, kJoin>(a, sg, st))
-      return ATLAS_ERR_CUDA;
+    find_rising<T>(a, sg, st);
+    if (!segment_pass<T, V, LN, kEnds>(a, sg, st)) return ATLAS_ERR_CUDA;
+    sg.known = 1;
+    if (!segment_pass<T, V, LN, kJoin>(a, sg, st)) return ATLAS_ERR_CUDA;
   } else {
     sg.S = a.s.L > 0 ? a.s.L : 1;
     if (!segment_pass<T, V, LN, kOut>(a, sg, st)) return ATLAS_ERR_CUDA;

@@ -69,7 +69,7 @@ struct Back {
   float *seg_h, *seg_g, *seg_dt;  // [segs][D][N] (start state; adjoint behind the end), [segs][D]
   float *pA, *pD, *pb;      // [segs][D][N], [segs][D] twice
   float* pbc;               // [cb][rows][2][NP]
-  float* rising;            // a word, as an int: seq_rising
+  float* rising;            // a word, as an int: how many sequences count
   size_t bytes;
   Back(const ScanArgs& a, void* ws) {
     cb = blocks_over<kBackCB<LN>>(a);
@@ -101,7 +101,7 @@ struct Back {
   // in the kernels behind the first
   __device__ int rising_of(const SeqArgs& a) const { return a.start ? *reinterpret_cast<const int*>(rising) : a.B; }
   Segments segments() const {
-    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub, reinterpret_cast<int*>(rising)};
+    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub, reinterpret_cast<int*>(rising), 0};
   }
 };
 
@@ -112,23 +112,22 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
   const long dn = (long)a.D * a.N;
   const int b = blockIdx.y;
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
-  long seg;
-  const int rising = w.rising_of(a.s);
+  int s = 0, len = a.s.L;
   if (a.s.start) {
-    const int s = a.s.start[b];
-    if (b >= rising || s < 0) return;
-    seg = (long)s / w.S + b;
-  } else {
-    seg = (long)b * seq_tiles_of(a.s.L, w.S);
+    const int e = a.s.start[b + 1], rising = w.rising_of(a.s);
+    s = a.s.start[b];
+    if (b >= rising || s < 0 || e < s || e > a.s.L) return;
+    len = e - s;
   }
-  SeqTile t;
-  if (!seq_tile(a.s, rising, seg, w.S, t) || i >= dn) return;
+  if (i >= dn) return;
+  const bool carry = a.s.carry ? a.s.carry[b] != 0 : true;
+  const long seg = a.s.start ? (long)s / w.S + b : (long)b * seq_tiles_of(a.s.L, w.S);
   const int c = (int)(i / a.N);
   const float A2 = a.A[i] * ATLAS_LOG2E;
-  const int n = seq_tiles_of(t.len, w.S);
+  const int n = seq_tiles_of(len, w.S);
   // eight segments' values are under way at a time
   constexpr int U = 8;
-  float h = a.h_in && t.carry ? a.h_in[(long)b * dn + i] : 0.f;
+  float h = a.h_in && carry ? a.h_in[(long)b * dn + i] : 0.f;
   for (int k0 = 0; k0 < n; k0 += U) {
     float own[U], d[U];
 #pragma unroll
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
       g = ex2(A2 * d[j]) * g + own[j];
     }
   }
-  if (a.dh) a.dh[(long)b * dn + i] = t.carry ? g : 0.f;
+  if (a.dh) a.dh[(long)b * dn + i] = carry ? g : 0.f;
 }
 
 // Shared memory of back_kernel.
@@ -655,7 +654,9 @@ int backward(const ScanArgs& a, cudaStream_t st) {
   const int by = blocks_over<Shape<LN>::kCB>(a);
   if (by > 65535 || a.s.B > 65535 || w.segs > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   if (w.segs > 0) {
-    if (!segment_pass<T, V, LN, kKeep>(a, w.segments(), st)) return ATLAS_ERR_CUDA;
+    Segments sg = w.segments();
+    find_rising<T>(a, sg, st);
+    if (!segment_pass<T, V, LN, kKeep>(a, sg, st)) return ATLAS_ERR_CUDA;
     if (w.split)
       join_back_kernel<LN><<<dim3((unsigned)(((long)a.D * a.N + 255) / 256), a.s.B), 256, 0, st>>>(a, w);
     if (!(a.wide_n ? back_pass<T, VV, LN, true>(a, w, st) : back_pass<T, VV, LN, false>(a, w, st)))

@@ -167,3 +167,40 @@ def test_starts_that_fall(start, dtype, C, N):
     assert all((host(dh)[b] == d.dh_h[b]).all() for b in range(B) if b not in good)
 
 
+def device_us(f, n=5):
+    """Least time of a call on the device, of n after two."""
+    t = []
+    for _ in range(n + 2):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        t.append(a.elapsed_time(b) * 1e3)
+    return min(t[2:])
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_conv_time_goes_by_rows(back):
+    """65536 rows in 256 sequences, equal ones or one of half the rows, take about as long as in eight
+    (a share of work that goes by the number of sequences would make it many times as long)."""
+    T, C, W = 65536, 2048, 4
+    g = torch.Generator(device="cuda").manual_seed(0)
+    x, dy = (torch.randn(T, C, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w, b = torch.randn(C, W, generator=g, device="cuda").bfloat16(), torch.randn(C, generator=g, device="cuda").bfloat16()
+    y, dw, db = torch.empty_like(x), torch.empty(C, W, device="cuda"), torch.empty(C, device="cuda")
+    us = {}
+    for name, lens in (("eight", [T // 8] * 8), ("equal", [256] * 256), ("half", [T // 2] + [T // 2 // 255] * 254 + [T // 2 - 254 * (T // 2 // 255)])):
+        B = len(lens)
+        start = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+        s = torch.randn(B, W - 1, C, generator=g, device="cuda").bfloat16()
+        cfg = A.make_conv_cfg(B, T, C, W, seq_start=start)
+        if back:
+            space(cfg, A.atlas_conv_backward_workspace_bytes(cfg))
+            us[name] = device_us(lambda: A.atlas_conv_backward(x, w, b, cfg, s, dy, None, y, dw, db))
+        else:
+            us[name] = device_us(lambda: A.atlas_conv_forward(x, w, b, cfg, y, s))
+    print({k: round(v) for k, v in us.items()})
+    assert max(us.values()) <= 1.5 * us["eight"], us
+
+
