@@ -195,13 +195,20 @@ struct SegmentShared {
   int swap;
 };
 
+// Kept states lie by row, a place every kSub tokens of a sequence: a packed one's from start[b] / kSub + b
+// on, L / kSub + B places in all however short the sequences are.
+inline __host__ __device__ int kept_each(const SeqArgs& a) { return a.L / kSub + (a.L % kSub != 0); }
+inline long kept_places(const SeqArgs& a) { return a.start ? (long)a.L / kSub + a.B : (long)a.B * kept_each(a); }
+__device__ __forceinline__ long kept_at(const SeqArgs& a, const SeqTile& t) {  // of the token t.t0, a multiple of kSub
+  return (a.start ? (long)t.first / kSub + t.b : (long)t.b * kept_each(a)) + t.t0 / kSub;
+}
+
 // Where the segments' states go: h and dt of kEnds and kKeep (kJoin reads them), the
 // rest of kKeep.
 struct Segments {
   int S;                          // tokens of a segment
   float *h, *dt;                  // [segments][D][N], [segments][D]
-  float *g, *keep_h, *keep_dt;    // [segments][D][N], [segments][nsub][D][N], [segments][nsub][D]
-  int nsub;
+  float *g, *keep_h, *keep_dt;    // [segments][D][N], [places][D][N], [places][D]
   int* rising;                    // how many sequences count, for the kernels behind the one that finds it
   int known;                      // whether it is there already
 };
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
     float2 y[G];
   };
   // kKeep: the states in front of the next token, and the sum of dt so far
-  long kept = KEEP ? (seg * sg.nsub) * a.D + k.c0 + 2 * cp : 0;
+  long kept = KEEP ? kept_at(a.s, t) * a.D + k.c0 + 2 * cp : 0;
   auto keep = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -62,10 +62,10 @@ inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
 // Sizes and workspace of a backward call.
 template <int LN>
 struct Back {
-  int S, nsub, cb;  // segment tokens, kept states a segment, channel blocks
+  int S, cb;        // segment tokens, channel blocks
   bool split;       // more than one segment a sequence is possible
   long segs, rows;
-  float *keep_h, *keep_dt;  // [segs * nsub][D][N], [segs * nsub][D]
+  float *keep_h, *keep_dt;  // [places][D][N], [places][D]
   float *seg_h, *seg_g, *seg_dt;  // [segs][D][N] (start state; adjoint behind the end), [segs][D]
   float *pA, *pD, *pb;      // [segs][D][N], [segs][D] twice
   float* pbc;               // [cb][rows][2][NP]
@@ -76,7 +76,6 @@ struct Back {
     S = back_segment_tokens(a, cb);
     split = S != 0;
     if (!S) S = a.s.L > 0 ? a.s.L : 1;
-    nsub = (S + kSub - 1) / kSub;
     segs = seq_tiles(a.s, S);
     rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
     const size_t D = a.D, DN = D * a.N;
@@ -87,8 +86,8 @@ struct Back {
       bytes += (n + 3) / 4 * 4;
     };
     take(rising, kRisingBytes / 4);
-    take(keep_h, (size_t)segs * nsub * DN);
-    take(keep_dt, (size_t)segs * nsub * D);
+    take(keep_h, kept_places(a.s) * DN);
+    take(keep_dt, kept_places(a.s) * D);
     take(seg_h, split ? segs * DN : 0);
     take(seg_g, split ? segs * DN : 0);
     take(seg_dt, split ? segs * D : 0);
@@ -101,7 +100,7 @@ struct Back {
   // in the kernels behind the first
   __device__ int rising_of(const SeqArgs& a) const { return a.start ? *reinterpret_cast<const int*>(rising) : a.B; }
   Segments segments() const {
-    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, nsub, reinterpret_cast<int*>(rising), 0};
+    return Segments{S, split ? seg_h : nullptr, seg_dt, seg_g, keep_h, keep_dt, reinterpret_cast<int*>(rising), 0};
   }
 };
 
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
       constexpr int KN = P::kCB * LN / kThreads;
       static_assert(P::kCB * LN % kThreads == 0, "every lane has the same number of pieces");
       int kept_to[KN], kept_from[KN], kept_n[KN];  // places in the ring, offsets, states (of four)
-      const long at = (seg * w.nsub + tiles - 1) * a.D;
+      const long at = (kept_at(a.s, t) + tiles - 1) * a.D;
 #pragma unroll
       for (int i = 0; i < KN; ++i) {
         const int q = i * kThreads + lane, ch = q / LN, n = q % LN * 4;

@@ -1,0 +1,21 @@
+"""Layer operators without a GPU: sizes of workspaces."""
+import pytest
+
+import test_memorization_recurrent_gb300 as A
+from test_memorization_recurrent_gb300 import build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    build.build()
+
+
+@pytest.mark.parametrize("B,L,D,N", [(1000, 10000, 2048, 16), (64, 200, 512, 16), (5, 100000, 64, 16), (4000, 4000, 64, 64), (300, 70000, 33, 7)])
+def test_scan_backward_workspace_goes_by_rows(B, L, D, N):
+    """A packed batch keeps a state every eight rows and one more a sequence, and a few a segment; segments
+    have 128 tokens or more, and there is one more a sequence."""
+    got = A.atlas_scan_backward_workspace_bytes(A.make_scan_cfg(B, L, D, N, seq_start=16))
+    kept, segments, padded = L // 8 + B, L // 128 + B, 4 * max(2, 1 << (-(-N // 4) - 1).bit_length())
+    blocks = -(-D // (256 // (padded // 4)))  # of the main pass, over channels
+    most = 4 * D * ((N + 1) * kept + 3 * (N + 1) * segments) + 8 * padded * blocks * L + 256
+    assert got <= most, (got, most)
