@@ -227,7 +227,9 @@ struct SeqTile {
   bool carry; // whether it starts from its state
 };
 
-inline __host__ __device__ int seq_tiles_of(int L, int TT) { return L > TT ? (L + TT - 1) / TT : 1; }
+// (lengths may be next to 2^31: sums with a tile's do not fit)
+inline __host__ __device__ int seq_tiles_of(int L, int TT) { return L > TT ? (L - 1) / TT + 1 : 1; }
+__device__ __forceinline__ int seq_tile_end(const SeqTile& t, int TT) { return (int)min((unsigned)t.t0 + TT, (unsigned)t.len); }
 
 // Number of tile numbers for a description.
 inline __host__ __device__ long seq_tiles(const SeqArgs& a, int TT) {

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
   if ((ENDS || KEEP) && !sg.known && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *sg.rising = rising;
   SeqTile t;
   if (!seq_tile(a.s, rising, seg, sg.S, t)) return;
-  const int end = min(t.t0 + sg.S, t.len);
+  const int end = seq_tile_end(t, sg.S);
   if (ENDS && end == t.len) return;  // (the last segment, or the only one)
   const Channels k = channels_at<P::kCB>(a, blockIdx.y);
   const int tiles = (end - t.t0 + kTile - 1) / kTile;

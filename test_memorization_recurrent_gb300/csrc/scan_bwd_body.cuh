@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
   const int rising = w.rising_of(a.s);
   SeqTile t;
   const bool some = seq_tile(a.s, rising, seg, w.S, t);
-  const int end = some ? min(t.t0 + w.S, t.len) : 0;
+  const int end = some ? seq_tile_end(t, w.S) : 0;
   const int tiles = some ? (end - t.t0 + kSub - 1) / kSub : 0;
   const int first = tiles > 0 ? t.t0 + (tiles - 1) * kSub : 0;  // the last tile comes first
 

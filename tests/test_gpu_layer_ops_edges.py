@@ -204,3 +204,45 @@ def test_conv_time_goes_by_rows(back):
     assert max(us.values()) <= 1.5 * us["eight"], us
 
 
+def test_lengths_next_to_2_to_the_31():
+    """Rows up to the largest int: the last ones as they are in a short sequence."""
+    L, n, W = 2 ** 31 - 1, 50, 3
+    r = rng(35)
+    x = torch.zeros(L, 1, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = dev(r.standard_normal((n, 1)), "bf16")
+    w, dy = draw(r, (1, W), "bf16")[0], torch.zeros_like(x)
+    dy[-n:] = dev(r.standard_normal((n, 1)), "bf16")
+    got = []
+    for rows in (L, n):
+        y, s = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda"), torch.empty(1, W - 1, 1, dtype=torch.bfloat16, device="cuda")
+        A.atlas_conv_forward(x[-rows:], w, None, A.make_conv_cfg(1, rows, 1, W), y, None, s)
+        cfg = A.make_conv_cfg(1, rows, 1, W)
+        space(cfg, A.atlas_conv_backward_workspace_bytes(cfg))
+        dx, dw = torch.empty_like(y), torch.empty(1, W, device="cuda")
+        A.atlas_conv_backward(x[-rows:], w, None, cfg, None, dy[-rows:], None, dx, dw, None)
+        torch.cuda.synchronize()
+        got.append((y[-n:].clone(), s, dx[-n:].clone(), dw))
+    assert all(torch.equal(a, b) for a, b in zip(got[0][:3], got[1][:3]))
+    xs = host(x[-n:])
+    mag = R.conv_back(xs, host(w), None, True, np.zeros((W - 1, 1)), host(dy[-n:]), None, mag=True)
+    close(got[0][3], host(got[1][3]), mag["dw"], "fp32", n, "dw")
+    del y, dx, dy
+    # one channel, one state
+    dt, Bm, Cm = (torch.zeros(L, 1, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    for t in (dt, Bm, Cm):
+        t[-n:] = dev(r.standard_normal((n, 1)), "bf16")
+    a, got = torch.full((1, 1), -0.5, device="cuda"), []
+    for rows in (L, n):
+        cfg = A.make_scan_cfg(1, rows, 1, 1)
+        space(cfg, A.atlas_scan_workspace_bytes(cfg))
+        y, h = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 1, 1, device="cuda")
+        A.atlas_scan_forward(x[-rows:], dt[-rows:], a, Bm[-rows:], Cm[-rows:], None, None, None, cfg, y, None, h)
+        torch.cuda.synchronize()
+        got.append((y[-n:].clone(), h))
+    dth, Bh, Ch = (host(t[-n:]) for t in (dt, Bm, Cm))
+    ref, mag = (R.scan(xs, dth, host(a), Bh[:, None], Ch[:, None], None, None, None, True, np.zeros((1, 1)), 1, mag=m) for m in (False, True))
+    for y, h in got:
+        close(y, ref["y"], mag["y"], "bf16", n + 1, "y")
+        close(h[0], ref["h"], mag["h"], "fp32", n + 1, "h")
+
+

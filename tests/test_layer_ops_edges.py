@@ -19,3 +19,12 @@ def test_scan_backward_workspace_goes_by_rows(B, L, D, N):
     blocks = -(-D // (256 // (padded // 4)))  # of the main pass, over channels
     most = 4 * D * ((N + 1) * kept + 3 * (N + 1) * segments) + 8 * padded * blocks * L + 256
     assert got <= most, (got, most)
+
+
+def test_workspaces_of_lengths_next_to_2_to_the_31():
+    """Segments of the longest sequences are counted, not wrapped: two states and a decay each."""
+    for kw in (dict(B=1), dict(B=1, seq_start=16)):
+        cfg = A.make_scan_cfg(L=2 ** 31 - 1, D=1, N=1, **kw)
+        assert 0 < A.atlas_scan_workspace_bytes(cfg) < 1 << 20
+        assert 0 < A.atlas_scan_backward_workspace_bytes(cfg) < 1 << 39
+    assert 0 < A.atlas_conv_backward_workspace_bytes(A.make_conv_cfg(1, 2 ** 31 - 1, 1, 4)) < 1 << 20
