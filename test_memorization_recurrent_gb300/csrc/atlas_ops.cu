@@ -2,6 +2,10 @@
 // the choice between wide (16-byte) and element-wise accesses.  Every computation happens
 // in norm.cu, conv_*.cu and scan_*.cu.
 #include "atlas_ops.h"
+
+#include <algorithm>
+#include <initializer_list>
+
 #include "ops.h"
 
 using namespace atlas;
@@ -61,13 +65,28 @@ void strides(long& sb, long& st, long width, int L) {
   }
 }
 
-// Whether the rows of a tensor that is written lie apart: tokens of `width` elements, then
-// whole sequences (or sequences interleaved between tokens).
+struct Dim {
+  long n, stride;
+};
+// Whether the elements of a tensor that is written lie apart: blocks of `width` neighbours, along dimensions
+// nested in any order, each with a stride of at least what those inside it span.
+bool apart(std::initializer_list<Dim> dims, long width) {
+  Dim d[3];
+  int k = 0;
+  for (const Dim& v : dims) {
+    if (v.n == 0) return true;  // none
+    if (v.n > 1) d[k++] = v;
+  }
+  std::sort(d, d + k, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  long span = width;
+  for (int i = 0; i < k; ++i) {
+    if (d[i].stride < span) return false;
+    span += (d[i].n - 1) * d[i].stride;
+  }
+  return true;
+}
 bool apart(long sb, long st, long width, int B, int L, bool packed) {
-  if (st < 0 || sb < 0) return false;
-  if (L > 1 && st < width) return false;
-  if (packed || B <= 1 || L < 1) return true;
-  return sb >= (long)(L - 1) * st + width || (sb >= width && (L == 1 || st >= (long)(B - 1) * sb + width));
+  return apart({{packed ? 1 : B, sb}, {L, st}}, width);
 }
 
 // ------------------------------------------------------------------ conv
@@ -114,18 +133,7 @@ ConvArgs conv_args(const atlas_conv_cfg* c) {
 
 bool conv_y_apart(const ConvArgs& a) {
   if (!a.hd) return apart(a.yb, a.yt, a.C, a.s.B, a.s.L, a.s.start);
-  // heads inside tokens, or tokens inside heads; then sequences
-  const long nh = a.C / a.hd, L = a.s.L;
-  long span;
-  if (L > 1 && a.yt < a.hd) return false;
-  if (nh > 1 && a.yh < a.hd) return false;
-  if (nh <= 1 || L <= 1)
-    span = (nh - 1) * a.yh + (L > 0 ? L - 1 : 0) * a.yt + a.hd;
-  else if (a.yh >= (L - 1) * a.yt + a.hd || a.yt >= (nh - 1) * a.yh + a.hd)
-    span = (nh - 1) * a.yh + (L - 1) * a.yt + a.hd;
-  else
-    return false;
-  return a.s.start || a.s.B <= 1 || a.yb >= span;
+  return apart({{a.s.start ? 1 : a.s.B, a.yb}, {a.s.L, a.yt}, {a.C / a.hd, a.yh}}, a.hd);
 }
 
 // Whether rows, heads and states keep `bytes` (a power of two) aligned.

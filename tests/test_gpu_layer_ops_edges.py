@@ -246,3 +246,31 @@ def test_lengths_next_to_2_to_the_31():
         close(h[0], ref["h"], mag["h"], "fp32", n + 1, "h")
 
 
+@pytest.mark.parametrize("order", ["LBHd", "HBLd", "HLBd", "BLHd", "LHBd", "BHLd"])
+@pytest.mark.parametrize("B,L,H,hd,dtype", [(3, 37, 4, 8, "bf16"), (2, 20, 3, 5, "fp32"), (2, 1, 4, 8, "bf16"), (1, 9, 4, 8, "fp32")])
+def test_conv_heads_in_any_order(order, B, L, H, hd, dtype):
+    """y with batch, tokens and heads nested in any order, each with room to spare; dy read from there."""
+    r, W, C = rng(34, B, L, H), 4, H * hd
+    d = Conv(r, B, L, C, W, dtype)
+    size = dict(B=B, L=L, H=H, d=hd)
+    wide = torch.full([size[k] + (k == "H") for k in order[:3]] + [hd + 3], 77.0, dtype=DT[dtype], device="cuda")
+    y = wide.permute(*(order.index(k) for k in "BLHd"))[:, :, :H, :hd]
+    strides = (y.stride(0), y.stride(1), y.stride(2))
+    cfg = A.make_conv_cfg(B, L, C, W, dtype=CODE[dtype], head_dim=hd, y_strides=strides)
+    A.atlas_conv_forward(d.x, d.w, d.b, cfg, y, d.s)
+    flat = torch.empty_like(d.x)
+    A.atlas_conv_forward(d.x, d.w, d.b, A.make_conv_cfg(B, L, C, W, dtype=CODE[dtype]), flat, d.s)
+    assert torch.equal(y, flat.view(B, L, H, hd)) and int((wide != 77).sum()) <= y.numel()
+    y.copy_(d.dy.view(B, L, H, hd))
+    out = []
+    for c, dy in ((cfg, y), (A.make_conv_cfg(B, L, C, W, dtype=CODE[dtype]), d.dy)):
+        space(c, A.atlas_conv_backward_workspace_bytes(c))
+        o = [torch.zeros_like(d.x), torch.zeros(C, W, device="cuda"), torch.zeros(C, device="cuda"), d.ds.clone()]
+        A.atlas_conv_backward(d.x, d.w, d.b, c, d.s, dy, o[3], *o[:3])
+        out.append(o)
+        torch.cuda.synchronize()
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][3], out[1][3])
+    mag = sum(R.conv_back(d.xh[b], d.wh, d.bh, True, d.sh[b], d.dyh[b], d.dsh[b], mag=True)["dw"] for b in range(B))
+    close(out[0][1], host(out[1][1]), mag, "fp32", B * L, "dw")
+
+
