@@ -199,7 +199,8 @@ def _arg(t, code, extent, name, device):
             raise _error(f"{name} is not contiguous")
         if t.numel() < extent >> 1:
             raise _error(f"{name} has fewer than the {extent >> 1} elements the description names")
-    elif t.numel() < extent >> 1:  # a strided view ends further on than its elements count
+    elif t.numel() < extent >> 1 or not t.is_contiguous():
+        # a strided view ends further on than its elements count, an expanded one, whose elements repeat, before
         if t.is_contiguous() or t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < extent >> 1:
             raise _error(f"{name} ends before the {extent >> 1} elements the description names")
     return t.data_ptr()

@@ -28,3 +28,21 @@ def test_workspaces_of_lengths_next_to_2_to_the_31():
         assert 0 < A.atlas_scan_workspace_bytes(cfg) < 1 << 20
         assert 0 < A.atlas_scan_backward_workspace_bytes(cfg) < 1 << 39
     assert 0 < A.atlas_conv_backward_workspace_bytes(A.make_conv_cfg(1, 2 ** 31 - 1, 1, 4)) < 1 << 20
+
+
+def test_views_that_end_too_early_are_refused(monkeypatch):
+    """An expanded or narrowed view may count more elements than its storage holds: what is checked is the
+    storage from its first element on."""
+    torch = pytest.importorskip("torch")
+    from test_memorization_recurrent_gb300 import ops
+    monkeypatch.setattr(ops, "_types", (torch.float32, torch.bfloat16, torch.float16))
+    strided = 2 * 40  # 40 elements from the first to the last, not necessarily dense
+
+    def ok(t):
+        return ops._arg(t, A.F32, strided, "x", -1) == t.data_ptr()
+    row = torch.zeros(8)
+    wide = torch.zeros(5, 16)
+    assert ok(torch.zeros(40)) and ok(wide[:, :8]) and ok(torch.zeros(8, 5).t())
+    for bad in (row.expand(100, 8), row[:, None].expand(8, 100), torch.zeros(39), wide[3:, :8], torch.zeros(20, 2)[:, 0][1:], torch.zeros(10, 4)[4:].t()):
+        with pytest.raises(A.AtlasError):
+            ok(bad)
