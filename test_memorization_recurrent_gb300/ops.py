@@ -27,10 +27,12 @@ _int, _long, _vp, _size = ctypes.c_int, ctypes.c_long, ctypes.c_void_p, ctypes.c
 class _Cfg(ctypes.Structure):
     """A description whose tensors' extents are worked out once, and again after a field that
     they depend on is set."""
+    extents = None
+    home = None  # the device of the tensors it was made with
 
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
-        if name not in ("workspace", "workspace_bytes", "held", "extents"):
+        if name not in ("workspace", "workspace_bytes", "held", "extents", "home"):
             super().__setattr__("extents", None)
 
 
@@ -92,6 +94,7 @@ def make_norm_cfg(rows, d, dtype=BF16, r_dtype=None, w_dtype=None, out_dtype=Non
                        or_dtype(out_dtype), int(group), float(eps), int(x_stride), int(r_stride),
                        int(y_stride), _space(workspace, workspace_bytes), int(workspace_bytes))
     cfg.held = workspace
+    cfg.home = _home(workspace)
     return cfg
 
 
@@ -109,6 +112,7 @@ def make_conv_cfg(B, L, C, W, act=ACT_SILU, dtype=BF16, w_dtype=None, head_dim=0
                        _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
                        int(workspace_bytes))
     cfg.held = (seq_start, slot, carry, status_dev, workspace)  # as long as the description
+    cfg.home = _home(*cfg.held)
     return cfg
 
 
@@ -125,6 +129,7 @@ def make_scan_cfg(B, L, D, N, G=1, dtype=BF16, softplus=True, x_strides=(0, 0),
                        _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
                        int(workspace_bytes))
     cfg.held = (seq_start, slot, carry, status_dev, workspace)
+    cfg.home = _home(*cfg.held)
     return cfg
 
 
@@ -154,6 +159,14 @@ def _checked(t, dtype, n, name):
     return t.data_ptr()
 
 
+def _home(*tensors):
+    """The device of a description's tensors, which have to agree; None without any."""
+    home = {t.get_device() for t in tensors if t is not None and not isinstance(t, int)}
+    if len(home) > 1:
+        raise _error("the tensors of a description are on different devices")
+    return home.pop() if home else None
+
+
 def _sequences(B, seq_start, slot, n_slots, carry):
     return (_checked(seq_start, "int32", int(B) + 1, "seq_start"),
             _checked(slot, "int32", int(B), "slot"), int(n_slots),
@@ -177,11 +190,14 @@ def _setup():
     _fn = {name: getattr(lib, name) for name in OPS_EXPORTS}
 
 
-def _begin():
-    """The current device; before anything else of a call."""
+def _begin(cfg):
+    """The current device, that of the description's tensors too; before anything else of a call."""
     if _fn is None:
         _setup()
-    return _device()
+    device = _device()
+    if cfg.home is not None and cfg.home != device:
+        raise _error(f"the description's tensors are not on the current device (cuda:{device})")
+    return device
 
 
 def _arg(t, code, extent, name, device):
@@ -257,7 +273,7 @@ def atlas_norm_forward(x, residual, weight, cfg: AtlasNormCfg, y, residual_out=N
                        stream=None) -> None:
     """y = norm(x + residual) * weight; residual_out receives x + residual, scale the scales
     of an E4M3 output.  residual, weight and residual_out may be None."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, r, w, o, d, nx, nr, ny, ns = cfg.extents or _norm_extents(cfg)
     _call("atlas_norm_forward",
           (_arg(x, t, nx, "x", dev), _arg(residual, r, nr, "residual", dev), _arg(weight, w, d, "weight", dev), cfg,
@@ -272,7 +288,7 @@ def atlas_norm_backward_workspace_bytes(cfg: AtlasNormCfg) -> int:
 def atlas_norm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, stream=None) -> None:
     """dx = dL/dh and dw = dL/d weight from dy = dL/dy and (or None) dh, the gradient that
     reaches the residual stream from later layers."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, r, w, _, d, _, nr, ny, _ = cfg.extents or _norm_extents(cfg)
     _call("atlas_norm_backward",
           (_arg(h, r, nr, "h", dev), _arg(weight, w, d, "weight", dev), _arg(dy, t, ny, "dy", dev),
@@ -301,7 +317,7 @@ def atlas_conv_forward(x, weight, bias, cfg: AtlasConvCfg, y, state_in=None, sta
                        stream=None) -> None:
     """Short causal convolution of every channel; L = 1 is the single-token form.  state_in
     and state_out ([B or n_slots, W - 1, C]) may be None or the same tensor."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, w, C, nw, nx, ny, n, _ = cfg.extents or _conv_extents(cfg)
     _call("atlas_conv_forward",
           (_arg(x, t, nx, "x", dev), _arg(weight, w, nw, "weight", dev), _arg(bias, w, C, "bias", dev), cfg,
@@ -317,7 +333,7 @@ def atlas_conv_backward(x, weight, bias, cfg: AtlasConvCfg, state_in, dy, dstate
                         stream=None) -> None:
     """Gradients of the convolution (see include/atlas_ops.h); dstate is dL/d state_out on
     entry and dL/d state_in on return."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, w, C, nw, nx, ny, _, n = cfg.extents or _conv_extents(cfg)
     _call("atlas_conv_backward",
           (_arg(x, t, nx, "x", dev), _arg(weight, w, nw, "weight", dev), _arg(bias, w, C, "bias", dev), cfg,
@@ -351,7 +367,7 @@ def atlas_scan_forward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, y
                        h_out=None, stream=None) -> None:
     """Selective scan; L = 1 is the single-token form.  Dskip, z, dt_bias, h_in and h_out
     may be None; h_in and h_out ([B or n_slots, D, N]) may be the same tensor."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, D, dn, nx, nt, nb, nc, nz, ny, n, _ = cfg.extents or _scan_extents(cfg)
     _call("atlas_scan_forward",
           (_arg(x, t, nx, "x", dev), _arg(dt, t, nt, "dt", dev), _arg(A, F32, dn, "A", dev), _arg(Bm, t, nb, "B", dev),
@@ -364,7 +380,7 @@ def atlas_scan_backward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, 
                         ddt, dA, dB, dC, dD, dz, ddt_bias, stream=None) -> None:
     """Gradients of the scan (see include/atlas_ops.h); dh is dL/d h_out on entry and
     dL/d h_in on return."""
-    dev = _begin()
+    dev = _begin(cfg)
     t, D, dn, nx, nt, nb, nc, nz, ny, _, n = cfg.extents or _scan_extents(cfg)
     _call("atlas_scan_backward",
           (_arg(x, t, nx, "x", dev), _arg(dt, t, nt, "dt", dev), _arg(A, F32, dn, "A", dev), _arg(Bm, t, nb, "B", dev),

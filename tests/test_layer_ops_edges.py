@@ -46,3 +46,49 @@ def test_views_that_end_too_early_are_refused(monkeypatch):
     for bad in (row.expand(100, 8), row[:, None].expand(8, 100), torch.zeros(39), wide[3:, :8], torch.zeros(20, 2)[:, 0][1:], torch.zeros(10, 4)[4:].t()):
         with pytest.raises(A.AtlasError):
             ok(bad)
+
+
+class OnDevice:
+    """What the binding looks at of a tensor of a description."""
+
+    def __init__(self, dtype, n, device):
+        self.dtype, self.n, self.device, self.is_cuda = dtype, n, device, True
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return 4
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 16
+
+    def get_device(self):
+        return self.device
+
+
+def test_tensors_of_a_description_are_on_the_current_device(monkeypatch):
+    torch = pytest.importorskip("torch")
+    from test_memorization_recurrent_gb300 import ops
+    launched = []
+    monkeypatch.setattr(ops, "_types", (torch.float32, torch.bfloat16, torch.float16))
+    monkeypatch.setattr(ops, "_fn", {name: lambda *a: launched.append(a) or 0 for name in A.OPS_EXPORTS})
+    monkeypatch.setattr(ops, "_device", lambda: 0)
+    i32 = torch.int32
+    for device in (0, 1):
+        start, slot, space = OnDevice(i32, 3, device), OnDevice(i32, 2, device), OnDevice(torch.float32, 64, device)
+        cfgs = ((A.atlas_conv_forward, [16, 16, None], A.make_conv_cfg(2, 4, 8, 4, seq_start=start), [16]),
+                (A.atlas_scan_forward, [16] * 5 + [None] * 3, A.make_scan_cfg(2, 4, 8, 4, slot=slot, n_slots=2), [16]),
+                (A.atlas_norm_backward, [16, 16, 16, None], A.make_norm_cfg(2, 8, workspace=space, workspace_bytes=64), [16]))
+        for f, before, cfg, after in cfgs:
+            if device == 0:
+                f(*before, cfg, *after, stream=0)
+            else:
+                with pytest.raises(A.AtlasError):
+                    f(*before, cfg, *after, stream=0)
+    assert len(launched) == 3
+    with pytest.raises(A.AtlasError):  # not all on one device
+        A.make_conv_cfg(2, 4, 8, 4, seq_start=OnDevice(i32, 3, 0), slot=OnDevice(i32, 2, 1), n_slots=2)
