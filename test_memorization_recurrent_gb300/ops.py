@@ -241,6 +241,12 @@ def _bytes(fn, cfg):
     return n
 
 
+def _known(*codes):
+    for code in codes:
+        if not 0 <= code <= E4M3:
+            raise _error(f"no element type {code}")
+
+
 def _dense(n):
     return 2 * n + 1
 
@@ -263,6 +269,7 @@ def _rows(cfg, stride):
 # ------------------------------------------------------------------ norm
 
 def _norm_extents(c):
+    _known(c.dtype, c.r_dtype, c.w_dtype, c.out_dtype)
     groups = 1 if c.group <= 0 or c.group >= c.d else -(-c.d // c.group)
     c.extents = e = (c.dtype, c.r_dtype, c.w_dtype, c.out_dtype, _dense(c.d), _rows(c, c.x_stride), _rows(c, c.r_stride),
                      _rows(c, c.y_stride), _dense(c.rows * groups))
@@ -298,6 +305,7 @@ def atlas_norm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, strea
 # ------------------------------------------------------------------ conv
 
 def _conv_extents(c):
+    _known(c.dtype, c.w_dtype)
     hd, C, n = c.head_dim, c.C, c.n_slots if c.slot else c.B
     if c.L < 1 or c.B < 1:
         ny = 0
@@ -344,6 +352,7 @@ def atlas_conv_backward(x, weight, bias, cfg: AtlasConvCfg, state_in, dy, dstate
 # ------------------------------------------------------------------ scan
 
 def _scan_extents(c):
+    _known(c.dtype)
     D, gn, dn = c.D, c.G * c.N, c.D * c.N
     c.extents = e = (c.dtype, _dense(D), _dense(dn), _tokens(c, c.x_batch_stride, c.x_token_stride, D),
                      _tokens(c, c.dt_batch_stride, c.dt_token_stride, D),

@@ -92,3 +92,17 @@ def test_tensors_of_a_description_are_on_the_current_device(monkeypatch):
     assert len(launched) == 3
     with pytest.raises(A.AtlasError):  # not all on one device
         A.make_conv_cfg(2, 4, 8, 4, seq_start=OnDevice(i32, 3, 0), slot=OnDevice(i32, 2, 1), n_slots=2)
+
+
+@pytest.mark.parametrize("bad", [4, 9, -1])
+def test_unknown_element_types_are_refused_by_the_calls(monkeypatch, bad):
+    torch = pytest.importorskip("torch")
+    from test_memorization_recurrent_gb300 import ops
+    monkeypatch.setattr(ops, "_types", (torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn))
+    monkeypatch.setattr(ops, "_fn", {name: lambda *a: A.OK for name in A.OPS_EXPORTS})
+    monkeypatch.setattr(ops, "_device", lambda: -1)
+    x = torch.zeros(2, 8)
+    for f, args, cfg in ((A.atlas_norm_forward, [x, None, None], A.make_norm_cfg(2, 8, dtype=bad)), (A.atlas_norm_forward, [x, None, None], A.make_norm_cfg(2, 8, dtype=A.F32, out_dtype=bad)),
+                         (A.atlas_conv_forward, [x, x, None], A.make_conv_cfg(1, 2, 8, 2, dtype=A.F32, w_dtype=bad)), (A.atlas_scan_forward, [x] * 5 + [None] * 3, A.make_scan_cfg(1, 2, 8, 1, dtype=bad))):
+        with pytest.raises(A.AtlasError):
+            f(*args, cfg, x, stream=0)
