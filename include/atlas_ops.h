@@ -117,7 +117,7 @@ int atlas_norm_backward(const void* h, const void* weight, const void* dy, const
  * of an empty sequence is passed on unchanged.
  *   slot   NULL: sequence b has state b.  Else device int [B]: sequence b has state
  *          slot[b] of n_slots; a negative entry marks b as padding: nothing of it is
- *          read or written.
+ *          written and its state is not read (its rows may be).
  *   carry  NULL: every sequence starts from its state.  Else device bytes [B]: a
  *          sequence with carry[b] == 0 starts from zeros.
  * The arrays on the device cannot be checked before the launch.  The kernels check
