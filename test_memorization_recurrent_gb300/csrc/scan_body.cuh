@@ -134,6 +134,13 @@ __device__ __forceinline__ void steps_of(const ScanArgs& a, const Pack<T, V>& ra
   }
 }
 
+// A log2(e): exp(dt A) is 2 to its product with dt.  Held above -infinity, whose product with a step of 0 (as
+// places behind a sequence's end have) would not be 0.
+__device__ __forceinline__ float log2_decay(float A) {
+  const float v = A * ATLAS_LOG2E;
+  return v < -3.4e38f ? -3.4e38f : v;
+}
+
 // This lane's four states at p (one channel's N states), 0 past N.
 __device__ __forceinline__ void ld_states4(const float* p, int n0, int N, float* h) {
   if (N % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
@@ -444,7 +451,7 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
             for (int q = 0; q < 4; ++q)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                h4[j] = ex2(A4[j] * ATLAS_LOG2E * d[q]) * h4[j] + own[q][j];
+                h4[j] = ex2(log2_decay(A4[j]) * d[q]) * h4[j] + own[q][j];
           }
         }
       } else if (!KEEP && (!ENDS || seg == first) && a.h_in && t.carry) {
@@ -454,8 +461,8 @@ __global__ void __launch_bounds__(2 * kThreads, 7) segment_kernel(ScanArgs a, Se
       }
       if (ENDS && seg == first) st_states4(sg.h + (last * a.D + c) * a.N, n0, a.N, h4);
     }
-    A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
-    A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
+    A01[i] = pair(log2_decay(A4[0]), log2_decay(A4[1]));
+    A23[i] = pair(log2_decay(A4[2]), log2_decay(A4[3]));
     h01[i] = pair(h4[0], h4[1]);
     h23[i] = pair(h4[2], h4[3]);
   }
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
     float y = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      h[i][j] = ex2(dt * (A[i][j] * ATLAS_LOG2E)) * h[i][j] + dt * x[i] * B[i][j];
+      h[i][j] = ex2(dt * log2_decay(A[i][j])) * h[i][j] + dt * x[i] * B[i][j];
       y += h[i][j] * C[i][j];
     }
     lane_sums<1, LN, 1>(&y, lane);

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) join_back_kernel(ScanArgs a, Back<LN> w) 
   const bool carry = a.s.carry ? a.s.carry[b] != 0 : true;
   const long seg = a.s.start ? (long)s / w.S + b : (long)b * seq_tiles_of(a.s.L, w.S);
   const int c = (int)(i / a.N);
-  const float A2 = a.A[i] * ATLAS_LOG2E;
+  const float A2 = log2_decay(a.A[i]);
   const int n = seq_tiles_of(len, w.S);
   // eight segments' values are under way at a time
   constexpr int U = 8;
@@ -466,8 +466,8 @@ __global__ void __launch_bounds__(kBackThreads, 2) back_kernel(ScanArgs a, Back<
         ld_states4(a.dh + ((long)t.b * a.D + c) * a.N, n0, a.N, g4);
       }
     }
-    A01[i] = pair(A4[0] * ATLAS_LOG2E, A4[1] * ATLAS_LOG2E);
-    A23[i] = pair(A4[2] * ATLAS_LOG2E, A4[3] * ATLAS_LOG2E);
+    A01[i] = pair(log2_decay(A4[0]), log2_decay(A4[1]));
+    A23[i] = pair(log2_decay(A4[2]), log2_decay(A4[3]));
     // read by this lane alone
     *reinterpret_cast<float4*>(s.hs[wi][i][lane]) = make_float4(h4[0], h4[1], h4[2], h4[3]);
     g01[i] = pair(g4[0], g4[1]);

@@ -9,7 +9,7 @@ import layer_ops_ref as R
 
 torch = pytest.importorskip("torch")
 import test_memorization_recurrent_gb300 as A  # noqa: E402
-from test_gpu_layer_ops import CODE, DT, TYPES, Conv, Scan, _lib, close, dev, draw, host, rng, run_scan, space, status  # noqa: E402,F401
+from test_gpu_layer_ops import CODE, DT, TYPES, Conv, Scan, _lib, check_grads, close, dev, draw, host, rng, run_scan, space, status  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -272,5 +272,25 @@ def test_conv_heads_in_any_order(order, B, L, H, hd, dtype):
     assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][3], out[1][3])
     mag = sum(R.conv_back(d.xh[b], d.wh, d.bh, True, d.sh[b], d.dyh[b], d.dsh[b], mag=True)["dw"] for b in range(B))
     close(out[0][1], host(out[1][1]), mag, "fp32", B * L, "dw")
+
+
+@pytest.mark.parametrize("L", [1, 20, 700])
+def test_scan_decay_next_to_the_largest_number(L):
+    """A of -3e38 forgets at once, and leaves the state alone where dt is 0 (raw steps of -200, and places
+    behind a sequence's end): its product with log2(e) is not a 32-bit number."""
+    r = rng(37, L)
+    d = Scan(r, 2, L, 24, 16, 1, "fp32")
+    d.A[:, 0], d.A_h[:, 0] = -3e38, float(np.float32(-3e38))
+    steps = d.dt.clone(), d.dt_h.copy()
+    d.dt[:, L // 2], d.dt_h[:, L // 2] = -200, -200
+    d.bias, d.bias_h = None, None
+    cfg = A.make_scan_cfg(2, L, 24, 16, dtype=A.F32)
+    h = torch.zeros_like(d.h)
+    y = run_scan(d, cfg, d.h, h)
+    for b in range(2):
+        d.check(y[b], h[b], (b,), d.h_h[b], f"sequence {b}")
+    (d.dt, d.dt_h), dh = steps, d.dh.clone()  # (at a step of 0 the gradient's A times a state is no number of 32 bits)
+    o = d.backward(A.make_scan_cfg(2, L, 24, 16, dtype=A.F32), d.h, dh)
+    check_grads(d, o, dh, [((b,), d.h_h[b], True) for b in range(2)])
 
 
