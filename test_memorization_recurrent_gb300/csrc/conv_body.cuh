@@ -408,7 +408,7 @@ inline long lane_groups(const ConvArgs& a, int V) { return (a.C + kLanes * V - 1
 // Workers over the groups of channels: as many warps as run at once, so that few tokens are read twice
 // (forward 24 an SM at up to four taps, backward twelve).
 inline long workers(const ConvArgs& a, int V, int an_sm) {
-  const long n = 152 * an_sm / lane_groups(a, V) / kWarps * kWarps;
+  const long n = kSMs * an_sm / lane_groups(a, V) / kWarps * kWarps;
   return n < kWarps ? kWarps : n;
 }
 constexpr int kForwardWarps = 24, kBackWarps = 12;

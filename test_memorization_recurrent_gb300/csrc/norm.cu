@@ -688,7 +688,7 @@ RowPlan rows_plan(int d, int lanes_k) {
 int back_blocks(const NormArgs& a, const RowPlan& p) {
   const long rpb = p.block / p.tpr;
   const long need = (a.rows + rpb - 1) / rpb;
-  const long most = 152L * (1536 / (p.block < 256 ? 256 : p.block));
+  const long most = (long)kSMs * (1536 / (p.block < 256 ? 256 : p.block));
   return (int)(need < most ? need : most);
 }
 
@@ -704,7 +704,7 @@ int forward_ring(const NormArgs& a, int threads, size_t smem, cudaStream_t st) {
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATLAS_ERR_CUDA;
-  const long most = 152L * resident(smem, 8 * 256 / threads);
+  const long most = (long)kSMs * resident(smem, 8 * 256 / threads);
   f<<<(unsigned)(a.rows < most ? a.rows : most), threads, smem, st>>>(a);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;
 }
@@ -712,7 +712,7 @@ int forward_ring(const NormArgs& a, int threads, size_t smem, cudaStream_t st) {
 template <int XB, int RB>
 int forward_rows(const NormArgs& a, cudaStream_t st) {
   // rows of up to 256 channels: lanes of a warp; longer ones: a block
-  const bool few = a.rows <= 152 * 8;
+  const bool few = a.rows <= kSMs * 8;
   const RowPlan p = rows_plan(a.d, 1);
   const size_t ring = 512 + (size_t)kStages * a.d * (XB + RB);
   if (!few && p.tpr > 32 && ring <= 200 * 1024) {
@@ -748,7 +748,7 @@ int backward_rows(const NormArgs& a, const RowPlan& p, int& blocks, cudaStream_t
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return ATLAS_ERR_CUDA;
   // no more blocks than run at once
-  const int most = 152 * resident(smem, (MT == 320 ? 640 : 512) / p.block);
+  const int most = kSMs * resident(smem, (MT == 320 ? 640 : 512) / p.block);
   blocks = blocks < most ? blocks : most;
   f<<<blocks, p.block, smem, st>>>(a, p.tpr);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;

@@ -7,6 +7,8 @@
 
 namespace atlas {
 
+constexpr int kSMs = 152;  // of a GB300
+
 struct NormArgs {
   const void* x;    // backward: h
   const void* r;    // backward: dh

@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
 // at once (three packed prompts of 16384 tokens x 1024: 170 us with six, 150 with seven, 183 with
 // eight), but none below 256 tokens.
 inline int segment_tokens(const ScanArgs& a, long blocks_per_seq) {
-  const long want = 152 * 7;
+  const long want = kSMs * 7;
   const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;
   if (!a.s.start && a.s.B * blocks_per_seq >= 250) return 0;
   if (a.s.L <= 256) return 0;

@@ -48,7 +48,7 @@ inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
     const bool whole = c >= L;
     const long m = whole ? 1 : (L + c - 1) / c;  // segments a sequence
     const long S = whole ? L : ((L + m - 1) / m + kTile - 1) / kTile * kTile;
-    const double n = (double)(B * m + more) * blocks_per_seq / (152 * 2);
+    const double n = (double)(B * m + more) * blocks_per_seq / (kSMs * 2);
     const double cost = n <= 1 ? 1.05 * S + 30 : (n + 0.5) * S + n * 30;
     if (best == 0 || cost < least) {
       best = whole ? -1 : (int)S;
@@ -662,7 +662,7 @@ int backward(const ScanArgs& a, cudaStream_t st) {
       return ATLAS_ERR_CUDA;
   }
   const long nb = (w.rows * a.G * 2 * Shape<LN>::kNP + 255) / 256;
-  const int nbc = (int)(nb < 152 * 16 ? nb : 152 * 16);
+  const int nbc = (int)(nb < kSMs * 16 ? nb : kSMs * 16);
   const long na = ((long)a.D * (a.N + 2) + 255) / 256;
   finish_kernel<T, LN><<<nbc + (int)(na < 4096 ? na : 4096), 256, 0, st>>>(a, w, nbc);
   return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA;

@@ -294,3 +294,48 @@ def test_scan_decay_next_to_the_largest_number(L):
     check_grads(d, o, dh, [((b,), d.h_h[b], True) for b in range(2)])
 
 
+def test_graphs_replayed_on_other_starts():
+    """Forward and backward of packed convolutions and scans of many sequences, captured, and replayed after
+    the starts have changed in place: the bits of plain calls on them."""
+    r, B, T, C, N, W = rng(38), 100, 1400, 40, 16, 4
+    starts = [np.concatenate([[0], np.cumsum(n)]) for n in (r.integers(0, 28, B), np.eye(B, dtype=int)[60] * 1200 + r.integers(0, 3, B))]
+    start = torch.tensor(starts[0], dtype=torch.int32, device="cuda")
+    d, c = Scan(r, B, 0, C, N, 1, "bf16", packed_rows=T), Conv(r, B, 0, C, W, "bf16", packed_rows=T)
+    st = status()
+    kw = dict(seq_start=start, status_dev=st)
+    sf, sb, cf, cb = A.make_scan_cfg(B, T, C, N, **kw), A.make_scan_cfg(B, T, C, N, **kw), A.make_conv_cfg(B, T, C, W, **kw), A.make_conv_cfg(B, T, C, W, **kw)
+    space(sf, A.atlas_scan_workspace_bytes(sf))
+    space(sb, A.atlas_scan_backward_workspace_bytes(sb))
+    space(cb, A.atlas_conv_backward_workspace_bytes(cb))
+    o = d.grads()
+    o.update(y=torch.zeros_like(d.x), h=d.h.clone(), dh=d.dh.clone(), cy=torch.zeros_like(c.x), cs=c.s.clone(), cdx=torch.zeros_like(c.x), cds=c.ds.clone(),
+             cdw=torch.zeros(C, W, device="cuda"), cdb=torch.zeros(C, device="cuda"))
+
+    def everything():
+        o["dh"].copy_(d.dh)
+        o["cds"].copy_(c.ds)
+        A.atlas_scan_forward(*d.inputs(), sf, o["y"], d.h, o["h"])
+        A.atlas_scan_backward(*d.inputs(), sb, d.h, d.dy, o["dh"], o["dx"], o["ddt"], o["dA"], o["dB"], o["dC"], o["dD"], o["dz"], o["ddt_bias"])
+        A.atlas_conv_forward(c.x, c.w, c.b, cf, o["cy"], c.s, o["cs"])
+        A.atlas_conv_backward(c.x, c.w, c.b, cb, c.s, c.dy, o["cds"], o["cdx"], o["cdw"], o["cdb"])
+    everything()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        everything()
+    for s in starts[::-1]:
+        start.copy_(torch.from_numpy(s))
+        for v in o.values():
+            v.zero_()
+        everything()
+        torch.cuda.synchronize()
+        want = {k: v.clone() for k, v in o.items()}
+        for v in o.values():
+            v.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(want[k], o[k]) for k in o) and int(st) == 0
+    for b in (0, 59, 60, 99):
+        rows = slice(starts[0][b], starts[0][b + 1])
+        d.check(o["y"][rows], o["h"][b], rows, d.h_h[b], f"sequence {b}")
+        c.check(o["cy"][rows], o["cs"][b], rows, c.sh[b], "bf16", f"sequence {b}")
