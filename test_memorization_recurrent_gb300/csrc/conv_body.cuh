@@ -8,12 +8,12 @@
 // channels and walks the tokens of its worker's pieces of the sequences with the last W - 1 inputs in
 // registers, so that only the tokens in front of a piece (and, backward, those behind it) are read
 // twice.  Workers have equal shares of the rows: 65536 rows x 2048 channels take 102 us in eight
-// sequences, 104 in 256 equal ones, 105 with half of the rows in one of 256 (backward 182, 195, 196; with
+// sequences, 104 in 256 equal ones, 105 with half of the rows in one of 256 (backward 176, 186, 187; with
 // tiles of a length that went by the number of sequences 6385 and 6223 us for the last).  V is
 // four: with eight, the taps, window and loads of a lane take 202 registers, and too few
 // warps are left to cover the latency.  8 x 4096 tokens x 2048 channels of bf16, four taps:
 // 126 us with eight, 59 with four, 53 (5.0 TB/s) without a second way to store, which spilled; 24
-// warps an SM, against 91 us with 20, 65 with 28, 78 with 32 where 24 took 59.  Backward: 103 us (3.9
+// warps an SM, against 91 us with 20, 65 with 28, 78 with 32 where 24 took 59.  Backward: 99 us (4.1
 // TB/s; 672 with loads in the worker's turn, 150 with the ring but the edges' conditions at every token).
 #pragma once
 #include "ops_common.cuh"
@@ -222,22 +222,29 @@ __global__ void __launch_bounds__(kLanes * kWarps)
     const T* x = reinterpret_cast<const T*>(a.x) + seq_at(a.s, t, t.t0, a.xb, a.xt) + cc;
     const T* dy = reinterpret_cast<const T*>(a.dy) + y_at(a, t, t.t0, cc);
     const T* st = a.st_in && t.carry ? reinterpret_cast<const T*>(a.st_in) + ((long)t.b * H + H) * a.C + cc : nullptr;
+    const int from = first && !st ? 0 : -H, upto = min(rest, n + H);  // positions there are of x and dy
     auto fetch = [&](int stage, int base) {
+      T vx[V > 1 ? 1 : kChunk], vy[V > 1 ? 1 : kChunk];  // V = 1: all loads before the first store
 #pragma unroll
       for (int r = 0; r < kChunk; r += RP) {
         const int u = r + lane / CL, q = base + u;
-        const bool token = q >= 0 || !first;
-        const bool fx = cin && q < rest && (token || st), fy = cin && q >= 0 && q < min(rest, n + H);
-        const T* px = !fx ? reinterpret_cast<const T*>(a.w) : token ? x + (long)q * a.xt : st + (long)q * a.C;
-        const T* py = fy ? dy + (long)q * a.yt : reinterpret_cast<const T*>(a.w);
-        T* ox = &ring.x[stage][u][lane % CL * CV];
-        T* oy = &ring.dy[stage][u][lane % CL * CV];
+        const bool fx = cin && q < rest && q >= from, fy = cin && q >= 0 && q < upto;
+        const T* px = q < 0 && first ? st + (long)q * a.C : x + (long)q * a.xt;
+        const T* py = dy + (long)q * a.yt;
         if constexpr (V > 1) {
-          cp_async<16>(ox, fx ? px : reinterpret_cast<const T*>(a.dx), fx);
-          cp_async<16>(oy, fy ? py : reinterpret_cast<const T*>(a.dx), fy);
+          cp_async<16>(&ring.x[stage][u][lane % CL * CV], fx ? px : reinterpret_cast<const T*>(a.dx), fx);
+          cp_async<16>(&ring.dy[stage][u][lane % CL * CV], fy ? py : reinterpret_cast<const T*>(a.dx), fy);
         } else {
-          *ox = fx ? *px : from_f<T>(0.f);
-          *oy = fy ? *py : from_f<T>(0.f);
+          vx[r] = vy[r] = from_f<T>(0.f);
+          if (fx) vx[r] = *px;
+          if (fy) vy[r] = *py;
+        }
+      }
+      if constexpr (V == 1) {
+#pragma unroll
+        for (int r = 0; r < kChunk; ++r) {
+          ring.x[stage][r][lane] = vx[r];
+          ring.dy[stage][r][lane] = vy[r];
         }
       }
     };
