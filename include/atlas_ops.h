@@ -181,7 +181,7 @@ int atlas_conv_backward(const void* x, const void* weight, const void* bias,
  *   y_t[c] = (sum_n C_t[g][n] h_t[c][n] + D[c] x_t[c]) * SiLU(z_t[c])
  * The state h [.., D, N], every sum and every exponential are held in 32 bits. */
 typedef struct atlas_scan_cfg {
-  int B, L, D;     /* sequences, tokens (packed: rows), channels */
+  int B, L, D;     /* sequences (at most 65535), tokens (packed: rows), channels */
   int N;           /* states per channel, 1 .. ATLAS_SCAN_MAX_N */
   int G;           /* groups that share B and C, divides D */
   int dtype;       /* x, dt, B, C, z, y and their gradients: ATLAS_F32, ATLAS_BF16, ATLAS_F16 */

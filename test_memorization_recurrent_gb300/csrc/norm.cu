@@ -15,7 +15,7 @@
 // Measured (copy rate 6.78 TB/s): 32768 x 2048 bf16 + residual to e4m3 with scales of 128: 82 us,
 // 85% (a warp a row, loads in its turn: 123 us; divisions and a loop over the warps' sums: 96);
 // 524288 x 128 bf16: 51 us, 77%; backward, 16384 x 2560, 32-bit stream: 99 us, 88% (one row's
-// loads ahead in registers: 134); 20000 x 1371 bf16 element by element: 119 and 329 us.
+// loads ahead in registers: 134); 20000 x 1371 bf16 element by element: 123 and 330 us.
 #include <cuda_fp8.h>
 
 #include <limits>

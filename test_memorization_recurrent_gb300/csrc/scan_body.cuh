@@ -18,7 +18,7 @@
 // With one channel x four states a lane the shared memory's 3 cycles were the bound.
 // 8 x 4096 tokens x 2048 channels x 16 states, bf16, gated: 1793 us for the first kernel of
 // one pass with everything in one warp's turn, 584 with a register tile prefetched, 525 with
-// the second warp, 438 with the two kinds of warps spread over the schedulers, 347 with the
+// the second warp, 438 with the two kinds of warps spread over the schedulers, 343 with the
 // second warp's addresses and conversions thinned out and seven blocks an SM: 4.3 times the
 // traffic's floor, 3.2 times the exponentials', 65% of the issue slots.
 //
@@ -26,7 +26,7 @@
 // segments: a first pass finds each segment's end state from a zero start (with the sum of
 // its dt: the decay over a segment is exp(A sum dt)); the second computes the outputs, each
 // segment from the start state that it joins from those in front of it.  Three packed prompts of
-// 16384 tokens x 1024 channels: 150 us.
+// 16384 tokens x 1024 channels: 154 us.
 #pragma once
 #include "ops_common.cuh"
 
@@ -645,8 +645,8 @@ __global__ void __launch_bounds__(kTokenThreads) token_kernel(ScanArgs a) {
 // about two of them on, and a second walk over the tokens costs two thirds of the first: one
 // segment from 250 blocks on (4 x 4096 tokens x 1024 channels: 144 us, in segments 150 to 168;
 // twice the sequences: 199 against 330).  Below, segments for seven blocks an SM, as many as run
-// at once (three packed prompts of 16384 tokens x 1024: 170 us with six, 150 with seven, 183 with
-// eight), but none below 256 tokens.
+// at once (three packed prompts of 16384 tokens x 1024, at the step that chose it: 170 us with six, 150
+// with seven, 183 with eight), but none below 256 tokens.
 inline int segment_tokens(const ScanArgs& a, long blocks_per_seq) {
   const long want = kSMs * 7;
   const long rows = a.s.start ? a.s.L : (long)a.s.B * a.s.L;

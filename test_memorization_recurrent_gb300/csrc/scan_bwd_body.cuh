@@ -19,7 +19,7 @@
 // What bounds it: instruction issue in the main pass, 26 for 32 updates (17 of them in the
 // walking warps: the decay and state twice, the adjoint, seven products, and the two kinds of
 // sums).  Holding a tile's decays instead of taking them again costs 64 registers and with
-// them half the warps.  4 x 2048 tokens x 2048 channels x 16 states, bf16, gated: 490 us, of
+// them half the warps.  4 x 2048 tokens x 2048 channels x 16 states, bf16, gated: 494 us, of
 // which the main pass takes two thirds (55% of the issue slots) and the kept states a quarter; the first
 // kernels, with one channel x four states a lane and loads in every warp's turn, took 1822.
 #pragma once
@@ -38,7 +38,7 @@ constexpr int kBackCB = kWalkers * Shape<LN>::kCB;  // channels of a block
 // Segment length, 0 for one segment a sequence.  The main pass runs n blocks, two an SM at a
 // time, for a little over S tokens each (30 more for a block's start): one round of blocks takes
 // that long, several about half a round more than their share.  The shortest of the lengths
-// from 128 on is taken (4 x 2048 tokens x 2048 channels: 478 us with 256, 501 with 128, 516 with
+// from 128 on is taken (4 x 2048 tokens x 2048 channels, in the sweep that chose it: 478 us with 256, 501 with 128, 516 with
 // 512, 624 with 2048; 8 x 512 x 2048: 252 with 512, 279 with 256).
 inline int back_segment_tokens(const ScanArgs& a, long blocks_per_seq) {
   const long L = a.s.L, B = a.s.start ? 1 : a.s.B, more = a.s.start ? a.s.B : 0;
