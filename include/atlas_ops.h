@@ -2,10 +2,11 @@
  * atlas_ops.h -- C ABI of the operators around the memory update in a recurrent
  * layer, in the same library (libatlasmem.so):
  *
- *   norm  residual addition and root-mean-square norm, output in 32, 16 or 8 bits
- *   conv  short causal convolution per channel, optionally through SiLU
- *   scan  selective state space scan: a diagonal recurrence whose decay depends on
- *         token, channel and state
+ *   norm       residual addition and root-mean-square norm, output in 32, 16 or 8 bits
+ *   layernorm  the same with the mean taken out and a bias
+ *   conv       short causal convolution per channel, optionally through SiLU
+ *   scan       selective state space scan: a diagonal recurrence whose decay depends on
+ *              token, channel and state
  *
  * each forward and backward; conv and scan run whole sequences, packed sequences of
  * unequal lengths and single tokens (L = 1) through the same entry point.
@@ -102,6 +103,30 @@ size_t atlas_norm_backward_workspace_bytes(const atlas_norm_cfg* cfg);
  *   dw  [d] fp32 out, or NULL (required to be NULL when weight is NULL) */
 int atlas_norm_backward(const void* h, const void* weight, const void* dy, const void* dh,
                         const atlas_norm_cfg* cfg, void* dx, float* dw, void* stream);
+
+/* ------------------------------------------------------------ layer norm
+ * Per row of d channels:
+ *   h = x + residual,   mu = mean(h),   v = mean((h - mu)^2)       (in 32 bits)
+ *   y = (h - mu) / sqrt(v + eps) * weight + bias
+ * with the norm's description: types, strides, residual_out, groups and scales of an 8-bit output and
+ * limits are as there, but eps has to be above 0 (a row of equal numbers has v = 0 and gives
+ * the bias).  bias has w_dtype.  The deviations of a row are taken about its mean before they are
+ * squared, and the mean's rounding is made up for, so a large mean costs v nothing. */
+
+/*   x, residual, y, residual_out, scale  as for atlas_norm_forward
+ *   weight [d] w_dtype or NULL (ones);  bias [d] w_dtype or NULL (zeros) */
+int atlas_layernorm_forward(const void* x, const void* residual, const void* weight, const void* bias,
+                            const atlas_norm_cfg* cfg, void* y, void* residual_out, float* scale,
+                            void* stream);
+
+/* What atlas_layernorm_backward needs where dw or dbias is asked for. */
+size_t atlas_layernorm_backward_workspace_bytes(const atlas_norm_cfg* cfg);
+
+/* Gradients as of atlas_norm_backward (the same h, dy, dh and dx), and
+ *   dw    [d] fp32 out, or NULL (required to be NULL when weight is NULL)
+ *   dbias [d] fp32 out, or NULL: the sum of dy over the rows */
+int atlas_layernorm_backward(const void* h, const void* weight, const void* dy, const void* dh,
+                             const atlas_norm_cfg* cfg, void* dx, float* dw, float* dbias, void* stream);
 
 /* ------------------------------------------------- sequences and their states
  * conv and scan take B sequences in one of two forms:

@@ -16,7 +16,9 @@ import threading
 from . import ops as _ops
 from .ops import (ACT_NONE, ACT_SILU, BF16, CONV_MAX_W, E4M3, F16, F32, NORM_MAX_D, OPS_EXPORTS,
                   SCAN_MAX_N, AtlasConvCfg, AtlasNormCfg, AtlasScanCfg, atlas_conv_backward,
-                  atlas_conv_backward_workspace_bytes, atlas_conv_forward, atlas_norm_backward,
+                  atlas_conv_backward_workspace_bytes, atlas_conv_forward,
+                  atlas_layernorm_backward, atlas_layernorm_backward_workspace_bytes,
+                  atlas_layernorm_forward, atlas_norm_backward,
                   atlas_norm_backward_workspace_bytes, atlas_norm_forward, atlas_scan_backward,
                   atlas_scan_backward_workspace_bytes, atlas_scan_forward,
                   atlas_scan_workspace_bytes, make_conv_cfg, make_norm_cfg, make_scan_cfg)

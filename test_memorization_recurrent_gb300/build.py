@@ -51,7 +51,7 @@ def _build(lib: str, objdir: str, extra, force: bool) -> str:
     if not force and up_to_date(lib):
         return lib
     os.makedirs(objdir, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
         objs = list(ex.map(lambda s: _compile(s, objdir, list(extra)), _sources()))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]

@@ -1,6 +1,6 @@
 // atlas_ops.cu -- C-ABI entry points of the layer operators: argument checks, strides and
 // the choice between wide (16-byte) and element-wise accesses.  Every computation happens
-// in norm.cu, conv_*.cu and scan_*.cu.
+// in norm.cu, layernorm_*.cu, conv_*.cu and scan_*.cu.
 #include "atlas_ops.h"
 
 #include <algorithm>
@@ -33,8 +33,13 @@ int check_norm(const atlas_norm_cfg* c) {
   return ATLAS_OK;
 }
 
-NormArgs norm_args(const atlas_norm_cfg* c) {
-  NormArgs a = {};
+int check_layernorm(const atlas_norm_cfg* c) {
+  const int rc = check_norm(c);
+  if (rc != ATLAS_OK) return rc;
+  return c->eps > 0.f ? ATLAS_OK : ATLAS_ERR_INVALID;
+}
+
+void norm_args(const atlas_norm_cfg* c, NormArgs& a) {
   a.rows = c->rows;
   a.d = c->d;
   a.dt = c->dtype;
@@ -46,6 +51,15 @@ NormArgs norm_args(const atlas_norm_cfg* c) {
   a.sx = c->x_stride ? c->x_stride : c->d;
   a.sr = c->r_stride ? c->r_stride : c->d;
   a.sy = c->y_stride ? c->y_stride : c->d;
+}
+NormArgs norm_args(const atlas_norm_cfg* c) {
+  NormArgs a = {};
+  norm_args(c, a);
+  return a;
+}
+LayerNormArgs layernorm_args(const atlas_norm_cfg* c) {
+  LayerNormArgs a = {};
+  norm_args(c, a);
   return a;
 }
 
@@ -257,6 +271,63 @@ int atlas_norm_backward(const void* h, const void* weight, const void* dy, const
   a.wide = a.d % 8 == 0 && a.sr % 8 == 0 && a.sy % 8 == 0 && aligned(h, 16) && aligned(weight, 16) &&
            aligned(dy, 16) && aligned(dh, 16) && aligned(dx, 16);
   return norm_backward_launch(a, stream_of(stream));
+}
+
+int atlas_layernorm_forward(const void* x, const void* residual, const void* weight, const void* bias,
+                            const atlas_norm_cfg* cfg, void* y, void* residual_out, float* scale,
+                            void* stream) {
+  const int rc = check_layernorm(cfg);
+  if (rc != ATLAS_OK) return rc;
+  if (cfg->rows == 0) return ATLAS_OK;
+  if (!x || !y || (cfg->out_dtype == ATLAS_E4M3) != (scale != nullptr)) return ATLAS_ERR_INVALID;
+  LayerNormArgs a = layernorm_args(cfg);
+  a.x = x;
+  a.r = residual;
+  a.w = weight;
+  a.b = bias;
+  a.y = y;
+  a.r_out = residual_out;
+  a.scale = scale;
+  if (!aligned(x, size_of(a.dt)) || !aligned(residual, size_of(a.rt)) ||
+      !aligned(weight, size_of(a.wt)) || !aligned(bias, size_of(a.wt)) || !aligned(y, size_of(a.ot)) ||
+      !aligned(residual_out, size_of(a.rt)) || !aligned(scale, 4))
+    return ATLAS_ERR_INVALID;
+  a.wide = a.d % 8 == 0 && a.sx % 8 == 0 && a.sr % 8 == 0 && a.sy % 8 == 0 && aligned(x, 16) &&
+           aligned(residual, 16) && aligned(weight, 16) && aligned(bias, 16) && aligned(y, 16) &&
+           aligned(residual_out, 16);
+  return layernorm_forward_launch(a, stream_of(stream));
+}
+
+size_t atlas_layernorm_backward_workspace_bytes(const atlas_norm_cfg* cfg) {
+  if (check_layernorm(cfg) != ATLAS_OK) return (size_t)-1;
+  return layernorm_backward_workspace(layernorm_args(cfg));
+}
+
+int atlas_layernorm_backward(const void* h, const void* weight, const void* dy, const void* dh,
+                             const atlas_norm_cfg* cfg, void* dx, float* dw, float* dbias, void* stream) {
+  const int rc = check_layernorm(cfg);
+  if (rc != ATLAS_OK) return rc;
+  if (dw && !weight) return ATLAS_ERR_INVALID;
+  if (cfg->rows > 0 && (!h || !dy || !dx)) return ATLAS_ERR_INVALID;
+  LayerNormArgs a = layernorm_args(cfg);
+  if (!aligned(h, size_of(a.rt)) || !aligned(weight, size_of(a.wt)) || !aligned(dy, size_of(a.dt)) ||
+      !aligned(dh, size_of(a.rt)) || !aligned(dx, size_of(a.rt)) || !aligned(dw, 4) || !aligned(dbias, 4))
+    return ATLAS_ERR_INVALID;
+  const size_t need = layernorm_backward_workspace(a);
+  if ((dw || dbias) && need && (!cfg->workspace || cfg->workspace_bytes < need || !aligned(cfg->workspace, 16)))
+    return ATLAS_ERR_WORKSPACE;
+  if (cfg->rows == 0 && !dw && !dbias) return ATLAS_OK;
+  a.x = h;
+  a.r = dh;
+  a.w = weight;
+  a.dy = dy;
+  a.y = dx;
+  a.dw = dw;
+  a.db = dbias;
+  a.part = reinterpret_cast<float*>(cfg->workspace);
+  a.wide = a.d % 8 == 0 && a.sr % 8 == 0 && a.sy % 8 == 0 && aligned(h, 16) && aligned(weight, 16) &&
+           aligned(dy, 16) && aligned(dh, 16) && aligned(dx, 16);
+  return layernorm_backward_launch(a, stream_of(stream));
 }
 
 int atlas_conv_forward(const void* x, const void* weight, const void* bias,

@@ -1,0 +1,320 @@
+// layernorm_bwd.cu -- layer norm, backward pass.
+//
+//   hat = (h - mu) rstd,  dx = rstd (w dy - mean(w dy) - hat mean(w dy hat)) + dh,
+//   dw = sum over rows of dy hat,  db = sum over rows of dy
+//
+// Rows of up to 8192 channels: a block walks rows (short ones: lanes of a warp each), the next one or two
+// on their way through shared memory; a row's statistics take two rounds of sums (h and w dy; then,
+// about the mean, what its rounding left out, the squares and the products with w dy).  A thread's
+// columns are the same in every row, so dw and db stay in its registers; blocks write partial sums,
+// which a second launch adds in a fixed order.  Longer rows: a block a row, which reads it three times
+// (from L2 but the first), then partial sums by column from the rows' kept statistics.
+#include "layernorm_body.cuh"
+
+namespace atlas {
+namespace layernorm {
+namespace {
+
+constexpr int kMaxRow = 8192;
+
+// MT: most threads; up to 320 (2560 channels), two blocks an SM without a register in memory.
+template <int HB, int DB, int GB, int K, bool AL, int MT>  // bytes of h, dy, dh (0: none)
+__global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, int tpr, int stages) {
+  extern __shared__ __align__(16) float sm[];  // 2 x 32 for the sums, then [stage][row of the block]: h, dy, dh
+  float *red = sm, *red2 = sm + 32;
+  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
+  const int lane = g.lane, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  clear_red(sm, 96);
+  float dw[K][8], db[K][8], w[K][8];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
+  }
+  const int hs = slot_bytes<HB, AL>(a.d), ds = slot_bytes<DB, AL>(a.d), bytes = hs + ds + slot_bytes<GB, AL>(a.d);
+  char* ring = reinterpret_cast<char*>(sm + 96) + mine * bytes;
+  const Rows th = rows_of<HB>(a.x, a.sr, a.rows, a.d), td = rows_of<DB>(a.dy, a.sy, a.rows, a.d),
+             tg = rows_of<GB>(a.r, a.sr, a.rows, a.d);
+  const long step = (long)gridDim.x * rpb;
+  auto fetch = [&](long row, int stage) {
+    char* s = ring + stage * rpb * bytes;
+    fetch_row<HB, K * HB / 2, AL>(s, th, row, a.rows, a.d, lane, tpr);
+    fetch_row<DB, K * DB / 2, AL>(s + hs, td, row, a.rows, a.d, lane, tpr);
+    fetch_row<GB, K * GB / 2, AL>(s + hs + ds, tg, row, a.rows, a.d, lane, tpr);
+    cp_commit();
+  };
+  auto next_done = [&] {
+    if (stages == 3)
+      cp_wait<1>();
+    else
+      cp_wait<0>();
+  };
+  const auto in = [&](int k, int i) { return col<AL>(k, AL ? 0 : i, tpr, lane) < a.d; };
+  long row = (long)blockIdx.x * rpb + mine;
+  for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
+  next_done();
+  __syncthreads();
+  int stage = 0;
+  for (; row - mine < a.rows; row += step) {
+    const bool live = row < a.rows;
+    fetch(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
+    const char* s = ring + stage * rpb * bytes;
+    stage = stage + 1 == stages ? 0 : stage + 1;
+    float h[K][8], dy[K][8], gv[K][8], sum = 0.f, dsum = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      slot_floats<HB, AL>(s, AL || !live ? 0 : ahead(th, row), a.rt, k, a.d, tpr, lane, h[k]);
+      slot_floats<DB, AL>(s + hs, AL || !live ? 0 : ahead(td, row), a.dt, k, a.d, tpr, lane, dy[k]);
+      if constexpr (GB > 0) slot_floats<GB, AL>(s + hs + ds, AL || !live ? 0 : ahead(tg, row), a.rt, k, a.d, tpr, lane, gv[k]);
+      if (!AL && !live) {  // nothing was copied for a place of the block without a row
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[k][i] = dy[k][i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum += h[k][i];
+        dsum = fmaf(w[k][i], dy[k][i], dsum);
+        db[k][i] += dy[k][i];
+      }
+    }
+    next_done();  // the next row's copies, handed over by the barriers below
+    if (tpr <= 32) __syncwarp();
+    row_sums2(sum, dsum, g, red);
+    const float mean = sum * a.inv_d;
+    float rest = 0.f, ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[k][i] = in(k, i) ? h[k][i] - mean : 0.f;
+        rest += h[k][i];
+        ss = fmaf(h[k][i], h[k][i], ss);
+        dot = fmaf(h[k][i], w[k][i] * dy[k][i], dot);
+      }
+    // three sums
+    for (int m = min(tpr, 32) >> 1; m; m >>= 1) {
+      rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
+      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
+    }
+    if (tpr > 32) {
+      if ((threadIdx.x & 31) == 0) *reinterpret_cast<float4*>(red2 + (threadIdx.x >> 5) * 4) = make_float4(rest, ss, dot, 0.f);
+      __syncthreads();
+      rest = ss = dot = 0.f;
+      for (int i = 0; i < tpr / 32; ++i) {
+        const float4 t = reinterpret_cast<const float4*>(red2)[i];
+        rest += t.x;
+        ss += t.y;
+        dot += t.z;
+      }
+    }
+    rest *= a.inv_d;
+    const float rstd = rsqrtf(fmaxf(fmaf(ss, a.inv_d, -rest * rest), 0.f) + a.eps), off = -rest * rstd;
+    const float mdy = dsum * a.inv_d, mhat = rstd * (dot * a.inv_d - rest * mdy);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float hat = fmaf(h[k][i], rstd, off);
+        dw[k][i] = fmaf(dy[k][i], hat, dw[k][i]);
+        o[i] = rstd * (fmaf(w[k][i], dy[k][i], -mdy) - hat * mhat) + (GB ? gv[k][i] : 0.f);
+      }
+      if (live) store<AL>(a.y, row * a.sr, a.rt, k, a.d, tpr, lane, o);
+    }
+  }
+  cp_wait<0>();
+  float* acc = sm + 96;  // over the rows' ring
+  for (int which = 0; which < 2; ++which) {
+    if (!(which ? a.db : a.dw)) continue;
+    float* part = a.part + ((long)blockIdx.x * 2 + which) * a.d;
+    for (int r = 0; r < rpb; ++r) {  // rows of one block in a fixed order
+      __syncthreads();
+      if (r == mine) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = col<AL>(k, i, tpr, lane);
+            if (c < a.d) {
+              const float v = (r == 0 ? 0.f : acc[c]) + (which ? db[k][i] : dw[k][i]);
+              if (r == rpb - 1)
+                part[c] = v;
+              else
+                acc[c] = v;
+            }
+          }
+      }
+    }
+  }
+}
+
+// dw[c] and db[c]: sums over the blocks' partial sums; 32 columns a block, 8 threads a column.
+__global__ void __launch_bounds__(256) sum_parts(const float* part, float* dw, float* db, int nblk, int d) {
+  __shared__ float s[8][33];
+  float* out = blockIdx.y ? db : dw;
+  if (!out) return;
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cx;
+  float v = 0.f;
+  if (c < d) {
+#pragma unroll 4
+    for (int r = ry; r < nblk; r += 8) v += part[((long)r * 2 + blockIdx.y) * d + c];
+  }
+  s[ry][cx] = v;
+  __syncthreads();
+  if (ry == 0 && c < d) {
+#pragma unroll
+    for (int r = 1; r < 8; ++r) v += s[r][cx];
+    out[c] = v;
+  }
+}
+
+// ------------------------------------------------------------------ rows of more than kMaxRow channels
+
+constexpr int kLongBlock = 512;
+
+// A block a row; stats receives (mu as two numbers whose sum it is, rstd) of each.
+__global__ void __launch_bounds__(kLongBlock) long_rows(Args a, float4* stats) {
+  __shared__ __align__(16) float red[96];
+  clear_red(red, 96);
+  const RowGroup g{kLongBlock, (int)threadIdx.x, (int)threadIdx.x};
+  for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const auto h = [&](int c) { return ld_any(a.x, row * a.sr + c, a.rt); };
+    const auto dy = [&](int c) { return ld_any(a.dy, row * a.sy + c, a.dt); };
+    const auto w = [&](int c) { return a.w ? ld_any(a.w, c, a.wt) : 1.f; };
+    float sum = 0.f, dsum = 0.f;
+#pragma unroll 8
+    for (int c = threadIdx.x; c < a.d; c += kLongBlock) sum += h(c), dsum = fmaf(w(c), dy(c), dsum);
+    row_sums2(sum, dsum, g, red);
+    const float mean = sum * a.inv_d, mdy = dsum * a.inv_d;
+    float rest = 0.f, ss = 0.f, dot = 0.f;
+#pragma unroll 8
+    for (int c = threadIdx.x; c < a.d; c += kLongBlock) {
+      const float v = h(c) - mean;
+      rest += v;
+      ss = fmaf(v, v, ss);
+      dot = fmaf(v, w(c) * dy(c), dot);
+    }
+    row_sums2(rest, ss, g, red + 32);
+    dot = row_sum(dot, g, red + 64);
+    rest *= a.inv_d;
+    const float rstd = rsqrtf(fmaxf(fmaf(ss, a.inv_d, -rest * rest), 0.f) + a.eps), off = -rest * rstd;
+    const float mhat = rstd * (dot * a.inv_d - rest * mdy);
+    if (threadIdx.x == 0 && stats) stats[row] = make_float4(mean, off, rstd, 0.f);
+#pragma unroll 8
+    for (int c = threadIdx.x; c < a.d; c += kLongBlock) {
+      const float hat = fmaf(h(c) - mean, rstd, off);
+      const float up = a.r ? ld_any(a.r, row * a.sr + c, a.rt) : 0.f;
+      st_elem(a.y, row * a.sr + c, a.rt, rstd * (fmaf(w(c), dy(c), -mdy) - hat * mhat) + up);
+    }
+  }
+}
+
+// Partial sums of dy hat and dy over blockIdx.y's rows, 256 columns a block.
+__global__ void __launch_bounds__(256) long_cols(Args a, const float4* stats) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.d) return;
+  float dw = 0.f, db = 0.f;
+#pragma unroll 4
+  for (long row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const float4 s = stats[row];
+    const float dy = ld_any(a.dy, row * a.sy + c, a.dt);
+    dw = fmaf(dy, fmaf(ld_any(a.x, row * a.sr + c, a.rt) - s.x, s.z, s.y), dw);
+    db += dy;
+  }
+  a.part[((long)blockIdx.y * 2) * a.d + c] = dw;
+  a.part[((long)blockIdx.y * 2 + 1) * a.d + c] = db;
+}
+
+// ------------------------------------------------------------------ launches
+
+RowPlan back_plan(int d) {
+  RowPlan p = forward_plan(d);
+  return p;
+}
+// Partial sums: at most so many blocks.
+int back_blocks(const Args& a) {
+  const RowPlan p = back_plan(a.d);
+  const long rpb = p.block / p.tpr, need = (a.rows + rpb - 1) / rpb;
+  const long most = (long)kSMs * (1536 / (p.block < 256 ? 256 : p.block));
+  return (int)(need < most ? need : most);
+}
+int long_splits(const Args& a) { return (int)(a.rows < 64 ? a.rows : 64); }
+
+template <int HB, int DB, int GB, int K, bool AL, int MT>
+int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
+  const int rpb = p.block / p.tpr;
+  const size_t row = slot_bytes<HB, AL>(a.d) + slot_bytes<DB, AL>(a.d) + slot_bytes<GB, AL>(a.d);
+  const int stages = 3 * rpb * row <= 200 * 1024 ? 3 : 2;
+  const size_t ring = stages * rpb * row, sums = (size_t)a.d * 4, smem = 96 * 4 + (ring > sums ? ring : sums);
+  auto* f = backward_rows<HB, DB, GB, K, AL, MT>;
+  if (const int rc = shared(f, smem)) return rc;
+  // no more blocks than run at once
+  const int most = kSMs * resident(smem, (MT == 320 ? 640 : 512) / p.block);
+  blocks = blocks < most ? blocks : most;
+  f<<<blocks, p.block, smem, st>>>(a, p.tpr, stages);
+  return status();
+}
+template <int HB, int DB, int GB, bool AL>
+int run(const Args& a, int& blocks, cudaStream_t st) {
+  const RowPlan p = back_plan(a.d);
+  if (p.k == 1 && p.block <= 320) return run_rows<HB, DB, GB, 1, AL, 320>(a, p, blocks, st);
+  if (p.k == 1) return run_rows<HB, DB, GB, 1, AL, 512>(a, p, blocks, st);
+  return run_rows<HB, DB, GB, 2, AL, 512>(a, p, blocks, st);
+}
+template <int HB, int DB, int GB>
+int run(const Args& a, int& blocks, cudaStream_t st) {
+  return a.wide ? run<HB, DB, GB, true>(a, blocks, st) : run<HB, DB, GB, false>(a, blocks, st);
+}
+template <int HB, int DB>
+int run(const Args& a, int& blocks, cudaStream_t st) {
+  return a.r ? run<HB, DB, HB>(a, blocks, st) : run<HB, DB, 0>(a, blocks, st);
+}
+
+}  // namespace
+}  // namespace layernorm
+
+int layernorm_run_2(const LayerNormArgs& a, cudaStream_t st);
+int layernorm_run_4(const LayerNormArgs& a, cudaStream_t st);
+
+int layernorm_forward_launch(const LayerNormArgs& args, cudaStream_t st) {
+  LayerNormArgs a = args;
+  a.inv_d = 1.f / a.d;
+  a.ng = a.group ? (a.d + a.group - 1) / a.group : 1;
+  for (a.gshift = 0; (1 << a.gshift) < a.group;) ++a.gshift;
+  return a.dt == ATLAS_F32 ? layernorm_run_4(a, st) : layernorm_run_2(a, st);
+}
+
+size_t layernorm_backward_workspace(const LayerNormArgs& a) {
+  using namespace layernorm;
+  if (a.d <= kMaxRow) return (size_t)back_blocks(a) * 2 * a.d * 4;
+  return (size_t)a.rows * 16 + (size_t)long_splits(a) * 2 * a.d * 4;
+}
+
+int layernorm_backward_launch(const LayerNormArgs& args, cudaStream_t st) {
+  using namespace layernorm;
+  LayerNormArgs a = args;
+  a.inv_d = 1.f / a.d;
+  const bool sums = a.dw || a.db;
+  int blocks = 0;
+  if (a.rows > 0 && a.d <= kMaxRow) {
+    blocks = back_blocks(a);
+    const bool h4 = a.rt == ATLAS_F32, d4 = a.dt == ATLAS_F32;
+    const int rc = h4 ? (d4 ? run<4, 4>(a, blocks, st) : run<4, 2>(a, blocks, st))
+                      : (d4 ? run<2, 4>(a, blocks, st) : run<2, 2>(a, blocks, st));
+    if (rc != ATLAS_OK) return rc;
+  } else if (a.rows > 0) {
+    float4* stats = sums ? reinterpret_cast<float4*>(a.part) : nullptr;
+    a.part += sums ? a.rows * 4 : 0;
+    const long most = 4L * kSMs;
+    long_rows<<<(unsigned)(a.rows < most ? a.rows : most), kLongBlock, 0, st>>>(a, stats);
+    blocks = long_splits(a);
+    if (sums) long_cols<<<dim3((a.d + 255) / 256, blocks), 256, 0, st>>>(a, stats);
+  }
+  if (sums) sum_parts<<<dim3((a.d + 31) / 32, 2), 256, 0, st>>>(a.part, a.dw, a.db, blocks, a.d);
+  return status();
+}
+
+}  // namespace atlas

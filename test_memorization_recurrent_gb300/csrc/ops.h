@@ -29,6 +29,16 @@ int norm_forward_launch(const NormArgs& a, cudaStream_t st);
 size_t norm_backward_workspace(const NormArgs& a);
 int norm_backward_launch(const NormArgs& a, cudaStream_t st);
 
+// Layer norm: as the norm, with a bias; dw and db in part as [blocks][2][d].
+struct LayerNormArgs : NormArgs {
+  const void* b;
+  float* db;
+  int lanes;  // an 8-bit output's groups are neighbouring lanes (or rows); set at the launch
+};
+int layernorm_forward_launch(const LayerNormArgs& a, cudaStream_t st);
+size_t layernorm_backward_workspace(const LayerNormArgs& a);
+int layernorm_backward_launch(const LayerNormArgs& a, cudaStream_t st);
+
 // Sequences and states, as described in atlas_ops.h.
 struct SeqArgs {
   const int* start;

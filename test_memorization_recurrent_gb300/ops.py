@@ -1,4 +1,5 @@
-"""Python binding of include/atlas_ops.h: norm, short convolution and selective scan.
+"""Python binding of include/atlas_ops.h: norm, layer norm, short convolution and
+selective scan.
 
 Like the binding of the memory update it only marshals: ``make_*_cfg`` fills a C
 description, the calls turn torch tensors into device pointers, enqueue on a stream and
@@ -17,6 +18,8 @@ ACT_NONE, ACT_SILU = 0, 1
 NORM_MAX_D, CONV_MAX_W, SCAN_MAX_N = 32768, 8, 128
 
 OPS_EXPORTS = ("atlas_norm_forward", "atlas_norm_backward", "atlas_norm_backward_workspace_bytes",
+               "atlas_layernorm_forward", "atlas_layernorm_backward",
+               "atlas_layernorm_backward_workspace_bytes",
                "atlas_conv_forward", "atlas_conv_backward", "atlas_conv_backward_workspace_bytes",
                "atlas_scan_forward", "atlas_scan_workspace_bytes", "atlas_scan_backward",
                "atlas_scan_backward_workspace_bytes")
@@ -69,6 +72,8 @@ def declare(lib) -> None:
     norm, conv, scan = (ctypes.POINTER(c) for c in (AtlasNormCfg, AtlasConvCfg, AtlasScanCfg))
     lib.atlas_norm_forward.argtypes = [_vp] * 3 + [norm] + [_vp] * 4
     lib.atlas_norm_backward.argtypes = [_vp] * 4 + [norm] + [_vp] * 3
+    lib.atlas_layernorm_forward.argtypes = [_vp] * 4 + [norm] + [_vp] * 4
+    lib.atlas_layernorm_backward.argtypes = [_vp] * 4 + [norm] + [_vp] * 4
     lib.atlas_conv_forward.argtypes = [_vp] * 3 + [conv] + [_vp] * 4
     lib.atlas_conv_backward.argtypes = [_vp] * 3 + [conv] + [_vp] * 7
     lib.atlas_scan_forward.argtypes = [_vp] * 8 + [scan] + [_vp] * 4
@@ -76,6 +81,7 @@ def declare(lib) -> None:
     for name in OPS_EXPORTS:
         getattr(lib, name).restype = _size if name.endswith("_bytes") else _int
     lib.atlas_norm_backward_workspace_bytes.argtypes = [norm]
+    lib.atlas_layernorm_backward_workspace_bytes.argtypes = [norm]
     lib.atlas_conv_backward_workspace_bytes.argtypes = [conv]
     lib.atlas_scan_workspace_bytes.argtypes = [scan]
     lib.atlas_scan_backward_workspace_bytes.argtypes = [scan]
@@ -300,6 +306,35 @@ def atlas_norm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, strea
     _call("atlas_norm_backward",
           (_arg(h, r, nr, "h", dev), _arg(weight, w, d, "weight", dev), _arg(dy, t, ny, "dy", dev),
            _arg(dh, r, nr, "dh", dev), cfg, _arg(dx, r, nr, "dx", dev), _arg(dw, F32, d, "dw", dev)), stream, dev)
+
+
+# ------------------------------------------------------------------ layer norm
+
+def atlas_layernorm_forward(x, residual, weight, bias, cfg: AtlasNormCfg, y, residual_out=None, scale=None,
+                            stream=None) -> None:
+    """y = layernorm(x + residual) * weight + bias, described as a norm (``make_norm_cfg``, eps > 0);
+    residual, weight, bias and residual_out may be None."""
+    dev = _begin(cfg)
+    t, r, w, o, d, nx, nr, ny, ns = cfg.extents or _norm_extents(cfg)
+    _call("atlas_layernorm_forward",
+          (_arg(x, t, nx, "x", dev), _arg(residual, r, nr, "residual", dev), _arg(weight, w, d, "weight", dev),
+           _arg(bias, w, d, "bias", dev), cfg, _arg(y, o, ny, "y", dev), _arg(residual_out, r, nr, "residual_out", dev),
+           _arg(scale, F32, ns, "scale", dev)), stream, dev)
+
+
+def atlas_layernorm_backward_workspace_bytes(cfg: AtlasNormCfg) -> int:
+    return _bytes("atlas_layernorm_backward_workspace_bytes", cfg)
+
+
+def atlas_layernorm_backward(h, weight, dy, dh, cfg: AtlasNormCfg, dx, dw=None, dbias=None, stream=None) -> None:
+    """dx = dL/dh, dw and dbias from dy = dL/dy and (or None) dh, the gradient that reaches the
+    residual stream from later layers."""
+    dev = _begin(cfg)
+    t, r, w, _, d, _, nr, ny, _ = cfg.extents or _norm_extents(cfg)
+    _call("atlas_layernorm_backward",
+          (_arg(h, r, nr, "h", dev), _arg(weight, w, d, "weight", dev), _arg(dy, t, ny, "dy", dev),
+           _arg(dh, r, nr, "dh", dev), cfg, _arg(dx, r, nr, "dx", dev), _arg(dw, F32, d, "dw", dev),
+           _arg(dbias, F32, d, "dbias", dev)), stream, dev)
 
 
 # ------------------------------------------------------------------ conv
