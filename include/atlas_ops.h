@@ -7,8 +7,10 @@
  *   conv       short causal convolution per channel, optionally through SiLU
  *   scan       selective state space scan: a diagonal recurrence whose decay depends on
  *              token, channel and state
+ *   glr        gated linear recurrence: one state a channel, its decay and its input each
+ *              behind a gate
  *
- * each forward and backward; conv and scan run whole sequences, packed sequences of
+ * each forward and backward; conv, scan and glr run whole sequences, packed sequences of
  * unequal lengths and single tokens (L = 1) through the same entry point.
  *
  * The conventions of atlas_mem.h hold: device pointers owned by the caller, work
@@ -129,7 +131,7 @@ int atlas_layernorm_backward(const void* h, const void* weight, const void* dy, 
                              const atlas_norm_cfg* cfg, void* dx, float* dw, float* dbias, void* stream);
 
 /* ------------------------------------------------- sequences and their states
- * conv and scan take B sequences in one of two forms:
+ * conv, scan and glr take B sequences in one of two forms:
  *   seq_start == NULL  every sequence has L tokens: row t of sequence b lies at
  *                      b * batch_stride + t * token_stride
  *   seq_start != NULL  the sequences are packed: L rows in all, sequence b has rows
@@ -255,6 +257,66 @@ int atlas_scan_backward(const void* x, const void* dt, const float* A, const voi
                         const atlas_scan_cfg* cfg, const float* h_in, const void* dy, float* dh,
                         void* dx, void* ddt, float* dA, void* dB, void* dC, float* dD, void* dz,
                         float* ddt_bias, void* stream);
+
+/* ------------------------------------------------------------------ glr
+ * Gated linear recurrence, one state per channel d of D:
+ *   s_t = c softplus(lambda[d]) sigmoid(r_t[d] + r_bias[d]),   a_t = exp(-s_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t[d] + i_bias[d]) x_t[d]
+ *   y_t = h_t SiLU(z_t[d])                                  (without z: y_t = h_t)
+ * r opens the decay: r = -infinity keeps the state and takes nothing in.  The state h [.., D], every gate
+ * and every sum are held in 32 bits; 1 - a^2 is computed from s, not from a, and keeps its relative precision next to
+ * a = 1.  The call reads its inputs once; its time goes by the rows, whatever their division into
+ * sequences. */
+typedef struct atlas_glr_cfg {
+  int B, L, D;     /* sequences (at most 65535), tokens (packed: rows), channels */
+  int dtype;       /* x, r, i, z, y and their gradients: ATLAS_F32, ATLAS_BF16, ATLAS_F16 */
+  float c;         /* > 0 */
+  long x_batch_stride, x_token_stride;
+  long r_batch_stride, r_token_stride;
+  long i_batch_stride, i_token_stride;
+  long z_batch_stride, z_token_stride;
+  long y_batch_stride, y_token_stride;
+  const int* seq_start;
+  const int* slot;
+  int n_slots;
+  const uint8_t* carry;
+  int* status_dev; /* also ATLAS_ERR_TIMEOUT, from a bounded wait that ran out */
+  void* workspace;
+  size_t workspace_bytes;
+} atlas_glr_cfg;
+
+/* Bytes of workspace atlas_glr_forward needs (0 for single tokens); (size_t)-1 for an invalid
+ * description. */
+size_t atlas_glr_workspace_bytes(const atlas_glr_cfg* cfg);
+
+/* Bytes of the states that the forward pass keeps for the backward pass. */
+size_t atlas_glr_kept_bytes(const atlas_glr_cfg* cfg);
+
+/*   x, r, i, z [.., L, D] dtype (i NULL: no input gate, i_bias is NULL then; z NULL: no output gate)
+ *   lambda [D], r_bias, i_bias [D] or NULL: fp32, contiguous
+ *   y [.., L, D] dtype out;  h_in, h_out [n, D] fp32, contiguous, or NULL
+ *   kept  atlas_glr_kept_bytes(cfg) out, or NULL */
+int atlas_glr_forward(const void* x, const void* r, const void* i, const void* z, const float* lambda,
+                      const float* r_bias, const float* i_bias, const atlas_glr_cfg* cfg, void* y,
+                      const float* h_in, float* h_out, void* kept, void* stream);
+
+size_t atlas_glr_backward_workspace_bytes(const atlas_glr_cfg* cfg);
+
+/* Gradients for L with dL/dy = dy and dL/d h_out = dh.  slot must be NULL.
+ *   h_in [B, D] as in the forward, or NULL
+ *   kept  what the forward pass of the same description, inputs and h_in kept, or NULL: those states
+ *      are then computed again, which reads x, r and i once more
+ *   dy [.., L, D] dtype, y's strides
+ *   dh [B, D] fp32 in/out or NULL: dL/d h_out on entry, dL/d h_in on return (zero for a
+ *      sequence with carry[b] == 0)
+ *   dx, dr, di, dz: dtype out, with the strides of x, r, i, z; di is NULL exactly when i is, dz
+ *      exactly when z is
+ *   dlambda [D], dr_bias [D] (NULL exactly when r_bias is), di_bias [D] (NULL exactly when
+ *      i_bias is): fp32 out */
+int atlas_glr_backward(const void* x, const void* r, const void* i, const void* z, const float* lambda,
+                       const float* r_bias, const float* i_bias, const atlas_glr_cfg* cfg,
+                       const float* h_in, const void* kept, const void* dy, float* dh, void* dx, void* dr,
+                       void* di, void* dz, float* dlambda, float* dr_bias, float* di_bias, void* stream);
 
 #ifdef __cplusplus
 }

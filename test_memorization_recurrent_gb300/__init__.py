@@ -14,14 +14,16 @@ import os
 import threading
 
 from . import ops as _ops
-from .ops import (ACT_NONE, ACT_SILU, BF16, CONV_MAX_W, E4M3, F16, F32, NORM_MAX_D, OPS_EXPORTS,
-                  SCAN_MAX_N, AtlasConvCfg, AtlasNormCfg, AtlasScanCfg, atlas_conv_backward,
-                  atlas_conv_backward_workspace_bytes, atlas_conv_forward,
-                  atlas_layernorm_backward, atlas_layernorm_backward_workspace_bytes,
-                  atlas_layernorm_forward, atlas_norm_backward,
-                  atlas_norm_backward_workspace_bytes, atlas_norm_forward, atlas_scan_backward,
-                  atlas_scan_backward_workspace_bytes, atlas_scan_forward,
-                  atlas_scan_workspace_bytes, make_conv_cfg, make_norm_cfg, make_scan_cfg)
+from .ops import (ACT_NONE, ACT_SILU, AtlasConvCfg, AtlasGlrCfg, AtlasNormCfg, AtlasScanCfg, BF16,
+                  CONV_MAX_W, E4M3, F16, F32, NORM_MAX_D, OPS_EXPORTS, SCAN_MAX_N,
+                  atlas_conv_backward, atlas_conv_backward_workspace_bytes, atlas_conv_forward,
+                  atlas_glr_backward, atlas_glr_backward_workspace_bytes, atlas_glr_forward,
+                  atlas_glr_kept_bytes, atlas_glr_workspace_bytes, atlas_layernorm_backward,
+                  atlas_layernorm_backward_workspace_bytes, atlas_layernorm_forward,
+                  atlas_norm_backward, atlas_norm_backward_workspace_bytes, atlas_norm_forward,
+                  atlas_scan_backward, atlas_scan_backward_workspace_bytes, atlas_scan_forward,
+                  atlas_scan_workspace_bytes, make_conv_cfg, make_glr_cfg, make_norm_cfg,
+                  make_scan_cfg)
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libatlasmem.so")

@@ -1,5 +1,6 @@
 """Build libatlasmem.so (sm_103a) in-tree with nvcc: one object per .cu file,
-compiled in parallel, then linked into a shared library under _build/.
+compiled in parallel (those alone whose sources changed), then linked into a shared library
+under _build/.
 
 ``build_variant`` builds a separately named copy with extra preprocessor
 definitions (used by tests that need a test-only switch compiled in); the
@@ -9,6 +10,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -38,8 +40,24 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _compile(src: str, objdir: str, extra) -> str:
+def _included(path: str, seen: set) -> set:
+    """A source file and the project's headers that it includes, directly or not."""
+    if path not in seen:
+        seen.add(path)
+        with open(path, encoding="utf-8") as f:
+            names = re.findall(r'^#include "([^"]+)"', f.read(), flags=re.M)
+        for name in names:
+            for where in (CSRC, os.path.join(ROOT, "include")):
+                if os.path.exists(os.path.join(where, name)):
+                    _included(os.path.join(where, name), seen)
+    return seen
+
+
+def _compile(src: str, objdir: str, extra, force: bool = True) -> str:
     obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
+    if not force and os.path.exists(obj) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(obj) for p in _included(src, set())):
+        return obj
     cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
@@ -52,7 +70,7 @@ def _build(lib: str, objdir: str, extra, force: bool) -> str:
         return lib
     os.makedirs(objdir, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=os.cpu_count() or 4) as ex:
-        objs = list(ex.map(lambda s: _compile(s, objdir, list(extra)), _sources()))
+        objs = list(ex.map(lambda s: _compile(s, objdir, list(extra), force), _sources()))
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)

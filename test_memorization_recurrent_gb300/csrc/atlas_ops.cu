@@ -1,6 +1,6 @@
 // atlas_ops.cu -- C-ABI entry points of the layer operators: argument checks, strides and
 // the choice between wide (16-byte) and element-wise accesses.  Every computation happens
-// in norm.cu, layernorm_*.cu, conv_*.cu and scan_*.cu.
+// in norm.cu, layernorm_*.cu, conv_*.cu, scan_*.cu and glr_*.cu.
 #include "atlas_ops.h"
 
 #include <algorithm>
@@ -213,6 +213,59 @@ bool scan_wide_n(const ScanArgs& a) {
   const int v = 16 / size_of(a.type);
   return a.N % v == 0 && a.bb % v == 0 && a.bt % v == 0 && a.cb % v == 0 && a.ct % v == 0 &&
          aligned(a.Bm, 16) && aligned(a.Cm, 16);
+}
+
+// ------------------------------------------------------------------ glr
+
+int check_glr(const atlas_glr_cfg* c) {
+  if (!c) return ATLAS_ERR_INVALID;
+  const int rc = check_seq(c->B, c->L, c->slot, c->n_slots);
+  if (rc != ATLAS_OK) return rc;
+  if (c->D < 1 || !float_type(c->dtype) || !(c->c > 0.f && c->c < 3e38f)) return ATLAS_ERR_INVALID;
+  const long s[] = {c->x_batch_stride, c->x_token_stride, c->r_batch_stride, c->r_token_stride,
+                    c->i_batch_stride, c->i_token_stride, c->z_batch_stride, c->z_token_stride,
+                    c->y_batch_stride, c->y_token_stride};
+  for (long v : s)
+    if (v < 0) return ATLAS_ERR_INVALID;
+  if (c->D > 0x7FFFFF00) return ATLAS_ERR_UNSUPPORTED;
+  return ATLAS_OK;
+}
+
+GlrArgs glr_args(const atlas_glr_cfg* c) {
+  GlrArgs a = {};
+  a.s = SeqArgs{c->seq_start, c->slot, c->carry, c->status_dev, c->B, c->L, c->n_slots};
+  a.D = c->D;
+  a.type = c->dtype;
+  a.c = c->c;
+  a.xb = c->x_batch_stride, a.xt = c->x_token_stride;
+  a.rbs = c->r_batch_stride, a.rt = c->r_token_stride;
+  a.ibs = c->i_batch_stride, a.it = c->i_token_stride;
+  a.zb = c->z_batch_stride, a.zt = c->z_token_stride;
+  a.yb = c->y_batch_stride, a.yt = c->y_token_stride;
+  strides(a.xb, a.xt, c->D, c->L);
+  strides(a.rbs, a.rt, c->D, c->L);
+  strides(a.ibs, a.it, c->D, c->L);
+  strides(a.zb, a.zt, c->D, c->L);
+  strides(a.yb, a.yt, c->D, c->L);
+  return a;
+}
+int check_glr(const atlas_glr_cfg* c, GlrArgs& a) {
+  const int rc = check_glr(c);
+  if (rc != ATLAS_OK) return rc;
+  a = glr_args(c);
+  return glr_covered(a) ? ATLAS_OK : ATLAS_ERR_UNSUPPORTED;
+}
+
+// How many elements of a row, 4, 2 or 1, are one access in every tensor.
+int glr_wide(const GlrArgs& a) {
+  const long s[] = {a.xb, a.xt, a.rbs, a.rt, a.ibs, a.it, a.zb, a.zt, a.yb, a.yt, a.D};
+  const void* p[] = {a.x, a.r, a.i, a.z, a.y, a.dy, a.dx, a.dr, a.di, a.dz};
+  int n = 4;
+  for (long v : s)
+    while (v % n) n /= 2;
+  for (const void* q : p)
+    while (!aligned(q, n * size_of(a.type))) n /= 2;
+  return n;
 }
 
 }  // namespace
@@ -487,6 +540,108 @@ int atlas_scan_backward(const void* x, const void* dt, const float* A, const voi
   a.wide = scan_wide(a);
   a.wide_n = scan_wide_n(a);
   return scan_backward_launch(a, stream_of(stream));
+}
+
+size_t atlas_glr_workspace_bytes(const atlas_glr_cfg* cfg) {
+  GlrArgs a;
+  return check_glr(cfg, a) == ATLAS_OK ? glr_workspace(a) : (size_t)-1;
+}
+
+size_t atlas_glr_kept_bytes(const atlas_glr_cfg* cfg) {
+  GlrArgs a;
+  return check_glr(cfg, a) == ATLAS_OK ? glr_kept(a) : (size_t)-1;
+}
+
+int atlas_glr_forward(const void* x, const void* r, const void* i, const void* z, const float* lambda,
+                      const float* r_bias, const float* i_bias, const atlas_glr_cfg* cfg, void* y,
+                      const float* h_in, float* h_out, void* kept, void* stream) {
+  GlrArgs a;
+  const int rc = check_glr(cfg, a);
+  if (rc != ATLAS_OK) return rc;
+  if (cfg->B == 0) return ATLAS_OK;
+  const int e = size_of(a.type);
+  if (!lambda || (cfg->L > 0 && (!x || !r || !y || (i_bias && !i)))) return ATLAS_ERR_INVALID;
+  const void* elems[] = {x, r, i, z, y};
+  for (const void* p : elems)
+    if (!aligned(p, e)) return ATLAS_ERR_INVALID;
+  const void* words[] = {lambda, r_bias, i_bias, h_in, h_out, kept};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return ATLAS_ERR_INVALID;
+  if (!apart(a.yb, a.yt, a.D, a.s.B, a.s.L, a.s.start)) return ATLAS_ERR_INVALID;
+  const size_t need = glr_workspace(a);
+  if (need && (!cfg->workspace || cfg->workspace_bytes < need || !aligned(cfg->workspace, 16)))
+    return ATLAS_ERR_WORKSPACE;
+  a.x = x;
+  a.r = r;
+  a.i = i;
+  a.z = z;
+  a.lam = lambda;
+  a.rb = r_bias;
+  a.ib = i_bias;
+  a.y = y;
+  a.h_in = h_in;
+  a.h_out = h_out;
+  a.kept = reinterpret_cast<float*>(kept);
+  a.ws = cfg->workspace;
+  a.wide = glr_wide(a);
+  return glr_forward_launch(a, stream_of(stream));
+}
+
+size_t atlas_glr_backward_workspace_bytes(const atlas_glr_cfg* cfg) {
+  GlrArgs a;
+  return check_glr(cfg, a) == ATLAS_OK && !cfg->slot ? glr_backward_workspace(a) : (size_t)-1;
+}
+
+int atlas_glr_backward(const void* x, const void* r, const void* i, const void* z, const float* lambda,
+                       const float* r_bias, const float* i_bias, const atlas_glr_cfg* cfg,
+                       const float* h_in, const void* kept, const void* dy, float* dh, void* dx, void* dr,
+                       void* di, void* dz, float* dlambda, float* dr_bias, float* di_bias, void* stream) {
+  GlrArgs a;
+  const int rc = check_glr(cfg, a);
+  if (rc != ATLAS_OK) return rc;
+  if (cfg->slot) return ATLAS_ERR_UNSUPPORTED;
+  const int e = size_of(a.type);
+  if (!lambda || !dlambda || (dr_bias != nullptr) != (r_bias != nullptr) ||
+      (di_bias != nullptr) != (i_bias != nullptr))
+    return ATLAS_ERR_INVALID;
+  if (cfg->L > 0 && cfg->B > 0 &&  // (tensors without elements may have no address)
+      (!x || !r || !dy || !dx || !dr || (i_bias && !i) || (di != nullptr) != (i != nullptr) ||
+       (dz != nullptr) != (z != nullptr)))
+    return ATLAS_ERR_INVALID;
+  const void* elems[] = {x, r, i, z, dy, dx, dr, di, dz};
+  for (const void* p : elems)
+    if (!aligned(p, e)) return ATLAS_ERR_INVALID;
+  const void* words[] = {lambda, r_bias, i_bias, h_in, kept, dh, dlambda, dr_bias, di_bias};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return ATLAS_ERR_INVALID;
+  const int nB = a.s.B, L = a.s.L;
+  if (!apart(a.xb, a.xt, a.D, nB, L, a.s.start) || !apart(a.rbs, a.rt, a.D, nB, L, a.s.start) ||
+      (i && !apart(a.ibs, a.it, a.D, nB, L, a.s.start)) || (z && !apart(a.zb, a.zt, a.D, nB, L, a.s.start)))
+    return ATLAS_ERR_INVALID;
+  const size_t need = glr_backward_workspace(a);
+  if (need && (!cfg->workspace || cfg->workspace_bytes < need || !aligned(cfg->workspace, 16)))
+    return ATLAS_ERR_WORKSPACE;
+  a.x = x;
+  a.r = r;
+  a.i = i;
+  a.z = z;
+  a.lam = lambda;
+  a.rb = r_bias;
+  a.ib = i_bias;
+  a.h_in = h_in;
+  a.kept = const_cast<float*>(reinterpret_cast<const float*>(kept));
+  a.dy = dy;
+  a.dh = dh;
+  a.dx = dx;
+  a.dr = dr;
+  a.di = di;
+  a.dz = dz;
+  a.dlam = dlambda;
+  a.drb = dr_bias;
+  a.dib = di_bias;
+  a.ws = cfg->workspace;
+  a.wide = glr_wide(a);
+  return glr_backward_launch(a, stream_of(stream));
 }
 
 }  // extern "C"

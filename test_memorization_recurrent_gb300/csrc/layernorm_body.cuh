@@ -2,12 +2,13 @@
 //
 //   h = x + r,  mu = mean h,  v = mean (h - mu)^2,  y = (h - mu) / sqrt(v + eps) w + b
 //
-// A row stays in registers from its load to its output, so the variance is taken of the deviations
-// themselves: a sum, then the sums of (h - m) and (h - m)^2 about the rounded mean m.  The first of
-// the two is what m's rounding left out, and enters mu and v: rows whose mean is large beside their
-// deviations lose nothing by the sum's roundings.
+// A row stays in registers from its load to its output.  Its sums are those of t = h - h_0, h_0 the row's first
+// element: mu = h_0 + mean t, v = mean t^2 - (mean t)^2.  A large mean thus enters no sum.  What the difference
+// cancels goes by (mean t)^2 / v; where that is above 16 (h_0 lies more than four deviations from the mean: it can
+// lie sqrt(d - 1) of them away) the row takes a second round of sums, of t - mean t.  So one round, and
+// one barrier of a block, is enough but for some rows of ten thousand of ordinary numbers.
 //
-// Rows of up to 256 channels belong to lanes of a warp, four rows under way; longer ones to a block,
+// Rows of up to 256 channels belong to lanes of a warp; longer ones to a block,
 // which walks rows with the next two on their way through shared memory (a few rows: a block each).
 // A thread has K times eight elements: eight neighbours of an aligned row, every tpr-th one of a row
 // that starts anywhere.  Such rows come to shared memory in whole pieces of 16 bytes too, from the
@@ -22,7 +23,7 @@ namespace layernorm {
 typedef LayerNormArgs Args;
 
 constexpr int kStages = 3;
-constexpr int kRed = 64;  // floats that a block's sums meet in: 16 sums, 16 pairs, 16 maxima
+constexpr int kRed = 160;  // floats that a block's sums meet in: twice 16 pairs (rows take turns), 16 pairs, 16 maxima twice
 
 // Column of element i of vector k.
 template <bool AL>
@@ -30,11 +31,20 @@ __device__ __forceinline__ int col(int k, int i, int tpr, int lane) {
   return AL ? (k * tpr + lane) * 8 + i : (k * 8 + i) * tpr + lane;
 }
 
-// Two sums over a row's threads, as row_reduce; words past the last warp's pair are zero.
+// Two sums over a row's threads.  A block's warps meet in red: pairs, of which those past the last warp's are
+// zero; the next use of the same words has to be another reduction's barrier away.
 __device__ __forceinline__ void row_sums2(float& x, float& y, const RowGroup& g, float* red) {
-  for (int m = min(g.tpr, 32) >> 1; m; m >>= 1) {
-    x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
-    y += __shfl_xor_sync(0xFFFFFFFFu, y, m);
+  if (g.tpr >= 32) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+      y += __shfl_xor_sync(0xFFFFFFFFu, y, m);
+    }
+  } else {
+    for (int m = g.tpr >> 1; m; m >>= 1) {
+      x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+      y += __shfl_xor_sync(0xFFFFFFFFu, y, m);
+    }
   }
   if (g.tpr > 32) {
     if ((g.tid & 31) == 0) *reinterpret_cast<float2*>(red + (g.tid >> 5) * 2) = make_float2(x, y);
@@ -75,30 +85,10 @@ __device__ __forceinline__ void load_params(const void* p, int type, float none,
   }
 }
 
-// A thread's weights and biases: kept in registers, or, of long rows (more than two vectors a thread), read
-// again for each row.
-template <int K, bool AL>
-struct Params {
-  static constexpr bool kKept = K <= 2;
-  float w[kKept ? K : 1][8], b[kKept ? K : 1][8];
-  __device__ __forceinline__ void load(const Args& a, int tpr, int lane) {
-    if constexpr (kKept) {
+__device__ __forceinline__ void add8(float* h, const float* v) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[k]);
-        load_params<AL>(a.b, a.wt, 0.f, k, a.d, tpr, lane, b[k]);
-      }
-    }
-  }
-  __device__ __forceinline__ void apply(const Args& a, int k, int tpr, int lane, float* h) {
-    if constexpr (!kKept) {
-      load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[0]);
-      load_params<AL>(a.b, a.wt, 0.f, k, a.d, tpr, lane, b[0]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = fmaf(h[i], w[kKept ? k : 0][i], b[kKept ? k : 0][i]);
-  }
-};
+  for (int i = 0; i < 8; i += 2) unpair(pair_add(pair(h[i], h[i + 1]), pair(v[i], v[i + 1])), h[i], h[i + 1]);
+}
 
 // Eight elements of a row that lies at p (`live` and inside the row), aligned or not; zeros elsewhere.
 template <int BYTES, bool AL>
@@ -145,46 +135,124 @@ __device__ __forceinline__ void store(void* p, long at, int type, int k, int d, 
   }
 }
 
-// One row from its elements h (zeros past its end).  red: kRed words; gm: this row's a.ng words for the
-// maxima of groups that are not neighbouring lanes' (every thread of the block comes here then).
+// A row's outputs in a type of 32 or 16 bits.  The type is looked at once: its branch around each element would
+// be most of an unaligned row's code.
 template <int K, bool AL>
-__device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, unsigned* gm, long row,
-                                            bool live, float (*h)[8], Params<K, AL>& par) {
-  const auto in = [&](int k, int i) { return col<AL>(k, AL ? 0 : i, g.tpr, g.lane) < a.d; };
-  float sum = 0.f;
+__device__ __forceinline__ void store_row(void* p, long at, int type, int d, int tpr, int lane, const float (*h)[8]) {
+  if (AL) {
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (a.r_out && live) store<AL>(a.r_out, row * a.sr, a.rt, k, a.d, g.tpr, g.lane, h[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += h[k][i];
+    for (int k = 0; k < K; ++k) store<AL>(p, at, type, k, d, tpr, lane, h[k]);
+    return;
   }
-  const float mean = row_sum(sum, g, red) * a.inv_d;
-  float rest = 0.f, ss = 0.f;
+  const auto each = [&](auto* q) {
+    typedef std::remove_pointer_t<decltype(q)> T;
 #pragma unroll
-  for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      h[k][i] = in(k, i) ? h[k][i] - mean : 0.f;
-      rest += h[k][i];
-      ss = fmaf(h[k][i], h[k][i], ss);
+      for (int i = 0; i < 8; ++i) {
+        const int c = col<AL>(k, i, tpr, lane);
+        if (c < d) q[c] = from_f<T>(h[k][i]);
+      }
+  };
+  if (type == ATLAS_F32)
+    each(reinterpret_cast<float*>(p) + at);
+  else if (type == ATLAS_BF16)
+    each(reinterpret_cast<__nv_bfloat16*>(p) + at);
+  else
+    each(reinterpret_cast<__half*>(p) + at);
+}
+// And in 8 bits.
+template <int K, bool AL>
+__device__ __forceinline__ void store_row8(void* p, long at, int d, int tpr, int lane, const float (*h)[8]) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) store<AL>(p, at, ATLAS_E4M3, k, d, tpr, lane, h[k]);
+}
+
+// A thread's weights and biases: kept in registers, or, of long rows (more than two vectors a thread), read
+// again for each row.
+template <int K, bool AL>
+struct Params {
+  static constexpr bool kKept = K <= 2;
+  float w[kKept ? K : 1][8], b[kKept ? K : 1][8];
+  __device__ __forceinline__ void load(const Args& a, int tpr, int lane) {
+    if constexpr (kKept) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[k]);
+        load_params<AL>(a.b, a.wt, 0.f, k, a.d, tpr, lane, b[k]);
+      }
     }
-  row_sums2(rest, ss, g, red + 16);
-  rest *= a.inv_d;
-  const float rstd = rsqrtf(fmaxf(fmaf(ss, a.inv_d, -rest * rest), 0.f) + a.eps), off = -rest * rstd;
+  }
+  __device__ __forceinline__ void apply(const Args& a, int k, int tpr, int lane, float rstd, float off, float* h) {
+    if constexpr (!kKept) {
+      load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[0]);
+      load_params<AL>(a.b, a.wt, 0.f, k, a.d, tpr, lane, b[0]);
+    }
+    const float *pw = w[kKept ? k : 0], *pb = b[kKept ? k : 0];
+    const pair32 rstd2 = pair(rstd, rstd), off2 = pair(off, off);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      unpair(pair_fma(pair_fma(pair(h[i], h[i + 1]), rstd2, off2), pair(pw[i], pw[i + 1]), pair(pb[i], pb[i + 1])), h[i], h[i + 1]);
+  }
+};
+
+// One row from its elements h (zeros past its end) and h0, its first.  red: kRed words, odd: every other row of a
+// block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
+// block comes here then).
+template <int K, bool AL>
+__device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, int odd, unsigned* gm,
+                                            long row, bool live, float h0, float (*h)[8], Params<K, AL>& par) {
+  const auto in = [&](int k, int i) { return col<AL>(k, AL ? 0 : i, g.tpr, g.lane) < a.d; };
+  // the elements less v, to h, and the sums of them and their squares; an aligned row's vectors past its end keep
+  // what comes out and stay out of the sums
+  const auto less = [&](float v, bool keep, float& s1, float& s2) {
+    const pair32 minus = pair(-v, -v);
+    s1 = s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      pair32 p1 = pair(0.f, 0.f), p2 = p1;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float t0, t1;
+        unpair(pair_add(pair(h[k][i], h[k][i + 1]), minus), t0, t1);
+        if (!AL) t0 = in(k, i) ? t0 : 0.f, t1 = in(k, i + 1) ? t1 : 0.f;
+        const pair32 t = pair(t0, t1);
+        p1 = pair_add(p1, t);
+        p2 = pair_fma(t, t, p2);
+        if (keep) h[k][i] = t0, h[k][i + 1] = t1;
+      }
+      const bool some = !AL || in(k, 0);
+      s1 += some ? pair_sum(p1) : 0.f;
+      s2 += some ? pair_sum(p2) : 0.f;
+    }
+  };
+  if (a.r_out && live) store_row<K, AL>(a.r_out, row * a.sr, a.rt, a.d, g.tpr, g.lane, h);
+  float s1, s2;
+  less(h0, true, s1, s2);
+  row_sums2(s1, s2, g, red + odd * 32);
+  float mean = s1 * a.inv_d, var = fmaf(s2, a.inv_d, -mean * mean);
+  const bool again = mean * mean > 16.f * var;
+  if (g.tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
+    less(mean, false, s1, s2);
+    row_sums2(s1, s2, g, red + 64);
+    if (again) {
+      s1 *= a.inv_d;
+      var = fmaf(s2, a.inv_d, -s1 * s1);
+      mean += s1;
+    }
+    if (g.tpr > 32) __syncthreads();  // (the next row may come here too)
+  }
+  const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), off = -mean * rstd;
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[k][i] = fmaf(h[k][i], rstd, off);
-    par.apply(a, k, g.tpr, g.lane, h[k]);
-    if (a.ot != ATLAS_E4M3) {
-      if (live) store<AL>(a.y, row * a.sy, a.ot, k, a.d, g.tpr, g.lane, h[k]);
-      continue;
-    }
+    par.apply(a, k, g.tpr, g.lane, rstd, off, h[k]);
+    if (a.ot != ATLAS_E4M3) continue;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (in(k, i)) m = fmaxf(m, fabsf(h[k][i]));
+      if (AL || in(k, i)) m = fmaxf(m, fabsf(h[k][i]));
+    if (AL && !in(k, 0)) m = 0.f;
     if (a.group == 0 || !a.lanes) {
       amax = fmaxf(amax, m);
       continue;
@@ -202,10 +270,14 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
       st8(a.y, row * a.sy + c, a.ot, h[k]);
     }
   }
-  if (a.ot != ATLAS_E4M3 || (a.group && a.lanes)) return;
+  if (a.ot != ATLAS_E4M3) {
+    if (live) store_row<K, AL>(a.y, row * a.sy, a.ot, a.d, g.tpr, g.lane, h);
+    return;
+  }
+  if (a.group && a.lanes) return;
   float inv = 0.f;
   if (a.group == 0) {
-    const float scale = scale_of(row_max(amax, g, red + 48));
+    const float scale = scale_of(row_max(amax, g, red + 96 + odd * 32));
     inv = inverse(scale);
     if (live && g.lane == 0) a.scale[row] = scale;
   } else {
@@ -235,45 +307,99 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
       const int c = col<AL>(k, i, g.tpr, g.lane);
       h[k][i] *= a.group == 0 ? inv : c < a.d ? __uint_as_float(gm[c / a.group]) : 0.f;
     }
-    if (live) store<AL>(a.y, row * a.sy, a.ot, k, a.d, g.tpr, g.lane, h[k]);
   }
+  if (live) store_row8<K, AL>(a.y, row * a.sy, a.d, g.tpr, g.lane, h);
 }
 
-// R rows at a time, straight from memory.  tpr threads a row: up to 32 lanes, or the whole block (R = 1).
-template <int XB, int RB, int K, int R, bool AL>
-__global__ void __launch_bounds__(512) forward_rows(Args a, int tpr) {
-  extern __shared__ __align__(16) float sm[];
-  if (tpr > 32) clear_red(sm, kRed);
-  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
-  const int rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
-  const long row0 = (long)blockIdx.x * rpb * R + mine;
-  Raw<XB, AL> x[R][K];
-  Raw<RB, AL> r[R][K];
-#pragma unroll
-  for (int j = 0; j < R; ++j)
+template <typename XT>
+constexpr int code_of() {
+  return std::is_same_v<XT, float> ? ATLAS_F32 : std::is_same_v<XT, __half> ? ATLAS_F16 : ATLAS_BF16;
+}
+// The residual's type: an aligned row's of 16 bits is x's where that has 16 bits (the launch sees to it).
+template <typename XT, int RB, bool AL>
+__device__ __forceinline__ int r_code(const Args& a) {
+  return RB == 4 ? ATLAS_F32 : AL && sizeof(XT) == 2 ? code_of<XT>() : a.rt;
+}
+
+// The two tensors' elements as they lie in memory, to h.
+template <typename XT, int RB, int K, bool AL>
+struct RawRow {
+  Raw<sizeof(XT), AL> x[K];
+  Raw<RB, AL> r[K];
+  __device__ __forceinline__ void load(const Args& a, long row, int tpr, int lane) {
+    const bool live = row < a.rows;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const long row = row0 + j * rpb;
-      x[j][k].load(a.x, row * a.sx, k, a.d, tpr, g.lane, row < a.rows);
-      r[j][k].load(a.r, row * a.sr, k, a.d, tpr, g.lane, row < a.rows);
+      x[k].load(a.x, row * a.sx, k, a.d, tpr, lane, live);
+      r[k].load(a.r, row * a.sr, k, a.d, tpr, lane, live);
     }
-  Params<K, AL> par;
-  par.load(a, tpr, g.lane);
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    float h[K][8];
+  }
+  __device__ __forceinline__ void floats(const Args& a, float (*h)[8]) const {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      x[j][k].floats(a.dt, h[k]);
+      x[k].floats(code_of<XT>(), h[k]);
       if (RB) {
         float v[8];
-        r[j][k].floats(a.rt, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] += v[i];
+        r[k].floats(r_code<XT, RB, AL>(a), v);
+        add8(h[k], v);
       }
     }
-    forward_row<K, AL>(a, g, sm, reinterpret_cast<unsigned*>(sm + kRed) + mine * a.ng, row0 + j * rpb,
-                       row0 + j * rpb < a.rows, h, par);
+  }
+};
+
+
+// A row's first element.
+template <typename XT, int RB>
+__device__ __forceinline__ float first_of(const Args& a, long row) {
+  float v = to_f(reinterpret_cast<const XT*>(a.x)[row * a.sx]);
+  if (RB) v += ld_any(a.r, row * a.sr, a.rt);
+  return v;
+}
+
+// A block a row, straight from memory.
+template <typename XT, int RB, int K, bool AL>
+__global__ void __launch_bounds__(512) forward_rows(Args a) {
+  extern __shared__ __align__(16) float sm[];
+  const int tpr = blockDim.x;
+  const RowGroup g{tpr, (int)threadIdx.x, (int)threadIdx.x};
+  const long row = blockIdx.x;
+  RawRow<XT, RB, K, AL> raw;
+  raw.load(a, row, tpr, g.lane);
+  const float h0 = first_of<XT, RB>(a, row);
+  Params<K, AL> par;
+  par.load(a, tpr, g.lane);
+  clear_red(sm, kRed);
+  float h[K][8];
+  raw.floats(a, h);
+  forward_row<K, AL>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm + kRed), row, true, h0, h, par);
+}
+
+// Rows of up to 256 channels: tpr lanes of a warp each.  Warps walk rows, the next two of their lanes' under way
+// while they compute two.
+template <typename XT, int RB, bool AL>
+__global__ void __launch_bounds__(128, 5) forward_lanes(Args a, int tpr) {
+  extern __shared__ __align__(16) float sm[];
+  constexpr int R = 2;
+  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
+  const int rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  RawRow<XT, RB, 1, AL> raw[R];
+  const long step = (long)gridDim.x * rpb;
+  long row = (long)blockIdx.x * rpb + mine;
+#pragma unroll
+  for (int j = 0; j < R; ++j) raw[j].load(a, row + j * step, tpr, g.lane);
+  Params<1, AL> par;
+  par.load(a, tpr, g.lane);
+  for (; row - mine < a.rows; row += R * step) {  // (the same turns for a block's threads)
+    float h[R][1][8];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      raw[j].floats(a, h[j]);
+      raw[j].load(a, row + (j + R) * step, tpr, g.lane);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+      forward_row<1, AL>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm) + mine * a.ng, row + j * step, row + j * step < a.rows,
+                         __shfl_sync(0xFFFFFFFFu, h[j][0][0], (threadIdx.x & 31) - g.lane), h[j], par);
   }
 }
 
@@ -306,18 +432,26 @@ __device__ __forceinline__ int ahead(const Rows& t, long row) {
 // beyond the tensor's ends come element by element.
 template <int E, int Q, bool AL>
 __device__ __forceinline__ void fetch_row(char* s, const Rows& t, long row, long rows, int d, int lane, int threads) {
-  if (E == 0) return;
+  if (E == 0 || row >= rows) return;
   if (AL) {
-    copy_row<Q>(s, t.lo, row * t.stride, d * E, row < rows, lane, threads);
+    const char* p = t.lo + row * t.stride + lane * 16;
+#pragma unroll
+    for (int k = 0; k < Q; ++k)
+      if ((k * threads + lane) * 16 < d * E) cp_async<16>(s + (k * threads + lane) * 16, p + k * threads * 16, true);
     return;
   }
-  if (row >= rows) return;
   const int shift = ahead(t, row), n = shift + d * E;
   const char* p = t.lo + row * t.stride - shift;
+  if (p >= t.lo && p + (n + 15) / 16 * 16 <= t.hi) {
 #pragma unroll
-  for (int k = 0; k <= Q; ++k) {
-    const int i = (k * threads + lane) * 16;
-    if (i >= n) continue;
+    for (int k = 0; k <= Q; ++k) {
+      const int i = (k * threads + lane) * 16;
+      if (i < n) cp_async<16>(s + i, p + i, true);
+    }
+    return;
+  }
+#pragma unroll 1
+  for (int i = lane * 16; i < n; i += threads * 16) {
     if (p + i >= t.lo && p + i + 16 <= t.hi) {
       cp_async<16>(s + i, p + i, true);
     } else {
@@ -348,9 +482,12 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
   }
 }
 
-template <int XB, int RB, int K, bool AL>
-__global__ void __launch_bounds__(512) forward_ring(Args a) {
+// Many rows of a block each: a block walks rows and copies the next kStages - 1 to shared memory while it computes
+// one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it.
+template <typename XT, int RB, int K, bool AL>
+__global__ void __maxnreg__(80) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
+  constexpr int XB = sizeof(XT);
   clear_red(sm, kRed);
   const RowGroup g{(int)blockDim.x, (int)threadIdx.x, (int)threadIdx.x};
   const int xs = slot_bytes<XB, AL>(a.d), bytes = xs + slot_bytes<RB, AL>(a.d);
@@ -371,22 +508,24 @@ __global__ void __launch_bounds__(512) forward_ring(Args a) {
   cp_wait<kStages - 2>();
   __syncthreads();
   int stage = 0;
-  for (; row < a.rows; row += gridDim.x) {
+  for (int odd = 0; row < a.rows; row += gridDim.x, odd ^= 1) {
     fetch(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
     const char* s = ring + stage * bytes;
+    const int ax = AL ? 0 : ahead(tx, row), ar = AL || RB == 0 ? 0 : ahead(tr, row);
+    float h0 = to_f(*reinterpret_cast<const XT*>(s + ax));
+    if constexpr (RB > 0) h0 += raw_float<RB>(ld_raw<RB>(s + xs + ar, 0), a.rt);
     float h[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      slot_floats<XB, AL>(s, AL ? 0 : ahead(tx, row), a.dt, k, a.d, g.tpr, g.lane, h[k]);
+      slot_floats<XB, AL>(s, ax, code_of<XT>(), k, a.d, g.tpr, g.lane, h[k]);
       if constexpr (RB > 0) {
         float v[8];
-        slot_floats<RB, AL>(s + xs, AL ? 0 : ahead(tr, row), a.rt, k, a.d, g.tpr, g.lane, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[k][i] += v[i];
+        slot_floats<RB, AL>(s + xs, ar, r_code<XT, RB, AL>(a), k, a.d, g.tpr, g.lane, v);
+        add8(h[k], v);
       }
     }
-    cp_wait<kStages - 2>();  // the next row's copies, handed over by the barriers of this one's sums
-    forward_row<K, AL>(a, g, sm, gm, row, true, h, par);
+    cp_wait<kStages - 2>();  // the next row's
+    forward_row<K, AL>(a, g, sm, odd, gm, row, true, h0, h, par);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_wait<0>();
@@ -394,12 +533,16 @@ __global__ void __launch_bounds__(512) forward_ring(Args a) {
 
 // ------------------------------------------------------------------ launches
 
-// Rows of up to 256 channels by the lanes that their vectors fill; longer ones by a block.
-inline RowPlan forward_plan(int d) {
+// Rows of up to 256 channels by the lanes that their vectors fill; longer ones by a block of at most 512 threads, of
+// one vector each while that is enough (`two`: two: what a row costs a thread besides its elements is then
+// shared by sixteen).
+inline RowPlan forward_plan(int d, bool two) {
   RowPlan p = rows_plan(d, 1);
+  const int nv = (d + 7) / 8;
   if (p.tpr <= 32) {
-    const int nv = (d + 7) / 8;
     for (p.tpr = 1; p.tpr < nv;) p.tpr *= 2;
+  } else if (two && p.k == 1) {
+    p = RowPlan{(nv + 63) / 64 * 32, 2, (nv + 63) / 64 * 32};
   }
   return p;
 }
@@ -414,47 +557,66 @@ int shared(F* f, size_t smem) {
   return ATLAS_OK;
 }
 
-template <int XB, int RB, int K, bool AL>
+// Blocks of a kernel that an SM holds by its registers, as many as run at once: rows are dealt to them in equal shares, and
+// a second wave of blocks for the rest would take as long as the first.
+template <typename F>
+int by_registers(F* f, int threads) {
+  static const int regs = [f] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, f) == cudaSuccess && at.numRegs > 0 ? (at.numRegs + 7) / 8 * 8 : 128;
+  }();
+  const int n = 65536 / (regs * threads), most = 2048 / threads;
+  return n < 1 ? 1 : n < most ? n : most;
+}
+
+template <typename XT, int RB, int K, bool AL>
 int run_ring(const Args& a, int threads, size_t smem, cudaStream_t st) {
-  auto* f = forward_ring<XB, RB, K, AL>;
+  auto* f = forward_ring<XT, RB, K, AL>;
   if (const int rc = shared(f, smem)) return rc;
-  const long most = (long)kSMs * resident(smem, 8 * 256 / threads);
+  const long most = (long)kSMs * resident(smem, by_registers(f, threads));
   f<<<(unsigned)(a.rows < most ? a.rows : most), threads, smem, st>>>(a);
   return status();
 }
 
-template <int XB, int RB, int K, int R, bool AL>
-int run_rows(const Args& a, const RowPlan& p, cudaStream_t st) {
-  const long rpb = p.block / p.tpr, blocks = (a.rows + rpb * R - 1) / (rpb * R);
-  if (blocks > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
-  const size_t smem = (kRed + (a.lanes ? 0 : (size_t)rpb * a.ng)) * 4;
-  auto* f = forward_rows<XB, RB, K, R, AL>;
+template <typename XT, int RB, int K, bool AL>
+int run_rows(const Args& a, int threads, cudaStream_t st) {
+  if (a.rows > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
+  const size_t smem = (kRed + (a.lanes ? 0 : (size_t)a.ng)) * 4;
+  auto* f = forward_rows<XT, RB, K, AL>;
   if (const int rc = shared(f, smem)) return rc;
-  f<<<(unsigned)blocks, p.block, smem, st>>>(a, p.tpr);
+  f<<<(unsigned)a.rows, threads, smem, st>>>(a);
   return status();
 }
 
-template <int XB, int RB, bool AL>
+template <typename XT, int RB, bool AL>
 int forward(const Args& args, cudaStream_t st) {
   Args a = args;
   // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
   a.lanes = a.ot != ATLAS_E4M3 || a.group == 0 || (AL && a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
-  const RowPlan p = forward_plan(a.d);
-  const bool few = a.rows <= kSMs * 8;
-  const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<XB, AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
-  if (!few && p.tpr > 32 && p.k <= 2 && ring <= 200 * 1024)
-    return p.k == 1 ? run_ring<XB, RB, 1, AL>(a, p.block, ring, st) : run_ring<XB, RB, 2, AL>(a, p.block, ring, st);
-  if (p.tpr <= 32) return few ? run_rows<XB, RB, 1, 1, AL>(a, p, st) : run_rows<XB, RB, 1, 4, AL>(a, p, st);
-  if (p.k == 1) return run_rows<XB, RB, 1, 1, AL>(a, p, st);
-  if (p.k == 2) return run_rows<XB, RB, 2, 1, AL>(a, p, st);
-  if (p.k == 4) return run_rows<XB, RB, 4, 1, AL>(a, p, st);
-  return run_rows<XB, RB, 8, 1, AL>(a, p, st);
+  const bool many = a.rows > kSMs * 8;
+  const RowPlan p = forward_plan(a.d, many);
+  if (a.d <= 256) {
+    const int rpb = p.block / p.tpr;
+    const size_t smem = a.lanes ? 0 : (size_t)rpb * a.ng * 4;
+    auto* f = forward_lanes<XT, RB, AL>;
+    if (const int rc = shared(f, smem)) return rc;
+    const long need = (a.rows + rpb - 1) / rpb, most = 5L * kSMs;
+    f<<<(unsigned)(need < most ? need : most), p.block, smem, st>>>(a, p.tpr);
+    return status();
+  }
+  const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<sizeof(XT), AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
+  if (many && p.k == 2 && ring <= 200 * 1024) return run_ring<XT, RB, 2, AL>(a, p.block, ring, st);
+  if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
+  if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
+  if (p.k == 4) return run_rows<XT, RB, 4, AL>(a, p.block, st);
+  return run_rows<XT, RB, 8, AL>(a, p.block, st);
 }
-template <int XB>
+template <typename XT>
 int forward(const Args& a, cudaStream_t st) {
   const int rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
-  if (a.wide) return rb == 0 ? forward<XB, 0, true>(a, st) : rb == 2 ? forward<XB, 2, true>(a, st) : forward<XB, 4, true>(a, st);
-  return rb == 0 ? forward<XB, 0, false>(a, st) : rb == 2 ? forward<XB, 2, false>(a, st) : forward<XB, 4, false>(a, st);
+  const bool mixed = rb == 2 && sizeof(XT) == 2 && a.rt != a.dt;  // bf16 and fp16: element by element
+  if (a.wide && !mixed) return rb == 0 ? forward<XT, 0, true>(a, st) : rb == 2 ? forward<XT, 2, true>(a, st) : forward<XT, 4, true>(a, st);
+  return rb == 0 ? forward<XT, 0, false>(a, st) : rb == 2 ? forward<XT, 2, false>(a, st) : forward<XT, 4, false>(a, st);
 }
 
 }  // namespace layernorm

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, i
       slot_floats<HB, AL>(s, AL || !live ? 0 : ahead(th, row), a.rt, k, a.d, tpr, lane, h[k]);
       slot_floats<DB, AL>(s + hs, AL || !live ? 0 : ahead(td, row), a.dt, k, a.d, tpr, lane, dy[k]);
       if constexpr (GB > 0) slot_floats<GB, AL>(s + hs + ds, AL || !live ? 0 : ahead(tg, row), a.rt, k, a.d, tpr, lane, gv[k]);
-      if (!AL && !live) {  // nothing was copied for a place of the block without a row
+      if (!live) {  // nothing was copied for a place of the block without a row
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] = dy[k][i] = 0.f;
       }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(256) long_cols(Args a, const float4* stats) {
 // ------------------------------------------------------------------ launches
 
 RowPlan back_plan(int d) {
-  RowPlan p = forward_plan(d);
+  RowPlan p = forward_plan(d, false);
   return p;
 }
 // Partial sums: at most so many blocks.
@@ -276,15 +276,18 @@ int run(const Args& a, int& blocks, cudaStream_t st) {
 }  // namespace
 }  // namespace layernorm
 
-int layernorm_run_2(const LayerNormArgs& a, cudaStream_t st);
-int layernorm_run_4(const LayerNormArgs& a, cudaStream_t st);
+int layernorm_run_f32(const LayerNormArgs& a, cudaStream_t st);
+int layernorm_run_bf16(const LayerNormArgs& a, cudaStream_t st);
+int layernorm_run_f16(const LayerNormArgs& a, cudaStream_t st);
 
 int layernorm_forward_launch(const LayerNormArgs& args, cudaStream_t st) {
   LayerNormArgs a = args;
   a.inv_d = 1.f / a.d;
   a.ng = a.group ? (a.d + a.group - 1) / a.group : 1;
   for (a.gshift = 0; (1 << a.gshift) < a.group;) ++a.gshift;
-  return a.dt == ATLAS_F32 ? layernorm_run_4(a, st) : layernorm_run_2(a, st);
+  if (a.dt == ATLAS_BF16) return layernorm_run_bf16(a, st);
+  if (a.dt == ATLAS_F16) return layernorm_run_f16(a, st);
+  return layernorm_run_f32(a, st);
 }
 
 size_t layernorm_backward_workspace(const LayerNormArgs& a) {

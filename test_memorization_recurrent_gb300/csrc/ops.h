@@ -105,4 +105,40 @@ int scan_forward_launch(const ScanArgs& a, cudaStream_t st);
 size_t scan_backward_workspace(const ScanArgs& a);
 int scan_backward_launch(const ScanArgs& a, cudaStream_t st);
 
+struct GlrArgs {
+  SeqArgs s;
+  const void* x;
+  const void* r;
+  const void* i;
+  const void* z;
+  const float* lam;
+  const float* rb;
+  const float* ib;
+  void* y;  // null: only the kept states
+  const float* h_in;
+  float* h_out;
+  float* kept;  // forward: written where given; backward: read where given
+  void* ws;
+  int D, type;
+  float c;
+  long xb, xt, rbs, rt, ibs, it, zb, zt, yb, yt;
+  int wide;  // 4, 2 or 1: neighbouring elements that are one access
+  // backward
+  const void* dy;
+  float* dh;
+  void* dx;
+  void* dr;
+  void* di;
+  void* dz;
+  float* dlam;
+  float* drb;
+  float* dib;
+};
+bool glr_covered(const GlrArgs& a);
+size_t glr_workspace(const GlrArgs& a);
+size_t glr_kept(const GlrArgs& a);
+int glr_forward_launch(const GlrArgs& a, cudaStream_t st);
+size_t glr_backward_workspace(const GlrArgs& a);
+int glr_backward_launch(const GlrArgs& a, cudaStream_t st);
+
 }  // namespace atlas

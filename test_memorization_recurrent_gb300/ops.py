@@ -1,5 +1,5 @@
-"""Python binding of include/atlas_ops.h: norm, layer norm, short convolution and
-selective scan.
+"""Python binding of include/atlas_ops.h: norm, layer norm, short convolution, selective
+scan and gated linear recurrence.
 
 Like the binding of the memory update it only marshals: ``make_*_cfg`` fills a C
 description, the calls turn torch tensors into device pointers, enqueue on a stream and
@@ -22,7 +22,8 @@ OPS_EXPORTS = ("atlas_norm_forward", "atlas_norm_backward", "atlas_norm_backward
                "atlas_layernorm_backward_workspace_bytes",
                "atlas_conv_forward", "atlas_conv_backward", "atlas_conv_backward_workspace_bytes",
                "atlas_scan_forward", "atlas_scan_workspace_bytes", "atlas_scan_backward",
-               "atlas_scan_backward_workspace_bytes")
+               "atlas_scan_backward_workspace_bytes", "atlas_glr_forward", "atlas_glr_workspace_bytes",
+               "atlas_glr_kept_bytes", "atlas_glr_backward", "atlas_glr_backward_workspace_bytes")
 
 _int, _long, _vp, _size = ctypes.c_int, ctypes.c_long, ctypes.c_void_p, ctypes.c_size_t
 
@@ -67,9 +68,19 @@ class AtlasScanCfg(_Cfg):
                 ("carry", _vp), ("status_dev", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
 
 
+class AtlasGlrCfg(_Cfg):
+    """Mirror of ``atlas_glr_cfg`` in include/atlas_ops.h."""
+    _fields_ = [("B", _int), ("L", _int), ("D", _int), ("dtype", _int), ("c", ctypes.c_float),
+                ("x_batch_stride", _long), ("x_token_stride", _long), ("r_batch_stride", _long),
+                ("r_token_stride", _long), ("i_batch_stride", _long), ("i_token_stride", _long),
+                ("z_batch_stride", _long), ("z_token_stride", _long), ("y_batch_stride", _long),
+                ("y_token_stride", _long), ("seq_start", _vp), ("slot", _vp), ("n_slots", _int),
+                ("carry", _vp), ("status_dev", _vp), ("workspace", _vp), ("workspace_bytes", _size)]
+
+
 def declare(lib) -> None:
     """Argument types of the operators' entry points in an opened library."""
-    norm, conv, scan = (ctypes.POINTER(c) for c in (AtlasNormCfg, AtlasConvCfg, AtlasScanCfg))
+    norm, conv, scan, glr = (ctypes.POINTER(c) for c in (AtlasNormCfg, AtlasConvCfg, AtlasScanCfg, AtlasGlrCfg))
     lib.atlas_norm_forward.argtypes = [_vp] * 3 + [norm] + [_vp] * 4
     lib.atlas_norm_backward.argtypes = [_vp] * 4 + [norm] + [_vp] * 3
     lib.atlas_layernorm_forward.argtypes = [_vp] * 4 + [norm] + [_vp] * 4
@@ -78,6 +89,8 @@ def declare(lib) -> None:
     lib.atlas_conv_backward.argtypes = [_vp] * 3 + [conv] + [_vp] * 7
     lib.atlas_scan_forward.argtypes = [_vp] * 8 + [scan] + [_vp] * 4
     lib.atlas_scan_backward.argtypes = [_vp] * 8 + [scan] + [_vp] * 12
+    lib.atlas_glr_forward.argtypes = [_vp] * 7 + [glr] + [_vp] * 5
+    lib.atlas_glr_backward.argtypes = [_vp] * 7 + [glr] + [_vp] * 12
     for name in OPS_EXPORTS:
         getattr(lib, name).restype = _size if name.endswith("_bytes") else _int
     lib.atlas_norm_backward_workspace_bytes.argtypes = [norm]
@@ -85,6 +98,8 @@ def declare(lib) -> None:
     lib.atlas_conv_backward_workspace_bytes.argtypes = [conv]
     lib.atlas_scan_workspace_bytes.argtypes = [scan]
     lib.atlas_scan_backward_workspace_bytes.argtypes = [scan]
+    for name in ("atlas_glr_workspace_bytes", "atlas_glr_kept_bytes", "atlas_glr_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [glr]
 
 
 # ------------------------------------------------------------------ descriptions
@@ -134,6 +149,21 @@ def make_scan_cfg(B, L, D, N, G=1, dtype=BF16, softplus=True, x_strides=(0, 0),
                        *s, *_sequences(B, seq_start, slot, n_slots, carry),
                        _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
                        int(workspace_bytes))
+    cfg.held = (seq_start, slot, carry, status_dev, workspace)
+    cfg.home = _home(*cfg.held)
+    return cfg
+
+
+def make_glr_cfg(B, L, D, c=8.0, dtype=BF16, x_strides=(0, 0), r_strides=(0, 0), i_strides=(0, 0),
+                 z_strides=(0, 0), y_strides=(0, 0), seq_start=None, slot=None, n_slots=0, carry=None,
+                 status_dev=None, workspace=None, workspace_bytes=0) -> AtlasGlrCfg:
+    """Strides: (batch, token) in elements, (0, 0) = contiguous.  Device tensors as for
+    ``make_conv_cfg``."""
+    s = [int(v) for p in (x_strides, r_strides, i_strides, z_strides, y_strides) for v in p]
+    cfg = AtlasGlrCfg(int(B), int(L), int(D), int(dtype), float(c), *s,
+                      *_sequences(B, seq_start, slot, n_slots, carry),
+                      _checked(status_dev, "int32", 1, "status_dev"), _space(workspace, workspace_bytes),
+                      int(workspace_bytes))
     cfg.held = (seq_start, slot, carry, status_dev, workspace)
     cfg.home = _home(*cfg.held)
     return cfg
@@ -433,3 +463,66 @@ def atlas_scan_backward(x, dt, A, Bm, Cm, Dskip, z, dt_bias, cfg: AtlasScanCfg, 
            _arg(dh, F32, n, "dh", dev), _arg(dx, t, nx, "dx", dev), _arg(ddt, t, nt, "ddt", dev),
            _arg(dA, F32, dn, "dA", dev), _arg(dB, t, nb, "dB", dev), _arg(dC, t, nc, "dC", dev),
            _arg(dD, F32, D, "dD", dev), _arg(dz, t, nz, "dz", dev), _arg(ddt_bias, F32, D, "ddt_bias", dev)), stream, dev)
+
+
+# ------------------------------------------------------------------ glr
+
+def _glr_extents(c):
+    _known(c.dtype)
+    D = c.D
+    c.extents = e = (c.dtype, _dense(D), _tokens(c, c.x_batch_stride, c.x_token_stride, D),
+                     _tokens(c, c.r_batch_stride, c.r_token_stride, D), _tokens(c, c.i_batch_stride, c.i_token_stride, D),
+                     _tokens(c, c.z_batch_stride, c.z_token_stride, D), _tokens(c, c.y_batch_stride, c.y_token_stride, D),
+                     _dense((c.n_slots if c.slot else c.B) * D), _dense(c.B * D))
+    return e
+
+
+def _kept(t, cfg, device):
+    """Address of the kept states, a tensor of any type."""
+    if t is None or type(t) is int:
+        return t
+    nbytes = _bytes("atlas_glr_kept_bytes", cfg)
+    if t.get_device() != device or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise _error(f"kept must be a contiguous tensor of at least {nbytes} bytes on the current device (cuda:{device})")
+    return t.data_ptr()
+
+
+def atlas_glr_workspace_bytes(cfg: AtlasGlrCfg) -> int:
+    return _bytes("atlas_glr_workspace_bytes", cfg)
+
+
+def atlas_glr_kept_bytes(cfg: AtlasGlrCfg) -> int:
+    return _bytes("atlas_glr_kept_bytes", cfg)
+
+
+def atlas_glr_backward_workspace_bytes(cfg: AtlasGlrCfg) -> int:
+    return _bytes("atlas_glr_backward_workspace_bytes", cfg)
+
+
+def atlas_glr_forward(x, r, i, z, lam, r_bias, i_bias, cfg: AtlasGlrCfg, y, h_in=None, h_out=None, kept=None,
+                      stream=None) -> None:
+    """Gated linear recurrence; L = 1 is the single-token form.  i, z, r_bias, i_bias, h_in, h_out and kept may be
+    None; h_in and h_out ([B or n_slots, D]) may be the same tensor.  kept (``atlas_glr_kept_bytes``)
+    receives what the backward pass starts from."""
+    dev = _begin(cfg)
+    t, D, nx, nr, ni, nz, ny, n, _ = cfg.extents or _glr_extents(cfg)
+    _call("atlas_glr_forward",
+          (_arg(x, t, nx, "x", dev), _arg(r, t, nr, "r", dev), _arg(i, t, ni, "i", dev), _arg(z, t, nz, "z", dev),
+           _arg(lam, F32, D, "lam", dev), _arg(r_bias, F32, D, "r_bias", dev), _arg(i_bias, F32, D, "i_bias", dev), cfg,
+           _arg(y, t, ny, "y", dev), _arg(h_in, F32, n, "h_in", dev), _arg(h_out, F32, n, "h_out", dev),
+           _kept(kept, cfg, dev)), stream, dev)
+
+
+def atlas_glr_backward(x, r, i, z, lam, r_bias, i_bias, cfg: AtlasGlrCfg, h_in, kept, dy, dh, dx, dr, di, dz, dlam,
+                       dr_bias, di_bias, stream=None) -> None:
+    """Gradients of the recurrence (see include/atlas_ops.h); dh is dL/d h_out on entry and dL/d h_in on return,
+    kept what the forward pass kept, or None."""
+    dev = _begin(cfg)
+    t, D, nx, nr, ni, nz, ny, _, n = cfg.extents or _glr_extents(cfg)
+    _call("atlas_glr_backward",
+          (_arg(x, t, nx, "x", dev), _arg(r, t, nr, "r", dev), _arg(i, t, ni, "i", dev), _arg(z, t, nz, "z", dev),
+           _arg(lam, F32, D, "lam", dev), _arg(r_bias, F32, D, "r_bias", dev), _arg(i_bias, F32, D, "i_bias", dev), cfg,
+           _arg(h_in, F32, n, "h_in", dev), _kept(kept, cfg, dev), _arg(dy, t, ny, "dy", dev), _arg(dh, F32, n, "dh", dev),
+           _arg(dx, t, nx, "dx", dev), _arg(dr, t, nr, "dr", dev), _arg(di, t, ni, "di", dev), _arg(dz, t, nz, "dz", dev),
+           _arg(dlam, F32, D, "dlam", dev), _arg(dr_bias, F32, D, "dr_bias", dev), _arg(di_bias, F32, D, "di_bias", dev)),
+          stream, dev)
