@@ -32,7 +32,10 @@ namespace glr {
 
 constexpr int kRows = 128, kCh = 32, kWarps = 8, kGroup = 16;
 constexpr int kPer = kRows / kWarps;  // rows of a warp
-constexpr int kBlocks = 2;            // of an SM: a thread's elements and the work on them take 128 registers
+#ifndef GLR_B
+#define GLR_B 2
+#endif
+constexpr int kBlocks = GLR_B;            // of an SM: a thread's elements and the work on them take 128 registers
 constexpr unsigned long long kAbsent = ~0ull;
 constexpr int kPolls = 1 << 22;  // seconds; never reached unless a block of an earlier ticket is lost
 
@@ -203,8 +206,10 @@ __device__ __forceinline__ void post(unsigned long long* p, unsigned long long v
 }
 
 // What a warp's lanes (a channel each) get from the tiles j0 .. k - 1 of a string in walking order, whose words lie at
-// words + j * width: their maps, one after the other, of 0.
-__device__ __forceinline__ float carry_from(const unsigned long long* words, size_t width, long j0, long k, int* status) {
+// words + j * width: their maps, one after the other, of 0.  early: the word of k - 1 as it was some time ago.
+__device__ __forceinline__ float carry_from(const unsigned long long* words, size_t width, long j0, long k, unsigned long long early, int* status) {
+  if (j0 == k - 1 && __all_sync(0xFFFFFFFFu, early != kAbsent))
+    return apply(__uint_as_float((unsigned)(early >> 32)), __uint_as_float((unsigned)early), 0.f);
   float c = 0.f;
   for (long j = j0; j < k; j += 8) {
     unsigned long long v[8];
@@ -244,9 +249,10 @@ struct alignas(16) Tile {
   __device__ __forceinline__ long row0(const GlrArgs& a) const { return (long)string * a.s.L + (long)(k - first) * kRows; }
 };
 // The state that reaches a tile whose string's carry begins at place `from`.
-__device__ __forceinline__ float carry_to(const Strings& t, const Tile& q, unsigned from, const unsigned long long* words, size_t width, int* status) {
-  const long lead = (long)(q.at / t.group * t.group) - 1;
-  return carry_from(words + q.first * width, width, (long)from > lead ? (long)from : lead, q.at, status);
+__device__ __forceinline__ float carry_to(const Strings& t, const Tile& q, unsigned from, const unsigned long long* words, size_t width,
+                                          unsigned long long early, int* status) {
+  const long lead = (long)(t.group == 1 ? q.at : q.at / t.group * t.group) - 1;
+  return carry_from(words + q.first * width, width, (long)from > lead ? (long)from : lead, q.at, early, status);
 }
 
 // ------------------------------------------------------------------ rows
@@ -433,8 +439,8 @@ static __global__ void __launch_bounds__(256) prepare(GlrArgs a, Space w, long t
 
 // ------------------------------------------------------------------ forward
 
-// A block takes its next ticket when a tile's states are known, and copies the next tile while it puts this one out.  (Tickets
-// taken earlier would keep tiles waiting for others that no block has begun.)
+// A block copies its next tile while it puts this one out.  It takes the ticket not before it begins a tile: tickets taken
+// earlier would keep tiles waiting for others that no block has begun.
 template <typename T, int V, bool FLAT>
 __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w, Strings t) {
   typedef Shape<V> Sh;
@@ -475,6 +481,12 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
     fetch(q, info, 0);
   }
   for (int p = 0; q.some; p ^= 1) {
+    unsigned next = 0;
+    unsigned long long early = kAbsent;
+    if (warp == 0) {  // on their way while the tile is computed
+      if (lane == 0) next = atomicAdd(w.ticket, 1u);
+      if (q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
+    }
     const int c = q.c0 + ch;
     const unsigned live = Info::bits<S>(info.live, tg * S, c < a.D), first = Info::bits<S>(info.first, tg * S, c < a.D);
     float rate[V], rb[V], ib[V];
@@ -572,8 +584,6 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
     }
     __syncthreads();
     if (warp == 0) {
-      unsigned next = 0;
-      if (lane == 0) next = atomicAdd(w.ticket, 1u);
       float2 m[kWarps];
       unsigned long long* words = w.words + q.c0 + lane;
       const bool last = t.group == 1 || q.at % t.group == t.group - 1;
@@ -592,7 +602,7 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
       const int b = info.seq(0);
       if (info.live & ~info.first & 1) {
         const unsigned from = t.n > 1 ? 0u : (unsigned)((a.s.start ? (long)a.s.start[b] : (long)b * a.s.L) / kRows);
-        cin = carry_to(t, q, from, words, width, a.s.status);
+        cin = carry_to(t, q, from, words, width, early, a.s.status);
       }
       if (a.kept && q.c0 + lane < a.D) a.kept[(long)q.k * a.D + q.c0 + lane] = cin;
 #pragma unroll
@@ -743,6 +753,12 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
     fetch(q, info, 0);
   }
   for (int p = 0; q.some; p ^= 1) {
+    unsigned next = 0;
+    unsigned long long early = kAbsent;
+    if (warp == kWarps - 1) {
+      if (lane == 0) next = atomicAdd(w.ticket, 1u);
+      if (q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
+    }
     const int c = q.c0 + ch;
     char* stage = buf + (kAhead ? p : 0) * slots_bytes<T>(5);
     const Slots<T, V, S> bx(stage, 0), br(stage, 1), bi(stage, 2), bz(stage, 3), by(stage, 4);
@@ -884,8 +900,6 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         h = apply(s_map[0][i][lane], s_map[1][i][lane], h);
       }
     } else if (warp == kWarps - 1) {  // the gradients behind them (its rows are the last)
-      unsigned next = 0;
-      if (lane == 0) next = atomicAdd(w.ticket, 1u);
       float2 m[kWarps];
       unsigned long long* words = w.words + q.c0 + lane;
       const bool last = t.group == 1 || q.at % t.group == t.group - 1;
@@ -904,7 +918,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
       const int b = info.seq(kPer - 1);
       if ((info.live & ~info.last) >> (kPer - 1) & 1) {
         const unsigned from = t.n > 1 ? 0u : t.tiles - 1 - (unsigned)(((a.s.start ? (long)a.s.start[b + 1] : (long)(b + 1) * a.s.L) - 1) / kRows);
-        cin = carry_to(t, q, from, words, width, a.s.status);
+        cin = carry_to(t, q, from, words, width, early, a.s.status);
       }
 #pragma unroll
       for (int i = kWarps - 1; i >= 0; --i) {
