@@ -30,7 +30,10 @@
 namespace atlas {
 namespace glr {
 
-constexpr int kRows = 128, kCh = 32, kWarps = 8, kGroup = 16;
+#ifndef GLR_G
+#define GLR_G 16
+#endif
+constexpr int kRows = 128, kCh = 32, kWarps = 8, kGroup = GLR_G;
 constexpr int kPer = kRows / kWarps;  // rows of a warp
 #ifndef GLR_B
 #define GLR_B 2
@@ -205,30 +208,19 @@ __device__ __forceinline__ void post(unsigned long long* p, unsigned long long v
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
-// What a warp's lanes (a channel each) get from the tiles j0 .. k - 1 of a string in walking order, whose words lie at
-// words + j * width: their maps, one after the other, of 0.  early: the word of k - 1 as it was some time ago.
-__device__ __forceinline__ float carry_from(const unsigned long long* words, size_t width, long j0, long k, unsigned long long early, int* status) {
-  if (j0 == k - 1 && __all_sync(0xFFFFFFFFu, early != kAbsent))
-    return apply(__uint_as_float((unsigned)(early >> 32)), __uint_as_float((unsigned)early), 0.f);
-  float c = 0.f;
-  for (long j = j0; j < k; j += 8) {
-    unsigned long long v[8];
-    for (int polls = 0;; ++polls) {
-      bool all = true;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (j + i < k) v[i] = peek(words + (j + i) * width), all &= v[i] != kAbsent;
-      if (__all_sync(0xFFFFFFFFu, all)) break;
-      if (polls >= kPolls) {
-        if (status) *status = ATLAS_ERR_TIMEOUT;
-        break;
-      }
+// A word that another block leaves, once it is there.  By a whole warp, a channel each.
+__device__ __forceinline__ unsigned long long await(const unsigned long long* p, unsigned long long v, int* status) {
+  for (int polls = 0; !__all_sync(0xFFFFFFFFu, v != kAbsent); ++polls) {
+    if (polls >= kPolls) {
+      if (status) *status = ATLAS_ERR_TIMEOUT;
+      break;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (j + i < k) c = apply(__uint_as_float((unsigned)(v[i] >> 32)), __uint_as_float((unsigned)v[i]), c);
+    v = peek(p);
   }
-  return c;
+  return v;
+}
+__device__ __forceinline__ float apply(unsigned long long word, float c) {
+  return apply(__uint_as_float((unsigned)(word >> 32)), __uint_as_float((unsigned)word), c);
 }
 
 // Which tile a ticket is: string, place in it in walking order, tile (of all, and the first of the string), first channel.
@@ -248,12 +240,25 @@ struct alignas(16) Tile {
   // the call's row that the tile begins with
   __device__ __forceinline__ long row0(const GlrArgs& a) const { return (long)string * a.s.L + (long)(k - first) * kRows; }
 };
-// The state that reaches a tile whose string's carry begins at place `from`.
-__device__ __forceinline__ float carry_to(const Strings& t, const Tile& q, unsigned from, const unsigned long long* words, size_t width,
-                                          unsigned long long early, int* status) {
-  const long lead = (long)(t.group == 1 ? q.at : q.at / t.group * t.group) - 1;
-  return carry_from(words + q.first * width, width, (long)from > lead ? (long)from : lead, q.at, early, status);
-}
+// What a tile gets through the words of its group: those from place j0 on (and, first, what the group before left), where
+// its string's carry begins.  Each warp asks for two, so that all are on their way at once.
+struct Group {
+  unsigned long long word[kGroup][kCh];
+  unsigned j0;  // == the tile's place: nothing reaches it
+  __device__ __forceinline__ void begin(const Strings& t, const Tile& q, bool some, unsigned from) {
+    const unsigned own = q.at / t.group * t.group, lead = own > 0 ? own - 1 : 0;
+    j0 = !some ? q.at : from > lead ? from : lead;
+  }
+  __device__ __forceinline__ void gather(const Tile& q, const unsigned long long* words, size_t width, int* status) {
+    for (unsigned i = threadIdx.x >> 5; j0 + i < q.at; i += kWarps)
+      word[i][threadIdx.x & 31] = await(words + (q.first + j0 + i) * width, kAbsent, status);
+  }
+  __device__ __forceinline__ float carry(const Tile& q) const {
+    float c = 0.f;
+    for (unsigned i = 0; j0 + i < q.at; ++i) c = apply(word[i][threadIdx.x & 31], c);
+    return c;
+  }
+};
 
 // ------------------------------------------------------------------ rows
 
@@ -448,6 +453,7 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
   extern __shared__ __align__(16) char buf[];  // x, r, i, z twice
   __shared__ float2 s_map[kWarps][kCh];
   __shared__ __align__(16) float s_carry[kWarps][kCh];
+  __shared__ Group s_group;
   __shared__ Tile s_tile;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % Sh::lanes * V, tg = lane / Sh::lanes;
   const int r0 = warp * kPer + tg * S;  // the thread's first row
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
     unsigned long long early = kAbsent;
     if (warp == 0) {  // on their way while the tile is computed
       if (lane == 0) next = atomicAdd(w.ticket, 1u);
-      if (q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
+      if (t.group == 1 && q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
     }
     const int c = q.c0 + ch;
     const unsigned live = Info::bits<S>(info.live, tg * S, c < a.D), first = Info::bits<S>(info.first, tg * S, c < a.D);
@@ -582,35 +588,40 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
       }
       if (tg == 0) fd[v] = fh[v] = 0.f;  // nothing in front: the identity
     }
+    const unsigned long long* words = w.words + q.c0 + lane;
+    const bool last = t.group == 1 || q.at % t.group == t.group - 1;
+    bool some = false;
+    if (warp == 0) {  // whether a state reaches the tile, and from where in its string
+      const int b = info.seq(0);
+      some = info.live & ~info.first & 1;
+      if (t.group > 1 && lane == 0)
+        s_group.begin(t, q, some, t.n > 1 || !some ? 0u : (unsigned)((a.s.start ? (long)a.s.start[b] : (long)b * a.s.L) / kRows));
+    }
     __syncthreads();
-    if (warp == 0) {
-      float2 m[kWarps];
-      unsigned long long* words = w.words + q.c0 + lane;
-      const bool last = t.group == 1 || q.at % t.group == t.group - 1;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) m[i] = s_map[i][lane];
-      if (!last) {
-        float td = m[0].x, th = m[0].y;
+    if (t.group > 1) {
+      if (warp == 1 && !last) {  // the tile's own map
+        float2 m = s_map[0][lane];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) {
-          th = apply(m[i].x, m[i].y, th);
-          td = after(m[i].x, td);
+          const float2 o = s_map[i][lane];
+          m.y = apply(o.x, o.y, m.y);
+          m.x = after(o.x, m.x);
         }
-        post(words + (q.first + q.at) * width, word_of(td, th));
+        post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(m.x, m.y));
       }
-      float cin = 0.f;
-      const int b = info.seq(0);
-      if (info.live & ~info.first & 1) {
-        const unsigned from = t.n > 1 ? 0u : (unsigned)((a.s.start ? (long)a.s.start[b] : (long)b * a.s.L) / kRows);
-        cin = carry_to(t, q, from, words, width, early, a.s.status);
-      }
+      s_group.gather(q, words, width, a.s.status);
+      __syncthreads();
+    }
+    if (warp == 0) {
+      float cin = t.group > 1 ? s_group.carry(q) : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
       if (a.kept && q.c0 + lane < a.D) a.kept[(long)q.k * a.D + q.c0 + lane] = cin;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
         s_carry[i][lane] = cin;
-        cin = apply(m[i].x, m[i].y, cin);
+        const float2 m = s_map[i][lane];
+        cin = apply(m.x, m.y, cin);
       }
-      if (last) post(words + (q.first + q.at) * width, word_of(kCut, cin));
+      if (last) post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(kCut, cin));
       if (lane == 0) s_tile.find(t, next, false);
     }
     __syncthreads();
@@ -719,6 +730,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
   __shared__ float s_map[3][kWarps][kCh];
   __shared__ __align__(16) float s_carry[2][kWarps][kCh];
   __shared__ float s_sum[kWarps][3][kCh];
+  __shared__ Group s_group;
   __shared__ Tile s_tile;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch = lane % Sh::lanes * V, tg = lane / Sh::lanes;
   const int r0 = warp * kPer + tg * S;
@@ -757,7 +769,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
     unsigned long long early = kAbsent;
     if (warp == kWarps - 1) {
       if (lane == 0) next = atomicAdd(w.ticket, 1u);
-      if (q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
+      if (t.group == 1 && q.at > 0) early = peek(w.words + q.c0 + lane + (q.first + q.at - 1) * width);
     }
     const int c = q.c0 + ch;
     char* stage = buf + (kAhead ? p : 0) * slots_bytes<T>(5);
@@ -891,7 +903,29 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
       if (tg == 0) fd[v] = fh[v] = 0.f;
       if (tg == Sh::groups - 1) bd[v] = bc[v] = 0.f;
     }
+    const unsigned long long* words = w.words + q.c0 + lane;
+    const bool end = t.group == 1 || q.at % t.group == t.group - 1;
+    bool some = false;
+    if (warp == kWarps - 1) {  // whether a gradient reaches the tile, and from where in its string (its rows are the last)
+      const int b = info.seq(kPer - 1);
+      some = (info.live & ~info.last) >> (kPer - 1) & 1;
+      if (t.group > 1 && lane == 0)
+        s_group.begin(t, q, some, t.n > 1 || !some ? 0u : t.tiles - 1 - (unsigned)(((a.s.start ? (long)a.s.start[b + 1] : (long)(b + 1) * a.s.L) - 1) / kRows));
+    }
     __syncthreads();
+    if (t.group > 1) {
+      if (warp == 1 && !end) {
+        float d = s_map[0][kWarps - 1][lane], g = s_map[2][kWarps - 1][lane];
+#pragma unroll
+        for (int i = kWarps - 2; i >= 0; --i) {
+          g = apply(s_map[0][i][lane], s_map[2][i][lane], g);
+          d = after(s_map[0][i][lane], d);
+        }
+        post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(d, g));
+      }
+      s_group.gather(q, words, width, a.s.status);
+      __syncthreads();
+    }
     if (warp == 0) {  // the states in front of the warps
       float h = q.c0 + lane < a.D ? kept[(long)q.k * a.D + q.c0 + lane] : 0.f;
 #pragma unroll
@@ -899,33 +933,14 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         s_carry[0][i][lane] = h;
         h = apply(s_map[0][i][lane], s_map[1][i][lane], h);
       }
-    } else if (warp == kWarps - 1) {  // the gradients behind them (its rows are the last)
-      float2 m[kWarps];
-      unsigned long long* words = w.words + q.c0 + lane;
-      const bool last = t.group == 1 || q.at % t.group == t.group - 1;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) m[i] = make_float2(s_map[0][i][lane], s_map[2][i][lane]);
-      if (!last) {
-        float ta = m[kWarps - 1].x, tc = m[kWarps - 1].y;
-#pragma unroll
-        for (int i = kWarps - 2; i >= 0; --i) {
-          tc = apply(m[i].x, m[i].y, tc);
-          ta = after(m[i].x, ta);
-        }
-        post(words + (q.first + q.at) * width, word_of(ta, tc));
-      }
-      float cin = 0.f;
-      const int b = info.seq(kPer - 1);
-      if ((info.live & ~info.last) >> (kPer - 1) & 1) {
-        const unsigned from = t.n > 1 ? 0u : t.tiles - 1 - (unsigned)(((a.s.start ? (long)a.s.start[b + 1] : (long)(b + 1) * a.s.L) - 1) / kRows);
-        cin = carry_to(t, q, from, words, width, early, a.s.status);
-      }
+    } else if (warp == kWarps - 1) {  // the gradients behind them
+      float cin = t.group > 1 ? s_group.carry(q) : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
 #pragma unroll
       for (int i = kWarps - 1; i >= 0; --i) {
         s_carry[1][i][lane] = cin;
-        cin = apply(m[i].x, m[i].y, cin);
+        cin = apply(s_map[0][i][lane], s_map[2][i][lane], cin);
       }
-      if (last) post(words + (q.first + q.at) * width, word_of(kCut, cin));
+      if (end) post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(kCut, cin));
       if (lane == 0) s_tile.find(t, next, true);
     }
     __syncthreads();
