@@ -444,8 +444,8 @@ static __global__ void __launch_bounds__(256) prepare(GlrArgs a, Space w, long t
 
 // ------------------------------------------------------------------ forward
 
-// A block copies its next tile while it puts this one out.  It takes the ticket not before it begins a tile: tickets taken
-// earlier would keep tiles waiting for others that no block has begun.
+// A block copies its next tile from when it has this one's maps.  It takes the ticket not before it begins a tile: tickets
+// taken earlier would keep tiles waiting for others that no block has begun.
 template <typename T, int V, bool FLAT>
 __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w, Strings t) {
   typedef Shape<V> Sh;
@@ -596,8 +596,11 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
       some = info.live & ~info.first & 1;
       if (t.group > 1 && lane == 0)
         s_group.begin(t, q, some, t.n > 1 || !some ? 0u : (unsigned)((a.s.start ? (long)a.s.start[b] : (long)b * a.s.L) / kRows));
+      if (lane == 0) s_tile.find(t, next, false);
     }
     __syncthreads();
+    const Tile q1 = s_tile;
+    Info info1;
     if (t.group > 1) {
       if (warp == 1 && !last) {  // the tile's own map
         float2 m = s_map[0][lane];
@@ -622,15 +625,12 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
         cin = apply(m.x, m.y, cin);
       }
       if (last) post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(kCut, cin));
-      if (lane == 0) s_tile.find(t, next, false);
     }
-    __syncthreads();
-    const Tile q1 = s_tile;
-    Info info1;
-    if (q1.some) {
+    if (q1.some) {  // the next tile's rows: x, r and i are in registers, z has another place
       info1.look(a, w, t, q1);
       fetch(q1, info1, p ^ 1);
     }
+    __syncthreads();
     float h[V];
     ld_vec<V>(&s_carry[warp][ch], h);
 #pragma unroll
@@ -911,8 +911,11 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
       some = (info.live & ~info.last) >> (kPer - 1) & 1;
       if (t.group > 1 && lane == 0)
         s_group.begin(t, q, some, t.n > 1 || !some ? 0u : t.tiles - 1 - (unsigned)(((a.s.start ? (long)a.s.start[b + 1] : (long)(b + 1) * a.s.L) - 1) / kRows));
+      if (lane == 0) s_tile.find(t, next, true);
     }
     __syncthreads();
+    const Tile q1 = s_tile;
+    Info info1;
     if (t.group > 1) {
       if (warp == 1 && !end) {
         float d = s_map[0][kWarps - 1][lane], g = s_map[2][kWarps - 1][lane];
@@ -941,15 +944,12 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         cin = apply(s_map[0][i][lane], s_map[2][i][lane], cin);
       }
       if (end) post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(kCut, cin));
-      if (lane == 0) s_tile.find(t, next, true);
     }
-    __syncthreads();
-    const Tile q1 = s_tile;
-    Info info1;
     if (q1.some) {
       info1.look(a, w, t, q1);
       if (kAhead) fetch(q1, info1, p ^ 1);
     }
+    __syncthreads();
     float h[V], g[V], sum[3][V];
     ld_vec<V>(&s_carry[0][warp][ch], h);
     ld_vec<V>(&s_carry[1][warp][ch], g);
