@@ -423,21 +423,38 @@ static __global__ void __launch_bounds__(256) prepare(GlrArgs a, Space w, long t
   for (long b = id / 32; b < a.s.B; b += n / 32) {  // a warp each
     SeqTile t = {};
     t.b = (int)b;
-    bool ok = true, empty = a.s.L == 0;
+    bool ok = true;
     if (packed) {
       const int s = a.s.start[b], e = a.s.start[b + 1];
       ok = b < rising && s >= 0 && e >= s && e <= a.s.L;
-      empty = s == e;
     }
     ok = ok && seq_state(a.s, t);
     if ((packed || a.s.slot) && lane == 0) w.state[b] = ok ? t.slot : -1;
-    if (!ok || !empty) continue;
-    if (back) {
-      if (a.dh && !t.carry)
-        for (long c = lane; c < a.D; c += 32) a.dh[b * a.D + c] = 0.f;
-    } else if (a.h_out) {
-      for (long c = lane; c < a.D; c += 32)
-        a.h_out[(long)t.slot * a.D + c] = a.h_in && t.carry ? a.h_in[(long)t.slot * a.D + c] : 0.f;
+  }
+  // the states of empty sequences, 256 channels a warp
+  if (!packed && a.s.L > 0) return;
+  const long parts = (a.D + 255) / 256;
+  for (long task = id / 32; task < a.s.B * parts; task += n / 32) {
+    const long b = task / parts;
+    SeqTile t = {};
+    t.b = (int)b;
+    if (packed) {
+      const int s = a.s.start[b], e = a.s.start[b + 1];
+      if (s != e || b >= rising || s < 0 || e > a.s.L) continue;
+    }
+    if (!seq_state(a.s, t)) continue;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long c = (task - b * parts) * 256 + i * 32 + lane;
+      v[i] = !back && a.h_in && t.carry && c < a.D ? a.h_in[(long)t.slot * a.D + c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long c = (task - b * parts) * 256 + i * 32 + lane;
+      if (c >= a.D) continue;
+      if (!back && a.h_out) a.h_out[(long)t.slot * a.D + c] = v[i];
+      if (back && a.dh && !t.carry) a.dh[b * a.D + c] = 0.f;
     }
   }
 }
@@ -1113,8 +1130,8 @@ static __global__ void __launch_bounds__(1024) add_sums(GlrArgs a, const float* 
 inline int status() { return cudaGetLastError() == cudaSuccess ? ATLAS_OK : ATLAS_ERR_CUDA; }
 
 inline int run_prepare(const GlrArgs& a, const Space& w, bool back, cudaStream_t st) {
-  const long tiles = tiles_of(a), fill = tiles * groups_of(a) * (kCh / 2), tasks = (long)a.s.B * 32;
-  long n = (fill > tasks ? fill : tasks) / 256 / 4 + 1;
+  const long tiles = tiles_of(a), fill = tiles * groups_of(a) * (kCh / 2), tasks = (long)a.s.B * (a.s.start ? 1 + (a.D + 255) / 256 : 1) * 32;
+  long n = (fill / 4 > tasks ? fill / 4 : tasks) / 256 + 1;
   n = n < 4L * kSMs ? n : 4L * kSMs;
   prepare<<<(unsigned)n, 256, 0, st>>>(a, w, tiles, groups_of(a), back);
   return status();

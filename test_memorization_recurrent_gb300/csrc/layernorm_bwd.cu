@@ -4,8 +4,8 @@
 //   dw = sum over rows of dy hat,  db = sum over rows of dy
 //
 // Rows of up to 8192 channels: a block walks rows (short ones: lanes of a warp each), the next one or two
-// on their way through shared memory; a row's statistics take two rounds of sums (h and w dy; then,
-// about the mean, what its rounding left out, the squares and the products with w dy).  A thread's
+// on their way through shared memory; a row's four sums are taken about its first element, as in the forward
+// pass.  A thread's
 // columns are the same in every row, so dw and db stay in its registers; blocks write partial sums,
 // which a second launch adds in a fixed order.  Longer rows: a block a row, which reads it three times
 // (from L2 but the first), then partial sums by column from the rows' kept statistics.
@@ -16,15 +16,13 @@ namespace layernorm {
 namespace {
 
 constexpr int kMaxRow = 8192;
+constexpr int kSums = 192;  // floats that a block's sums meet in: twice 16 fours (rows take turns), 16 fours
 
-// MT: most threads; up to 320 (2560 channels), two blocks an SM without a register in memory.
-template <int HB, int DB, int GB, int K, bool AL, int MT>  // bytes of h, dy, dh (0: none)
-__global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, int tpr, int stages) {
-  extern __shared__ __align__(16) float sm[];  // 2 x 32 for the sums, then [stage][row of the block]: h, dy, dh
-  float *red = sm, *red2 = sm + 32;
-  const RowGroup g{tpr, (int)threadIdx.x % tpr, (int)threadIdx.x};
-  const int lane = g.lane, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
-  clear_red(sm, 96);
+// A thread's two vectors take 128 registers with dw, db and the weights.
+template <int HB, int DB, int GB, int K, bool AL>  // bytes of h, dy, dh (0: none)
+__global__ void __launch_bounds__(512) backward_rows(Args a, int tpr, int stages) {
+  extern __shared__ __align__(16) float sm[];  // 3 x 64 for the sums, then [stage][row of the block]: h, dy, dh
+  const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
   float dw[K][8], db[K][8], w[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -33,7 +31,7 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, i
     for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
   }
   const int hs = slot_bytes<HB, AL>(a.d), ds = slot_bytes<DB, AL>(a.d), bytes = hs + ds + slot_bytes<GB, AL>(a.d);
-  char* ring = reinterpret_cast<char*>(sm + 96) + mine * bytes;
+  char* ring = reinterpret_cast<char*>(sm + kSums) + mine * bytes;
   const Rows th = rows_of<HB>(a.x, a.sr, a.rows, a.d), td = rows_of<DB>(a.dy, a.sy, a.rows, a.d),
              tg = rows_of<GB>(a.r, a.sr, a.rows, a.d);
   const long step = (long)gridDim.x * rpb;
@@ -56,76 +54,98 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, i
   next_done();
   __syncthreads();
   int stage = 0;
-  for (; row - mine < a.rows; row += step) {
+  for (int odd = 0; row - mine < a.rows; row += step, odd ^= 1) {
     const bool live = row < a.rows;
     fetch(row + (stages - 1) * step, stage == 0 ? stages - 1 : stage - 1);
     const char* s = ring + stage * rpb * bytes;
     stage = stage + 1 == stages ? 0 : stage + 1;
-    float h[K][8], dy[K][8], gv[K][8], sum = 0.f, dsum = 0.f;
+    float h[K][8], dy[K][8], gv[K][8];
+    const int ah = AL || !live ? 0 : ahead(th, row), ad = AL || !live ? 0 : ahead(td, row), ag = AL || !live || GB == 0 ? 0 : ahead(tg, row);
+    const float h0 = live ? raw_float<HB>(ld_raw<HB>(s + ah, 0), a.rt) : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      slot_floats<HB, AL>(s, AL || !live ? 0 : ahead(th, row), a.rt, k, a.d, tpr, lane, h[k]);
-      slot_floats<DB, AL>(s + hs, AL || !live ? 0 : ahead(td, row), a.dt, k, a.d, tpr, lane, dy[k]);
-      if constexpr (GB > 0) slot_floats<GB, AL>(s + hs + ds, AL || !live ? 0 : ahead(tg, row), a.rt, k, a.d, tpr, lane, gv[k]);
+      slot_floats<HB, AL>(s, ah, a.rt, k, a.d, tpr, lane, h[k]);
+      slot_floats<DB, AL>(s + hs, ad, a.dt, k, a.d, tpr, lane, dy[k]);
+      if constexpr (GB > 0) slot_floats<GB, AL>(s + hs + ds, ag, a.rt, k, a.d, tpr, lane, gv[k]);
       if (!live) {  // nothing was copied for a place of the block without a row
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[k][i] = dy[k][i] = 0.f;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sum += h[k][i];
-        dsum = fmaf(w[k][i], dy[k][i], dsum);
-        db[k][i] += dy[k][i];
-      }
     }
     next_done();  // the next row's copies, handed over by the barriers below
     if (tpr <= 32) __syncwarp();
-    row_sums2(sum, dsum, g, red);
-    const float mean = sum * a.inv_d;
-    float rest = 0.f, ss = 0.f, dot = 0.f;
+    // Sums of t, t^2, w dy and t w dy, t = h - h0, the row's first element; and again of t - mean t where what the
+    // differences cancel is more than 16 times what is left (as in the forward pass).
+    float sum[4];
+    const auto sums = [&](float minus) {
+      pair32 s1 = pair(0.f, 0.f), s2 = s1, s3 = s1, s4 = s1;
+      const pair32 less = pair(-minus, -minus);
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[k][i] = in(k, i) ? h[k][i] - mean : 0.f;
-        rest += h[k][i];
-        ss = fmaf(h[k][i], h[k][i], ss);
-        dot = fmaf(h[k][i], w[k][i] * dy[k][i], dot);
+        for (int i = 0; i < 8; i += 2) {
+          float t0, t1;
+          unpair(pair_add(pair(h[k][i], h[k][i + 1]), less), t0, t1);
+          if (!in(k, i)) t0 = 0.f;
+          if (!in(k, i + 1)) t1 = 0.f;
+          const pair32 t = pair(t0, t1), wdy = pair_mul(pair(w[k][i], w[k][i + 1]), pair(dy[k][i], dy[k][i + 1]));
+          s1 = pair_add(s1, t);
+          s2 = pair_fma(t, t, s2);
+          s3 = pair_add(s3, wdy);
+          s4 = pair_fma(t, wdy, s4);
+        }
+      sum[0] = pair_sum(s1), sum[1] = pair_sum(s2), sum[2] = pair_sum(s3), sum[3] = pair_sum(s4);
+    };
+    const auto meet = [&](float* red) {
+      for (int m = min(tpr, 32) >> 1; m; m >>= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], m);
+      if (tpr > 32) {
+        if ((threadIdx.x & 31) == 0) *reinterpret_cast<float4*>(red + (threadIdx.x >> 5) * 4) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        __syncthreads();
+        float4 v = reinterpret_cast<const float4*>(red)[0];
+        for (int i = 1; i < tpr / 32; ++i) {
+          const float4 o = reinterpret_cast<const float4*>(red)[i];
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        }
+        sum[0] = v.x, sum[1] = v.y, sum[2] = v.z, sum[3] = v.w;
       }
-    // three sums
-    for (int m = min(tpr, 32) >> 1; m; m >>= 1) {
-      rest += __shfl_xor_sync(0xFFFFFFFFu, rest, m);
-      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, m);
-      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, m);
-    }
-    if (tpr > 32) {
-      if ((threadIdx.x & 31) == 0) *reinterpret_cast<float4*>(red2 + (threadIdx.x >> 5) * 4) = make_float4(rest, ss, dot, 0.f);
-      __syncthreads();
-      rest = ss = dot = 0.f;
-      for (int i = 0; i < tpr / 32; ++i) {
-        const float4 t = reinterpret_cast<const float4*>(red2)[i];
-        rest += t.x;
-        ss += t.y;
-        dot += t.z;
+    };
+    sums(h0);
+    meet(sm + odd * 64);
+    float mean = sum[0] * a.inv_d, var = fmaf(sum[1], a.inv_d, -mean * mean), dot = fmaf(-mean, sum[2], sum[3]), base = h0;
+    const bool again = mean * mean > 16.f * var;
+    if (tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
+      sums(h0 + mean);
+      meet(sm + 128);
+      if (again) {
+        base = h0 + mean;
+        mean = sum[0] * a.inv_d;
+        var = fmaf(sum[1], a.inv_d, -mean * mean);
+        dot = fmaf(-mean, sum[2], sum[3]);
       }
+      if (tpr > 32) __syncthreads();  // (the next row may come here too)
     }
-    rest *= a.inv_d;
-    const float rstd = rsqrtf(fmaxf(fmaf(ss, a.inv_d, -rest * rest), 0.f) + a.eps), off = -rest * rstd;
-    const float mdy = dsum * a.inv_d, mhat = rstd * (dot * a.inv_d - rest * mdy);
+    const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), mdy = sum[2] * a.inv_d, mhat = rstd * dot * a.inv_d;
+    // hat = (h - base) rstd - mean rstd;  dx = rstd (w dy - mdy - hat mhat) + dh
+    const pair32 less = pair(-base, -base), rstd2 = pair(rstd, rstd), off2 = pair(-mean * rstd, -mean * rstd),
+                 mdy2 = pair(-mdy, -mdy), mhat2 = pair(-mhat, -mhat);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float hat = fmaf(h[k][i], rstd, off);
-        dw[k][i] = fmaf(dy[k][i], hat, dw[k][i]);
-        o[i] = rstd * (fmaf(w[k][i], dy[k][i], -mdy) - hat * mhat) + (GB ? gv[k][i] : 0.f);
+      for (int i = 0; i < 8; i += 2) {
+        const pair32 d2 = pair(dy[k][i], dy[k][i + 1]);
+        const pair32 hat = pair_fma(pair_add(pair(h[k][i], h[k][i + 1]), less), rstd2, off2);
+        unpair(pair_fma(d2, hat, pair(dw[k][i], dw[k][i + 1])), dw[k][i], dw[k][i + 1]);
+        unpair(pair_add(d2, pair(db[k][i], db[k][i + 1])), db[k][i], db[k][i + 1]);
+        const pair32 o = pair_fma(hat, mhat2, pair_fma(pair(w[k][i], w[k][i + 1]), d2, mdy2));
+        unpair(GB ? pair_fma(rstd2, o, pair(gv[k][i], gv[k][i + 1])) : pair_mul(rstd2, o), h[k][i], h[k][i + 1]);
       }
-      if (live) store<AL>(a.y, row * a.sr, a.rt, k, a.d, tpr, lane, o);
     }
+    if (live) store_row<K, AL>(a.y, row * a.sr, a.rt, a.d, tpr, lane, h);
   }
   cp_wait<0>();
-  float* acc = sm + 96;  // over the rows' ring
+  float* acc = sm + kSums;  // over the rows' ring
   for (int which = 0; which < 2; ++which) {
     if (!(which ? a.db : a.dw)) continue;
     float* part = a.part + ((long)blockIdx.x * 2 + which) * a.d;
@@ -150,23 +170,24 @@ __global__ void __launch_bounds__(MT, MT == 320 ? 2 : 1) backward_rows(Args a, i
   }
 }
 
-// dw[c] and db[c]: sums over the blocks' partial sums; 32 columns a block, 8 threads a column.
-__global__ void __launch_bounds__(256) sum_parts(const float* part, float* dw, float* db, int nblk, int d) {
-  __shared__ float s[8][33];
+// dw[c] and db[c]: sums over the blocks' partial sums; 32 columns a block, 32 threads a column (8, with four loads under
+// way: 10.6 us for 304 blocks' of 2560).
+__global__ void __launch_bounds__(1024) sum_parts(const float* part, float* dw, float* db, int nblk, int d) {
+  __shared__ float s[32][33];
   float* out = blockIdx.y ? db : dw;
   if (!out) return;
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + cx;
   float v = 0.f;
   if (c < d) {
-#pragma unroll 4
-    for (int r = ry; r < nblk; r += 8) v += part[((long)r * 2 + blockIdx.y) * d + c];
+#pragma unroll 8
+    for (int r = ry; r < nblk; r += 32) v += part[((long)r * 2 + blockIdx.y) * d + c];
   }
   s[ry][cx] = v;
   __syncthreads();
   if (ry == 0 && c < d) {
 #pragma unroll
-    for (int r = 1; r < 8; ++r) v += s[r][cx];
+    for (int r = 1; r < 32; ++r) v += s[r][cx];
     out[c] = v;
   }
 }
@@ -230,39 +251,34 @@ __global__ void __launch_bounds__(256) long_cols(Args a, const float4* stats) {
 
 // ------------------------------------------------------------------ launches
 
-RowPlan back_plan(int d) {
-  RowPlan p = forward_plan(d, false);
-  return p;
-}
+// Unaligned rows have one vector a thread while that is enough: two, with their conditions, do not fit the registers.
+RowPlan back_plan(const Args& a, bool aligned) { return forward_plan(a.d, aligned); }
 // Partial sums: at most so many blocks.
-int back_blocks(const Args& a) {
-  const RowPlan p = back_plan(a.d);
+int back_blocks(const Args& a, bool aligned) {
+  const RowPlan p = back_plan(a, aligned);
   const long rpb = p.block / p.tpr, need = (a.rows + rpb - 1) / rpb;
-  const long most = (long)kSMs * (1536 / (p.block < 256 ? 256 : p.block));
+  const long most = (long)kSMs * (p.block < 128 ? 8 : 1024 / p.block);
   return (int)(need < most ? need : most);
 }
 int long_splits(const Args& a) { return (int)(a.rows < 64 ? a.rows : 64); }
 
-template <int HB, int DB, int GB, int K, bool AL, int MT>
+template <int HB, int DB, int GB, int K, bool AL>
 int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
   const int rpb = p.block / p.tpr;
   const size_t row = slot_bytes<HB, AL>(a.d) + slot_bytes<DB, AL>(a.d) + slot_bytes<GB, AL>(a.d);
   const int stages = 3 * rpb * row <= 200 * 1024 ? 3 : 2;
-  const size_t ring = stages * rpb * row, sums = (size_t)a.d * 4, smem = 96 * 4 + (ring > sums ? ring : sums);
-  auto* f = backward_rows<HB, DB, GB, K, AL, MT>;
+  const size_t ring = stages * rpb * row, sums = (size_t)a.d * 4, smem = kSums * 4 + (ring > sums ? ring : sums);
+  auto* f = backward_rows<HB, DB, GB, K, AL>;
   if (const int rc = shared(f, smem)) return rc;
-  // no more blocks than run at once
-  const int most = kSMs * resident(smem, (MT == 320 ? 640 : 512) / p.block);
+  const int most = kSMs * resident(smem, by_registers(f, p.block));  // no more blocks than run at once
   blocks = blocks < most ? blocks : most;
   f<<<blocks, p.block, smem, st>>>(a, p.tpr, stages);
   return status();
 }
 template <int HB, int DB, int GB, bool AL>
 int run(const Args& a, int& blocks, cudaStream_t st) {
-  const RowPlan p = back_plan(a.d);
-  if (p.k == 1 && p.block <= 320) return run_rows<HB, DB, GB, 1, AL, 320>(a, p, blocks, st);
-  if (p.k == 1) return run_rows<HB, DB, GB, 1, AL, 512>(a, p, blocks, st);
-  return run_rows<HB, DB, GB, 2, AL, 512>(a, p, blocks, st);
+  const RowPlan p = back_plan(a, AL);
+  return p.k == 1 ? run_rows<HB, DB, GB, 1, AL>(a, p, blocks, st) : run_rows<HB, DB, GB, 2, AL>(a, p, blocks, st);
 }
 template <int HB, int DB, int GB>
 int run(const Args& a, int& blocks, cudaStream_t st) {
@@ -292,7 +308,10 @@ int layernorm_forward_launch(const LayerNormArgs& args, cudaStream_t st) {
 
 size_t layernorm_backward_workspace(const LayerNormArgs& a) {
   using namespace layernorm;
-  if (a.d <= kMaxRow) return (size_t)back_blocks(a) * 2 * a.d * 4;
+  if (a.d <= kMaxRow) {  // (which of the two is known at the call)
+    const int n = back_blocks(a, true), m = back_blocks(a, false);
+    return (size_t)(n > m ? n : m) * 2 * a.d * 4;
+  }
   return (size_t)a.rows * 16 + (size_t)long_splits(a) * 2 * a.d * 4;
 }
 
@@ -303,7 +322,7 @@ int layernorm_backward_launch(const LayerNormArgs& args, cudaStream_t st) {
   const bool sums = a.dw || a.db;
   int blocks = 0;
   if (a.rows > 0 && a.d <= kMaxRow) {
-    blocks = back_blocks(a);
+    blocks = back_blocks(a, a.wide);
     const bool h4 = a.rt == ATLAS_F32, d4 = a.dt == ATLAS_F32;
     const int rc = h4 ? (d4 ? run<4, 4>(a, blocks, st) : run<4, 2>(a, blocks, st))
                       : (d4 ? run<2, 4>(a, blocks, st) : run<2, 2>(a, blocks, st));
@@ -316,7 +335,7 @@ int layernorm_backward_launch(const LayerNormArgs& args, cudaStream_t st) {
     blocks = long_splits(a);
     if (sums) long_cols<<<dim3((a.d + 255) / 256, blocks), 256, 0, st>>>(a, stats);
   }
-  if (sums) sum_parts<<<dim3((a.d + 31) / 32, 2), 256, 0, st>>>(a.part, a.dw, a.db, blocks, a.d);
+  if (sums) sum_parts<<<dim3((a.d + 31) / 32, 2), 1024, 0, st>>>(a.part, a.dw, a.db, blocks, a.d);
   return status();
 }
 
