@@ -31,7 +31,7 @@ namespace atlas {
 namespace glr {
 
 #ifndef GLR_G
-#define GLR_G 16
+#define GLR_G 32
 #endif
 constexpr int kRows = 128, kCh = 32, kWarps = 8, kGroup = GLR_G;
 constexpr int kPer = kRows / kWarps;  // rows of a warp
@@ -241,24 +241,44 @@ struct alignas(16) Tile {
   __device__ __forceinline__ long row0(const GlrArgs& a) const { return (long)string * a.s.L + (long)(k - first) * kRows; }
 };
 // What a tile gets through the words of its group: those from place j0 on (and, first, what the group before left), where
-// its string's carry begins.  Each warp asks for two, so that all are on their way at once.
+// its string's carry begins.  Each warp asks for four neighbours at once and composes them.
 struct Group {
-  unsigned long long word[kGroup][kCh];
-  unsigned j0;  // == the tile's place: nothing reaches it
+  float2 part[kWarps][kCh];
+  unsigned j0, lead;  // j0 == the tile's place: nothing reaches it
   __device__ __forceinline__ void begin(const Strings& t, const Tile& q, bool some, unsigned from) {
-    const unsigned own = q.at / t.group * t.group, lead = own > 0 ? own - 1 : 0;
+    const unsigned own = q.at / t.group * t.group;
+    lead = own > 0 ? own - 1 : 0;
     j0 = !some ? q.at : from > lead ? from : lead;
   }
   __device__ __forceinline__ void gather(const Tile& q, const unsigned long long* words, size_t width, int* status) {
-    for (unsigned i = threadIdx.x >> 5; j0 + i < q.at; i += kWarps)
-      word[i][threadIdx.x & 31] = await(words + (q.first + j0 + i) * width, kAbsent, status);
+    const unsigned j = lead + (threadIdx.x >> 5) * 4;
+    const auto there = [&](int i) { return j + i >= j0 && j + i < q.at; };
+    unsigned long long v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (there(i)) v[i] = peek(words + (q.first + j + i) * width);
+    float2 m = make_float2(0.f, 0.f);  // the identity
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (there(i)) {
+        const unsigned long long word = await(words + (q.first + j + i) * width, v[i], status);
+        const float d = __uint_as_float((unsigned)(word >> 32));
+        m.y = apply(word, m.y);
+        m.x = after(d, m.x);
+      }
+    part[threadIdx.x >> 5][threadIdx.x & 31] = m;
   }
-  __device__ __forceinline__ float carry(const Tile& q) const {
+  __device__ __forceinline__ float carry() const {
+    float2 m[kWarps];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) m[i] = part[i][threadIdx.x & 31];
     float c = 0.f;
-    for (unsigned i = 0; j0 + i < q.at; ++i) c = apply(word[i][threadIdx.x & 31], c);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) c = apply(m[i].x, m[i].y, c);
     return c;
   }
 };
+static_assert(kGroup <= 4 * kWarps, "a group's words, and that of the group before, in its first tile's place");
 
 // ------------------------------------------------------------------ rows
 
@@ -620,12 +640,14 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
     Info info1;
     if (t.group > 1) {
       if (warp == 1 && !last) {  // the tile's own map
-        float2 m = s_map[0][lane];
+        float2 o[kWarps];
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) o[i] = s_map[i][lane];
+        float2 m = o[0];
 #pragma unroll
         for (int i = 1; i < kWarps; ++i) {
-          const float2 o = s_map[i][lane];
-          m.y = apply(o.x, o.y, m.y);
-          m.x = after(o.x, m.x);
+          m.y = apply(o[i].x, o[i].y, m.y);
+          m.x = after(o[i].x, m.x);
         }
         post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(m.x, m.y));
       }
@@ -633,13 +655,15 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
       __syncthreads();
     }
     if (warp == 0) {
-      float cin = t.group > 1 ? s_group.carry(q) : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
+      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
       if (a.kept && q.c0 + lane < a.D) a.kept[(long)q.k * a.D + q.c0 + lane] = cin;
+      float2 m[kWarps];
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) m[i] = s_map[i][lane];
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
         s_carry[i][lane] = cin;
-        const float2 m = s_map[i][lane];
-        cin = apply(m.x, m.y, cin);
+        cin = apply(m[i].x, m[i].y, cin);
       }
       if (last) post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(kCut, cin));
     }
@@ -954,7 +978,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         h = apply(s_map[0][i][lane], s_map[1][i][lane], h);
       }
     } else if (warp == kWarps - 1) {  // the gradients behind them
-      float cin = t.group > 1 ? s_group.carry(q) : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
+      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
 #pragma unroll
       for (int i = kWarps - 1; i >= 0; --i) {
         s_carry[1][i][lane] = cin;

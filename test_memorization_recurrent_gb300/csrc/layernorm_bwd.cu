@@ -18,9 +18,10 @@ namespace {
 constexpr int kMaxRow = 8192;
 constexpr int kSums = 192;  // floats that a block's sums meet in: twice 16 fours (rows take turns), 16 fours
 
-// A thread's two vectors take 128 registers with dw, db and the weights.
+// One vector a thread while 512 threads are enough (2560 channels with a 32-bit stream: two vectors on half as many
+// threads have a quarter fewer instructions, but too few warps: 139 us against 111; 80 registers 141, 112: 141).
 template <int HB, int DB, int GB, int K, bool AL>  // bytes of h, dy, dh (0: none)
-__global__ void __launch_bounds__(512) backward_rows(Args a, int tpr, int stages) {
+__global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, int stages) {
   extern __shared__ __align__(16) float sm[];  // 3 x 64 for the sums, then [stage][row of the block]: h, dy, dh
   const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
   float dw[K][8], db[K][8], w[K][8];
@@ -251,11 +252,10 @@ __global__ void __launch_bounds__(256) long_cols(Args a, const float4* stats) {
 
 // ------------------------------------------------------------------ launches
 
-// Unaligned rows have one vector a thread while that is enough: two, with their conditions, do not fit the registers.
-RowPlan back_plan(const Args& a, bool aligned) { return forward_plan(a.d, aligned); }
+RowPlan back_plan(int d) { return forward_plan(d, false); }
 // Partial sums: at most so many blocks.
-int back_blocks(const Args& a, bool aligned) {
-  const RowPlan p = back_plan(a, aligned);
+int back_blocks(const Args& a) {
+  const RowPlan p = back_plan(a.d);
   const long rpb = p.block / p.tpr, need = (a.rows + rpb - 1) / rpb;
   const long most = (long)kSMs * (p.block < 128 ? 8 : 1024 / p.block);
   return (int)(need < most ? need : most);
@@ -266,18 +266,24 @@ template <int HB, int DB, int GB, int K, bool AL>
 int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
   const int rpb = p.block / p.tpr;
   const size_t row = slot_bytes<HB, AL>(a.d) + slot_bytes<DB, AL>(a.d) + slot_bytes<GB, AL>(a.d);
-  const int stages = 3 * rpb * row <= 200 * 1024 ? 3 : 2;
-  const size_t ring = stages * rpb * row, sums = (size_t)a.d * 4, smem = kSums * 4 + (ring > sums ? ring : sums);
   auto* f = backward_rows<HB, DB, GB, K, AL>;
+  const size_t sums = (size_t)a.d * 4;
+  const auto bytes = [&](int stages) {
+    const size_t ring = stages * rpb * row;
+    return kSums * 4 + (ring > sums ? ring : sums);
+  };
+  // three stages where they cost no block of an SM (and fit)
+  const int held = by_registers(f, p.block), stages = bytes(3) <= 200 * 1024 && resident(bytes(3), held) == resident(bytes(2), held) ? 3 : 2;
+  const size_t smem = bytes(stages);
   if (const int rc = shared(f, smem)) return rc;
-  const int most = kSMs * resident(smem, by_registers(f, p.block));  // no more blocks than run at once
+  const int most = kSMs * resident(smem, held);  // no more blocks than run at once
   blocks = blocks < most ? blocks : most;
   f<<<blocks, p.block, smem, st>>>(a, p.tpr, stages);
   return status();
 }
 template <int HB, int DB, int GB, bool AL>
 int run(const Args& a, int& blocks, cudaStream_t st) {
-  const RowPlan p = back_plan(a, AL);
+  const RowPlan p = back_plan(a.d);
   return p.k == 1 ? run_rows<HB, DB, GB, 1, AL>(a, p, blocks, st) : run_rows<HB, DB, GB, 2, AL>(a, p, blocks, st);
 }
 template <int HB, int DB, int GB>
@@ -308,10 +314,7 @@ int layernorm_forward_launch(const LayerNormArgs& args, cudaStream_t st) {
 
 size_t layernorm_backward_workspace(const LayerNormArgs& a) {
   using namespace layernorm;
-  if (a.d <= kMaxRow) {  // (which of the two is known at the call)
-    const int n = back_blocks(a, true), m = back_blocks(a, false);
-    return (size_t)(n > m ? n : m) * 2 * a.d * 4;
-  }
+  if (a.d <= kMaxRow) return (size_t)back_blocks(a) * 2 * a.d * 4;
   return (size_t)a.rows * 16 + (size_t)long_splits(a) * 2 * a.d * 4;
 }
 
@@ -322,7 +325,7 @@ int layernorm_backward_launch(const LayerNormArgs& args, cudaStream_t st) {
   const bool sums = a.dw || a.db;
   int blocks = 0;
   if (a.rows > 0 && a.d <= kMaxRow) {
-    blocks = back_blocks(a, a.wide);
+    blocks = back_blocks(a);
     const bool h4 = a.rt == ATLAS_F32, d4 = a.dt == ATLAS_F32;
     const int rc = h4 ? (d4 ? run<4, 4>(a, blocks, st) : run<4, 2>(a, blocks, st))
                       : (d4 ? run<2, 4>(a, blocks, st) : run<2, 2>(a, blocks, st));
