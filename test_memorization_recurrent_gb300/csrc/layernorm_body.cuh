@@ -15,6 +15,8 @@
 // boundary in front of the row on, and keep their distance from it there; neighbouring lanes then
 // read and store neighbouring elements.
 #pragma once
+#include <initializer_list>
+
 #include "rows.cuh"
 
 namespace atlas {
@@ -25,11 +27,16 @@ typedef LayerNormArgs Args;
 constexpr int kStages = 3;
 constexpr int kRed = 160;  // floats that a block's sums meet in: twice 16 pairs (rows take turns), 16 pairs, 16 maxima twice
 
-// Column of element i of vector k.
-template <bool AL>
+// AL, how a thread's elements lie: 1: eight neighbours; 2: pairs of neighbours, of rows in 16 bits that begin anywhere (four bytes an
+// access; a block's rows all begin on the same side of four); 0: one by one.
+// Column of element i of vector k.  lane: the thread's place in its row, of pairs (AL == 2) twice that, less one where the
+// rows begin between two words.
+template <int AL>
 __device__ __forceinline__ int col(int k, int i, int tpr, int lane) {
-  return AL ? (k * tpr + lane) * 8 + i : (k * 8 + i) * tpr + lane;
+  if (AL == 2) return (k * 4 + i / 2) * 2 * tpr + lane + (i & 1);
+  return AL == 1 ? (k * tpr + lane) * 8 + i : (k * 8 + i) * tpr + lane;
 }
+__device__ __forceinline__ bool inside(int c, int d) { return (unsigned)c < (unsigned)d; }
 
 // Two sums over a row's threads.  A block's warps meet in red: pairs, of which those past the last warp's are
 // zero; the next use of the same words has to be another reduction's barrier away.
@@ -59,12 +66,12 @@ __device__ __forceinline__ void row_sums2(float& x, float& y, const RowGroup& g,
 }
 
 // Parameters of vector k: eight of a type, `none` without a tensor.
-template <bool AL>
+template <int AL>
 __device__ __forceinline__ void load_params(const void* p, int type, float none, int k, int d, int tpr, int lane, float* w) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = none;
   if (!p) return;
-  if (AL) {
+  if (AL == 1) {
     const int c = col<AL>(k, 0, tpr, lane);
     if (c >= d) return;
     if (type == ATLAS_F32) {
@@ -80,7 +87,7 @@ __device__ __forceinline__ void load_params(const void* p, int type, float none,
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = col<AL>(k, i, tpr, lane);
-      if (c < d) w[i] = ld_any(p, c, type);
+      if (inside(c, d)) w[i] = ld_any(p, c, type);
     }
   }
 }
@@ -91,13 +98,13 @@ __device__ __forceinline__ void add8(float* h, const float* v) {
 }
 
 // Eight elements of a row that lies at p (`live` and inside the row), aligned or not; zeros elsewhere.
-template <int BYTES, bool AL>
+template <int BYTES, int AL>
 struct Raw {
   Raw8<BYTES> v;
   __device__ __forceinline__ void load(const void* p, long at, int k, int d, int tpr, int lane, bool live) {
     v.zero();
     if (BYTES == 0) return;
-    if (AL) {
+    if (AL == 1) {
       const int c = col<AL>(k, 0, tpr, lane);
       if (live && c < d) v.load(p, at + c);
     }
@@ -105,12 +112,12 @@ struct Raw {
   __device__ __forceinline__ void floats(int type, float* f) const { v.floats(type, f); }
 };
 template <int BYTES>
-struct Raw<BYTES, false> {
+struct Raw<BYTES, 0> {
   uint32_t v[8];
   __device__ __forceinline__ void load(const void* p, long at, int k, int d, int tpr, int lane, bool live) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = col<false>(k, i, tpr, lane);
+      const int c = col<0>(k, i, tpr, lane);
       v[i] = BYTES && live && c < d ? ld_raw<BYTES>(p, at + c) : 0u;
     }
   }
@@ -121,25 +128,25 @@ struct Raw<BYTES, false> {
 };
 
 // Eight outputs of vector k.
-template <bool AL>
+template <int AL>
 __device__ __forceinline__ void store(void* p, long at, int type, int k, int d, int tpr, int lane, const float* v) {
-  if (AL) {
+  if (AL == 1) {
     const int c = col<AL>(k, 0, tpr, lane);
     if (c < d) st8(p, at + c, type, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = col<AL>(k, i, tpr, lane);
-      if (c < d) st_elem(p, at + c, type, v[i]);
+      if (inside(c, d)) st_elem(p, at + c, type, v[i]);
     }
   }
 }
 
 // A row's outputs in a type of 32 or 16 bits.  The type is looked at once: its branch around each element would
 // be most of an unaligned row's code.
-template <int K, bool AL>
+template <int K, int AL>
 __device__ __forceinline__ void store_row(void* p, long at, int type, int d, int tpr, int lane, const float (*h)[8]) {
-  if (AL) {
+  if (AL == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) store<AL>(p, at, type, k, d, tpr, lane, h[k]);
     return;
@@ -149,9 +156,16 @@ __device__ __forceinline__ void store_row(void* p, long at, int type, int d, int
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int c = col<AL>(k, i, tpr, lane);
-        if (c < d) q[c] = from_f<T>(h[k][i]);
+      for (int i = 0; i < 8; i += 2) {
+        const int c = col<AL>(k, i, tpr, lane), c1 = col<AL>(k, i + 1, tpr, lane);
+        if (AL == 2 && sizeof(T) == 2 && inside(c, d) && inside(c1, d)) {
+          Pack<T, 2> two;
+          two.set2(0, h[k][i], h[k][i + 1]);
+          st_pack<T, 2>(q + c, two);
+        } else {
+          if (inside(c, d)) q[c] = from_f<T>(h[k][i]);
+          if (inside(c1, d)) q[c1] = from_f<T>(h[k][i + 1]);
+        }
       }
   };
   if (type == ATLAS_F32)
@@ -162,7 +176,7 @@ __device__ __forceinline__ void store_row(void* p, long at, int type, int d, int
     each(reinterpret_cast<__half*>(p) + at);
 }
 // And in 8 bits.
-template <int K, bool AL>
+template <int K, int AL>
 __device__ __forceinline__ void store_row8(void* p, long at, int d, int tpr, int lane, const float (*h)[8]) {
 #pragma unroll
   for (int k = 0; k < K; ++k) store<AL>(p, at, ATLAS_E4M3, k, d, tpr, lane, h[k]);
@@ -170,7 +184,7 @@ __device__ __forceinline__ void store_row8(void* p, long at, int d, int tpr, int
 
 // A thread's weights and biases: kept in registers, or, of long rows (more than two vectors a thread), read
 // again for each row.
-template <int K, bool AL>
+template <int K, int AL>
 struct Params {
   static constexpr bool kKept = K <= 2;
   float w[kKept ? K : 1][8], b[kKept ? K : 1][8];
@@ -199,10 +213,11 @@ struct Params {
 // One row from its elements h (zeros past its end) and h0, its first.  red: kRed words, odd: every other row of a
 // block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
 // block comes here then).
-template <int K, bool AL>
+template <int K, int AL>
 __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, int odd, unsigned* gm,
                                             long row, bool live, float h0, float (*h)[8], Params<K, AL>& par) {
-  const auto in = [&](int k, int i) { return col<AL>(k, AL ? 0 : i, g.tpr, g.lane) < a.d; };
+  const int lane = AL == 2 ? g.first : g.lane;
+  const auto in = [&](int k, int i) { return inside(col<AL>(k, AL == 1 ? 0 : i, g.tpr, lane), a.d); };
   // the elements less v, to h, and the sums of them and their squares; an aligned row's vectors past its end keep
   // what comes out and stay out of the sums
   const auto less = [&](float v, bool keep, float& s1, float& s2) {
@@ -215,18 +230,18 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
       for (int i = 0; i < 8; i += 2) {
         float t0, t1;
         unpair(pair_add(pair(h[k][i], h[k][i + 1]), minus), t0, t1);
-        if (!AL) t0 = in(k, i) ? t0 : 0.f, t1 = in(k, i + 1) ? t1 : 0.f;
+        if (AL != 1) t0 = in(k, i) ? t0 : 0.f, t1 = in(k, i + 1) ? t1 : 0.f;
         const pair32 t = pair(t0, t1);
         p1 = pair_add(p1, t);
         p2 = pair_fma(t, t, p2);
         if (keep) h[k][i] = t0, h[k][i + 1] = t1;
       }
-      const bool some = !AL || in(k, 0);
+      const bool some = AL != 1 || in(k, 0);
       s1 += some ? pair_sum(p1) : 0.f;
       s2 += some ? pair_sum(p2) : 0.f;
     }
   };
-  if (a.r_out && live) store_row<K, AL>(a.r_out, row * a.sr, a.rt, a.d, g.tpr, g.lane, h);
+  if (a.r_out && live) store_row<K, AL>(a.r_out, row * a.sr, a.rt, a.d, g.tpr, lane, h);
   float s1, s2;
   less(h0, true, s1, s2);
   row_sums2(s1, s2, g, red + odd * 32);
@@ -246,13 +261,13 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    par.apply(a, k, g.tpr, g.lane, rstd, off, h[k]);
+    par.apply(a, k, g.tpr, lane, rstd, off, h[k]);
     if (a.ot != ATLAS_E4M3) continue;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (AL || in(k, i)) m = fmaxf(m, fabsf(h[k][i]));
-    if (AL && !in(k, 0)) m = 0.f;
+      if (AL == 1 || in(k, i)) m = fmaxf(m, fabsf(h[k][i]));
+    if (AL == 1 && !in(k, 0)) m = 0.f;
     if (a.group == 0 || !a.lanes) {
       amax = fmaxf(amax, m);
       continue;
@@ -262,7 +277,7 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
     for (int o = 1; o < 32; o <<= 1)
       if (8 * o < a.group) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
     const float scale = scale_of(m), inv = inverse(scale);
-    const int c = col<AL>(k, 0, g.tpr, g.lane);
+    const int c = col<AL>(k, 0, g.tpr, lane);
     if (live && c < a.d) {
       if ((c & (a.group - 1)) == 0) a.scale[row * a.ng + (c >> a.gshift)] = scale;
 #pragma unroll
@@ -271,7 +286,7 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
     }
   }
   if (a.ot != ATLAS_E4M3) {
-    if (live) store_row<K, AL>(a.y, row * a.sy, a.ot, a.d, g.tpr, g.lane, h);
+    if (live) store_row<K, AL>(a.y, row * a.sy, a.ot, a.d, g.tpr, lane, h);
     return;
   }
   if (a.group && a.lanes) return;
@@ -289,8 +304,8 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int c = col<AL>(k, i, g.tpr, g.lane);
-        if (c < a.d) atomicMax(&gm[c / a.group], __float_as_uint(fmaxf(0.f, fabsf(h[k][i]))));
+        const int c = col<AL>(k, i, g.tpr, lane);
+        if (inside(c, a.d)) atomicMax(&gm[c / a.group], __float_as_uint(fmaxf(0.f, fabsf(h[k][i]))));
       }
     __syncthreads();
     for (int i = g.lane; i < a.ng; i += g.tpr) {
@@ -304,11 +319,11 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   for (int k = 0; k < K; ++k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int c = col<AL>(k, i, g.tpr, g.lane);
-      h[k][i] *= a.group == 0 ? inv : c < a.d ? __uint_as_float(gm[c / a.group]) : 0.f;
+      const int c = col<AL>(k, i, g.tpr, lane);
+      h[k][i] *= a.group == 0 ? inv : inside(c, a.d) ? __uint_as_float(gm[c / a.group]) : 0.f;
     }
   }
-  if (live) store_row8<K, AL>(a.y, row * a.sy, a.d, g.tpr, g.lane, h);
+  if (live) store_row8<K, AL>(a.y, row * a.sy, a.d, g.tpr, lane, h);
 }
 
 template <typename XT>
@@ -316,13 +331,13 @@ constexpr int code_of() {
   return std::is_same_v<XT, float> ? ATLAS_F32 : std::is_same_v<XT, __half> ? ATLAS_F16 : ATLAS_BF16;
 }
 // The residual's type: an aligned row's of 16 bits is x's where that has 16 bits (the launch sees to it).
-template <typename XT, int RB, bool AL>
+template <typename XT, int RB, int AL>
 __device__ __forceinline__ int r_code(const Args& a) {
-  return RB == 4 ? ATLAS_F32 : AL && sizeof(XT) == 2 ? code_of<XT>() : a.rt;
+  return RB == 4 ? ATLAS_F32 : AL == 1 && sizeof(XT) == 2 ? code_of<XT>() : a.rt;
 }
 
 // The two tensors' elements as they lie in memory, to h.
-template <typename XT, int RB, int K, bool AL>
+template <typename XT, int RB, int K, int AL>
 struct RawRow {
   Raw<sizeof(XT), AL> x[K];
   Raw<RB, AL> r[K];
@@ -357,7 +372,7 @@ __device__ __forceinline__ float first_of(const Args& a, long row) {
 }
 
 // A block a row, straight from memory.
-template <typename XT, int RB, int K, bool AL>
+template <typename XT, int RB, int K, int AL>
 __global__ void __launch_bounds__(512) forward_rows(Args a) {
   extern __shared__ __align__(16) float sm[];
   const int tpr = blockDim.x;
@@ -376,7 +391,7 @@ __global__ void __launch_bounds__(512) forward_rows(Args a) {
 
 // Rows of up to 256 channels: tpr lanes of a warp each.  Warps walk rows, the next two of their lanes' under way
 // while they compute two.
-template <typename XT, int RB, bool AL>
+template <typename XT, int RB, int AL>
 __global__ void __launch_bounds__(128, 5) forward_lanes(Args a, int tpr) {
   extern __shared__ __align__(16) float sm[];
   constexpr int R = 2;
@@ -417,9 +432,9 @@ __device__ __forceinline__ Rows rows_of(const void* p, long stride, long rows, i
 }
 
 // Bytes that a row of d elements takes in shared memory.
-template <int E, bool AL>
+template <int E, int AL>
 __host__ __device__ __forceinline__ int slot_bytes(int d) {
-  return AL || E == 0 ? d * E : (d * E + 30) / 16 * 16;
+  return AL == 1 || E == 0 ? d * E : (d * E + 30) / 16 * 16;
 }
 
 // Distance of a row's first byte from the boundary of 16 in front of it.
@@ -430,10 +445,10 @@ __device__ __forceinline__ int ahead(const Rows& t, long row) {
 // One row to shared memory; Q pieces of 16 bytes a thread cover an aligned one.  The pieces at the ends of a row that starts
 // anywhere hold bytes of its neighbours or of the gaps between rows, which nothing uses; those that reach
 // beyond the tensor's ends come element by element.
-template <int E, int Q, bool AL>
+template <int E, int Q, int AL>
 __device__ __forceinline__ void fetch_row(char* s, const Rows& t, long row, long rows, int d, int lane, int threads) {
   if (E == 0 || row >= rows) return;
-  if (AL) {
+  if (AL == 1) {
     const char* p = t.lo + row * t.stride + lane * 16;
 #pragma unroll
     for (int k = 0; k < Q; ++k)
@@ -465,9 +480,9 @@ __device__ __forceinline__ void fetch_row(char* s, const Rows& t, long row, long
 }
 
 // Vector k of a row in shared memory, zeros past its end.
-template <int E, bool AL>
+template <int E, int AL>
 __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, int k, int d, int tpr, int lane, float* f) {
-  if (AL) {
+  if (AL == 1) {
     Raw8<E> q;
     q.zero();
     const int c = col<AL>(k, 0, tpr, lane);
@@ -475,21 +490,31 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
     q.floats(type, f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = col<AL>(k, i, tpr, lane);
-      f[i] = c < d ? raw_float<E>(ld_raw<E>(s + shift, c), type) : 0.f;
+    for (int i = 0; i < 8; i += 2) {
+      const int c = col<AL>(k, i, tpr, lane), c1 = col<AL>(k, i + 1, tpr, lane);
+      if (AL == 2 && E == 2) {  // (the slot has room for a pair's other element)
+        const uint32_t two = c < d ? *reinterpret_cast<const uint32_t*>(s + shift + c * 2) : 0u;
+        f[i] = inside(c, d) ? raw_float<E>(two & 0xFFFFu, type) : 0.f;
+        f[i + 1] = inside(c1, d) ? raw_float<E>(two >> 16, type) : 0.f;
+      } else {
+        f[i] = inside(c, d) ? raw_float<E>(ld_raw<E>(s + shift, c), type) : 0.f;
+        f[i + 1] = inside(c1, d) ? raw_float<E>(ld_raw<E>(s + shift, c1), type) : 0.f;
+      }
     }
   }
 }
 
 // Many rows of a block each: a block walks rows and copies the next kStages - 1 to shared memory while it computes
 // one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it.
-template <typename XT, int RB, int K, bool AL>
+template <typename XT, int RB, int K, int AL>
 __global__ void __maxnreg__(80) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
   constexpr int XB = sizeof(XT);
   clear_red(sm, kRed);
-  const RowGroup g{(int)blockDim.x, (int)threadIdx.x, (int)threadIdx.x};
+  RowGroup g{(int)blockDim.x, (int)threadIdx.x, (int)threadIdx.x};
+  // (the grid is even, so a block's rows begin alike)
+  if (AL == 2) g.first = 2 * g.lane - (int)((reinterpret_cast<uintptr_t>(a.x) / 2 + blockIdx.x * a.sx) & 1);
+  const int lane = AL == 2 ? g.first : g.lane;
   const int xs = slot_bytes<XB, AL>(a.d), bytes = xs + slot_bytes<RB, AL>(a.d);
   char* ring = reinterpret_cast<char*>(sm + kRed);
   unsigned* gm = reinterpret_cast<unsigned*>(ring + kStages * bytes);
@@ -501,7 +526,7 @@ __global__ void __maxnreg__(80) forward_ring(Args a) {
     cp_commit();
   };
   Params<K, AL> par;
-  par.load(a, g.tpr, g.lane);
+  par.load(a, g.tpr, lane);
   long row = blockIdx.x;
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(row + (long)i * gridDim.x, i);
@@ -511,16 +536,16 @@ __global__ void __maxnreg__(80) forward_ring(Args a) {
   for (int odd = 0; row < a.rows; row += gridDim.x, odd ^= 1) {
     fetch(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
     const char* s = ring + stage * bytes;
-    const int ax = AL ? 0 : ahead(tx, row), ar = AL || RB == 0 ? 0 : ahead(tr, row);
+    const int ax = AL == 1 ? 0 : ahead(tx, row), ar = AL == 1 || RB == 0 ? 0 : ahead(tr, row);
     float h0 = to_f(*reinterpret_cast<const XT*>(s + ax));
     if constexpr (RB > 0) h0 += raw_float<RB>(ld_raw<RB>(s + xs + ar, 0), a.rt);
     float h[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      slot_floats<XB, AL>(s, ax, code_of<XT>(), k, a.d, g.tpr, g.lane, h[k]);
+      slot_floats<XB, AL>(s, ax, code_of<XT>(), k, a.d, g.tpr, lane, h[k]);
       if constexpr (RB > 0) {
         float v[8];
-        slot_floats<RB, AL>(s + xs, ar, r_code<XT, RB, AL>(a), k, a.d, g.tpr, g.lane, v);
+        slot_floats<RB, AL>(s + xs, ar, r_code<XT, RB, AL>(a), k, a.d, g.tpr, lane, v);
         add8(h[k], v);
       }
     }
@@ -569,16 +594,16 @@ int by_registers(F* f, int threads) {
   return n < 1 ? 1 : n < most ? n : most;
 }
 
-template <typename XT, int RB, int K, bool AL>
+template <typename XT, int RB, int K, int AL>
 int run_ring(const Args& a, int threads, size_t smem, cudaStream_t st) {
   auto* f = forward_ring<XT, RB, K, AL>;
   if (const int rc = shared(f, smem)) return rc;
-  const long most = (long)kSMs * resident(smem, by_registers(f, threads));
-  f<<<(unsigned)(a.rows < most ? a.rows : most), threads, smem, st>>>(a);
+  const long most = (long)kSMs * resident(smem, by_registers(f, threads));  // (even)
+  f<<<(unsigned)(a.rows < most ? a.rows & ~1L : most), threads, smem, st>>>(a);
   return status();
 }
 
-template <typename XT, int RB, int K, bool AL>
+template <typename XT, int RB, int K, int AL>
 int run_rows(const Args& a, int threads, cudaStream_t st) {
   if (a.rows > 0x7FFFFFFFL) return ATLAS_ERR_UNSUPPORTED;
   const size_t smem = (kRed + (a.lanes ? 0 : (size_t)a.ng)) * 4;
@@ -588,11 +613,29 @@ int run_rows(const Args& a, int threads, cudaStream_t st) {
   return status();
 }
 
-template <typename XT, int RB, bool AL>
+// Whether the 16-bit tensors' rows all begin on the same side of four bytes, row by row, and the plan's threads reach
+// one column further.
+struct Begins {
+  const void* p;
+  long stride;
+  int type;
+};
+inline bool pairs(const Args& a, std::initializer_list<Begins> tensors, const RowPlan& p) {
+  int base = -1, step = 0;
+  for (const Begins& t : tensors) {
+    if (!t.p || (t.type != ATLAS_BF16 && t.type != ATLAS_F16)) continue;
+    const int b = (int)(reinterpret_cast<uintptr_t>(t.p) / 2 & 1), s = (int)(t.stride & 1);
+    if (base >= 0 && (b != base || s != step)) return false;
+    base = b, step = s;
+  }
+  return base >= 0 && p.tpr * 8 * p.k > a.d;
+}
+
+template <typename XT, int RB, int AL>
 int forward(const Args& args, cudaStream_t st) {
   Args a = args;
   // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
-  a.lanes = a.ot != ATLAS_E4M3 || a.group == 0 || (AL && a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
+  a.lanes = a.ot != ATLAS_E4M3 || a.group == 0 || (AL == 1 && a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
   const bool many = a.rows > kSMs * 8;
   const RowPlan p = forward_plan(a.d, many);
   if (a.d <= 256) {
@@ -605,7 +648,11 @@ int forward(const Args& args, cudaStream_t st) {
     return status();
   }
   const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<sizeof(XT), AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
-  if (many && p.k == 2 && ring <= 200 * 1024) return run_ring<XT, RB, 2, AL>(a, p.block, ring, st);
+  if (many && p.k == 2 && ring <= 200 * 1024) {
+    if constexpr (AL == 0 && sizeof(XT) == 2)
+      if (pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, 2, 2>(a, p.block, ring, st);
+    return run_ring<XT, RB, 2, AL>(a, p.block, ring, st);
+  }
   if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
   if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
   if (p.k == 4) return run_rows<XT, RB, 4, AL>(a, p.block, st);
@@ -615,8 +662,8 @@ template <typename XT>
 int forward(const Args& a, cudaStream_t st) {
   const int rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
   const bool mixed = rb == 2 && sizeof(XT) == 2 && a.rt != a.dt;  // bf16 and fp16: element by element
-  if (a.wide && !mixed) return rb == 0 ? forward<XT, 0, true>(a, st) : rb == 2 ? forward<XT, 2, true>(a, st) : forward<XT, 4, true>(a, st);
-  return rb == 0 ? forward<XT, 0, false>(a, st) : rb == 2 ? forward<XT, 2, false>(a, st) : forward<XT, 4, false>(a, st);
+  if (a.wide && !mixed) return rb == 0 ? forward<XT, 0, 1>(a, st) : rb == 2 ? forward<XT, 2, 1>(a, st) : forward<XT, 4, 1>(a, st);
+  return rb == 0 ? forward<XT, 0, 0>(a, st) : rb == 2 ? forward<XT, 2, 0>(a, st) : forward<XT, 4, 0>(a, st);
 }
 
 }  // namespace layernorm

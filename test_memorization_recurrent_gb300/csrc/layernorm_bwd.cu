@@ -20,10 +20,12 @@ constexpr int kSums = 192;  // floats that a block's sums meet in: twice 16 four
 
 // One vector a thread while 512 threads are enough (2560 channels with a 32-bit stream: two vectors on half as many
 // threads have a quarter fewer instructions, but too few warps: 139 us against 111; 80 registers 141, 112: 141).
-template <int HB, int DB, int GB, int K, bool AL>  // bytes of h, dy, dh (0: none)
+template <int HB, int DB, int GB, int K, int AL>  // bytes of h, dy, dh (0: none)
 __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, int stages) {
   extern __shared__ __align__(16) float sm[];  // 3 x 64 for the sums, then [stage][row of the block]: h, dy, dh
-  const int lane = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  const int place = threadIdx.x % tpr, rpb = blockDim.x / tpr, mine = threadIdx.x / tpr;
+  // (pairs: one row a block, an even grid)
+  const int lane = AL == 2 ? 2 * place - (int)((reinterpret_cast<uintptr_t>(DB == 2 ? a.dy : a.x) / 2 + blockIdx.x * (DB == 2 ? a.sy : a.sr)) & 1) : place;
   float dw[K][8], db[K][8], w[K][8];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
@@ -38,9 +40,9 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
   const long step = (long)gridDim.x * rpb;
   auto fetch = [&](long row, int stage) {
     char* s = ring + stage * rpb * bytes;
-    fetch_row<HB, K * HB / 2, AL>(s, th, row, a.rows, a.d, lane, tpr);
-    fetch_row<DB, K * DB / 2, AL>(s + hs, td, row, a.rows, a.d, lane, tpr);
-    fetch_row<GB, K * GB / 2, AL>(s + hs + ds, tg, row, a.rows, a.d, lane, tpr);
+    fetch_row<HB, K * HB / 2, AL>(s, th, row, a.rows, a.d, place, tpr);
+    fetch_row<DB, K * DB / 2, AL>(s + hs, td, row, a.rows, a.d, place, tpr);
+    fetch_row<GB, K * GB / 2, AL>(s + hs + ds, tg, row, a.rows, a.d, place, tpr);
     cp_commit();
   };
   auto next_done = [&] {
@@ -49,7 +51,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
     else
       cp_wait<0>();
   };
-  const auto in = [&](int k, int i) { return col<AL>(k, AL ? 0 : i, tpr, lane) < a.d; };
+  const auto in = [&](int k, int i) { return inside(col<AL>(k, AL == 1 ? 0 : i, tpr, lane), a.d); };
   long row = (long)blockIdx.x * rpb + mine;
   for (int i = 0; i < stages - 1; ++i) fetch(row + i * step, i);
   next_done();
@@ -61,7 +63,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
     const char* s = ring + stage * rpb * bytes;
     stage = stage + 1 == stages ? 0 : stage + 1;
     float h[K][8], dy[K][8], gv[K][8];
-    const int ah = AL || !live ? 0 : ahead(th, row), ad = AL || !live ? 0 : ahead(td, row), ag = AL || !live || GB == 0 ? 0 : ahead(tg, row);
+    const int ah = AL == 1 || !live ? 0 : ahead(th, row), ad = AL == 1 || !live ? 0 : ahead(td, row), ag = AL == 1 || !live || GB == 0 ? 0 : ahead(tg, row);
     const float h0 = live ? raw_float<HB>(ld_raw<HB>(s + ah, 0), a.rt) : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -158,7 +160,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int c = col<AL>(k, i, tpr, lane);
-            if (c < a.d) {
+            if (inside(c, a.d)) {
               const float v = (r == 0 ? 0.f : acc[c]) + (which ? db[k][i] : dw[k][i]);
               if (r == rpb - 1)
                 part[c] = v;
@@ -262,7 +264,7 @@ int back_blocks(const Args& a) {
 }
 int long_splits(const Args& a) { return (int)(a.rows < 64 ? a.rows : 64); }
 
-template <int HB, int DB, int GB, int K, bool AL>
+template <int HB, int DB, int GB, int K, int AL>
 int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
   const int rpb = p.block / p.tpr;
   const size_t row = slot_bytes<HB, AL>(a.d) + slot_bytes<DB, AL>(a.d) + slot_bytes<GB, AL>(a.d);
@@ -278,17 +280,23 @@ int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
   if (const int rc = shared(f, smem)) return rc;
   const int most = kSMs * resident(smem, held);  // no more blocks than run at once
   blocks = blocks < most ? blocks : most;
+  if (AL == 2) blocks &= ~1;
   f<<<blocks, p.block, smem, st>>>(a, p.tpr, stages);
   return status();
 }
-template <int HB, int DB, int GB, bool AL>
+template <int HB, int DB, int GB, int AL>
 int run(const Args& a, int& blocks, cudaStream_t st) {
   const RowPlan p = back_plan(a.d);
   return p.k == 1 ? run_rows<HB, DB, GB, 1, AL>(a, p, blocks, st) : run_rows<HB, DB, GB, 2, AL>(a, p, blocks, st);
 }
 template <int HB, int DB, int GB>
 int run(const Args& a, int& blocks, cudaStream_t st) {
-  return a.wide ? run<HB, DB, GB, true>(a, blocks, st) : run<HB, DB, GB, false>(a, blocks, st);
+  if (a.wide) return run<HB, DB, GB, 1>(a, blocks, st);
+  if constexpr (HB == 2 || DB == 2)
+    if (a.d > 256 && a.rows >= 2 * kSMs &&
+        pairs(a, {{a.x, a.sr, a.rt}, {a.dy, a.sy, a.dt}, {a.r, a.sr, a.rt}, {a.y, a.sr, a.rt}}, back_plan(a.d)))
+      return run<HB, DB, GB, 2>(a, blocks, st);
+  return run<HB, DB, GB, 0>(a, blocks, st);
 }
 template <int HB, int DB>
 int run(const Args& a, int& blocks, cudaStream_t st) {

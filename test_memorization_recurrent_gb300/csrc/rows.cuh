@@ -24,6 +24,7 @@ __device__ __forceinline__ float inverse(float scale) {
 // The threads that share a row: TPR lanes of a warp (TPR <= 32), or the whole block.
 struct RowGroup {
   int tpr, lane, tid;  // threads per row, lane within them
+  int first = 0;       // (layer norm: what a thread's columns go by)
 };
 
 // Sum and maximum over a row's threads.  A block's warps meet in red[0 .. 31], of which the
