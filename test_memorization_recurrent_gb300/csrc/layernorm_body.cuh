@@ -330,10 +330,10 @@ template <typename XT>
 constexpr int code_of() {
   return std::is_same_v<XT, float> ? ATLAS_F32 : std::is_same_v<XT, __half> ? ATLAS_F16 : ATLAS_BF16;
 }
-// The residual's type: an aligned row's of 16 bits is x's where that has 16 bits (the launch sees to it).
+// The residual's type: of 16 bits it is x's where that has 16 bits, but for elements one by one (the launch sees to it).
 template <typename XT, int RB, int AL>
 __device__ __forceinline__ int r_code(const Args& a) {
-  return RB == 4 ? ATLAS_F32 : AL == 1 && sizeof(XT) == 2 ? code_of<XT>() : a.rt;
+  return RB == 4 ? ATLAS_F32 : AL != 0 && sizeof(XT) == 2 ? code_of<XT>() : a.rt;
 }
 
 // The two tensors' elements as they lie in memory, to h.
@@ -488,20 +488,27 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
     const int c = col<AL>(k, 0, tpr, lane);
     if (c < d) q.load_kept(s, c);
     q.floats(type, f);
-  } else {
+    return;
+  }
+  const auto each = [&](auto code) {  // (the type looked at once, not for each element)
+    constexpr int kType = decltype(code)::value;
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
       const int c = col<AL>(k, i, tpr, lane), c1 = col<AL>(k, i + 1, tpr, lane);
       if (AL == 2 && E == 2) {  // (the slot has room for a pair's other element)
         const uint32_t two = c < d ? *reinterpret_cast<const uint32_t*>(s + shift + c * 2) : 0u;
-        f[i] = inside(c, d) ? raw_float<E>(two & 0xFFFFu, type) : 0.f;
-        f[i + 1] = inside(c1, d) ? raw_float<E>(two >> 16, type) : 0.f;
+        f[i] = inside(c, d) ? raw_float<E>(two & 0xFFFFu, kType) : 0.f;
+        f[i + 1] = inside(c1, d) ? raw_float<E>(two >> 16, kType) : 0.f;
       } else {
-        f[i] = inside(c, d) ? raw_float<E>(ld_raw<E>(s + shift, c), type) : 0.f;
-        f[i + 1] = inside(c1, d) ? raw_float<E>(ld_raw<E>(s + shift, c1), type) : 0.f;
+        f[i] = inside(c, d) ? raw_float<E>(ld_raw<E>(s + shift, c), kType) : 0.f;
+        f[i + 1] = inside(c1, d) ? raw_float<E>(ld_raw<E>(s + shift, c1), kType) : 0.f;
       }
     }
-  }
+  };
+  if (E == 4 || type == ATLAS_BF16)
+    each(std::integral_constant<int, ATLAS_BF16>());
+  else
+    each(std::integral_constant<int, ATLAS_F16>());
 }
 
 // Many rows of a block each: a block walks rows and copies the next kStages - 1 to shared memory while it computes
@@ -650,7 +657,7 @@ int forward(const Args& args, cudaStream_t st) {
   const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<sizeof(XT), AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
   if (many && p.k == 2 && ring <= 200 * 1024) {
     if constexpr (AL == 0 && sizeof(XT) == 2)
-      if (pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, 2, 2>(a, p.block, ring, st);
+      if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, 2, 2>(a, p.block, ring, st);
     return run_ring<XT, RB, 2, AL>(a, p.block, ring, st);
   }
   if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
