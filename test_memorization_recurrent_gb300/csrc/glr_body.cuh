@@ -381,17 +381,25 @@ struct Slots {
     else
       p[s * 256] = ld_pack<T, V>(from);
   }
-  // elements e, e + 1
-  __device__ __forceinline__ pair32 two(int e) const {
-    float lo, hi;
-    if constexpr (V > 1) {
-      typedef Pack<T, 2> Two;
-      reinterpret_cast<const Two*>(p + e / V * 256)[e % V / 2].get2(0, lo, hi);
+  // elements e .. e + 3 (e a multiple of four) as two pairs
+  struct Four {
+    pair32 lo, hi;
+    __device__ __forceinline__ pair32 operator[](int j) const { return j ? hi : lo; }
+  };
+  __device__ __forceinline__ Four four(int e) const {
+    float v[4];
+    if constexpr (V == 4) {
+      p[e / 4 * 256].unpack(v);
+    } else if constexpr (V == 2) {
+      p[e / 2 * 256].unpack(v);
+      p[(e / 2 + 1) * 256].unpack(v + 2);
     } else {
-      lo = p[e * 256].get(0), hi = p[(e + 1) * 256].get(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = p[(e + i) * 256].get(0);
     }
-    return pair(lo, hi);
+    return Four{pair(v[0], v[1]), pair(v[2], v[3])};
   }
+  __device__ __forceinline__ pair32 two(int e) const { return four(e & ~3)[e >> 1 & 1]; }
 };
 template <typename T>
 constexpr int slots_bytes(int tensors) {
