@@ -30,22 +30,23 @@
 namespace atlas {
 namespace glr {
 
-#ifndef GLR_G
-#define GLR_G 32
-#endif
-constexpr int kRows = 128, kCh = 32, kWarps = 8, kGroup = GLR_G;
+constexpr int kCh = 32, kWarps = 8, kThreads = 32 * kWarps, kRows = 16 * kWarps, kGroup = 4 * kWarps;
 constexpr int kPer = kRows / kWarps;  // rows of a warp
-#ifndef GLR_B
-#define GLR_B 2
-#endif
-constexpr int kBlocks = GLR_B;            // of an SM: a thread's elements and the work on them take 128 registers
+constexpr int kBlocks = 2;            // of an SM: a thread's elements and the work on them take 128 registers
 constexpr unsigned long long kAbsent = ~0ull;
-constexpr int kPolls = 1 << 22;  // seconds; never reached unless a block of an earlier ticket is lost
+// Looks at a word until a wait gives up, most of a second; never reached unless two calls share a workspace.  Test builds only:
+// with ATLAS_TEST_WITHHOLD_LOADS defined, the second tile of the first channels never hands on its map.
+constexpr int kPolls = 1 << 20;
+#ifdef ATLAS_TEST_WITHHOLD_LOADS
+constexpr bool kWithhold = true;
+#else
+constexpr bool kWithhold = false;
+#endif
 
 // ------------------------------------------------------------------ workspace
 
 struct Space {
-  unsigned* ticket;
+  unsigned* ticket;                // and, behind it, whether a wait has given up
   float *rate, *rb, *ib;           // [groups * kCh]: c softplus(lambda), -log2(e) biases
   unsigned long long* words;       // [tiles][groups * kCh]
   int* tile_seq;                   // [tiles + 1]: packed, the sequence of a tile's first row
@@ -94,7 +95,7 @@ inline Space space(const GlrArgs& a, bool back, bool keep) {
     return q;
   };
   const size_t tiles = tiles_of(a), width = (size_t)groups_of(a) * kCh;
-  s.ticket = reinterpret_cast<unsigned*>(take(4));
+  s.ticket = reinterpret_cast<unsigned*>(take(8));
   s.rate = reinterpret_cast<float*>(take(width * 4));
   s.rb = reinterpret_cast<float*>(take(width * 4));
   s.ib = reinterpret_cast<float*>(take(width * 4));
@@ -208,12 +209,17 @@ __device__ __forceinline__ void post(unsigned long long* p, unsigned long long v
   asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
-// A word that another block leaves, once it is there.  By a whole warp, a channel each.
-__device__ __forceinline__ unsigned long long await(const unsigned long long* p, unsigned long long v, int* status) {
+// A word that another block leaves, once it is there.  By a whole warp, a channel each.  A wait that runs out is the last
+// of the call: the others then give up at once, with NaN for what they miss.
+__device__ __forceinline__ unsigned long long await(const unsigned long long* p, unsigned long long v, unsigned* lost, int* status) {
   for (int polls = 0; !__all_sync(0xFFFFFFFFu, v != kAbsent); ++polls) {
-    if (polls >= kPolls) {
-      if (status) *status = ATLAS_ERR_TIMEOUT;
-      break;
+    const bool over = polls >= kPolls;
+    if (over || (polls & 63) == 63) {
+      if (over) {
+        *reinterpret_cast<volatile unsigned*>(lost) = 1;
+        if (status) *status = ATLAS_ERR_TIMEOUT;
+      }
+      if (__any_sync(0xFFFFFFFFu, over || *reinterpret_cast<volatile unsigned*>(lost))) break;
     }
     v = peek(p);
   }
@@ -250,7 +256,7 @@ struct Group {
     lead = own > 0 ? own - 1 : 0;
     j0 = !some ? q.at : from > lead ? from : lead;
   }
-  __device__ __forceinline__ void gather(const Tile& q, const unsigned long long* words, size_t width, int* status) {
+  __device__ __forceinline__ void gather(const Tile& q, const unsigned long long* words, size_t width, unsigned* lost, int* status) {
     const unsigned j = lead + (threadIdx.x >> 5) * 4;
     const auto there = [&](int i) { return j + i >= j0 && j + i < q.at; };
     unsigned long long v[4];
@@ -261,7 +267,7 @@ struct Group {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (there(i)) {
-        const unsigned long long word = await(words + (q.first + j + i) * width, v[i], status);
+        const unsigned long long word = await(words + (q.first + j + i) * width, v[i], lost, status);
         const float d = __uint_as_float((unsigned)(word >> 32));
         m.y = apply(word, m.y);
         m.x = after(d, m.x);
@@ -373,13 +379,13 @@ struct Cursor {
 // asynchronous copy.)
 template <typename T, int V, int S>
 struct Slots {
-  Pack<T, V>* p;  // [S][256], this thread's
-  __device__ __forceinline__ Slots(char* base, int tensor) : p(reinterpret_cast<Pack<T, V>*>(base) + tensor * S * 256 + threadIdx.x) {}
+  Pack<T, V>* p;  // [S][kThreads], this thread's
+  __device__ __forceinline__ Slots(char* base, int tensor) : p(reinterpret_cast<Pack<T, V>*>(base) + tensor * S * kThreads + threadIdx.x) {}
   __device__ __forceinline__ void fetch(int s, const T* from) const {
     if constexpr (sizeof(T) * V >= 4)
-      cp_async<sizeof(T) * V>(p + s * 256, from, true);
+      cp_async<sizeof(T) * V>(p + s * kThreads, from, true);
     else
-      p[s * 256] = ld_pack<T, V>(from);
+      p[s * kThreads] = ld_pack<T, V>(from);
   }
   // elements e .. e + 3 (e a multiple of four) as two pairs
   struct Four {
@@ -389,13 +395,13 @@ struct Slots {
   __device__ __forceinline__ Four four(int e) const {
     float v[4];
     if constexpr (V == 4) {
-      p[e / 4 * 256].unpack(v);
+      p[e / 4 * kThreads].unpack(v);
     } else if constexpr (V == 2) {
-      p[e / 2 * 256].unpack(v);
-      p[(e / 2 + 1) * 256].unpack(v + 2);
+      p[e / 2 * kThreads].unpack(v);
+      p[(e / 2 + 1) * kThreads].unpack(v + 2);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = p[(e + i) * 256].get(0);
+      for (int i = 0; i < 4; ++i) v[i] = p[(e + i) * kThreads].get(0);
     }
     return Four{pair(v[0], v[1]), pair(v[2], v[3])};
   }
@@ -403,7 +409,7 @@ struct Slots {
 };
 template <typename T>
 constexpr int slots_bytes(int tensors) {
-  return tensors * kPer * 256 * (int)sizeof(T);
+  return tensors * kPer * kThreads * (int)sizeof(T);
 }
 
 // Elements e, e + 1 of values that rows share.
@@ -420,7 +426,7 @@ __device__ __forceinline__ pair32 silu(pair32 z) {
 // Parameters, absent words, sequences' states, tiles' sequences; the states of empty sequences pass on.
 static __global__ void __launch_bounds__(256) prepare(GlrArgs a, Space w, long tiles, int groups, int back) {
   const long id = (long)blockIdx.x * 256 + threadIdx.x, n = (long)gridDim.x * 256;
-  if (id == 0) *w.ticket = 0;
+  if (id == 0) w.ticket[0] = w.ticket[1] = 0;
   for (long c = id; c < (long)groups * kCh; c += n) {
     const bool in = c < a.D;
     w.rate[c] = in ? a.c * soft(a.lam[c]) : 0.f;
@@ -492,7 +498,7 @@ static __global__ void __launch_bounds__(256) prepare(GlrArgs a, Space w, long t
 // A block copies its next tile from when it has this one's maps.  It takes the ticket not before it begins a tile: tickets
 // taken earlier would keep tiles waiting for others that no block has begun.
 template <typename T, int V, bool FLAT>
-__global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w, Strings t) {
+__global__ void __launch_bounds__(kThreads, kBlocks) forward_tiles(GlrArgs a, Space w, Strings t) {
   typedef Shape<V> Sh;
   constexpr int S = Sh::S, N = Sh::N;
   extern __shared__ __align__(16) char buf[];  // x, r, i, z twice
@@ -647,7 +653,7 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
     const Tile q1 = s_tile;
     Info info1;
     if (t.group > 1) {
-      if (warp == 1 && !last) {  // the tile's own map
+      if (warp == 1 && !last && !(kWithhold && q.at == 1 && q.c0 == 0)) {  // the tile's own map
         float2 o[kWarps];
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) o[i] = s_map[i][lane];
@@ -659,11 +665,11 @@ __global__ void __launch_bounds__(256, kBlocks) forward_tiles(GlrArgs a, Space w
         }
         post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(m.x, m.y));
       }
-      s_group.gather(q, words, width, a.s.status);
+      s_group.gather(q, words, width, w.ticket + 1, a.s.status);
       __syncthreads();
     }
     if (warp == 0) {
-      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
+      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, w.ticket + 1, a.s.status), 0.f) : 0.f;
       if (a.kept && q.c0 + lane < a.D) a.kept[(long)q.k * a.D + q.c0 + lane] = cin;
       float2 m[kWarps];
 #pragma unroll
@@ -771,7 +777,7 @@ constexpr int back_stages() {
   return sizeof(T) == 2 ? 2 : 1;
 }
 template <typename T, int V, bool FLAT>
-__global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space w, Strings t, const float* kept) {
+__global__ void __launch_bounds__(kThreads, kBlocks) backward_tiles(GlrArgs a, Space w, Strings t, const float* kept) {
   typedef Shape<V> Sh;
   constexpr int S = Sh::S, N = Sh::N;
   constexpr bool kAhead = back_stages<T>() == 2;  // the next tile's copies under way (32-bit elements: no room)
@@ -975,7 +981,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         }
         post(w.words + q.c0 + lane + (q.first + q.at) * width, word_of(d, g));
       }
-      s_group.gather(q, words, width, a.s.status);
+      s_group.gather(q, words, width, w.ticket + 1, a.s.status);
       __syncthreads();
     }
     if (warp == 0) {  // the states in front of the warps
@@ -986,7 +992,7 @@ __global__ void __launch_bounds__(256, kBlocks) backward_tiles(GlrArgs a, Space 
         h = apply(s_map[0][i][lane], s_map[1][i][lane], h);
       }
     } else if (warp == kWarps - 1) {  // the gradients behind them
-      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, a.s.status), 0.f) : 0.f;
+      float cin = t.group > 1 ? s_group.carry() : some ? apply(await(words + (q.first + q.at - 1) * width, early, w.ticket + 1, a.s.status), 0.f) : 0.f;
 #pragma unroll
       for (int i = kWarps - 1; i >= 0; --i) {
         s_carry[1][i][lane] = cin;
@@ -1183,7 +1189,7 @@ template <typename F, typename... X>
 int launch(F* f, int smem, const Strings& t, cudaStream_t st, X... args) {
   if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return ATLAS_ERR_CUDA;
   const unsigned most = kBlocks * kSMs;
-  f<<<t.total < most ? t.total : most, 256, smem, st>>>(args...);
+  f<<<t.total < most ? t.total : most, kThreads, smem, st>>>(args...);
   return status();
 }
 

@@ -454,6 +454,69 @@ def test_tensors_are_checked():
             call(**{k: bad})
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [40, 33])
+@pytest.mark.parametrize("lens", [[5, 7, 6], [300, 129, 700, 2], [128, 128, 128], [5000, 40, 5000]], ids=str)
+def test_what_is_not_finite_stays_in_its_sequence(lens, D, dtype):
+    """The second sequence has NaN inputs and gates and an infinite state: the others' outputs and gradients are, bit by
+    bit, those beside a finite one."""
+    r = rng(66, len(lens), D)
+    start, rows, at = packed(lens, 0)
+    B = len(lens)
+    g = Glr(r, B, 0, D, dtype, packed_rows=rows)
+    dy, dh0 = draw(r, (rows, D), dtype)[0], draw(r, (B, D), "fp32")[0]
+    cfg = g.cfg(B, rows, seq_start=start)
+
+    def run():
+        y, h, dh, kept = torch.zeros_like(g.x), torch.zeros_like(g.h), dh0.clone(), kept_of(cfg)
+        g.forward(cfg, y, h, kept)
+        o = g.backward(cfg, dy, dh, kept)
+        return [y, o["dx"], o["dr"], o["di"], o["dz"]], [h, dh]
+    want = run()
+    mid = slice(at[1], at[2])
+    g.x[mid], g.h[1] = float("nan"), float("inf")
+    g.r[mid.start + 1:mid.stop] = float("nan")
+    dy[mid], dh0[1] = float("inf"), float("nan")
+    got = run()
+    others = torch.ones(rows, dtype=torch.bool, device="cuda")
+    others[mid] = False
+    for a, b in zip(got[0], want[0]):
+        assert torch.equal(a[others], b[others])
+        assert not torch.isfinite(a[mid].float()).all()
+    for a, b in zip(got[1], want[1]):
+        assert torch.equal(a[[b for b in range(B) if b != 1]], b[[b for b in range(B) if b != 1]])
+
+
+def test_a_tile_that_is_lost_ends_the_waits_and_is_reported():
+    """A separately built copy of the library in which the second tile of the first 32 channels never hands on its map: the
+    wait for it runs out, the others give up at once, the status word says so, the other channels are right, and the
+    next call is."""
+    import time
+
+    from test_memorization_recurrent_gb300 import build
+    lib = A.open_library(build.build_variant("atlasmem_withhold", ["ATLAS_TEST_WITHHOLD_LOADS"]))
+    L, D = 128 * 40, 40
+    g = Glr(rng(67), 1, L, D, "fp32")
+    st = status()
+    cfg = g.cfg(1, L, status_dev=st)
+    want, y = torch.empty_like(g.x), torch.zeros_like(g.x)
+    g.forward(cfg, want)
+    torch.cuda.synchronize()
+    begin = time.monotonic()
+    p = lambda t: t.data_ptr()  # noqa: E731
+    assert lib.atlas_glr_forward(p(g.x), p(g.r), p(g.i), p(g.z), p(g.lam), p(g.rb), p(g.ib), cfg, p(y), p(g.h), None, None,
+                                 torch.cuda.current_stream().cuda_stream) == A.OK
+    torch.cuda.synchronize()
+    assert time.monotonic() - begin < 30
+    assert int(st) == A.ERR_TIMEOUT
+    assert torch.equal(y[..., 32:], want[..., 32:]) and torch.equal(y[:, :256], want[:, :256])
+    assert torch.isnan(y[:, 256:384, :32]).all()
+    st.zero_()
+    g.forward(cfg, y)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(y, want)
+
+
 def test_a_layer_of_them():
     """Layer norm, short convolution, gated linear recurrence and a residual layer norm, forward and backward through
     each, against differences along directions of the input and of parameters (in 32 bits)."""
