@@ -119,15 +119,17 @@ __device__ __forceinline__ pair32 gate(pair32 b) {
   unpair(pair_add(twice(1.f), pair_ex2(b)), x, y);
   return pair(rcp(x), rcp(y));
 }
-// And 1 - sigmoid to its own relative precision: 2^b sigma, or, where 2^b may be infinite, the difference.
+// And 1 - sigmoid to its own relative precision, 2^b sigma.  The exponent is held below 126, so that it has no
+// infinity; NONE: sigmoid is then 0, as beyond, and not 2^-126.
+template <bool NONE>
 __device__ __forceinline__ pair32 gate(pair32 b, pair32& rest) {
-  float e0, e1, x, y;
-  const pair32 e = pair_ex2(b);
-  unpair(e, e0, e1);
+  float b0, b1, x, y;
+  unpair(b, b0, b1);
+  const pair32 e = pair(ex2(fminf(b0, 126.f)), ex2(fminf(b1, 126.f)));
   unpair(pair_add(twice(1.f), e), x, y);
   x = rcp(x), y = rcp(y);
-  rest = pair(e0 > 1.f ? 1.f - x : e0 * x, e1 > 1.f ? 1.f - y : e1 * y);
-  return pair(x, y);
+  rest = pair_mul(e, pair(x, y));
+  return NONE ? pair(b0 >= 126.f ? 0.f : x, b1 >= 126.f ? 0.f : y) : pair(x, y);
 }
 
 // 1 - exp(-s) for 0 <= s < kSlow: s P(s), P fitted to (1 - exp(-s)) / s at Chebyshev nodes (relative error 1.7e-8, 9e-8
@@ -1040,86 +1042,102 @@ __global__ void __launch_bounds__(kThreads, kBlocks) backward_tiles(GlrArgs a, S
     const Cursor<T, FLAT> ox(a.dx, a.xb, a.xt, a, c), orr(a.dr, a.rbs, a.rt, a, c), oi(a.di, a.ibs, a.it, a, c), oz(a.dz, a.zb, a.zt, a, c);
     const long row0 = q.row0(a) + r0;
     constexpr int P = V > 1 ? 1 : 2;  // rows that a step takes, whose elements are pairs
+    const auto put = [&](auto is_plain) {  // (two copies: what the other way asks for is a tenth of this one's instructions)
+      constexpr bool kPlain = decltype(is_plain)::value;
 #pragma unroll
-    for (int s = 0; s < S; s += P) {
-      float before[P * V], here[P * V], dx[P * V], dr[P * V], di[P * V], dz[P * V];
+      for (int s = 0; s < S; s += P) {
+        float before[P * V], here[P * V], dx[P * V], dr[P * V], di[P * V], dz[P * V];
 #pragma unroll
-      for (int f = 0; f < P * V; ++f) {
-        const int e = s * V + f, v = f % V;
-        if (!plain) {
-          const int b = info.seq(tg * S + e / V);
-          if (first >> e / V & 1) h[v] = start_of(a, w, b, c + v);
+        for (int f = 0; f < P * V; ++f) {
+          const int e = s * V + f, v = f % V;
+          if (!kPlain) {
+            const int b = info.seq(tg * S + e / V);
+            if (first >> e / V & 1) h[v] = start_of(a, w, b, c + v);
+          }
+          before[f] = h[v];
+          if (kPlain)
+            h[v] += fmaf(-M[e], h[v], U[e]);
+          else
+            h[v] = apply(M[e], U[e], h[v]);
+          here[f] = h[v];
         }
-        before[f] = h[v];
-        if (plain)
-          h[v] += fmaf(-M[e], h[v], U[e]);
-        else
-          h[v] = apply(M[e], U[e], h[v]);
-        here[f] = h[v];
+#pragma unroll
+        for (int f = 0; f < P * V; f += 2) {
+          const int e = s * V + f, v = f % V;
+          const pair32 G2 = pair(G[e], G[e + 1]), U2 = pair(U[e], U[e + 1]);
+          pair32 rrest, irest = twice(0.f), m = pair(M[e], M[e + 1]), ig = twice(1.f), A2;
+          const pair32 rg = gate<true>(pair_fma(br.two(e), twice(-ATLAS_LOG2E), two<V>(rb, e)), rrest);
+          if (a.i) ig = gate<false>(pair_fma(bi.two(e), twice(-ATLAS_LOG2E), two<V>(ib, e)), irest);
+          const pair32 sv = pair_mul(two<V>(rate, e), rg);
+          if (kPlain) {
+            A2 = pair_fma(m, twice(-1.f), twice(1.f));
+          } else {
+            const float a0 = factor(M[e]), a1 = factor(M[e + 1]);
+            A2 = pair(a0, a1);
+            m = pair(is_kept(M[e]) ? 1.f - a0 : M[e], is_kept(M[e + 1]) ? 1.f - a1 : M[e + 1]);
+          }
+          const pair32 b2 = pair_mul(m, pair_fma(m, twice(-1.f), twice(2.f)));
+          float q0, q1;
+          unpair(b2, q0, q1);
+          // s / beta^2 is 1/2 in the limit of s = 0, where u is 0 too
+          const pair32 ratio = pair_mul(sv, pair(rcp(fmaxf(q0, 1e-37f)), rcp(fmaxf(q1, 1e-37f))));
+          // Q = G (u a^2 ratio - s a h) = G a (u a ratio - s h)
+          const pair32 in2 = pair_fma(pair_mul(U2, A2), ratio, pair_mul(pair_mul(sv, twice(-1.f)), pair(before[f], before[f + 1])));
+          pair32 Q = pair_mul(pair_mul(G2, A2), in2), r2 = pair_mul(Q, rrest), i2 = pair_mul(pair_mul(G2, U2), irest);
+          unpair(r2, dr[f], dr[f + 1]);
+          unpair(i2, di[f], di[f + 1]);
+          unpair(pair_mul(pair_mul(G2, root(b2)), ig), dx[f], dx[f + 1]);
+          if (a.z) {
+            const pair32 zv = bz.two(e);
+            pair32 zr;
+            const pair32 zg = gate<true>(pair_mul(zv, twice(-ATLAS_LOG2E)), zr);
+            const pair32 slope = pair_mul(zg, pair_fma(zv, zr, twice(1.f)));
+            unpair(pair_mul(pair_mul(by.two(e), pair(here[f], here[f + 1])), slope), dz[f], dz[f + 1]);
+          }
+          if (!kPlain) {  // a slot without a row may hold anything
+            const float l0 = live >> e / V & 1 ? 1.f : 0.f, l1 = live >> (e + 1) / V & 1 ? 1.f : 0.f;
+            const auto masked = [&](pair32 x) {
+              float x0, x1;
+              unpair(x, x0, x1);
+              return pair(l0 != 0.f ? x0 : 0.f, l1 != 0.f ? x1 : 0.f);
+            };
+            Q = masked(Q), r2 = masked(r2), i2 = masked(i2);
+          }
+          const auto add = [&](float* to, pair32 x) {
+            if (V > 1)
+              unpair(pair_add(pair(to[v], to[v + (V > 1)]), x), to[v], to[v + (V > 1)]);
+            else
+              to[0] += pair_sum(x);
+          };
+          add(sum[0], Q);
+          add(sum[1], r2);
+          add(sum[2], i2);
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const int b = FLAT ? 0 : info.seq(tg * S + s + j);
+          if (!kPlain && !(live >> (s + j) & 1)) continue;
+          const long row = row0 + s + j;
+          Pack<T, V> o;
+          o.pack(dx + j * V);
+          st_pack<T, V>(ox.at(row, b), o);
+          o.pack(dr + j * V);
+          st_pack<T, V>(orr.at(row, b), o);
+          if (a.i) {
+            o.pack(di + j * V);
+            st_pack<T, V>(oi.at(row, b), o);
+          }
+          if (a.z) {
+            o.pack(dz + j * V);
+            st_pack<T, V>(oz.at(row, b), o);
+          }
+        }
       }
-#pragma unroll
-      for (int f = 0; f < P * V; f += 2) {
-        const int e = s * V + f;
-        const pair32 G2 = pair(G[e], G[e + 1]), U2 = pair(U[e], U[e + 1]);
-        pair32 rrest, irest = twice(0.f), m = pair(M[e], M[e + 1]), ig = twice(1.f), A2;
-        const pair32 rg = gate(pair_fma(br.two(e), twice(-ATLAS_LOG2E), two<V>(rb, e)), rrest);
-        if (a.i) ig = gate(pair_fma(bi.two(e), twice(-ATLAS_LOG2E), two<V>(ib, e)), irest);
-        const pair32 sv = pair_mul(two<V>(rate, e), rg);
-        if (plain) {
-          A2 = pair_fma(m, twice(-1.f), twice(1.f));
-        } else {
-          const float a0 = factor(M[e]), a1 = factor(M[e + 1]);
-          A2 = pair(a0, a1);
-          m = pair(is_kept(M[e]) ? 1.f - a0 : M[e], is_kept(M[e + 1]) ? 1.f - a1 : M[e + 1]);
-        }
-        const pair32 b2 = pair_mul(m, pair_fma(m, twice(-1.f), twice(2.f)));
-        float q0, q1;
-        unpair(b2, q0, q1);
-        // s / beta^2 is 1/2 in the limit of s = 0, where u is 0 too
-        const pair32 ratio = pair_mul(sv, pair(rcp(fmaxf(q0, 1e-37f)), rcp(fmaxf(q1, 1e-37f))));
-        // Q = G (u a^2 ratio - s a h) = G a (u a ratio - s h)
-        const pair32 in2 = pair_fma(pair_mul(U2, A2), ratio, pair_mul(pair_mul(sv, twice(-1.f)), pair(before[f], before[f + 1])));
-        const pair32 Q = pair_mul(pair_mul(G2, A2), in2);
-        unpair(pair_mul(Q, rrest), dr[f], dr[f + 1]);
-        unpair(pair_mul(pair_mul(G2, root(b2)), ig), dx[f], dx[f + 1]);
-        if (a.i) unpair(pair_mul(pair_mul(G2, U2), irest), di[f], di[f + 1]);
-        if (a.z) {
-          const pair32 zv = bz.two(e);
-          pair32 zr;
-          const pair32 zg = gate(pair_mul(zv, twice(-ATLAS_LOG2E)), zr);
-          const pair32 slope = pair_mul(zg, pair_fma(zv, zr, twice(1.f)));
-          unpair(pair_mul(pair_mul(by.two(e), pair(here[f], here[f + 1])), slope), dz[f], dz[f + 1]);
-        }
-        float Q0, Q1;
-        unpair(Q, Q0, Q1);
-        // (a slot without a row may hold anything)
-        const bool l0 = plain || (live >> e / V & 1), l1 = plain || (live >> (e + 1) / V & 1);
-        constexpr int v1 = V > 1;
-        const int v = f % V;
-        sum[0][v] += l0 ? Q0 : 0.f, sum[0][v + v1] += l1 ? Q1 : 0.f;
-        sum[1][v] += l0 ? dr[f] : 0.f, sum[1][v + v1] += l1 ? dr[f + 1] : 0.f;
-        if (a.i) sum[2][v] += l0 ? di[f] : 0.f, sum[2][v + v1] += l1 ? di[f + 1] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const int b = FLAT ? 0 : info.seq(tg * S + s + j);
-        if (!(live >> (s + j) & 1)) continue;
-        const long row = row0 + s + j;
-        Pack<T, V> o;
-        o.pack(dx + j * V);
-        st_pack<T, V>(ox.at(row, b), o);
-        o.pack(dr + j * V);
-        st_pack<T, V>(orr.at(row, b), o);
-        if (a.i) {
-          o.pack(di + j * V);
-          st_pack<T, V>(oi.at(row, b), o);
-        }
-        if (a.z) {
-          o.pack(dz + j * V);
-          st_pack<T, V>(oz.at(row, b), o);
-        }
-      }
-    }
+    };
+    if (plain)
+      put(std::true_type());
+    else
+      put(std::false_type());
 #pragma unroll
     for (int j = 0; j < 3; ++j)
 #pragma unroll

@@ -269,6 +269,27 @@ def test_extreme_gates(D):
             close(o[k], grads[0][k], grads[1][k] + 2.0 ** -38, "fp32", L, k)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gates_of_the_lowest_value(dtype):
+    """Output and input gates of the type's lowest and largest number: outputs and gradients of 0 where the gate is
+    closed, as of a token that is masked, and none that are not finite."""
+    L, D = 200, 40
+    low, high = -float(torch.finfo(DT[dtype]).max), 40.0
+    g = Glr(rng(68), 1, L, D, dtype)
+    g.z[:, ::2], g.i[:, ::3], g.r[:, ::5] = low, low, low
+    g.z[:, 1::4], g.r[:, 1::5] = high, high
+    dy, dh = torch.ones_like(g.x), torch.ones_like(g.h)
+    cfg = g.cfg(1, L)
+    y = torch.empty_like(g.x)
+    g.forward(cfg, y)
+    o = g.backward(cfg, dy, dh)
+    for t in (y, *o.values()):
+        assert torch.isfinite(t).all()
+    assert not y[:, ::2].any() and not o["dz"][:, ::2].any()
+    assert not o["di"][:, ::3].any() and not o["dr"][:, ::5].any()
+    assert o["dz"][:, 1::4].any()
+
+
 def test_a_slow_channel_over_many_tokens():
     """Decays of 1 - 1e-4 .. 1 - 1e-6 over 40000 tokens: the rounding of a does not add up to a drift.  u keeps its
     relative precision there (1 - a^2 of a rounded a would be off by up to 2^-25 / 1e-6)."""
