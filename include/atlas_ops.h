@@ -289,7 +289,8 @@ typedef struct atlas_glr_cfg {
  * description. */
 size_t atlas_glr_workspace_bytes(const atlas_glr_cfg* cfg);
 
-/* Bytes of the states that the forward pass keeps for the backward pass. */
+/* Bytes of the states that the forward pass keeps for the backward pass (one every 128 tokens; a call for
+ * single tokens leaves them as they are, and its backward pass reads none). */
 size_t atlas_glr_kept_bytes(const atlas_glr_cfg* cfg);
 
 /*   x, r, i, z [.., L, D] dtype (i NULL: no input gate, i_bias is NULL then; z NULL: no output gate)

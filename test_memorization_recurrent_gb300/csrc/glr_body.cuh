@@ -24,6 +24,11 @@
 //
 // Backward the same with the rows in reverse: c -> a (v + c) carries a g to the token in front.  The states inside a
 // tile come from the state in front of it, which the forward pass keeps (one for kRows rows, in 32 bits).
+//
+// An element takes eight results of the exponential pipe and 65 instructions (147 backward), so issue and latency bound it,
+// then memory.  Measured (copy rate 6.79 TB/s): 8 x 4096 x 2048 bf16, gated: 211 us, 47%, with the backward pass 702, 39%; with
+// one string, 65536 x 512: 184 us, 22%; 9001 packed rows x 1500: 91 us.  Tiles of 64 rows on blocks of four warps:
+// 252 us; of 256 rows on sixteen: 234; three blocks of an SM (80 registers): 227.
 #pragma once
 #include "ops_common.cuh"
 
@@ -66,8 +71,8 @@ struct Strings {
   unsigned group;               // tiles of a group
   unsigned total;               // tiles x channels in all
 };
-// Sequences of one length are strings of their own where that leaves few places of tiles empty (one of 512 rows: at
-// most an eighth).
+// Sequences of one length are strings of their own where that leaves few places of tiles empty (of 512 rows: at
+// most an eighth).  (As one string, 8 x 4096 x 2048 took 299 us against 211, its training pass 916 against 702.)
 inline bool apart_of(const GlrArgs& a) { return !a.s.start && a.s.L > 0 && (a.s.L >= 4 * kRows || a.s.L % kRows == 0); }
 inline long tiles_of(const GlrArgs& a) {  // in all
   if (apart_of(a)) return (long)a.s.B * ((a.s.L - 1L) / kRows + 1);
@@ -79,7 +84,8 @@ inline Strings strings(const GlrArgs& a) {
   t.n = apart_of(a) ? a.s.B : 1;
   t.tiles = (unsigned)(tiles_of(a) / t.n);
   t.groups = groups_of(a);
-  // a tile's predecessor in its string lies n x groups tickets behind it: done, if no more blocks run
+  // a tile's predecessor in its string lies n x groups tickets behind it: done, if no more blocks run (in groups of tiles
+  // all the same, 8 x 4096 x 2048 took 276 us against 211)
   t.group = (long)t.n * t.groups >= (long)kBlocks * kSMs ? 1 : kGroup;
   t.total = t.n * t.tiles * t.groups;
   return t;

@@ -9,11 +9,16 @@
 // one barrier of a block, is enough but for some rows of ten thousand of ordinary numbers.
 //
 // Rows of up to 256 channels belong to lanes of a warp; longer ones to a block,
-// which walks rows with the next two on their way through shared memory (a few rows: a block each).
+// which walks rows with the next two on their way through shared memory (up to 1216 rows, eight an SM: a block each, straight
+// from memory: 8 rows of 2048 in 5.9 us a call, which is the launch).
 // A thread has K times eight elements: eight neighbours of an aligned row, every tpr-th one of a row
 // that starts anywhere.  Such rows come to shared memory in whole pieces of 16 bytes too, from the
 // boundary in front of the row on, and keep their distance from it there; neighbouring lanes then
-// read and store neighbouring elements.
+// read and store neighbouring elements, in 16 bits by pairs where the tensors' rows begin alike.
+//
+// Bound by memory, and next to it by instructions.  Measured (copy rate 6.79 TB/s): 32768 x 2048 bf16 + residual to e4m3 with
+// scales of 128: 88 us, 79% (a round of sums for the mean and one about it: 119; one vector a thread: 115; a warp a
+// row: 135); 524288 x 128 fp32 to bf16: 68 us, 87%; 20000 x 1371 fp16 + residual: 59 us, 55% (one by one: 85).
 #pragma once
 #include <initializer_list>
 

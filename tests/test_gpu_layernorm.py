@@ -164,6 +164,47 @@ def test_backward(rows, d, stride, shift, dtype, r_dtype):
         close(db, *(ref["db"] if bias else (np.full(d, 9.0), np.zeros(d))), "fp32", rows / 32, "db")
 
 
+@pytest.mark.parametrize("dtype,r_dtype", [("bf16", "fp16"), ("fp16", "bf16")])
+@pytest.mark.parametrize("rows,d", [(3, 24), (2000, 128), (5, 1032), (1300, 1032), (1300, 1371), (1300, 1370)])
+def test_both_16_bit_types_at_once(rows, d, dtype, r_dtype):
+    r = rng(49, rows, d)
+    (x, xh), (res, rh), (w, wh) = draw(r, (rows, d), dtype), draw(r, (rows, d), r_dtype), draw(r, d, "fp16")
+    cfg = cfg_of(rows, d, dtype, r_dtype, w_dtype=A.F16, out_dtype=A.F32)
+    y, ro = torch.empty(rows, d, device="cuda"), torch.empty_like(res)
+    A.atlas_layernorm_forward(x, res, w, w, cfg, y, ro)
+    h, want, mag = R.layernorm(xh, rh, wh, wh, EPS)
+    close(y, want, mag, "fp32", 0, "y")
+    close(ro, h, np.abs(xh) + np.abs(rh), r_dtype, 0, "residual")
+    space(cfg, A.atlas_layernorm_backward_workspace_bytes(cfg))
+    dx, dw, db = torch.empty_like(res), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    A.atlas_layernorm_backward(res, w, x, res, cfg, dx, dw, db)
+    ref = R.layernorm_back(rh, wh, xh, rh, EPS)
+    close(dx, *ref["dx"], r_dtype, 0, "dx")
+    close(dw, *ref["dw"], "fp32", rows / 32, "dw")
+    close(db, *ref["db"], "fp32", rows / 32, "db")
+
+
+@pytest.mark.parametrize("d", [1371, 1370, 1024])
+@pytest.mark.parametrize("shifts", [(0, 0, 0), (1, 1, 1), (0, 1, 0), (1, 0, 1)])
+def test_rows_that_begin_on_either_side_of_four_bytes(d, shifts):
+    """Pairs where all tensors' rows begin alike, one by one where they do not; strides odd and even."""
+    rows = 1400
+    for stride in (d, d + 1):
+        r = rng(50, d, stride)
+        (x, xh), (res, rh) = (strided(r, rows, d, "bf16", stride, n) for n in shifts[:2])
+        y = strided(r, rows, d, "bf16", stride, shifts[2])[0]
+        cfg = cfg_of(rows, d, "bf16", x_stride=stride, r_stride=stride, y_stride=stride)
+        A.atlas_layernorm_forward(x, res, None, None, cfg, y)
+        _, want, mag = R.layernorm(xh, rh, None, None, EPS)
+        close(y, want, mag, "bf16", 0, "y")
+        space(cfg, A.atlas_layernorm_backward_workspace_bytes(cfg))
+        db = torch.empty(d, device="cuda")
+        A.atlas_layernorm_backward(res, None, x, None, cfg, y, None, db)
+        ref = R.layernorm_back(rh, None, xh, None, EPS)
+        close(y, *ref["dx"], "bf16", 0, "dx")
+        close(db, *ref["db"], "fp32", rows / 32, "db")
+
+
 def test_gradients_are_the_differences():
     """The kernels' gradients along a direction against differences of the kernels' own outputs, in 32 bits: the
     difference of the sums of rows * d products, each off by a few 2^-24, divided by a step of 2^-5."""
