@@ -112,8 +112,9 @@ int atlas_norm_backward(const void* h, const void* weight, const void* dy, const
  *   y = (h - mu) / sqrt(v + eps) * weight + bias
  * with the norm's description: types, strides, residual_out, groups and scales of an 8-bit output and
  * limits are as there, but eps has to be above 0 (a row of equal numbers has v = 0 and gives
- * the bias).  bias has w_dtype.  The deviations of a row are taken about its mean before they are
- * squared, and the mean's rounding is made up for, so a large mean costs v nothing. */
+ * the bias).  bias has w_dtype.  A row's sums are those of its distances to its first element, and
+ * where that lies far from the mean once more to the mean: a large mean costs v nothing.  A row whose
+ * squared deviations leave the 32-bit range has an infinite v: it gives the bias. */
 
 /*   x, residual, y, residual_out, scale  as for atlas_norm_forward
  *   weight [d] w_dtype or NULL (ones);  bias [d] w_dtype or NULL (zeros) */
@@ -265,7 +266,7 @@ int atlas_scan_backward(const void* x, const void* dt, const float* A, const voi
  *   y_t = h_t SiLU(z_t[d])                                  (without z: y_t = h_t)
  * r opens the decay: r = -infinity keeps the state and takes nothing in.  The state h [.., D], every gate
  * and every sum are held in 32 bits; 1 - a^2 is computed from s, not from a, and keeps its relative precision next to
- * a = 1.  The call reads its inputs once; its time goes by the rows, whatever their division into
+ * a = 1.  A state that becomes infinite is NaN from the next token on (h - (1 - a) h).  The call reads its inputs once; its time goes by the rows, whatever their division into
  * sequences. */
 typedef struct atlas_glr_cfg {
   int B, L, D;     /* sequences (at most 65535), tokens (packed: rows), channels */

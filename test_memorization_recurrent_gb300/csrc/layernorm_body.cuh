@@ -5,7 +5,7 @@
 // A row stays in registers from its load to its output.  Its sums are those of t = h - h_0, h_0 the row's first
 // element: mu = h_0 + mean t, v = mean t^2 - (mean t)^2.  A large mean thus enters no sum.  What the difference
 // cancels goes by (mean t)^2 / v; where that is above 16 (h_0 lies more than four deviations from the mean: it can
-// lie sqrt(d - 1) of them away) the row takes a second round of sums, of t - mean t.  So one round, and
+// lie sqrt(d - 1) of them away), or t^2 leaves the 32-bit range, the row takes a second round of sums, of t - mean t.  So one round, and
 // one barrier of a block, is enough but for some rows of ten thousand of ordinary numbers.
 //
 // Rows of up to 256 channels belong to lanes of a warp; longer ones to a block,
@@ -215,6 +215,14 @@ struct Params {
   }
 };
 
+// Whether sums about the first element are not enough: its distance to the mean, or squares that leave the 32-bit range (and a
+// row that is not finite).
+__device__ __forceinline__ bool far(float mean, float var) { return !(mean * mean <= 16.f * var && var < 3e38f); }
+// The variance from sums about the mean: infinite where their squares are, and the row then its bias.
+__device__ __forceinline__ float var_of(float mean, float squares, float inv_d) {
+  return squares < 3e38f ? fmaf(squares, inv_d, -mean * mean) : squares;
+}
+
 // One row from its elements h (zeros past its end) and h0, its first.  red: kRed words, odd: every other row of a
 // block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
 // block comes here then).
@@ -251,13 +259,13 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   less(h0, true, s1, s2);
   row_sums2(s1, s2, g, red + odd * 32);
   float mean = s1 * a.inv_d, var = fmaf(s2, a.inv_d, -mean * mean);
-  const bool again = mean * mean > 16.f * var;
+  const bool again = far(mean, var);
   if (g.tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
     less(mean, false, s1, s2);
     row_sums2(s1, s2, g, red + 64);
     if (again) {
       s1 *= a.inv_d;
-      var = fmaf(s2, a.inv_d, -s1 * s1);
+      var = var_of(s1, s2, a.inv_d);
       mean += s1;
     }
     if (g.tpr > 32) __syncthreads();  // (the next row may come here too)
@@ -303,6 +311,7 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   } else {
     // maxima of non-negative floats order like their bits, so integer maxima in shared memory
     // give the same result in any order
+    if (g.tpr <= 32) __syncwarp();  // (the row before has read them)
     for (int i = g.lane; i < a.ng; i += g.tpr) gm[i] = 0u;
     __syncthreads();
 #pragma unroll
@@ -596,11 +605,11 @@ int shared(F* f, size_t smem) {
 
 // Blocks of a kernel that an SM holds by its registers, as many as run at once: rows are dealt to them in equal shares, and
 // a second wave of blocks for the rest would take as long as the first.
-template <typename F>
-int by_registers(F* f, int threads) {
-  static const int regs = [f] {
+template <auto F>
+int by_registers(int threads) {
+  static const int regs = [] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, f) == cudaSuccess && at.numRegs > 0 ? (at.numRegs + 7) / 8 * 8 : 128;
+    return cudaFuncGetAttributes(&at, F) == cudaSuccess && at.numRegs > 0 ? (at.numRegs + 7) / 8 * 8 : 128;
   }();
   const int n = 65536 / (regs * threads), most = 2048 / threads;
   return n < 1 ? 1 : n < most ? n : most;
@@ -610,7 +619,7 @@ template <typename XT, int RB, int K, int AL>
 int run_ring(const Args& a, int threads, size_t smem, cudaStream_t st) {
   auto* f = forward_ring<XT, RB, K, AL>;
   if (const int rc = shared(f, smem)) return rc;
-  const long most = (long)kSMs * resident(smem, by_registers(f, threads));  // (even)
+  const long most = (long)kSMs * resident(smem, by_registers<forward_ring<XT, RB, K, AL>>(threads));  // (even)
   f<<<(unsigned)(a.rows < most ? a.rows & ~1L : most), threads, smem, st>>>(a);
   return status();
 }

@@ -120,14 +120,14 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
     sums(h0);
     meet(sm + odd * 64);
     float mean = sum[0] * a.inv_d, var = fmaf(sum[1], a.inv_d, -mean * mean), dot = fmaf(-mean, sum[2], sum[3]), base = h0;
-    const bool again = mean * mean > 16.f * var;
+    const bool again = far(mean, var);
     if (tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
       sums(h0 + mean);
       meet(sm + 128);
       if (again) {
         base = h0 + mean;
         mean = sum[0] * a.inv_d;
-        var = fmaf(sum[1], a.inv_d, -mean * mean);
+        var = var_of(mean, sum[1], a.inv_d);
         dot = fmaf(-mean, sum[2], sum[3]);
       }
       if (tpr > 32) __syncthreads();  // (the next row may come here too)
@@ -292,7 +292,7 @@ int run_rows(const Args& a, const RowPlan& p, int& blocks, cudaStream_t st) {
     return kSums * 4 + (ring > sums ? ring : sums);
   };
   // three stages where they cost no block of an SM (and fit)
-  const int held = by_registers(f, p.block), stages = bytes(3) <= 200 * 1024 && resident(bytes(3), held) == resident(bytes(2), held) ? 3 : 2;
+  const int held = by_registers<backward_rows<HB, DB, GB, K, AL>>(p.block), stages = bytes(3) <= 200 * 1024 && resident(bytes(3), held) == resident(bytes(2), held) ? 3 : 2;
   const size_t smem = bytes(stages);
   if (const int rc = shared(f, smem)) return rc;
   const int most = kSMs * resident(smem, held);  // no more blocks than run at once

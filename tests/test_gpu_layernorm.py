@@ -1,6 +1,10 @@
 """Layer norm on the GPU against the 64-bit reference of more_ops_ref.py: types, widths and alignments,
 rows that start anywhere, 8-bit outputs, large means, rows that are not finite, gradients.  Tolerances:
 see more_ops_ref.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -12,6 +16,7 @@ from test_gpu_layer_ops import CODE, DT, _lib, close, dev, draw, host, rng, spac
 
 pytestmark = pytest.mark.gpu
 EPS = 1e-5
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def cfg_of(rows, d, dtype, r_dtype=None, **kw):
@@ -289,3 +294,50 @@ def test_tensors_are_checked():
     for dw, db in ((n, f), (f, n), (f.bfloat16(), f), (f, f.cpu())):
         with pytest.raises(A.AtlasError):
             A.atlas_layernorm_backward(x, w, x, None, cfg, x.clone(), dw, db)
+
+
+@pytest.mark.parametrize("rows,d", [(3, 128), (5, 200), (4, 2048), (1300, 1024), (1300, 1371), (3, 8200), (2, 32767)])
+def test_deviations_whose_squares_leave_32_bits(rows, d):
+    """A first element of 1e18: the squares of the distances to it do not add up in 32 bits, those of the distances to the mean
+    do.  Where they do not either (1e25), the standard deviation is infinite: the row is its bias, and its dx is 0."""
+    r = rng(51, rows, d)
+    x, _ = draw(r, (rows, d), "fp32")
+    x[0, 0], x[1, 0], x[-1, 0] = 1e18, 1e18, 1e25
+    xh = host(x)
+    (w, wh), (b, bh) = draw(r, d, "fp32"), draw(r, d, "fp32")
+    (dy, dyh) = draw(r, (rows, d), "fp32")
+    cfg = cfg_of(rows, d, "fp32")
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    A.atlas_layernorm_forward(x, None, w, b, cfg, y)
+    A.atlas_layernorm_backward(x, w, dy, None, cfg, dx)
+    _, want, mag = R.layernorm(xh[:-1], None, wh, bh, EPS)
+    # (an element's distance to the first one is rounded to that one's last place: 2^-24 |h_0 - mu| rstd <= 2^-24 sqrt(d))
+    mag[:2] += np.sqrt(d) * np.abs(wh)
+    close(y[:-1], want, mag, "fp32", 0, "y")
+    assert torch.equal(y[-1], b) and not dx[-1].any()
+    close(dx[2:-1], *[v[2:] for v in R.layernorm_back(xh[:-1], wh, dyh[:-1], None, EPS)["dx"]], "fp32", 0, "dx")
+    assert torch.isfinite(dx).all()
+
+
+def test_sums_do_not_depend_on_earlier_calls():
+    """The blocks that share the rows are the same whatever ran before: dw's bits are those of a fresh process."""
+    code = """if True:
+        import sys, zlib, torch
+        import test_memorization_recurrent_gb300 as A
+        for d in map(int, sys.argv[1:]):
+            torch.manual_seed(0)
+            h, dy = torch.randn(3000, d, device="cuda"), torch.randn(3000, d, device="cuda")
+            cfg = A.make_norm_cfg(3000, d, dtype=A.F32, r_dtype=A.F32, w_dtype=A.F32, out_dtype=A.F32)
+            n = A.atlas_layernorm_backward_workspace_bytes(cfg)
+            ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+            cfg.workspace, cfg.workspace_bytes, cfg.held = ws.data_ptr(), n, (ws,)
+            dw, w = torch.empty(d, device="cuda"), torch.ones(d, device="cuda")
+            A.atlas_layernorm_backward(h, w, dy, None, cfg, torch.empty_like(h), dw)
+            print(d, zlib.crc32(dw.cpu().numpy().tobytes()))
+    """
+    runs = [subprocess.run([sys.executable, "-c", code, *order], capture_output=True, text=True, timeout=300, cwd=ROOT)
+            for order in (("4200", "512"), ("512", "4200"))]
+    for run in runs:
+        assert run.returncode == 0, run.stderr
+    first, second = (sorted(run.stdout.split("\n")) for run in runs)
+    assert first == second
