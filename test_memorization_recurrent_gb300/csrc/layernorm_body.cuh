@@ -89,11 +89,19 @@ __device__ __forceinline__ void load_params(const void* p, int type, float none,
       q.floats(type, w);
     }
   } else {
+    const auto each = [&](auto* q) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = col<AL>(k, i, tpr, lane);
-      if (inside(c, d)) w[i] = ld_any(p, c, type);
-    }
+      for (int i = 0; i < 8; ++i) {
+        const int c = col<AL>(k, i, tpr, lane);
+        if (inside(c, d)) w[i] = to_f(q[c]);
+      }
+    };
+    if (type == ATLAS_F32)
+      each(reinterpret_cast<const float*>(p));
+    else if (type == ATLAS_BF16)
+      each(reinterpret_cast<const __nv_bfloat16*>(p));
+    else
+      each(reinterpret_cast<const __half*>(p));
   }
 }
 
@@ -525,10 +533,10 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
     each(std::integral_constant<int, ATLAS_F16>());
 }
 
-// Many rows of a block each: a block walks rows and copies the next kStages - 1 to shared memory while it computes
+// Many rows of a block each (long ones, unaligned: more than there are SMs): a block walks rows and copies the next kStages - 1 to shared memory while it computes
 // one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it.
 template <typename XT, int RB, int K, int AL>
-__global__ void __maxnreg__(80) forward_ring(Args a) {
+__global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
   constexpr int XB = sizeof(XT);
   clear_red(sm, kRed);
@@ -669,10 +677,20 @@ int forward(const Args& args, cudaStream_t st) {
     return status();
   }
   const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<sizeof(XT), AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
-  if (many && p.k == 2 && ring <= 200 * 1024) {
-    if constexpr (AL == 0 && sizeof(XT) == 2)
-      if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, 2, 2>(a, p.block, ring, st);
-    return run_ring<XT, RB, 2, AL>(a, p.block, ring, st);
+  // (rows of more than 8192 channels: only of those that start anywhere; 2000 x 9001 bf16: 125 us straight from memory, 55
+  // so, x 32767: 558 and 156; aligned 2000 x 9000: 25 and 34, x 32768: 89 and 95)
+  if ((p.k == 2 ? many : AL != 1 && p.k > 2 && a.rows > kSMs) && ring <= 200 * 1024) {
+    const auto run = [&](auto k) -> int {
+      constexpr int K = decltype(k)::value;
+      if constexpr (AL == 0 && sizeof(XT) == 2)
+        if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, K, 2>(a, p.block, ring, st);
+      return run_ring<XT, RB, K, AL>(a, p.block, ring, st);
+    };
+    if constexpr (AL != 1) {
+      if (p.k == 4) return run(std::integral_constant<int, 4>());
+      if (p.k == 8) return run(std::integral_constant<int, 8>());
+    }
+    return run(std::integral_constant<int, 2>());
   }
   if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
   if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
