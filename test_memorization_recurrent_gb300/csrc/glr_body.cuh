@@ -26,7 +26,7 @@
 // tile come from the state in front of it, which the forward pass keeps (one for kRows rows, in 32 bits).
 //
 // An element takes eight results of the exponential pipe and 65 instructions (147 backward), so issue and latency bound it,
-// then memory.  Measured (copy rate 6.79 TB/s): 8 x 4096 x 2048 bf16, gated: 211 us, 47%, with the backward pass 702, 39%; with
+// then memory.  Measured (copy rate 6.79 TB/s): 8 x 4096 x 2048 bf16, gated: 211 us, 47%, with the backward pass 695, 40%; with
 // one string, 65536 x 512: 184 us, 22%; 9001 packed rows x 1500: 91 us.  Tiles of 64 rows on blocks of four warps:
 // 252 us; of 256 rows on sixteen: 234; three blocks of an SM (80 registers): 227.
 #pragma once
@@ -72,7 +72,7 @@ struct Strings {
   unsigned total;               // tiles x channels in all
 };
 // Sequences of one length are strings of their own where that leaves few places of tiles empty (of 512 rows: at
-// most an eighth).  (As one string, 8 x 4096 x 2048 took 299 us against 211, its training pass 916 against 702.)
+// most an eighth).  (As one string, 8 x 4096 x 2048 took 299 us against 211, its training pass 916 against 706.)
 inline bool apart_of(const GlrArgs& a) { return !a.s.start && a.s.L > 0 && (a.s.L >= 4 * kRows || a.s.L % kRows == 0); }
 inline long tiles_of(const GlrArgs& a) {  // in all
   if (apart_of(a)) return (long)a.s.B * ((a.s.L - 1L) / kRows + 1);
@@ -1048,9 +1048,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) backward_tiles(GlrArgs a, S
     const Cursor<T, FLAT> ox(a.dx, a.xb, a.xt, a, c), orr(a.dr, a.rbs, a.rt, a, c), oi(a.di, a.ibs, a.it, a, c), oz(a.dz, a.zb, a.zt, a, c);
     const long row0 = q.row0(a) + r0;
     constexpr int P = V > 1 ? 1 : 2;  // rows that a step takes, whose elements are pairs
-    const auto put = [&](auto is_plain) {  // (two copies: what the other way asks for is a tenth of this one's instructions)
+    // Two copies: what the other way asks for is a tenth of this one's instructions.  The other is a loop, its values in local
+    // memory: run by few warps, and longer than what it would share the instruction cache with (unrolled too: 706 us for 695,
+    // of packed documents 239 for 235).
+    const auto put = [&](auto is_plain) {
       constexpr bool kPlain = decltype(is_plain)::value;
+      constexpr int kUnroll = kPlain ? S / P : 1;
+      float lM[N], lU[N], lG[N];
 #pragma unroll
+      for (int e = 0; e < N; ++e) lM[e] = M[e], lU[e] = U[e], lG[e] = G[e];
+#pragma unroll kUnroll
       for (int s = 0; s < S; s += P) {
         float before[P * V], here[P * V], dx[P * V], dr[P * V], di[P * V], dz[P * V];
 #pragma unroll
@@ -1062,25 +1069,25 @@ __global__ void __launch_bounds__(kThreads, kBlocks) backward_tiles(GlrArgs a, S
           }
           before[f] = h[v];
           if (kPlain)
-            h[v] += fmaf(-M[e], h[v], U[e]);
+            h[v] += fmaf(-lM[e], h[v], lU[e]);
           else
-            h[v] = apply(M[e], U[e], h[v]);
+            h[v] = apply(lM[e], lU[e], h[v]);
           here[f] = h[v];
         }
 #pragma unroll
         for (int f = 0; f < P * V; f += 2) {
           const int e = s * V + f, v = f % V;
-          const pair32 G2 = pair(G[e], G[e + 1]), U2 = pair(U[e], U[e + 1]);
-          pair32 rrest, irest = twice(0.f), m = pair(M[e], M[e + 1]), ig = twice(1.f), A2;
+          const pair32 G2 = pair(lG[e], lG[e + 1]), U2 = pair(lU[e], lU[e + 1]);
+          pair32 rrest, irest = twice(0.f), m = pair(lM[e], lM[e + 1]), ig = twice(1.f), A2;
           const pair32 rg = gate<true>(pair_fma(br.two(e), twice(-ATLAS_LOG2E), two<V>(rb, e)), rrest);
           if (a.i) ig = gate<false>(pair_fma(bi.two(e), twice(-ATLAS_LOG2E), two<V>(ib, e)), irest);
           const pair32 sv = pair_mul(two<V>(rate, e), rg);
           if (kPlain) {
             A2 = pair_fma(m, twice(-1.f), twice(1.f));
           } else {
-            const float a0 = factor(M[e]), a1 = factor(M[e + 1]);
+            const float a0 = factor(lM[e]), a1 = factor(lM[e + 1]);
             A2 = pair(a0, a1);
-            m = pair(is_kept(M[e]) ? 1.f - a0 : M[e], is_kept(M[e + 1]) ? 1.f - a1 : M[e + 1]);
+            m = pair(is_kept(lM[e]) ? 1.f - a0 : lM[e], is_kept(lM[e + 1]) ? 1.f - a1 : lM[e + 1]);
           }
           const pair32 b2 = pair_mul(m, pair_fma(m, twice(-1.f), twice(2.f)));
           float q0, q1;

@@ -32,12 +32,14 @@ class _Cfg(ctypes.Structure):
     """A description whose tensors' extents are worked out once, and again after a field that
     they depend on is set."""
     extents = None
+    kept_bytes = None
     home = None  # the device of the tensors it was made with
 
     def __setattr__(self, name, value):
         super().__setattr__(name, value)
-        if name not in ("workspace", "workspace_bytes", "held", "extents", "home"):
+        if name not in ("workspace", "workspace_bytes", "held", "extents", "kept_bytes", "home"):
             super().__setattr__("extents", None)
+            super().__setattr__("kept_bytes", None)
 
 
 class AtlasNormCfg(_Cfg):
@@ -481,7 +483,9 @@ def _kept(t, cfg, device):
     """Address of the kept states, a tensor of any type."""
     if t is None or type(t) is int:
         return t
-    nbytes = _bytes("atlas_glr_kept_bytes", cfg)
+    nbytes = cfg.kept_bytes
+    if nbytes is None:
+        nbytes = cfg.kept_bytes = _bytes("atlas_glr_kept_bytes", cfg)
     if t.get_device() != device or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
         raise _error(f"kept must be a contiguous tensor of at least {nbytes} bytes on the current device (cuda:{device})")
     return t.data_ptr()

@@ -87,3 +87,13 @@ def test_reference_gradient(gated):
         d = r.standard_normal(v[k].shape)
         step = (loss(**{k: v[k] + 1e-5 * d}) - loss(**{k: v[k] - 1e-5 * d})) / 2e-5
         assert abs(step - (g[gk] * d).sum()) < 1e-7, k
+
+
+def test_size_of_the_kept_states_follows_the_description():
+    """The binding works it out once, and again after a field that it depends on is set."""
+    cfg = A.make_glr_cfg(2, 300, 40)
+    cfg.kept_bytes = A.atlas_glr_kept_bytes(cfg)
+    cfg.workspace_bytes = 5
+    assert cfg.kept_bytes == 5 * 40 * 4  # one string: 600 rows
+    cfg.L = 600
+    assert cfg.kept_bytes is None and A.atlas_glr_kept_bytes(cfg) == 2 * 5 * 40 * 4
