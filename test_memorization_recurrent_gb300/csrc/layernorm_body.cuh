@@ -18,7 +18,7 @@
 //
 // Bound by memory, and next to it by instructions.  Measured (copy rate 6.79 TB/s): 32768 x 2048 bf16 + residual to e4m3 with
 // scales of 128: 88 us, 79% (a round of sums for the mean and one about it: 119; one vector a thread: 115; a warp a
-// row: 135); 524288 x 128 fp32 to bf16: 68 us, 87%; 20000 x 1371 fp16 + residual: 59 us, 55% (one by one: 85).
+// row: 135); 524288 x 128 fp32 to bf16: 69 us, 86%; 20000 x 1371 fp16 + residual: 59 us, 55% (one by one: 85).
 #pragma once
 #include <initializer_list>
 
