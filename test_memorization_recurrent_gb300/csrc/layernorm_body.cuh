@@ -534,7 +534,8 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
 }
 
 // Many rows of a block each (long ones, unaligned: more than there are SMs): a block walks rows and copies the next kStages - 1 to shared memory while it computes
-// one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it.
+// one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it, and this
+// row's place; a block of one warp (rows of 257 to 512 channels) has no barrier there, and takes one of its own.
 template <typename XT, int RB, int K, int AL>
 __global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
@@ -579,6 +580,7 @@ __global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
       }
     }
     cp_wait<kStages - 2>();  // the next row's
+    if (g.tpr <= 32) __syncwarp();
     forward_row<K, AL>(a, g, sm, odd, gm, row, true, h0, h, par);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
