@@ -540,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) forward_tiles(GlrArgs a, Sp
   if (threadIdx.x == 0) s_tile.find(t, atomicAdd(w.ticket, 1u), false);
   __syncthreads();
   Tile q = s_tile;
+  __syncthreads();  // (the next ticket's tile takes its place; later ones have a pass's other barriers between)
   Info info;
   if (q.some) {
     info.look(a, w, t, q);
@@ -822,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) backward_tiles(GlrArgs a, S
   if (threadIdx.x == 0) s_tile.find(t, atomicAdd(w.ticket, 1u), true);
   __syncthreads();
   Tile q = s_tile;
+  __syncthreads();  // (the next ticket's tile takes its place; later ones have a pass's other barriers between)
   Info info;
   if (q.some) {
     info.look(a, w, t, q);
