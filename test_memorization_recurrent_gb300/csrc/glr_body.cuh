@@ -61,7 +61,8 @@ struct Space {
   size_t bytes;
 };
 
-inline long rows_of(const GlrArgs& a) { return a.s.start ? a.s.L : (long)a.s.B * a.s.L; }
+// (without sequences no row belongs to one, and seq_start has one element)
+inline long rows_of(const GlrArgs& a) { return a.s.start && a.s.B > 0 ? a.s.L : (long)a.s.B * a.s.L; }
 inline int groups_of(const GlrArgs& a) { return (a.D + kCh - 1) / kCh; }
 
 // The strings of tiles.

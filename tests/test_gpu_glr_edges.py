@@ -34,3 +34,17 @@ def test_every_warp_of_a_block_begins_with_the_same_tile(B, L, D):
             for b in (0, B - 1):
                 close(y[b], g.ref(b, g.hh[b])["y"], g.ref(b, g.hh[b], mag=True)["y"], "bf16", L, "y")
         assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_no_sequences():
+    """A packed batch without sequences has no rows of theirs: nothing is read or written but the parameters' gradients,
+    which are zeros."""
+    D = 40
+    start = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = Glr(rng(81), 1, 0, D, "fp32", packed_rows=300)
+    cfg = g.cfg(0, 300, seq_start=start)
+    y = torch.full_like(g.x, 5.0)
+    g.forward(cfg, y)
+    o = g.backward(cfg, torch.ones_like(g.x), None)
+    assert (y == 5).all() and all((o[k] == 7).all() for k in ("dx", "dr", "di", "dz"))
+    assert not any(o[k].any() for k in ("dlam", "drb", "dib"))
