@@ -20,7 +20,9 @@
 //
 // A map's factor is held as d: 1 - a where a is near 1 (h + (u - d h) then rounds by h's last place, not by that of a,
 // which would be the same in every step of a slow channel, and products of factors just below 1 would all be
-// rounded down), else -a; -0 is a cut, which lets nothing through, not even what is not finite.
+// rounded down), else -a; 2 is a cut, which lets nothing through, not even what is not finite.  No factor is coded so: one
+// that has left the range is -0 and multiplies, so NaN reaches the rest of its sequence however fast that decays and wherever
+// its tiles end.
 //
 // Backward the same with the rows in reverse: c -> a (v + c) carries a g to the token in front.  The states inside a
 // tile come from the state in front of it, which the forward pass keeps (one for kRows rows, in 32 bits).
@@ -156,10 +158,10 @@ __device__ __forceinline__ float lost(float s) {
 }
 __device__ __forceinline__ float kept_of(float s) { return ex2(-ATLAS_LOG2E * s); }
 
-// A factor a as d: 1 - a, or -a (-0 a cut).
+// A factor a as d: 1 - a, or -a (2 a cut).
 __device__ __forceinline__ bool is_kept(float d) { return __float_as_int(d) < 0; }
-__device__ __forceinline__ bool is_cut(float d) { return __float_as_uint(d) == 0x80000000u; }
-constexpr float kCut = -0.f;
+__device__ __forceinline__ bool is_cut(float d) { return d > 1.f; }
+constexpr float kCut = 2.f;
 __device__ __forceinline__ float factor(float d) { return is_kept(d) ? -d : 1.f - d; }
 // Of 1 - a and a, both to their own precision.
 __device__ __forceinline__ float coded(float m, float a) { return m < kSlow ? m : -a; }

@@ -48,3 +48,55 @@ def test_no_sequences():
     o = g.backward(cfg, torch.ones_like(g.x), None)
     assert (y == 5).all() and all((o[k] == 7).all() for k in ("dx", "dr", "di", "dz"))
     assert not any(o[k].any() for k in ("dlam", "drb", "dib"))
+
+
+def spread_like(got, want, what):
+    """NaN in the places where the recurrence, token by token, has NaN, and nowhere else."""
+    got, want = np.isnan(host(got)), np.isnan(want)
+    assert (got == want).all(), f"{what}: {int((got & ~want).sum())} too many, {int((want & ~got).sum())} lost"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,lens", [(64, [1300, 1300, 1300]), (33, [90, 1400, 200]), (8, [4000]), (1024, [640] * 10)], ids=str)
+def test_nan_reaches_the_rest_of_its_sequence(lens, D, dtype):
+    """Decays of e^-1 to e^-200 a token, whose products over a warp's, a tile's or a group's rows leave the range: a NaN of
+    one token is in all later states and outputs, and one of a gradient in those of all earlier tokens."""
+    even, B = len(set(lens)) == 1, len(lens)
+    r = rng(82, D, B)
+    start, rows, at = packed(lens, 0)
+    g = Glr(r, B, lens[0], D, dtype, **({} if even else dict(packed_rows=rows)))
+    g.lam = dev(np.resize([0.5, 2.0, 5.0, 25.0, -6.0], D))
+    g.lamh = host(g.lam)
+    shape = tuple(g.x.shape)
+    (dy, dyh), (dh, dhh) = draw(r, shape, dtype), draw(r, (B, D), "fp32")
+    pick = (lambda b, t: (b, t)) if even else (lambda b, t: (at[b] + t,))
+    seq = (lambda b: b) if even else (lambda b: slice(at[b], at[b] + lens[b]))
+    b, n = B // 2, lens[B // 2]
+    g.x[pick(b, 5)], g.xh[pick(b, 5)] = float("nan"), np.nan
+    dy[pick(b, n - 3)], dyh[pick(b, n - 3)] = float("nan"), np.nan
+    cfg = g.cfg(B, lens[0] if even else rows, **({} if even else dict(seq_start=start)))
+    y, out, kept = torch.empty_like(g.x), torch.empty_like(g.h), kept_of(cfg)
+    g.forward(cfg, y, out, kept)
+    o = g.backward(cfg, dy, dh, kept)
+    for i in range(B):
+        with np.errstate(all="ignore"):
+            ref = g.ref(seq(i), g.hh[i], dyh[seq(i)], dhh[i])
+        spread_like(y[seq(i)], ref["y"], "y")
+        spread_like(out[i], ref["h"], "h")
+        spread_like(dh[i], ref["dh"], "dh")
+        for k in ("dx", "dr", "di", "dz"):
+            spread_like(o[k][seq(i)], ref[k], k)
+    for k in ("dlam", "drb", "dib"):
+        assert torch.isnan(o[k]).all(), k
+
+
+def test_nan_stays_in_a_state_token_by_token():
+    """Single tokens whose factor underflows: a state of NaN stays, one of zeros takes the token's input."""
+    D, B = 40, 4
+    g = Glr(rng(83), B, 1, D, "fp32", bias=False)
+    g.lam.fill_(300.0)
+    g.r.fill_(2.0)
+    g.h[1], g.h[2, ::3] = float("nan"), float("nan")
+    y, out = torch.empty_like(g.x), torch.empty_like(g.h)
+    g.forward(g.cfg(B, 1), y, out)
+    assert torch.equal(torch.isnan(out), torch.isnan(g.h)) and torch.equal(torch.isnan(y[:, 0]), torch.isnan(g.h))
