@@ -266,8 +266,9 @@ int atlas_scan_backward(const void* x, const void* dt, const float* A, const voi
  *   y_t = h_t SiLU(z_t[d])                                  (without z: y_t = h_t)
  * r opens the decay: r = -infinity keeps the state and takes nothing in.  The state h [.., D], every gate
  * and every sum are held in 32 bits; 1 - a^2 is computed from s, not from a, and keeps its relative precision next to
- * a = 1.  A state that becomes infinite is NaN from the next token on (h - (1 - a) h).  The call reads its inputs once; its time goes by the rows, whatever their division into
- * sequences. */
+ * a = 1.  A state that becomes infinite is never finite again in its sequence: it stays infinite or is NaN (h - (1 - a) h,
+ * or 0 times it where a product of decays has left the range), and so for gradients in front of an infinite one.  NaN stays
+ * NaN.  The call reads its inputs once; its time goes by the rows, whatever their division into sequences. */
 typedef struct atlas_glr_cfg {
   int B, L, D;     /* sequences (at most 65535), tokens (packed: rows), channels */
   int dtype;       /* x, r, i, z, y and their gradients: ATLAS_F32, ATLAS_BF16, ATLAS_F16 */

@@ -100,3 +100,31 @@ def test_nan_stays_in_a_state_token_by_token():
     y, out = torch.empty_like(g.x), torch.empty_like(g.h)
     g.forward(g.cfg(B, 1), y, out)
     assert torch.equal(torch.isnan(out), torch.isnan(g.h)) and torch.equal(torch.isnan(y[:, 0]), torch.isnan(g.h))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rate", [-6.0, 2.0, 25.0])
+@pytest.mark.parametrize("D,L", [(64, 1300), (33, 300), (8, 4000)])
+def test_an_infinite_state_is_never_finite_again(D, L, rate, dtype):
+    """Infinite inputs, first states and gradients: what is not finite token by token is not finite here (NaN, where the
+    recurrence says infinity, is allowed), and nothing else."""
+    B = 3
+    r = rng(84, D, L)
+    g = Glr(r, B, L, D, dtype)
+    g.lam.fill_(rate)
+    g.lamh = host(g.lam)
+    (dy, dyh), (dh, dhh) = draw(r, (B, L, D), dtype), draw(r, (B, D), "fp32")
+    inf = float("inf")
+    g.x[0, 40], g.xh[0, 40] = inf, inf
+    g.h[1], g.hh[1] = -inf, -inf
+    dy[0, L - 30], dyh[0, L - 30] = -inf, -inf
+    dh[2], dhh[2] = inf, inf
+    cfg = g.cfg(B, L)
+    y, out, kept = torch.empty_like(g.x), torch.empty_like(g.h), kept_of(cfg)
+    g.forward(cfg, y, out, kept)
+    o = g.backward(cfg, dy, dh, kept)
+    for b in range(B):
+        with np.errstate(all="ignore"):
+            ref = g.ref(b, g.hh[b], dyh[b], dhh[b])
+        for k, got in (("y", y[b]), ("h", out[b]), ("dh", dh[b]), *((k, o[k][b]) for k in ("dx", "dr", "di", "dz"))):
+            assert (np.isfinite(host(got)) == np.isfinite(ref[k])).all(), (b, k)
