@@ -112,8 +112,9 @@ int atlas_norm_backward(const void* h, const void* weight, const void* dy, const
  *   y = (h - mu) / sqrt(v + eps) * weight + bias
  * with the norm's description: types, strides, residual_out, groups and scales of an 8-bit output and
  * limits are as there, but eps has to be above 0 (a row of equal numbers has v = 0 and gives
- * the bias).  bias has w_dtype.  A row's sums are those of its distances to its first element, and
- * where that lies far from the mean once more to the mean: a large mean costs v nothing.  A row whose
+ * the bias).  bias has w_dtype.  A row's sums are those of its distances to a number near its
+ * first elements, and where that lies far from the mean once more to the mean: a large mean costs v nothing.  Outputs in 32 and
+ * 8 bits and gradients are as exact as of the mean first and then the deviations from it, whichever elements come first.  A row whose
  * squared deviations leave the 32-bit range has an infinite v: it gives the bias. */
 
 /*   x, residual, y, residual_out, scale  as for atlas_norm_forward

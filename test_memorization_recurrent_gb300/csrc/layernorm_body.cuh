@@ -2,11 +2,17 @@
 //
 //   h = x + r,  mu = mean h,  v = mean (h - mu)^2,  y = (h - mu) / sqrt(v + eps) w + b
 //
-// A row stays in registers from its load to its output.  Its sums are those of t = h - h_0, h_0 the row's first
-// element: mu = h_0 + mean t, v = mean t^2 - (mean t)^2.  A large mean thus enters no sum.  What the difference
-// cancels goes by (mean t)^2 / v; where that is above 16 (h_0 lies more than four deviations from the mean: it can
-// lie sqrt(d - 1) of them away), or t^2 leaves the 32-bit range, the row takes a second round of sums, of t - mean t.  So one round, and
-// one barrier of a block, is enough but for some rows of ten thousand of ordinary numbers.
+// A row stays in registers from its load to its output.  Its sums are those of t = h - c, c a number near the row's own:
+// mu = c + mean t, v = mean t^2 - (mean t)^2.  A large mean thus enters no sum.  What the difference cancels goes by
+// (mean t)^2 / v; where that is above a bound, or t^2 leaves the 32-bit range, the row takes a second round of sums, about
+// mu.  So one round, and one barrier of a block, is enough but for few rows of ordinary numbers.
+//   An output in 32 bits shows the last places, one in 8 bits has to be what those round to, and gradients are sums of many:
+// PRECISE, c is the mean of the first eight elements and the bound 1 (a row of two hundred of ordinary numbers is above), and mu,
+// held as two numbers (c + mean t rounded, and what that lost), is taken from h before the scaling.  The rms error is then at
+// most 1.3 times that of two passes, whichever elements come first.
+//   Outputs in 16 bits, whose rounding is a thousand times what is lost: c is the first element and the bound 16 (some rows of
+// ten thousand), and the row is held as t.  Its error is 2.4 times that of two passes in 32 bits, and 17 times with a first element
+// 3.9 deviations from the mean.  (As the others: 524288 x 128 fp32 to bf16 72 us, so 67; 500000 x 40 bf16 + residual 43, so 39.)
 //
 // Rows of up to 256 channels belong to lanes of a warp; longer ones to a block,
 // which walks rows with the next two on their way through shared memory (up to 1216 rows, eight an SM: a block each, straight
@@ -17,8 +23,9 @@
 // read and store neighbouring elements, in 16 bits by pairs where the tensors' rows begin alike.
 //
 // Bound by memory, and next to it by instructions.  Measured (copy rate 6.79 TB/s): 32768 x 2048 bf16 + residual to e4m3 with
-// scales of 128: 88 us, 79% (a round of sums for the mean and one about it: 119; one vector a thread: 115; a warp a
-// row: 135); 524288 x 128 fp32 to bf16: 69 us, 86%; 20000 x 1371 fp16 + residual: 59 us, 55% (one by one: 85).
+// scales of 128: 92 us, 75% (about the first element: 88; when that was so, a round of sums for the mean and one about it: 119, one
+// vector a thread: 115, a warp a row: 135); 524288 x 128 fp32 to bf16: 67 us, 89%; 20000 x 1371 fp16 + residual: 61 us, 53% (one by
+// one: 85).
 #pragma once
 #include <initializer_list>
 
@@ -210,37 +217,57 @@ struct Params {
       }
     }
   }
-  __device__ __forceinline__ void apply(const Args& a, int k, int tpr, int lane, float rstd, float off, float* h) {
+  // y of vector k: (h - less) rstd + off, through weight and bias (LESS: otherwise that is none)
+  template <bool LESS>
+  __device__ __forceinline__ void apply(const Args& a, int k, int tpr, int lane, float less, float rstd, float off, float* h) {
     if constexpr (!kKept) {
       load_params<AL>(a.w, a.wt, 1.f, k, a.d, tpr, lane, w[0]);
       load_params<AL>(a.b, a.wt, 0.f, k, a.d, tpr, lane, b[0]);
     }
     const float *pw = w[kKept ? k : 0], *pb = b[kKept ? k : 0];
-    const pair32 rstd2 = pair(rstd, rstd), off2 = pair(off, off);
+    const pair32 less2 = pair(-less, -less), rstd2 = pair(rstd, rstd), off2 = pair(off, off);
 #pragma unroll
-    for (int i = 0; i < 8; i += 2)
-      unpair(pair_fma(pair_fma(pair(h[i], h[i + 1]), rstd2, off2), pair(pw[i], pw[i + 1]), pair(pb[i], pb[i + 1])), h[i], h[i + 1]);
+    for (int i = 0; i < 8; i += 2) {
+      const pair32 t = LESS ? pair_add(pair(h[i], h[i + 1]), less2) : pair(h[i], h[i + 1]);
+      unpair(pair_fma(pair_fma(t, rstd2, off2), pair(pw[i], pw[i + 1]), pair(pb[i], pb[i + 1])), h[i], h[i + 1]);
+    }
   }
 };
 
-// Whether sums about the first element are not enough: its distance to the mean, or squares that leave the 32-bit range (and a
-// row that is not finite).
-__device__ __forceinline__ bool far(float mean, float var) { return !(mean * mean <= 16.f * var && var < 3e38f); }
+// Whether sums about c are not enough: its distance to the mean, or squares that leave the 32-bit range (and a row that is not
+// finite).
+template <bool PRECISE>
+__device__ __forceinline__ bool far(float mean, float var) {
+  return !(mean * mean <= (PRECISE ? 1.f : 16.f) * var && var < 3e38f);
+}
+// The mean of eight neighbouring lanes' numbers.
+__device__ __forceinline__ float mean8(float v) {
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  return v * 0.125f;
+}
+// The mean of those of a row's lanes' first one's eight elements h (of the first vector) that there are, zeros elsewhere.
+// base: that lane.  Equal numbers may be off by a rounding here if there are not eight: they take the second round.
+template <int AL>
+__device__ __forceinline__ float mean_first(const float* h, int d, int tpr, int base) {
+  const int n = AL == 1 ? 8 : min(8, (d - 1) / tpr + 1);
+  return __shfl_sync(0xFFFFFFFFu, pair_sum(pair_add(pair_add(pair(h[0], h[1]), pair(h[2], h[3])), pair_add(pair(h[4], h[5]), pair(h[6], h[7])))), base) *
+         (n == 8 ? 0.125f : 1.f / n);
+}
 // The variance from sums about the mean: infinite where their squares are, and the row then its bias.
 __device__ __forceinline__ float var_of(float mean, float squares, float inv_d) {
   return squares < 3e38f ? fmaf(squares, inv_d, -mean * mean) : squares;
 }
 
-// One row from its elements h (zeros past its end) and h0, its first.  red: kRed words, odd: every other row of a
+// One row from its elements h (zeros past its end) and c, a number near its mean.  red: kRed words, odd: every other row of a
 // block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
 // block comes here then).
-template <int K, int AL>
+template <int K, int AL, bool PRECISE>
 __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, int odd, unsigned* gm,
-                                            long row, bool live, float h0, float (*h)[8], Params<K, AL>& par) {
+                                            long row, bool live, float c, float (*h)[8], Params<K, AL>& par) {
   const int lane = AL == 2 ? g.first : g.lane;
   const auto in = [&](int k, int i) { return inside(col<AL>(k, AL == 1 ? 0 : i, g.tpr, lane), a.d); };
-  // the elements less v, to h, and the sums of them and their squares; an aligned row's vectors past its end keep
-  // what comes out and stay out of the sums
+  // the sums of the elements less v and of their squares, what is past the row's end left out; keep: the differences, to h
   const auto less = [&](float v, bool keep, float& s1, float& s2) {
     const pair32 minus = pair(-v, -v);
     s1 = s2 = 0.f;
@@ -264,26 +291,27 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   };
   if (a.r_out && live) store_row<K, AL>(a.r_out, row * a.sr, a.rt, a.d, g.tpr, lane, h);
   float s1, s2;
-  less(h0, true, s1, s2);
+  less(c, !PRECISE, s1, s2);
   row_sums2(s1, s2, g, red + odd * 32);
   float mean = s1 * a.inv_d, var = fmaf(s2, a.inv_d, -mean * mean);
-  const bool again = far(mean, var);
+  const bool again = far<PRECISE>(mean, var);
   if (g.tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
-    less(mean, false, s1, s2);
+    less(PRECISE ? c + mean : mean, false, s1, s2);
     row_sums2(s1, s2, g, red + 64);
     if (again) {
       s1 *= a.inv_d;
       var = var_of(s1, s2, a.inv_d);
-      mean += s1;
+      c += mean;
+      mean = PRECISE ? s1 : mean + s1;
     }
     if (g.tpr > 32) __syncthreads();  // (the next row may come here too)
   }
-  const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), off = -mean * rstd;
+  const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), mu = c + mean, off = (PRECISE ? (mu - c) - mean : -mean) * rstd;
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    par.apply(a, k, g.tpr, lane, rstd, off, h[k]);
-    if (a.ot != ATLAS_E4M3) continue;
+    par.template apply<PRECISE>(a, k, g.tpr, lane, mu, rstd, off, h[k]);
+    if (!PRECISE || a.ot != ATLAS_E4M3) continue;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -306,7 +334,7 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
       st8(a.y, row * a.sy + c, a.ot, h[k]);
     }
   }
-  if (a.ot != ATLAS_E4M3) {
+  if (!PRECISE || a.ot != ATLAS_E4M3) {
     if (live) store_row<K, AL>(a.y, row * a.sy, a.ot, a.d, g.tpr, lane, h);
     return;
   }
@@ -385,15 +413,15 @@ struct RawRow {
 };
 
 
-// A row's first element.
+// A row's element i.
 template <typename XT, int RB>
-__device__ __forceinline__ float first_of(const Args& a, long row) {
-  float v = to_f(reinterpret_cast<const XT*>(a.x)[row * a.sx]);
-  if (RB) v += ld_any(a.r, row * a.sr, a.rt);
+__device__ __forceinline__ float element_of(const Args& a, long row, int i) {
+  float v = to_f(reinterpret_cast<const XT*>(a.x)[row * a.sx + i]);
+  if (RB) v += ld_any(a.r, row * a.sr + i, a.rt);
   return v;
 }
 
-// A block a row, straight from memory.
+// A block a row, straight from memory; every output type the precise way.
 template <typename XT, int RB, int K, int AL>
 __global__ void __launch_bounds__(512) forward_rows(Args a) {
   extern __shared__ __align__(16) float sm[];
@@ -402,18 +430,18 @@ __global__ void __launch_bounds__(512) forward_rows(Args a) {
   const long row = blockIdx.x;
   RawRow<XT, RB, K, AL> raw;
   raw.load(a, row, tpr, g.lane);
-  const float h0 = first_of<XT, RB>(a, row);
+  const float first = element_of<XT, RB>(a, row, g.lane & 7);
   Params<K, AL> par;
   par.load(a, tpr, g.lane);
   clear_red(sm, kRed);
   float h[K][8];
   raw.floats(a, h);
-  forward_row<K, AL>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm + kRed), row, true, h0, h, par);
+  forward_row<K, AL, true>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm + kRed), row, true, mean8(first), h, par);
 }
 
 // Rows of up to 256 channels: tpr lanes of a warp each.  Warps walk rows, the next two of their lanes' under way
 // while they compute two.
-template <typename XT, int RB, int AL>
+template <typename XT, int RB, int AL, bool PRECISE>
 __global__ void __launch_bounds__(128, 5) forward_lanes(Args a, int tpr) {
   extern __shared__ __align__(16) float sm[];
   constexpr int R = 2;
@@ -434,9 +462,11 @@ __global__ void __launch_bounds__(128, 5) forward_lanes(Args a, int tpr) {
       raw[j].load(a, row + (j + R) * step, tpr, g.lane);
     }
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-      forward_row<1, AL>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm) + mine * a.ng, row + j * step, row + j * step < a.rows,
-                         __shfl_sync(0xFFFFFFFFu, h[j][0][0], (threadIdx.x & 31) - g.lane), h[j], par);
+    for (int j = 0; j < R; ++j) {
+      const int base = (threadIdx.x & 31) - g.lane;
+      const float c = PRECISE ? mean_first<AL>(h[j][0], a.d, tpr, base) : __shfl_sync(0xFFFFFFFFu, h[j][0][0], base);
+      forward_row<1, AL, PRECISE>(a, g, sm, 0, reinterpret_cast<unsigned*>(sm) + mine * a.ng, row + j * step, row + j * step < a.rows, c, h[j], par);
+    }
   }
 }
 
@@ -533,11 +563,54 @@ __device__ __forceinline__ void slot_floats(const char* s, int shift, int type, 
     each(std::integral_constant<int, ATLAS_F16>());
 }
 
+// About the mean of a row's first eight elements, for sums to be taken about: any number would do, so 16-bit elements
+// are added in their type.  Every thread reads them: what is handed on between lanes waits behind all copies and reads of
+// the others (backward 16384 x 2560 with a 32-bit stream: 120 us with three exchanges, so 111).  Of rows that begin anywhere
+// eight lanes read one each all the same: eight reads of a thread cost more (20000 x 1371 fp32 + residual: 113 us and 82).
+template <int E, int AL>
+__device__ __forceinline__ float near_mean(const char* s, int type, int d) {
+  if (E == 4) {
+    float f[8];
+    if (AL == 1) {
+      ld_vec<8>(reinterpret_cast<const float*>(s), f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = reinterpret_cast<const float*>(s)[min(i, d - 1)];
+    }
+    pair32 v = pair(f[0], f[1]);
+#pragma unroll
+    for (int i = 2; i < 8; i += 2) v = pair_add(v, pair(f[i], f[i + 1]));
+    return pair_sum(v) * 0.125f;
+  }
+  if (AL != 1 && d <= 8) return raw_float<E>(ld_raw<E>(s, 0), type);
+  uint32_t w[4];
+  if (AL == 1) {
+    *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(s);
+  } else {
+    // (a row that begins between two words: from its second element on)
+    const uint32_t* p = reinterpret_cast<const uint32_t*>((reinterpret_cast<uintptr_t>(s) + 2) & ~(uintptr_t)3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = p[i];
+  }
+  if (type == ATLAS_BF16) {
+    const auto h = [&](int i) { return *reinterpret_cast<const __nv_bfloat162*>(&w[i]); };
+    const __nv_bfloat162 v = __hadd2(__hadd2(h(0), h(1)), __hadd2(h(2), h(3)));
+    return (__low2float(v) + __high2float(v)) * 0.125f;
+  }
+  // an eighth of each, whose sum stays in the range
+  const auto h = [&](int i) { return *reinterpret_cast<const __half2*>(&w[i]); };
+  const __half2 part = __float2half2_rn(0.125f);
+  const __half2 v = __hfma2(h(0), part, __hfma2(h(1), part, __hfma2(h(2), part, __hmul2(h(3), part))));
+  return __low2float(v) + __high2float(v);
+}
+
 // Many rows of a block each (long ones, unaligned: more than there are SMs): a block walks rows and copies the next kStages - 1 to shared memory while it computes
 // one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it, and this
 // row's place; a block of one warp (rows of 257 to 512 channels) has no barrier there, and takes one of its own.
-template <typename XT, int RB, int K, int AL>
-__global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
+// Registers: 80 (32768 x 2048 bf16 + residual to e4m3: 92 us; 64: 108, 72: 100, 88: 94), 72 of aligned rows of two 32-bit
+// tensors, whose stages leave room for four blocks of an SM anyway (20000 x 2048: 109 us, 80: 122; x 4096: 213 and 228).
+template <typename XT, int RB, int K, int AL, bool PRECISE>
+__global__ void __maxnreg__(K > 2 ? 128 : AL == 1 && RB == 4 && sizeof(XT) == 4 ? 72 : 80) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
   constexpr int XB = sizeof(XT);
   clear_red(sm, kRed);
@@ -567,8 +640,16 @@ __global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
     fetch(row + (long)(kStages - 1) * gridDim.x, stage == 0 ? kStages - 1 : stage - 1);
     const char* s = ring + stage * bytes;
     const int ax = AL == 1 ? 0 : ahead(tx, row), ar = AL == 1 || RB == 0 ? 0 : ahead(tr, row);
-    float h0 = to_f(*reinterpret_cast<const XT*>(s + ax));
-    if constexpr (RB > 0) h0 += raw_float<RB>(ld_raw<RB>(s + xs + ar, 0), a.rt);
+    float c;
+    if (PRECISE && AL == 1) {
+      c = near_mean<XB, AL>(s, code_of<XT>(), a.d);
+      if constexpr (RB > 0) c += near_mean<RB, AL>(s + xs, a.rt, a.d);
+    } else {
+      const int at = PRECISE ? g.lane & 7 : 0;
+      c = to_f(reinterpret_cast<const XT*>(s + ax)[at]);
+      if constexpr (RB > 0) c += raw_float<RB>(ld_raw<RB>(s + xs + ar, at), a.rt);
+      if (PRECISE) c = mean8(c);
+    }
     float h[K][8];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -581,7 +662,7 @@ __global__ void __maxnreg__(K <= 2 ? 80 : 128) forward_ring(Args a) {
     }
     cp_wait<kStages - 2>();  // the next row's
     if (g.tpr <= 32) __syncwarp();
-    forward_row<K, AL>(a, g, sm, odd, gm, row, true, h0, h, par);
+    forward_row<K, AL, PRECISE>(a, g, sm, odd, gm, row, true, c, h, par);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_wait<0>();
@@ -625,11 +706,11 @@ int by_registers(int threads) {
   return n < 1 ? 1 : n < most ? n : most;
 }
 
-template <typename XT, int RB, int K, int AL>
+template <typename XT, int RB, int K, int AL, bool PRECISE>
 int run_ring(const Args& a, int threads, size_t smem, cudaStream_t st) {
-  auto* f = forward_ring<XT, RB, K, AL>;
+  auto* f = forward_ring<XT, RB, K, AL, PRECISE>;
   if (const int rc = shared(f, smem)) return rc;
-  const long most = (long)kSMs * resident(smem, by_registers<forward_ring<XT, RB, K, AL>>(threads));  // (even)
+  const long most = (long)kSMs * resident(smem, by_registers<forward_ring<XT, RB, K, AL, PRECISE>>(threads));  // (even)
   f<<<(unsigned)(a.rows < most ? a.rows & ~1L : most), threads, smem, st>>>(a);
   return status();
 }
@@ -662,7 +743,7 @@ inline bool pairs(const Args& a, std::initializer_list<Begins> tensors, const Ro
   return base >= 0 && p.tpr * 8 * p.k > a.d;
 }
 
-template <typename XT, int RB, int AL>
+template <typename XT, int RB, int AL, bool PRECISE>
 int forward(const Args& args, cudaStream_t st) {
   Args a = args;
   // a group of an 8-bit output in neighbouring lanes of one warp: a power of two from 8 to 256
@@ -672,7 +753,7 @@ int forward(const Args& args, cudaStream_t st) {
   if (a.d <= 256) {
     const int rpb = p.block / p.tpr;
     const size_t smem = a.lanes ? 0 : (size_t)rpb * a.ng * 4;
-    auto* f = forward_lanes<XT, RB, AL>;
+    auto* f = forward_lanes<XT, RB, AL, PRECISE>;
     if (const int rc = shared(f, smem)) return rc;
     const long need = (a.rows + rpb - 1) / rpb, most = 5L * kSMs;
     f<<<(unsigned)(need < most ? need : most), p.block, smem, st>>>(a, p.tpr);
@@ -685,8 +766,8 @@ int forward(const Args& args, cudaStream_t st) {
     const auto run = [&](auto k) -> int {
       constexpr int K = decltype(k)::value;
       if constexpr (AL == 0 && sizeof(XT) == 2)
-        if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, K, 2>(a, p.block, ring, st);
-      return run_ring<XT, RB, K, AL>(a, p.block, ring, st);
+        if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, K, 2, PRECISE>(a, p.block, ring, st);
+      return run_ring<XT, RB, K, AL, PRECISE>(a, p.block, ring, st);
     };
     if constexpr (AL != 1) {
       if (p.k == 4) return run(std::integral_constant<int, 4>());
@@ -698,6 +779,10 @@ int forward(const Args& args, cudaStream_t st) {
   if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
   if (p.k == 4) return run_rows<XT, RB, 4, AL>(a, p.block, st);
   return run_rows<XT, RB, 8, AL>(a, p.block, st);
+}
+template <typename XT, int RB, int AL>
+int forward(const Args& a, cudaStream_t st) {
+  return a.ot == ATLAS_F32 || a.ot == ATLAS_E4M3 ? forward<XT, RB, AL, true>(a, st) : forward<XT, RB, AL, false>(a, st);
 }
 template <typename XT>
 int forward(const Args& a, cudaStream_t st) {

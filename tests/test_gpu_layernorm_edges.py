@@ -40,3 +40,32 @@ def test_rows_that_one_warp_walks(d, out, group, dtype, r_dtype):
         close(host(y), want / step, mag / step, out, 0, "y")
     else:
         close(y, want, mag, dtype, 0, "y")
+
+
+@pytest.mark.parametrize("rows,d,shift", [(5000, 24, 0), (5000, 37, 0), (4000, 128, 0), (40, 1000, 0), (1300, 512, 0), (1300, 1371, 0), (1300, 1371, 1),
+                                          (1300, 2560, 0), (40, 8192, 0), (300, 9001, 0)])
+@pytest.mark.parametrize("off,first", [(0.0, 1), (2.0, 1), (3.9, 1), (3.9, 8), (30.0, 8)])
+def test_errors_in_32_bits_are_those_of_two_passes(rows, d, shift, off, first):
+    """The rms error against 64 bits, whichever elements a row begins with (`first` of them, `off` deviations from the mean),
+    is at most 1.5 times that of the mean first, then the deviations from it, in 32 bits."""
+    r = rng(71, rows, d)
+    x = strided(r, rows, d, "fp32", 0, shift)[0]
+    x += 0.5 * dev(r.standard_normal((rows, 1)))
+    x[:, :first] = x[:, first:].mean(1, keepdim=True) + off
+    dy = draw(r, (rows, d), "fp32")[0]
+    y, dx = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, device="cuda")
+    cfg = cfg_of(rows, d, "fp32")
+    space(cfg, A.atlas_layernorm_backward_workspace_bytes(cfg))
+    A.atlas_layernorm_forward(x, None, None, None, cfg, y)
+    h = x if shift == 0 else x.clone()
+    A.atlas_layernorm_backward(h, None, dy, None, cfg, dx)
+
+    def two_passes(x, dy):
+        mid = x - x.mean(1, keepdim=True)
+        rstd = 1 / torch.sqrt(mid.square().mean(1, keepdim=True) + EPS)
+        hat = mid * rstd
+        return hat, rstd * (dy - dy.mean(1, keepdim=True) - hat * (dy * hat).mean(1, keepdim=True))
+    exact, plain = two_passes(x.double(), dy.double()), two_passes(x, dy)
+    for name, got, base, want in zip(("y", "dx"), (y, dx), plain, exact):
+        rms = [float((v.double() - want).square().mean().sqrt()) for v in (got, base)]
+        assert rms[0] <= 1.5 * rms[1], f"{name}: {rms[0]:.2e}, two passes {rms[1]:.2e}"
