@@ -7,9 +7,11 @@
 // (mean t)^2 / v; where that is above a bound, or t^2 leaves the 32-bit range, the row takes a second round of sums, about
 // mu.  So one round, and one barrier of a block, is enough but for few rows of ordinary numbers.
 //   An output in 32 bits shows the last places, one in 8 bits has to be what those round to, and gradients are sums of many:
-// PRECISE, c is the mean of the first eight elements and the bound 1 (a row of two hundred of ordinary numbers is above), and mu,
-// held as two numbers (c + mean t rounded, and what that lost), is taken from h before the scaling.  The rms error is then at
-// most 1.3 times that of two passes, whichever elements come first.
+// PRECISE, c is the mean of the first eight elements and the bound 1 (a row of two hundred of ordinary numbers is above).  The
+// scaling takes t, and after a second round h less the new c: aligned rows that are still in shared memory are read again there
+// (32768 x 2048 bf16 to e4m3: 90 us, so held 94); others are held as h, and mu, as two numbers (c + mean t rounded, and
+// what that lost), is taken from h before the scaling.  The rms error is then at most 1.3 times that of two passes, whichever
+// elements come first.
 //   Outputs in 16 bits, whose rounding is a thousand times what is lost: c is the first element and the bound 16 (some rows of
 // ten thousand), and the row is held as t.  Its error is 2.4 times that of two passes in 32 bits, and 17 times with a first element
 // 3.9 deviations from the mean.  (As the others: 524288 x 128 fp32 to bf16 72 us, so 67; 500000 x 40 bf16 + residual 43, so 39.)
@@ -23,8 +25,8 @@
 // read and store neighbouring elements, in 16 bits by pairs where the tensors' rows begin alike.
 //
 // Bound by memory, and next to it by instructions.  Measured (copy rate 6.79 TB/s): 32768 x 2048 bf16 + residual to e4m3 with
-// scales of 128: 92 us, 75% (about the first element: 88; when that was so, a round of sums for the mean and one about it: 119, one
-// vector a thread: 115, a warp a row: 135); 524288 x 128 fp32 to bf16: 67 us, 89%; 20000 x 1371 fp16 + residual: 61 us, 53% (one by
+// scales of 128: 90 us, 77% (about the first element: 88; when that was so, a round of sums for the mean and one about it: 119, one
+// vector a thread: 115, a warp a row: 135); 524288 x 128 fp32 to bf16: 67 us, 89%; 20000 x 1371 fp16 + residual: 57 us, 56% (one by
 // one: 85).
 #pragma once
 #include <initializer_list>
@@ -254,6 +256,11 @@ __device__ __forceinline__ float mean_first(const float* h, int d, int tpr, int 
   return __shfl_sync(0xFFFFFFFFu, pair_sum(pair_add(pair_add(pair(h[0], h[1]), pair(h[2], h[3])), pair_add(pair(h[4], h[5]), pair(h[6], h[7])))), base) *
          (n == 8 ? 0.125f : 1.f / n);
 }
+// c, or 0 if an element less c could leave the 32-bit range: differences are finite where the elements are.
+__device__ __forceinline__ float within(float c) { return fabsf(c) < 1e30f ? c : 0.f; }
+// The second round.  If the first one's mean is a number, so is every element, and the differences from it are summed.  Else
+// the elements times 0 are: 0 of a finite row, whose sum alone has left the range and whose squares do all the more, or NaN.
+__device__ __forceinline__ bool summed(float mean) { return fabsf(mean) < 3.4e38f; }
 // The variance from sums about the mean: infinite where their squares are, and the row then its bias.
 __device__ __forceinline__ float var_of(float mean, float squares, float inv_d) {
   return squares < 3e38f ? fmaf(squares, inv_d, -mean * mean) : squares;
@@ -262,13 +269,19 @@ __device__ __forceinline__ float var_of(float mean, float squares, float inv_d) 
 // One row from its elements h (zeros past its end) and c, a number near its mean.  red: kRed words, odd: every other row of a
 // block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
 // block comes here then).
-template <int K, int AL, bool PRECISE>
+// How a precise row comes to its elements in the second round: it holds them (HELD, and its outputs subtract mu), or holds
+// t and reads them again.
+struct NoReload {
+  __device__ __forceinline__ void operator()(float (*)[8]) const {}
+};
+template <int K, int AL, bool PRECISE, typename R = NoReload>
 __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, int odd, unsigned* gm,
-                                            long row, bool live, float c, float (*h)[8], Params<K, AL>& par) {
+                                            long row, bool live, float c, float (*h)[8], Params<K, AL>& par, const R& reload = R()) {
+  constexpr bool AGAIN = !std::is_same_v<R, NoReload>, HELD = PRECISE && !AGAIN;
   const int lane = AL == 2 ? g.first : g.lane;
   const auto in = [&](int k, int i) { return inside(col<AL>(k, AL == 1 ? 0 : i, g.tpr, lane), a.d); };
   // the sums of the elements less v and of their squares, what is past the row's end left out; keep: the differences, to h
-  const auto less = [&](float v, bool keep, float& s1, float& s2) {
+  const auto less = [&](float v, float times, bool keep, float& s1, float& s2) {
     const pair32 minus = pair(-v, -v);
     s1 = s2 = 0.f;
 #pragma unroll
@@ -279,7 +292,7 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
         float t0, t1;
         unpair(pair_add(pair(h[k][i], h[k][i + 1]), minus), t0, t1);
         if (AL != 1) t0 = in(k, i) ? t0 : 0.f, t1 = in(k, i + 1) ? t1 : 0.f;
-        const pair32 t = pair(t0, t1);
+        const pair32 t = pair(t0 * times, t1 * times);
         p1 = pair_add(p1, t);
         p2 = pair_fma(t, t, p2);
         if (keep) h[k][i] = t0, h[k][i + 1] = t1;
@@ -291,26 +304,40 @@ __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, fl
   };
   if (a.r_out && live) store_row<K, AL>(a.r_out, row * a.sr, a.rt, a.d, g.tpr, lane, h);
   float s1, s2;
-  less(c, !PRECISE, s1, s2);
+  c = within(c);
+  less(c, 1.f, !HELD, s1, s2);
   row_sums2(s1, s2, g, red + odd * 32);
   float mean = s1 * a.inv_d, var = fmaf(s2, a.inv_d, -mean * mean);
   const bool again = far<PRECISE>(mean, var);
   if (g.tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
-    less(PRECISE ? c + mean : mean, false, s1, s2);
+    const bool sum = summed(mean);
+    if (AGAIN) reload(h);
+    less(!sum ? 0.f : PRECISE ? c + mean : mean, sum ? 1.f : 0.f, false, s1, s2);
     row_sums2(s1, s2, g, red + 64);
     if (again) {
       s1 *= a.inv_d;
       var = var_of(s1, s2, a.inv_d);
       c += mean;
       mean = PRECISE ? s1 : mean + s1;
+      if (!sum || !(var < 3e38f)) {
+        c = 0.f, mean = sum ? 0.f : s1, var = __int_as_float(0x7F800000);
+      } else if (AGAIN) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[k][i] -= c;
+      }
     }
-    if (g.tpr > 32) __syncthreads();  // (the next row may come here too)
+    if (g.tpr > 32)
+      __syncthreads();  // (the next row may come here too)
+    else if (AGAIN)
+      __syncwarp();  // (the row's place is filled again when all lanes have read it)
   }
-  const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), mu = c + mean, off = (PRECISE ? (mu - c) - mean : -mean) * rstd;
+  const float rstd = rsqrtf(fmaxf(var, 0.f) + a.eps), mu = c + mean, off = (HELD ? (mu - c) - mean : -mean) * rstd;
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    par.template apply<PRECISE>(a, k, g.tpr, lane, mu, rstd, off, h[k]);
+    par.template apply<HELD>(a, k, g.tpr, lane, mu, rstd, off, h[k]);
     if (!PRECISE || a.ot != ATLAS_E4M3) continue;
     float m = 0.f;
 #pragma unroll
@@ -607,8 +634,9 @@ __device__ __forceinline__ float near_mean(const char* s, int type, int d) {
 // Many rows of a block each (long ones, unaligned: more than there are SMs): a block walks rows and copies the next kStages - 1 to shared memory while it computes
 // one.  The barrier in a row's sums also hands over the next row, whose copies have been waited for before it, and this
 // row's place; a block of one warp (rows of 257 to 512 channels) has no barrier there, and takes one of its own.
-// Registers: 80 (32768 x 2048 bf16 + residual to e4m3: 92 us; 64: 108, 72: 100, 88: 94), 72 of aligned rows of two 32-bit
-// tensors, whose stages leave room for four blocks of an SM anyway (20000 x 2048: 109 us, 80: 122; x 4096: 213 and 228).
+// Registers: 80 (32768 x 2048 bf16 + residual to e4m3, at the step that chose it: 92 us; 64: 108, 72: 100, 88: 94), 72 of
+// aligned rows of two 32-bit tensors, whose stages leave room for four blocks of an SM anyway (20000 x 2048: 109 us, 80: 122; x 4096:
+// 213 and 228).
 template <typename XT, int RB, int K, int AL, bool PRECISE>
 __global__ void __maxnreg__(K > 2 ? 128 : AL == 1 && RB == 4 && sizeof(XT) == 4 ? 72 : 80) forward_ring(Args a) {
   extern __shared__ __align__(16) float sm[];  // [kRed], [stage]: x, r, then the groups' maxima
@@ -650,19 +678,26 @@ __global__ void __maxnreg__(K > 2 ? 128 : AL == 1 && RB == 4 && sizeof(XT) == 4 
       if constexpr (RB > 0) c += raw_float<RB>(ld_raw<RB>(s + xs + ar, at), a.rt);
       if (PRECISE) c = mean8(c);
     }
-    float h[K][8];
+    const auto load = [&](float (*h)[8]) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      slot_floats<XB, AL>(s, ax, code_of<XT>(), k, a.d, g.tpr, lane, h[k]);
-      if constexpr (RB > 0) {
-        float v[8];
-        slot_floats<RB, AL>(s + xs, ar, r_code<XT, RB, AL>(a), k, a.d, g.tpr, lane, v);
-        add8(h[k], v);
+      for (int k = 0; k < K; ++k) {
+        slot_floats<XB, AL>(s, ax, code_of<XT>(), k, a.d, g.tpr, lane, h[k]);
+        if constexpr (RB > 0) {
+          float v[8];
+          slot_floats<RB, AL>(s + xs, ar, r_code<XT, RB, AL>(a), k, a.d, g.tpr, lane, v);
+          add8(h[k], v);
+        }
       }
-    }
+    };
+    float h[K][8];
+    load(h);
     cp_wait<kStages - 2>();  // the next row's
     if (g.tpr <= 32) __syncwarp();
-    forward_row<K, AL, PRECISE>(a, g, sm, odd, gm, row, true, c, h, par);
+    // (rows that begin anywhere stay held: read again 109 us for 82, 20000 x 1371 fp32 + residual)
+    if constexpr (PRECISE && AL == 1)
+      forward_row<K, AL, true>(a, g, sm, odd, gm, row, true, c, h, par, load);
+    else
+      forward_row<K, AL, PRECISE>(a, g, sm, odd, gm, row, true, c, h, par);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   cp_wait<0>();

@@ -69,7 +69,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
     const int ah = AL == 1 || !live ? 0 : ahead(th, row), ad = AL == 1 || !live ? 0 : ahead(td, row), ag = AL == 1 || !live || GB == 0 ? 0 : ahead(tg, row);
     // (pairs: eight lanes' mean, 12001 x 1371 bf16 67.5 us for 69.6)
     float base = AL == 2 ? mean8(raw_float<HB>(ld_raw<HB>(s + ah, place & 7), a.rt)) : near_mean<HB, AL>(s + ah, a.rt, a.d);
-    if (!live) base = 0.f;
+    base = live ? within(base) : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       slot_floats<HB, AL>(s, ah, a.rt, k, a.d, tpr, lane, h[k]);
@@ -85,7 +85,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
     // Sums of t, t^2, w dy and t w dy, t = h - base, a number near the row's mean; and again about base + mean t where what the
     // differences cancel is more than what is left (as in the forward pass).
     float sum[4];
-    const auto sums = [&](float minus) {
+    const auto sums = [&](float minus, float times) {
       pair32 s1 = pair(0.f, 0.f), s2 = s1, s3 = s1, s4 = s1;
       const pair32 less = pair(-minus, -minus);
 #pragma unroll
@@ -96,7 +96,7 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
           unpair(pair_add(pair(h[k][i], h[k][i + 1]), less), t0, t1);
           if (!in(k, i)) t0 = 0.f;
           if (!in(k, i + 1)) t1 = 0.f;
-          const pair32 t = pair(t0, t1), wdy = pair_mul(pair(w[k][i], w[k][i + 1]), pair(dy[k][i], dy[k][i + 1]));
+          const pair32 t = pair(t0 * times, t1 * times), wdy = pair_mul(pair(w[k][i], w[k][i + 1]), pair(dy[k][i], dy[k][i + 1]));
           s1 = pair_add(s1, t);
           s2 = pair_fma(t, t, s2);
           s3 = pair_add(s3, wdy);
@@ -119,18 +119,21 @@ __global__ void __maxnreg__(K == 1 ? 96 : 128) backward_rows(Args a, int tpr, in
         sum[0] = v.x, sum[1] = v.y, sum[2] = v.z, sum[3] = v.w;
       }
     };
-    sums(base);
+    sums(base, 1.f);
     meet(sm + odd * 64);
     float mean = sum[0] * a.inv_d, var = fmaf(sum[1], a.inv_d, -mean * mean), dot = fmaf(-mean, sum[2], sum[3]);
     const bool again = far<true>(mean, var);
     if (tpr > 32 ? again : __any_sync(0xFFFFFFFFu, again)) {
-      sums(base + mean);
+      const bool number = summed(mean);
+      sums(number ? base + mean : 0.f, number ? 1.f : 0.f);
       meet(sm + 128);
       if (again) {
         base += mean;
         mean = sum[0] * a.inv_d;
         var = var_of(mean, sum[1], a.inv_d);
         dot = fmaf(-mean, sum[2], sum[3]);
+        // (a row without a variance, as in the forward pass: nothing but dh reaches dx)
+        if (!number || !(var < 3e38f)) base = dot = 0.f, mean = number ? 0.f : mean, var = __int_as_float(0x7F800000);
       }
       if (tpr > 32) __syncthreads();  // (the next row may come here too)
     }
@@ -232,7 +235,8 @@ __global__ void __launch_bounds__(kLongBlock) long_rows(Args a, float4* stats) {
 #pragma unroll 8
     for (int c = threadIdx.x; c < a.d; c += kLongBlock) sum += h(c), dsum = fmaf(w(c), dy(c), dsum);
     row_sums2(sum, dsum, g, red);
-    const float mean = sum * a.inv_d, mdy = dsum * a.inv_d;
+    float mean = sum * a.inv_d;
+    const float mdy = dsum * a.inv_d;
     float rest = 0.f, ss = 0.f, dot = 0.f;
 #pragma unroll 8
     for (int c = threadIdx.x; c < a.d; c += kLongBlock) {
@@ -244,6 +248,14 @@ __global__ void __launch_bounds__(kLongBlock) long_rows(Args a, float4* stats) {
     row_sums2(rest, ss, g, red + 32);
     dot = row_sum(dot, g, red + 64);
     rest *= a.inv_d;
+    if (!(ss < 3e38f)) {  // no variance, as above: whether all elements are numbers
+      float zero = 0.f, none = 0.f;
+      for (int c = threadIdx.x; c < a.d; c += kLongBlock) zero = fmaf(h(c), 0.f, zero);
+      __syncthreads();
+      row_sums2(zero, none, g, red);
+      __syncthreads();
+      mean = zero, rest = dot = 0.f, ss = __int_as_float(0x7F800000);
+    }
     const float rstd = rsqrtf(fmaxf(fmaf(ss, a.inv_d, -rest * rest), 0.f) + a.eps), off = -rest * rstd;
     const float mhat = rstd * (dot * a.inv_d - rest * mdy);
     if (threadIdx.x == 0 && stats) stats[row] = make_float4(mean, off, rstd, 0.f);

@@ -69,3 +69,37 @@ def test_errors_in_32_bits_are_those_of_two_passes(rows, d, shift, off, first):
     for name, got, base, want in zip(("y", "dx"), (y, dx), plain, exact):
         rms = [float((v.double() - want).square().mean().sqrt()) for v in (got, base)]
         assert rms[0] <= 1.5 * rms[1], f"{name}: {rms[0]:.2e}, two passes {rms[1]:.2e}"
+
+
+@pytest.mark.parametrize("dtype,out", [("fp32", "fp32"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "bf16")])
+@pytest.mark.parametrize("rows,d,stride", [(9, 5, 0), (9, 24, 0), (40, 128, 0), (2000, 37, 0), (9, 1000, 0), (1300, 512, 0), (1300, 1371, 0), (1300, 1371, 1373),
+                                           (1300, 2048, 0), (9, 8200, 0), (200, 9001, 0), (9, 20000, 0)])
+def test_rows_next_to_the_largest_number(rows, d, stride, dtype, out):
+    """The type's lowest value as first element, as first eight, everywhere, and in turn with its largest: neither the distances to
+    a number nor their sums fit in 32 bits.  The variance does not either (or is 0): the row is its bias, its dx is dh, it adds
+    nothing to dw, and the other rows are theirs."""
+    r = rng(72, rows, d)
+    x, _ = strided(r, rows, d, dtype, stride)
+    low = float(torch.finfo(DT[dtype]).min)
+    where = {1: slice(0, 1), 2: slice(0, 8), 4: slice(0, d), 6: slice(0, d, 2), 7: slice(d - 1, d)}
+    for row, at in where.items():
+        x[row, at] = low
+    x[6, 1::2] = -low
+    (w, _), (b, bh), (dy, dyh), (up, _) = draw(r, d, dtype), draw(r, d, dtype), draw(r, (rows, d), dtype), draw(r, (rows, d), dtype)
+    y = torch.empty(rows, d, device="cuda", dtype=DT[out])
+    cfg = cfg_of(rows, d, dtype, x_stride=stride, out_dtype=CODE[out])
+    A.atlas_layernorm_forward(x, None, w, b, cfg, y)
+    h, dx, dw, db = x.contiguous(), torch.empty_like(up), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    space(cfg, A.atlas_layernorm_backward_workspace_bytes(cfg))
+    A.atlas_layernorm_backward(h, w, dy, up, cfg, dx, dw, db)
+    bias = b.to(DT[out])
+    for row in where:
+        assert torch.equal(y[row], bias), row
+        assert torch.equal(dx[row], up[row]), row
+    others = [i for i in range(rows) if i not in where]
+    _, want, mag = R.layernorm(host(h)[others], None, host(w), bh, EPS)
+    close(y[others], want, mag, out, 0, "y")
+    ref = R.layernorm_back(host(h)[others], host(w), dyh[others], host(up)[others], EPS)
+    close(dx[others], *ref["dx"], dtype, 0, "dx")
+    close(dw, *ref["dw"], "fp32", rows / 32, "dw")
+    assert torch.isfinite(db).all()
