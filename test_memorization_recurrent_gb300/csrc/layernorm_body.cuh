@@ -12,7 +12,7 @@
 // (32768 x 2048 bf16 to e4m3: 90 us, so held 94); others are held as h, and mu, as two numbers (c + mean t rounded, and
 // what that lost), is taken from h before the scaling.  The rms error is then at most 1.3 times that of two passes, whichever
 // elements come first.
-//   Outputs in 16 bits, whose rounding is a thousand times what is lost: c is the first element and the bound 16 (some rows of
+//   Outputs in 16 bits of the kernels that walk rows of up to 8192 channels, whose rounding is a thousand times what is lost: c is the first element and the bound 16 (some rows of
 // ten thousand), and the row is held as t.  Its error is 2.4 times that of two passes in 32 bits, and 17 times with a first element
 // 3.9 deviations from the mean.  (As the others: 524288 x 128 fp32 to bf16 72 us, so 67; 500000 x 40 bf16 + residual 43, so 39.)
 //
@@ -448,7 +448,7 @@ __device__ __forceinline__ float element_of(const Args& a, long row, int i) {
   return v;
 }
 
-// A block a row, straight from memory; every output type the precise way.
+// A block a row, straight from memory.
 template <typename XT, int RB, int K, int AL>
 __global__ void __launch_bounds__(512) forward_rows(Args a) {
   extern __shared__ __align__(16) float sm[];
@@ -778,6 +778,10 @@ inline bool pairs(const Args& a, std::initializer_list<Begins> tensors, const Ro
   return base >= 0 && p.tpr * 8 * p.k > a.d;
 }
 
+// The precise kernels of a type, which are compiled by themselves.
+template <typename XT>
+int precise(const Args& a, cudaStream_t st);
+
 template <typename XT, int RB, int AL, bool PRECISE>
 int forward(const Args& args, cudaStream_t st) {
   Args a = args;
@@ -785,6 +789,9 @@ int forward(const Args& args, cudaStream_t st) {
   a.lanes = a.ot != ATLAS_E4M3 || a.group == 0 || (AL == 1 && a.group >= 8 && a.group <= 256 && (a.group & (a.group - 1)) == 0);
   const bool many = a.rows > kSMs * 8;
   const RowPlan p = forward_plan(a.d, many);
+  // (rows straight from memory and those of more than 8192 channels: the precise way, whatever the output)
+  if constexpr (!PRECISE)
+    if (a.d > 256 && !(p.k == 2 && many)) return precise<XT>(args, st);
   if (a.d <= 256) {
     const int rpb = p.block / p.tpr;
     const size_t smem = a.lanes ? 0 : (size_t)rpb * a.ng * 4;
@@ -804,27 +811,28 @@ int forward(const Args& args, cudaStream_t st) {
         if ((RB != 2 || a.rt == a.dt) && pairs(a, {{a.x, a.sx, a.dt}, {a.r, a.sr, a.rt}, {a.r_out, a.sr, a.rt}, {a.y, a.sy, a.ot}}, p)) return run_ring<XT, RB, K, 2, PRECISE>(a, p.block, ring, st);
       return run_ring<XT, RB, K, AL, PRECISE>(a, p.block, ring, st);
     };
-    if constexpr (AL != 1) {
+    if constexpr (PRECISE && AL != 1) {
       if (p.k == 4) return run(std::integral_constant<int, 4>());
       if (p.k == 8) return run(std::integral_constant<int, 8>());
     }
     return run(std::integral_constant<int, 2>());
   }
-  if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
-  if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
-  if (p.k == 4) return run_rows<XT, RB, 4, AL>(a, p.block, st);
-  return run_rows<XT, RB, 8, AL>(a, p.block, st);
+  if constexpr (PRECISE) {
+    if (p.k == 1) return run_rows<XT, RB, 1, AL>(a, p.block, st);
+    if (p.k == 2) return run_rows<XT, RB, 2, AL>(a, p.block, st);
+    if (p.k == 4) return run_rows<XT, RB, 4, AL>(a, p.block, st);
+    return run_rows<XT, RB, 8, AL>(a, p.block, st);
+  } else {
+    return precise<XT>(args, st);
+  }
 }
-template <typename XT, int RB, int AL>
-int forward(const Args& a, cudaStream_t st) {
-  return a.ot == ATLAS_F32 || a.ot == ATLAS_E4M3 ? forward<XT, RB, AL, true>(a, st) : forward<XT, RB, AL, false>(a, st);
-}
-template <typename XT>
+template <typename XT, bool PRECISE>
 int forward(const Args& a, cudaStream_t st) {
   const int rb = !a.r ? 0 : a.rt == ATLAS_F32 ? 4 : 2;
   const bool mixed = rb == 2 && sizeof(XT) == 2 && a.rt != a.dt;  // bf16 and fp16: element by element
-  if (a.wide && !mixed) return rb == 0 ? forward<XT, 0, 1>(a, st) : rb == 2 ? forward<XT, 2, 1>(a, st) : forward<XT, 4, 1>(a, st);
-  return rb == 0 ? forward<XT, 0, 0>(a, st) : rb == 2 ? forward<XT, 2, 0>(a, st) : forward<XT, 4, 0>(a, st);
+  if (a.wide && !mixed)
+    return rb == 0 ? forward<XT, 0, 1, PRECISE>(a, st) : rb == 2 ? forward<XT, 2, 1, PRECISE>(a, st) : forward<XT, 4, 1, PRECISE>(a, st);
+  return rb == 0 ? forward<XT, 0, 0, PRECISE>(a, st) : rb == 2 ? forward<XT, 2, 0, PRECISE>(a, st) : forward<XT, 4, 0, PRECISE>(a, st);
 }
 
 }  // namespace layernorm
