@@ -1241,7 +1241,7 @@ int forward(const GlrArgs& a, const Space& w, cudaStream_t st) {
 template <typename T, int V>
 int run_forward(const GlrArgs& a, cudaStream_t st) {
   if (!a.s.start && a.s.L == 1 && a.y) {
-    forward_token<T, V><<<dim3((a.D + 128 * V - 1) / (128 * V), a.s.B), 128, 0, st>>>(a);
+    forward_token<T, V><<<dim3((a.D - 1) / (128 * V) + 1, a.s.B), 128, 0, st>>>(a);
     return status();
   }
   return forward<T, V>(a, space(a, false, false), st);

@@ -128,3 +128,24 @@ def test_an_infinite_state_is_never_finite_again(D, L, rate, dtype):
             ref = g.ref(b, g.hh[b], dyh[b], dhh[b])
         for k, got in (("y", y[b]), ("h", out[b]), ("dh", dh[b]), *((k, o[k][b]) for k in ("dx", "dr", "di", "dz"))):
             assert (np.isfinite(host(got)) == np.isfinite(ref[k])).all(), (b, k)
+
+
+def test_a_token_of_the_most_channels():
+    """2^31 - 256 channels: the last ones are as they are alone."""
+    D, n = 2 ** 31 - 256, 1000
+    r = rng(85)
+    tail = {k: dev(r.standard_normal(n), "bf16") for k in ("x", "r")}
+    lam, h = dev(r.uniform(-6, 1, n)), dev(r.standard_normal(n))
+
+    def padded(v):
+        t = torch.zeros(1, D, device="cuda", dtype=v.dtype)
+        t[0, -n:] = v
+        return t
+    outs = []
+    for D_, lay in ((D, padded), (n, lambda v: v[None])):
+        cfg = A.make_glr_cfg(1, 1, D_, c=C)
+        y, out = lay(torch.zeros_like(tail["x"])), lay(h)
+        A.atlas_glr_forward(lay(tail["x"]), lay(tail["r"]), None, None, lay(lam)[0], None, None, cfg, y, out, out)
+        outs.append((y[0, -n:].clone(), out[0, -n:].clone()))
+        del y, out
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][0].abs().max() > 0.1
