@@ -315,6 +315,7 @@ size_t atlas_glr_backward_workspace_bytes(const atlas_glr_cfg* cfg);
  *      sequence with carry[b] == 0)
  *   dx, dr, di, dz: dtype out, with the strides of x, r, i, z; di is NULL exactly when i is, dz
  *      exactly when z is
+ *   A sequence that is left out adds nothing: its rows and its dh stay as they are, the others' gradients are theirs.
  *   dlambda [D], dr_bias [D] (NULL exactly when r_bias is), di_bias [D] (NULL exactly when
  *      i_bias is): fp32 out */
 int atlas_glr_backward(const void* x, const void* r, const void* i, const void* z, const float* lambda,

@@ -149,3 +149,38 @@ def test_a_token_of_the_most_channels():
         outs.append((y[0, -n:].clone(), out[0, -n:].clone()))
         del y, out
     assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][0].abs().max() > 0.1
+
+
+@pytest.mark.parametrize("keep", [True, False])
+@pytest.mark.parametrize("D", [40, 33])
+@pytest.mark.parametrize("start,good", [([0, 100, 50, 300], [0]), ([0, 100, 200, 301], [0, 1]), ([-1, 100, 200, 300], [1, 2]),
+                                        ([0, 290, 300, 2 ** 31 - 1], [0, 1]), ([5, 2, 7, 300], [])], ids=str)
+def test_gradients_beside_a_bad_sequence(start, good, D, keep):
+    """A seq_start that falls, ends behind the rows or begins in front of them: the other sequences' gradients are theirs, the
+    rows of those left out stay as they were, and nothing of them is in the parameters' gradients."""
+    rows, B = 300, 3
+    r = rng(86, D)
+    g = Glr(r, B, 0, D, "fp32", packed_rows=rows)
+    (dy, dyh), (dh, dhh) = draw(r, (rows, D), "fp32"), draw(r, (B, D), "fp32")
+    before, st = dh.clone(), status()
+    cfg = g.cfg(B, rows, seq_start=torch.tensor(start, dtype=torch.int32, device="cuda"), status_dev=st)
+    kept = kept_of(cfg) if keep else None
+    y, out = torch.full_like(g.x, 5.0), torch.full_like(g.h, 5.0)
+    g.forward(cfg, y, out, kept)
+    assert int(st) == A.ERR_INVALID
+    st.zero_()
+    o = g.backward(cfg, dy, dh, kept)
+    assert int(st) == A.ERR_INVALID
+    at = {b: slice(start[b], start[b + 1]) for b in good}
+    # (check_grads adds up the good ones' sums; dh by their numbers)
+    check_grads(g, o, dh, [(at[b], b, start[b + 1] - start[b]) for b in good], dyh, dhh)
+    left = torch.ones(rows, dtype=torch.bool, device="cuda")
+    for b in good:
+        left[at[b]] = False
+        close(y[at[b]], g.ref(at[b], g.hh[b])["y"], g.ref(at[b], g.hh[b], mag=True)["y"], "fp32", rows, "y")
+    assert (y[left] == 5).all()
+    for k in ("dx", "dr", "di", "dz"):
+        assert (o[k][left] == 7).all(), k
+    for b in range(B):
+        if b not in good:
+            assert torch.equal(dh[b], before[b]) and (out[b] == 5).all()
