@@ -28,8 +28,10 @@
 // tile come from the state in front of it, which the forward pass keeps (one for kRows rows, in 32 bits).
 //
 // An element takes eight results of the exponential pipe and 65 instructions (147 backward), so issue and latency bound it,
-// then memory.  Measured (copy rate 6.79 TB/s): 8 x 4096 x 2048 bf16, gated: 211 us, 47%, with the backward pass 695, 40%; with
-// one string, 65536 x 512: 184 us, 22%; 9001 packed rows x 1500: 91 us.  Tiles of 64 rows on blocks of four warps:
+// then memory.  Measured (copy rate 6.79 TB/s): 8 x 4096 x 2048 bf16, gated: 211 us, 47%, with the backward pass 691, 40%; with
+// one string, 65536 x 512: 184 us, 22%; 9001 packed rows x 1500: 91 us.  A warp whose rows hold a factor below 0.70 or a first token, or
+// are not all of a sequence and its channels, goes through the maps one by one: with one such channel in 32, 8 x 4096 x 2048 takes
+// 333 us and 1174 with its backward pass, with no other channels 355 and 1218.  Tiles of 64 rows on blocks of four warps:
 // 252 us; of 256 rows on sixteen: 234; three blocks of an SM (80 registers): 227.
 #pragma once
 #include "ops_common.cuh"
@@ -74,8 +76,8 @@ struct Strings {
   unsigned group;               // tiles of a group
   unsigned total;               // tiles x channels in all
 };
-// Sequences of one length are strings of their own where that leaves few places of tiles empty (of 512 rows: at
-// most an eighth).  (As one string, 8 x 4096 x 2048 took 299 us against 211, its training pass 916 against 706.)
+// Sequences of one length are strings of their own where that leaves few places of tiles empty (a fifth at most: of 513
+// rows, 127 of 640 places).  (As one string, 8 x 4096 x 2048 took 299 us against 211, its training pass 916 against 706.)
 inline bool apart_of(const GlrArgs& a) { return !a.s.start && a.s.L > 0 && (a.s.L >= 4 * kRows || a.s.L % kRows == 0); }
 inline long tiles_of(const GlrArgs& a) {  // in all
   if (apart_of(a)) return (long)a.s.B * ((a.s.L - 1L) / kRows + 1);
@@ -142,7 +144,7 @@ __device__ __forceinline__ pair32 gate(pair32 b, pair32& rest) {
 }
 
 // 1 - exp(-s) for 0 <= s < kSlow: s P(s), P fitted to (1 - exp(-s)) / s at Chebyshev nodes (relative error 1.7e-8, 9e-8
-// with the roundings of its evaluation).  Above, the exponential, which most warps never need.
+// with the roundings of its evaluation).  Above, the exponential: decays below 0.70, which channels of long memory never have.
 constexpr float kSlow = 0.36f;
 __device__ __forceinline__ pair32 lost(pair32 s) {
   pair32 p = pair_fma(twice(0.0071831392f), s, twice(-0.041314516f));
