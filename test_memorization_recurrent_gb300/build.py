@@ -12,6 +12,7 @@ library the package loads is always the plain one."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import functools
 import glob
 import hashlib
@@ -19,6 +20,7 @@ import os
 import platform
 import re
 import subprocess
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -80,12 +82,12 @@ def _done(path: str, key: str) -> bool:
 
 def _make(path: str, key: str, cmd, what: str) -> None:
     """Runs cmd, which writes the file that its last argument names, here path under another name."""
-    tmp = f"{path}.tmp{os.getpid()}"
+    tmp = f"{path}.tmp{os.getpid()}.{threading.get_ident()}"
     try:
         r = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
-        if os.path.exists(path + ".made"):
+        with contextlib.suppress(FileNotFoundError):  # (another build may be at the same place)
             os.remove(path + ".made")
         os.replace(tmp, path)
         with open(tmp, "w", encoding="utf-8") as f:

@@ -125,3 +125,14 @@ def test_without_a_compiler_a_library_that_is_done_stays(tree, monkeypatch):
     (root / "nvcc").unlink()
     B._tool.cache_clear()
     assert B.build() == lib
+
+
+def test_builds_at_the_same_time(tree):
+    import concurrent.futures as cf
+    root, compiled = tree
+    with cf.ThreadPoolExecutor(8) as ex:
+        libs = list(ex.map(lambda _: B.build(force=True), range(8)))
+    assert len(set(libs)) == 1 and B.up_to_date()
+    text = open(libs[0]).read()
+    assert text.count("one") == text.count("three") == 1
+    assert not [p for p in os.listdir(root / "out") if ".tmp" in p]
