@@ -12,9 +12,9 @@
 // (32768 x 2048 bf16 to e4m3: 90 us, so held 94); others are held as h, and mu, as two numbers (c + mean t rounded, and
 // what that lost), is taken from h before the scaling.  The rms error is then at most 1.3 times that of two passes, whichever
 // elements come first.
-//   Outputs in 16 bits of the kernels that walk rows of up to 8192 channels, whose rounding is a thousand times what is lost: c is the first element and the bound 16 (some rows of
-// ten thousand), and the row is held as t.  Its error is 2.4 times that of two passes in 32 bits, and 17 times with a first element
-// 3.9 deviations from the mean.  (As the others: 524288 x 128 fp32 to bf16 72 us, so 67; 500000 x 40 bf16 + residual 43, so 39.)
+//   Outputs in 16 bits of the kernels that walk rows of up to 8192 channels, whose rounding is a thousand times what is lost: c is
+// the first element and the bound 16 (some rows of ten thousand), and the row is held as t.  Its error is 2.4 times that of two
+// passes in 32 bits, and 17 times with a first element 3.9 deviations from the mean.  (As the others: 524288 x 128 fp32 to bf16 72 us, so 67; 500000 x 40 bf16 + residual 43, so 39.)
 //
 // Rows of up to 256 channels belong to lanes of a warp; longer ones to a block,
 // which walks rows with the next two on their way through shared memory (up to 1216 rows, eight an SM: a block each, straight
@@ -266,14 +266,13 @@ __device__ __forceinline__ float var_of(float mean, float squares, float inv_d) 
   return squares < 3e38f ? fmaf(squares, inv_d, -mean * mean) : squares;
 }
 
-// One row from its elements h (zeros past its end) and c, a number near its mean.  red: kRed words, odd: every other row of a
-// block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
-// block comes here then).
-// How a precise row comes to its elements in the second round: it holds them (HELD, and its outputs subtract mu), or holds
-// t and reads them again.
+// A row that is not read again: in the second round a precise one has its elements (HELD, its outputs subtract mu).
 struct NoReload {
   __device__ __forceinline__ void operator()(float (*)[8]) const {}
 };
+// One row from its elements h (zeros past its end) and c, a number near its mean.  red: kRed words, odd: every other row of a
+// block; gm: this row's a.ng words for the maxima of groups that are not neighbouring lanes' (every thread of the
+// block comes here then); reload: reads h again, of rows that hold t.
 template <int K, int AL, bool PRECISE, typename R = NoReload>
 __device__ __forceinline__ void forward_row(const Args& a, const RowGroup& g, float* red, int odd, unsigned* gm,
                                             long row, bool live, float c, float (*h)[8], Params<K, AL>& par, const R& reload = R()) {
@@ -802,8 +801,8 @@ int forward(const Args& args, cudaStream_t st) {
     return status();
   }
   const size_t ring = kRed * 4 + (size_t)kStages * (slot_bytes<sizeof(XT), AL>(a.d) + slot_bytes<RB, AL>(a.d)) + (a.lanes ? 0 : (size_t)a.ng * 4);
-  // (rows of more than 8192 channels: only of those that start anywhere; 2000 x 9001 bf16: 125 us straight from memory, 55
-  // so, x 32767: 558 and 156; aligned 2000 x 9000: 25 and 34, x 32768: 89 and 95)
+  // (rows of more than 8192 channels: only of those that start anywhere; 2000 x 9001 bf16: 125 us straight from memory, 58
+  // so, x 32767: 558 and 168; aligned 2000 x 9000: 27 and, when it was chosen, 34, x 32768: 88 and 95)
   if ((p.k == 2 ? many : AL != 1 && p.k > 2 && a.rows > kSMs) && ring <= 200 * 1024) {
     const auto run = [&](auto k) -> int {
       constexpr int K = decltype(k)::value;
