@@ -184,3 +184,37 @@ def test_gradients_beside_a_bad_sequence(start, good, D, keep):
     for b in range(B):
         if b not in good:
             assert torch.equal(dh[b], before[b]) and (out[b] == 5).all()
+
+
+def test_the_longest_sequence():
+    """2^31 - 1 tokens of one channel, decays that forget within a few hundred: the last states, outputs and gradients are those
+    of the last tokens alone, the first gradients those of the first."""
+    L, n = 2 ** 31 - 1, 4096
+    lam = torch.full((1,), -1.0, device="cuda")
+    r = rng(87)
+    parts = {k: dev(r.standard_normal((2, n, 1)), "bf16") for k in ("x", "r", "dy")}
+
+    def whole(k):
+        t = torch.zeros(1, L, 1, device="cuda", dtype=torch.bfloat16)
+        t[0, :n], t[0, -n:] = parts[k][0], parts[k][1]
+        return t
+
+    def run(x, rr, dy, length):
+        cfg = A.make_glr_cfg(1, length, 1, c=C)
+        space(cfg, max(A.atlas_glr_workspace_bytes(cfg), A.atlas_glr_backward_workspace_bytes(cfg)))
+        y, h, kept = torch.empty_like(x), torch.empty(1, 1, device="cuda"), kept_of(cfg)
+        A.atlas_glr_forward(x, rr, None, None, lam, None, None, cfg, y, None, h, kept)
+        ends = [y[0, :n].clone(), y[0, -n:].clone(), h.clone()]
+        dx, dr, dlam = y, torch.empty_like(x), torch.empty_like(lam)  # (y has been read)
+        A.atlas_glr_backward(x, rr, None, None, lam, None, None, cfg, None, kept, dy, None, dx, dr, None, None, dlam, None, None)
+        return ends + [dx[0, :n].clone(), dx[0, -n:].clone(), dr[0, :n].clone(), dr[0, -n:].clone()], dlam.clone()
+    got, dlam = run(whole("x"), whole("r"), whole("dy"), L)
+    first, last = ([p[k][i:i + 1].contiguous() for k in ("x", "r", "dy")] for i, p in ((0, parts), (1, parts)))
+    (a, da), (b, db) = run(*first, n), run(*last, n)
+    # (the first part ends in zeros here and in nothing there, the last one begins with a state that has decayed to nothing)
+    for k, (g, want) in enumerate(zip(got, (a[0], b[1], b[2], a[3], b[4], a[5], b[6]))):
+        cut = slice(0, n - 600) if k in (3, 5) else slice(None)  # the first part's gradients
+        assert (g[cut].float() - want[cut].float()).abs().max() <= 2.0 ** -7 * want.float().abs().max(), k
+        # (the last state is one number, a h + sqrt(1 - a^2) x of normal ones: it may be any small one)
+        assert want.float().abs().max() > (0.1 if want.numel() > 1 else 0), k
+    assert (dlam - da - db).abs() <= 2.0 ** -12 * (da.abs() + db.abs())

@@ -103,3 +103,29 @@ def test_rows_next_to_the_largest_number(rows, d, stride, dtype, out):
     close(dx[others], *ref["dx"], dtype, 0, "dx")
     close(dw, *ref["dw"], "fp32", rows / 32, "dw")
     assert torch.isfinite(db).all()
+
+
+@pytest.mark.parametrize("d", [1, 2])
+def test_more_rows_than_32_bits_count(d):
+    """The last of 2^31 + 9 rows are as they are alone, forward and backward; dbias is of all."""
+    rows, n = 2 ** 31 + 9, 300
+    r = rng(73, d)
+    x = torch.zeros(rows, d, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = dev(r.standard_normal((n, d)), "bf16")
+    b = dev(r.standard_normal(d), "bf16")
+    y = torch.empty_like(x)
+    A.atlas_layernorm_forward(x, None, None, b, cfg_of(rows, d, "bf16"), y)
+    one = torch.empty(n, d, dtype=torch.bfloat16, device="cuda")
+    A.atlas_layernorm_forward(x[-n:], None, None, b, cfg_of(n, d, "bf16"), one)
+    assert torch.equal(y[-n:], one) and bool((y[:-n:99991] == b).all())
+    cfg = cfg_of(rows, d, "bf16")
+    space(cfg, A.atlas_layernorm_backward_workspace_bytes(cfg))
+    db = torch.empty(d, device="cuda")
+    A.atlas_layernorm_backward(x, None, x, None, cfg, y, None, db)
+    small = cfg_of(n, d, "bf16")
+    space(small, A.atlas_layernorm_backward_workspace_bytes(small))
+    A.atlas_layernorm_backward(x[-n:], None, x[-n:], None, small, one, None, None)
+    # (one row a lane or several: other orders of a row's sums)
+    assert (y[-n:].float() - one.float()).abs().max() <= 2.0 ** -6 * max(1.0, float(one.float().abs().max()))
+    ref = host(x[-n:])
+    close(db, ref.sum(0), np.abs(ref).sum(0), "fp32", n, "db")
